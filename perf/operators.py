@@ -345,12 +345,15 @@ def _run_groupnorm(s):
 
 # The 8-bit states. m: signed, 4 bits of exponent and 3 of mantissa (float8_e4m3fn), times its
 # block's scale, which takes the block's largest magnitude to 448. v: its root, unsigned, 4 bits of
-# exponent and 4 of mantissa, times its block's scale, which takes the largest root to 496. All
-# arithmetic in float32, each operation rounded by itself.
+# exponent and 4 of mantissa, times its block's scale, which takes the largest root to 496. A block
+# with nothing over 2^-100 holds zeros. All arithmetic in float32, each operation rounded by itself.
+
+TINY = 2.0 ** -100
+
 
 def _to_signed8(m):
     top = m.view(-1, BLOCK).abs().amax(1, keepdim=True)
-    inv = torch.where(top > 0, 448.0 / top, 0.0)
+    inv = torch.where(top > TINY, top.reciprocal() * 448.0, 0.0)
     return (m.view(-1, BLOCK) * inv).to(torch.float8_e4m3fn).view(-1), (top * (1.0 / 448.0)).view(-1)
 
 
@@ -361,7 +364,7 @@ def _from_signed8(code, scale):
 def _to_root8(v):
     root = torch.sqrt(v).view(-1, BLOCK)
     top = root.amax(1, keepdim=True)
-    x = root * torch.where(top > 0, 496.0 / top, 0.0)
+    x = root * torch.where(top > TINY, top.reciprocal() * 496.0, 0.0)
     # 2^-6 is the smallest value with a whole mantissa; below it steps of 2^-10
     bits = x.view(torch.int32)
     normal = ((bits + 0x3FFFF + ((bits >> 19) & 1)) >> 19) - (120 << 4)
