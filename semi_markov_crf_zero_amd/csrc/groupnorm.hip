@@ -1,0 +1,512 @@
+// groupnorm.hip -- group norm with an activation over channels-last
+// sequences [B][T][C], and its gradient.
+//
+//   h = (x - mean) rstd over the lengths[b] positions and C/G channels of a
+//   group;  z = h w + b;  y = act(z)
+//   dz = dy act'(z),  d = dz w:
+//   dx = rstd (d - mean(d) - h mean(d h)),  dw = sum dz h,  db = sum dz
+//
+// A thread owns V neighbouring channels (one 16-byte load of the tensor's
+// type) of every R-th position, so a wave's load covers whole rows.  The
+// sums over a sequence are split over workgroups (slabs of positions) that
+// leave one partial per channel vector; a small kernel adds them in a fixed
+// order in float64, and the last pass reads x again and writes the result.
+//
+// Sums.  mean and var come from sums of (x - pivot) and its square in
+// float64, the pivot the group's first element: the subtraction takes the
+// common offset out before anything is squared.
+#include "encoder.h"
+
+namespace semicrf {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+struct GnArgs {
+  int B, T, C, G, Cg;
+  int cv;     // channel vectors = C / V
+  int cvt;    // of them in one workgroup's tile
+  int tiles;  // of a row
+  int rows;   // positions a workgroup takes at once = kThreads / cvt
+  int slab;   // positions of one workgroup
+  int slabs;  // of a sequence
+  float eps;
+  const int32_t *lengths;
+  const float *weight, *bias;
+};
+
+template <int ACT>
+__device__ __forceinline__ float act(float z) {
+  if (ACT == SEMICRF_ACT_SILU) return z / (1.f + expf(-z));
+  if (ACT == SEMICRF_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
+  if (ACT == SEMICRF_ACT_RELU) return z > 0.f ? z : z == z ? 0.f : z;
+  return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if (ACT == SEMICRF_ACT_SILU) {
+    const float e = 1.f / (1.f + expf(-z));
+    return e * (1.f + z * (1.f - e));
+  }
+  if (ACT == SEMICRF_ACT_GELU)
+    return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
+           z * expf(-0.5f * z * z) * 0.39894228040143268f;
+  if (ACT == SEMICRF_ACT_RELU) return z > 0.f ? 1.f : 0.f;
+  return 1.f;
+}
+
+}  // namespace
+
+// Partial sums of x - pivot and its square: part[b][slab][channel vector].
+template <typename T, int V>
+__global__ __launch_bounds__(kThreads) void k_gn_sums(GnArgs p, const T *x, double2 *part) {
+  __shared__ double2 red[kThreads];
+  const int b = blockIdx.x / (p.slabs * p.tiles), s = blockIdx.x / p.tiles % p.slabs;
+  const int c = threadIdx.x % p.cvt, r = threadIdx.x / p.cvt;
+  const int v = blockIdx.x % p.tiles * p.cvt + c;
+  const int len = max(valid_length(p.lengths, b, p.T), 0);
+  const int t1 = min(len, (s + 1) * p.slab);
+  double sum = 0, sq = 0;
+  if (r < p.rows && v < p.cv && len > 0) {
+    const T *row = x + (int64_t)b * p.T * p.C;
+    const float pivot = (float)row[v * V / p.Cg * p.Cg];
+    row += (int64_t)v * V;
+    for (int t = s * p.slab + r; t < t1; t += p.rows) {
+      const Pack<T, V> d = *reinterpret_cast<const Pack<T, V> *>(row + (int64_t)t * p.C);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const double e = (float)d.v[i] - pivot;
+        sum += e;
+        sq += e * e;
+      }
+    }
+  }
+  red[threadIdx.x] = make_double2(sum, sq);
+  __syncthreads();
+  if (r == 0 && v < p.cv) {
+    for (int k = 1; k < p.rows; ++k) {
+      sum += red[k * p.cvt + c].x;
+      sq += red[k * p.cvt + c].y;
+    }
+    part[((int64_t)b * p.slabs + s) * p.cv + v] = make_double2(sum, sq);
+  }
+}
+
+// One wave per sequence and group: mean and 1/sqrt(var + eps).
+template <typename T>
+__global__ __launch_bounds__(64) void k_gn_stats(GnArgs p, int V, const T *x, const double2 *part,
+                                                 float *stats) {
+  const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
+  const int vg = p.Cg / V;  // channel vectors of a group
+  const int len = valid_length(p.lengths, b, p.T);
+  double sum = 0, sq = 0;
+  for (int e = threadIdx.x; e < p.slabs * vg; e += 64) {
+    const double2 d = part[((int64_t)b * p.slabs + e / vg) * p.cv + g * vg + e % vg];
+    sum += d.x;
+    sq += d.y;
+  }
+  for (int o = 32; o; o >>= 1) {
+    sum += __shfl_xor(sum, o);
+    sq += __shfl_xor(sq, o);
+  }
+  if (threadIdx.x == 0) {
+    float mean = 0.f, rstd = 0.f;
+    if (len > 0) {
+      const double n = (double)len * p.Cg, m = sum / n;
+      mean = (float)((double)(float)x[(int64_t)b * p.T * p.C + g * p.Cg] + m);
+      const double var = sq / n - m * m;
+      rstd = (float)(1.0 / sqrt((var > 0 ? var : var == var ? 0.0 : var) + (double)p.eps));
+    } else if (len < 0) {
+      mean = rstd = __builtin_nanf("");
+    }
+    stats[2 * ((int64_t)b * p.G + g)] = mean;
+    stats[2 * ((int64_t)b * p.G + g) + 1] = rstd;
+  }
+}
+
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(kThreads) void k_gn_apply(GnArgs p, const T *x, const float *stats,
+                                                       T *y) {
+  const int b = blockIdx.x / (p.slabs * p.tiles), s = blockIdx.x / p.tiles % p.slabs;
+  const int c = threadIdx.x % p.cvt, r = threadIdx.x / p.cvt;
+  const int v = blockIdx.x % p.tiles * p.cvt + c;
+  if (r >= p.rows || v >= p.cv) return;
+  const int valid = valid_length(p.lengths, b, p.T);
+  const int t1 = min(p.T, (s + 1) * p.slab), len = min(t1, max(valid, 0));
+  const float fill = valid < 0 ? __builtin_nanf("") : 0.f;
+  float mean[V], rstd[V], w[V], bi[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int ch = v * V + i;
+    const float *st = stats + 2 * ((int64_t)b * p.G + ch / p.Cg);
+    mean[i] = st[0];
+    rstd[i] = st[1];
+    w[i] = p.weight ? p.weight[ch] : 1.f;
+    bi[i] = p.bias ? p.bias[ch] : 0.f;
+  }
+  const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
+  for (int t = s * p.slab + r; t < t1; t += p.rows) {
+    Pack<T, V> d;
+    if (t < len) {
+      d = *reinterpret_cast<const Pack<T, V> *>(x + base + (int64_t)t * p.C);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        d.v[i] = (T)act<ACT>(((float)d.v[i] - mean[i]) * rstd[i] * w[i] + bi[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) d.v[i] = (T)fill;
+    }
+    *reinterpret_cast<Pack<T, V> *>(y + base + (int64_t)t * p.C) = d;
+  }
+}
+
+// Partial sums of dz and dz h per channel: part[b][slab][C].
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, const T *dy,
+                                                          const float *stats, float2 *part) {
+  __shared__ float2 red[kThreads * V];
+  const int b = blockIdx.x / (p.slabs * p.tiles), s = blockIdx.x / p.tiles % p.slabs;
+  const int c = threadIdx.x % p.cvt, r = threadIdx.x / p.cvt;
+  const int v = blockIdx.x % p.tiles * p.cvt + c;
+  const int len = max(valid_length(p.lengths, b, p.T), 0);
+  const int t1 = min(len, (s + 1) * p.slab);
+  float s1[V], s2[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.f;
+  if (r < p.rows && v < p.cv) {
+    float mean[V], rstd[V], w[V], bi[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int ch = v * V + i;
+      const float *st = stats + 2 * ((int64_t)b * p.G + ch / p.Cg);
+      mean[i] = st[0];
+      rstd[i] = st[1];
+      w[i] = p.weight ? p.weight[ch] : 1.f;
+      bi[i] = p.bias ? p.bias[ch] : 0.f;
+    }
+    const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
+    for (int t = s * p.slab + r; t < t1; t += p.rows) {
+      const Pack<T, V> d = *reinterpret_cast<const Pack<T, V> *>(x + base + (int64_t)t * p.C);
+      const Pack<T, V> e = *reinterpret_cast<const Pack<T, V> *>(dy + base + (int64_t)t * p.C);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float h = ((float)d.v[i] - mean[i]) * rstd[i];
+        const float dz = (float)e.v[i] * act_slope<ACT>(h * w[i] + bi[i]);
+        s1[i] += dz;
+        s2[i] += dz * h;
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) red[threadIdx.x * V + i] = make_float2(s1[i], s2[i]);
+  __syncthreads();
+  if (r == 0 && v < p.cv) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      double a1 = s1[i], a2 = s2[i];
+      for (int k = 1; k < p.rows; ++k) {
+        a1 += red[(k * p.cvt + c) * V + i].x;
+        a2 += red[(k * p.cvt + c) * V + i].y;
+      }
+      part[((int64_t)b * p.slabs + s) * p.C + v * V + i] = make_float2((float)a1, (float)a2);
+    }
+  }
+}
+
+// One wave per sequence and group: the channels' sums over the slabs, and
+// mean(d), mean(d h) of the group.
+__global__ __launch_bounds__(64) void k_gn_bwd_group(GnArgs p, const float2 *part, double2 *sums,
+                                                     float2 *coef) {
+  const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
+  const int len = valid_length(p.lengths, b, p.T);
+  double m1 = 0, m2 = 0;
+  for (int c = threadIdx.x; c < p.Cg; c += 64) {
+    const int ch = g * p.Cg + c;
+    double a1 = 0, a2 = 0;
+    for (int s = 0; s < p.slabs; ++s) {
+      const float2 d = part[((int64_t)b * p.slabs + s) * p.C + ch];
+      a1 += d.x;
+      a2 += d.y;
+    }
+    sums[(int64_t)b * p.C + ch] = make_double2(a1, a2);
+    const double w = p.weight ? p.weight[ch] : 1.0;
+    m1 += w * a1;
+    m2 += w * a2;
+  }
+  for (int o = 32; o; o >>= 1) {
+    m1 += __shfl_xor(m1, o);
+    m2 += __shfl_xor(m2, o);
+  }
+  if (threadIdx.x == 0) {
+    const double n = (double)max(len, 1) * p.Cg;
+    coef[(int64_t)b * p.G + g] = make_float2((float)(m1 / n), (float)(m2 / n));
+  }
+}
+
+// One workgroup per 64 channels: the sums over the batch.
+__global__ __launch_bounds__(256) void k_gn_bwd_params(GnArgs p, const double2 *sums, float *dw,
+                                                       float *db) {
+  __shared__ double2 red[256];
+  const int ch = blockIdx.x * 64 + threadIdx.x % 64, q = threadIdx.x / 64;
+  double a1 = 0, a2 = 0;
+  if (ch < p.C)
+    for (int b = q; b < p.B; b += 4) {
+      const double2 d = sums[(int64_t)b * p.C + ch];
+      a1 += d.x;
+      a2 += d.y;
+    }
+  red[threadIdx.x] = make_double2(a1, a2);
+  __syncthreads();
+  if (q == 0 && ch < p.C) {
+    for (int k = 1; k < 4; ++k) {
+      a1 += red[k * 64 + threadIdx.x].x;
+      a2 += red[k * 64 + threadIdx.x].y;
+    }
+    if (db) db[ch] = (float)a1;
+    if (dw) dw[ch] = (float)a2;
+  }
+}
+
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GnArgs p, const T *x, const T *dy,
+                                                           const float *stats, const float2 *coef,
+                                                           T *dx) {
+  const int b = blockIdx.x / (p.slabs * p.tiles), s = blockIdx.x / p.tiles % p.slabs;
+  const int c = threadIdx.x % p.cvt, r = threadIdx.x / p.cvt;
+  const int v = blockIdx.x % p.tiles * p.cvt + c;
+  if (r >= p.rows || v >= p.cv) return;
+  const int t1 = min(p.T, (s + 1) * p.slab);
+  const int len = min(t1, max(valid_length(p.lengths, b, p.T), 0));
+  float mean[V], rstd[V], w[V], bi[V], m1[V], m2[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int ch = v * V + i;
+    const int64_t bg = (int64_t)b * p.G + ch / p.Cg;
+    mean[i] = stats[2 * bg];
+    rstd[i] = stats[2 * bg + 1];
+    m1[i] = coef[bg].x;
+    m2[i] = coef[bg].y;
+    w[i] = p.weight ? p.weight[ch] : 1.f;
+    bi[i] = p.bias ? p.bias[ch] : 0.f;
+  }
+  const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
+  for (int t = s * p.slab + r; t < t1; t += p.rows) {
+    Pack<T, V> d;
+    if (t < len) {
+      d = *reinterpret_cast<const Pack<T, V> *>(x + base + (int64_t)t * p.C);
+      const Pack<T, V> e = *reinterpret_cast<const Pack<T, V> *>(dy + base + (int64_t)t * p.C);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float h = ((float)d.v[i] - mean[i]) * rstd[i];
+        const float dh = (float)e.v[i] * act_slope<ACT>(h * w[i] + bi[i]) * w[i];
+        d.v[i] = (T)(rstd[i] * (dh - m1[i] - h * m2[i]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) d.v[i] = (T)0.f;
+    }
+    *reinterpret_cast<Pack<T, V> *>(dx + base + (int64_t)t * p.C) = d;
+  }
+}
+
+namespace {
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+semicrf_status_t check(const semicrf_groupnorm_shape_t *s) {
+  if (!s) return SEMICRF_ERR_NULL;
+  if (s->B < 1 || s->T < 1 || s->C < 1 || s->G < 1 || s->C % s->G)
+    return SEMICRF_ERR_SHAPE;
+  // the grid counts sequences times groups, and times the tiles of a row
+  if (s->T > 1 << 30 || (int64_t)s->B * (s->C + 4096) > 0x7fffffff) return SEMICRF_ERR_SHAPE;
+  if (!dtype_ok(s->dtype) || s->act < SEMICRF_ACT_NONE || s->act > SEMICRF_ACT_RELU ||
+      !(s->eps >= 0.f))
+    return SEMICRF_ERR_ARG;
+  return SEMICRF_OK;
+}
+
+// Channels of a thread: 16 bytes of them, or the largest power of two below
+// that divides a group and that every pointer is aligned for.
+int vector_width(const semicrf_groupnorm_shape_t *s, const void *const *ptrs, int n) {
+  const int size = elem_size(s->dtype), Cg = s->C / s->G;
+  int V = 16 / size;
+  while (V > 1 && Cg % V) V /= 2;
+  for (int i = 0; i < n; ++i)
+    while (V > 1 && (uintptr_t)ptrs[i] % (V * size)) V /= 2;
+  return V;
+}
+
+GnArgs args(const semicrf_groupnorm_shape_t *s, int V) {
+  GnArgs p = {};
+  p.B = s->B, p.T = s->T, p.C = s->C, p.G = s->G, p.Cg = s->C / s->G;
+  p.cv = s->C / V;
+  p.cvt = p.cv < kThreads ? p.cv : kThreads;
+  p.tiles = (p.cv + p.cvt - 1) / p.cvt;
+  p.rows = kThreads / p.cvt;
+  // slabs: enough workgroups to fill the GPU several times over, but no
+  // shorter than four positions a thread
+  const int64_t tiles = (int64_t)s->B * p.tiles;
+  const int64_t most = (s->T + 4 * p.rows - 1) / (4 * p.rows);
+  int64_t slabs = (2048 + tiles - 1) / tiles;
+  if (slabs > most) slabs = most;
+  if (slabs < 1) slabs = 1;
+  p.slab = (int)((s->T + slabs - 1) / slabs);
+  p.slabs = (s->T + p.slab - 1) / p.slab;
+  p.eps = s->eps;
+  return p;
+}
+
+// Workspace for the narrowest vectors (the widest partials).
+size_t need(const semicrf_groupnorm_shape_t *s, int backward) {
+  size_t n = 0;
+  for (int V = 1; V <= 8; V *= 2) {
+    if ((s->C / s->G) % V) break;
+    const GnArgs p = args(s, V);
+    size_t m;
+    if (backward)
+      m = align256((size_t)p.B * p.slabs * p.C * sizeof(float2)) +
+          align256((size_t)p.B * p.C * sizeof(double2)) +
+          align256((size_t)p.B * p.G * sizeof(float2));
+    else
+      m = align256((size_t)p.B * p.slabs * p.cv * sizeof(double2));
+    if (m > n) n = m;
+  }
+  return n;
+}
+
+template <typename T, int V, int ACT>
+semicrf_status_t run_fwd(const GnArgs &p, const void *x, void *y, float *stats, void *ws,
+                         hipStream_t st) {
+  const unsigned grid = (unsigned)p.B * p.slabs * p.tiles;
+  k_gn_sums<T, V><<<grid, kThreads, 0, st>>>(p, (const T *)x, (double2 *)ws);
+  k_gn_stats<T><<<(unsigned)p.B * p.G, 64, 0, st>>>(p, V, (const T *)x, (const double2 *)ws, stats);
+  k_gn_apply<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, stats, (T *)y);
+  return launch_status();
+}
+
+template <typename T, int V, int ACT>
+semicrf_status_t run_bwd(const GnArgs &p, const void *x, const void *dy, const float *stats,
+                         void *dx, float *dw, float *db, void *ws, hipStream_t st) {
+  const unsigned grid = (unsigned)p.B * p.slabs * p.tiles;
+  char *w = (char *)ws;
+  float2 *part = (float2 *)w;
+  w += align256((size_t)p.B * p.slabs * p.C * sizeof(float2));
+  double2 *sums = (double2 *)w;
+  w += align256((size_t)p.B * p.C * sizeof(double2));
+  float2 *coef = (float2 *)w;
+  k_gn_bwd_sums<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats, part);
+  k_gn_bwd_group<<<(unsigned)p.B * p.G, 64, 0, st>>>(p, part, sums, coef);
+  if (dw || db) k_gn_bwd_params<<<(p.C + 63) / 64, 256, 0, st>>>(p, sums, dw, db);
+  k_gn_bwd_apply<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats, coef,
+                                                       (T *)dx);
+  return launch_status();
+}
+
+// f<T, V, ACT>() for the call's type, vector width and activation.
+template <typename T, int V, typename F>
+semicrf_status_t by_act(int act, F f) {
+  switch (act) {
+    case SEMICRF_ACT_SILU: return f.template run<T, V, SEMICRF_ACT_SILU>();
+    case SEMICRF_ACT_GELU: return f.template run<T, V, SEMICRF_ACT_GELU>();
+    case SEMICRF_ACT_RELU: return f.template run<T, V, SEMICRF_ACT_RELU>();
+    default: return f.template run<T, V, SEMICRF_ACT_NONE>();
+  }
+}
+template <typename F>
+semicrf_status_t dispatch(int dtype, int V, int act, F f) {
+  if (dtype == SEMICRF_F32) {
+    if (V == 4) return by_act<float, 4>(act, f);
+    return V == 2 ? by_act<float, 2>(act, f) : by_act<float, 1>(act, f);
+  }
+  if (dtype == SEMICRF_BF16) {
+    if (V == 8) return by_act<bf16, 8>(act, f);
+    if (V == 4) return by_act<bf16, 4>(act, f);
+    return V == 2 ? by_act<bf16, 2>(act, f) : by_act<bf16, 1>(act, f);
+  }
+  if (V == 8) return by_act<f16, 8>(act, f);
+  if (V == 4) return by_act<f16, 4>(act, f);
+  return V == 2 ? by_act<f16, 2>(act, f) : by_act<f16, 1>(act, f);
+}
+
+struct Fwd {
+  GnArgs p;
+  const void *x;
+  void *y;
+  float *stats;
+  void *ws;
+  hipStream_t st;
+  template <typename T, int V, int ACT>
+  semicrf_status_t run() {
+    return run_fwd<T, V, ACT>(p, x, y, stats, ws, st);
+  }
+};
+
+struct Bwd {
+  GnArgs p;
+  const void *x, *dy;
+  const float *stats;
+  void *dx;
+  float *dw, *db;
+  void *ws;
+  hipStream_t st;
+  template <typename T, int V, int ACT>
+  semicrf_status_t run() {
+    return run_bwd<T, V, ACT>(p, x, dy, stats, dx, dw, db, ws, st);
+  }
+};
+
+}  // namespace
+
+}  // namespace semicrf
+
+using namespace semicrf;
+
+extern "C" {
+
+semicrf_status_t semicrf_groupnorm_workspace_size(const semicrf_groupnorm_shape_t *s, int backward,
+                                                  size_t *bytes) {
+  if (!bytes) return SEMICRF_ERR_NULL;
+  const semicrf_status_t e = check(s);
+  if (e != SEMICRF_OK) return e;
+  *bytes = need(s, backward);
+  return SEMICRF_OK;
+}
+
+semicrf_status_t semicrf_groupnorm_fwd(const semicrf_groupnorm_shape_t *s, const void *x,
+                                       const float *weight, const float *bias,
+                                       const int32_t *lengths, void *y, float *stats,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+  if (!s || !x || !y || !stats) return SEMICRF_ERR_NULL;
+  const semicrf_status_t e = check(s);
+  if (e != SEMICRF_OK) return e;
+  if (!workspace || workspace_bytes < need(s, 0)) return SEMICRF_ERR_WORKSPACE;
+  (void)hipGetLastError();
+  const void *ptrs[] = {x, y};
+  const int V = vector_width(s, ptrs, 2);
+  Fwd f = {args(s, V), x, y, stats, workspace, (hipStream_t)stream};
+  f.p.lengths = lengths, f.p.weight = weight, f.p.bias = bias;
+  return dispatch(s->dtype, V, s->act, f);
+}
+
+semicrf_status_t semicrf_groupnorm_bwd(const semicrf_groupnorm_shape_t *s, const void *x,
+                                       const float *weight, const float *bias,
+                                       const int32_t *lengths, const void *grad_y,
+                                       const float *stats, void *grad_x, float *grad_weight,
+                                       float *grad_bias, void *workspace, size_t workspace_bytes,
+                                       void *stream) {
+  if (!s || !x || !grad_y || !stats || !grad_x) return SEMICRF_ERR_NULL;
+  const semicrf_status_t e = check(s);
+  if (e != SEMICRF_OK) return e;
+  if (!workspace || workspace_bytes < need(s, 1)) return SEMICRF_ERR_WORKSPACE;
+  (void)hipGetLastError();
+  const void *ptrs[] = {x, grad_y, grad_x};
+  const int V = vector_width(s, ptrs, 3);
+  Bwd f = {args(s, V), x, grad_y, stats, grad_x, grad_weight, grad_bias, workspace,
+           (hipStream_t)stream};
+  f.p.lengths = lengths, f.p.weight = weight, f.p.bias = bias;
+  return dispatch(s->dtype, V, s->act, f);
+}
+
+}  // extern "C"

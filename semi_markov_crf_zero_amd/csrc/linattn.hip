@@ -1,0 +1,612 @@
+// linattn.hip -- linear attention with a decay for each head.
+//
+//   S_t = e^g S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+//
+// Every pass of the operator, forward or backward, is one form of the sum
+//   out_i = sum_{j <= i} e^{g (i-j)} (a_i . b_j) c_j + e^{g (i + off)} X^T a_i
+// over positions taken forwards or backwards:
+//   o       (a, b, c) = (q, k, v), forwards, X = state_in;
+//   grad_q  (grad_o, v, k), forwards, X = state_in^T;
+//   grad_k  (v, grad_o, q), backwards, X = grad_state^T;
+//   grad_v  (k, q, grad_o), backwards, X = grad_state;
+// so one kernel serves all four.  It works in chunks of L positions:
+//   P = (A B^T) * decay, lower triangle;  O = P C + decay (A X);
+//   X <- e^{g L} X + (decay B)^T C,
+// products on the matrix cores, X in float32 accumulators of the wave that
+// owns its 16 columns, from the first chunk of a sequence to its last.
+//
+// Decays are e^{g n} with n >= 0 (at most 1 for g <= 0: no quotient of
+// decays is ever formed), and e^{g 0} = 1 also for g = -inf.
+//
+// Read forwards, X enters position i with e^{g (i+1)} and a chunk adds c_j
+// with e^{g (n-1-j)}; the gradient of a state, read backwards, enters with
+// e^{g i'} and adds with e^{g (n-j')}: off = 1 or 0 moves one step of the
+// decay from the reading to the adding side.
+//
+// Positions past the length are loaded as zeros (a select, so NaN there
+// stays out) and their rows of the output are written as 0.
+#include "encoder.h"
+
+namespace semicrf {
+
+namespace {
+
+typedef f32x4_t f4;
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef s4 __attribute__((address_space(3))) lds_s4;
+
+constexpr int kThreads = 256;  // four waves, 16 output columns each
+constexpr int kCols = 64;      // output columns of a workgroup
+
+// One tensor as the kernel reads it: element strides of batch, position and
+// head, and how many heads of the call share one of its heads.
+struct View {
+  const void *p;
+  int64_t sb, st, sh;
+  int share;
+};
+
+struct LaArgs {
+  View a, b, c;
+  const float *log_decay;
+  const int32_t *lengths;
+  const float *x_in;  // [B][H][Da][Dc], or [B][H][Dc][Da] if x_tr; or NULL
+  float *x_out;       // the same layout; or NULL
+  void *out;          // [B][T][H][Dc] contiguous; or NULL
+  int x_tr;
+  int rev, off;
+  float bad;  // what a sequence without a valid length gets: NaN, or 0 for gradients
+  float p_scale, x_scale, add_scale;  // of P, of A X, of what a chunk adds to X
+  int B, T, H, Da, Dc;
+  int ctiles;
+};
+
+// A fragment is a lane's part of one operand over a 32-wide stretch of the
+// contraction: indices {4g + r} and {16 + 4g + r} (g = lane / 16, r < 4) of
+// row or column lane % 16.  That is how two neighbouring 16x16 accumulator
+// tiles hold their rows, so X goes from accumulators to operands in place.
+template <typename T>
+struct Frag;
+template <>
+struct Frag<bf16> {
+  bf8 v;
+};
+template <>
+struct Frag<float> {
+  float v[8];
+};
+
+__device__ __forceinline__ f4 mma(const Frag<bf16> &a, const Frag<bf16> &b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4 mma(const Frag<float> &a, const Frag<float> &b, f4 c) {
+#pragma unroll
+  for (int r = 0; r < 8; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[r], b.v[r], c, 0, 0, 0);
+  return c;
+}
+
+// Fragment of a row whose contraction index is contiguous: p at index 4g.
+__device__ __forceinline__ Frag<bf16> frag_row(const bf16 *p) {
+  typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+  const bf4 lo = *reinterpret_cast<const bf4 *>(p), hi = *reinterpret_cast<const bf4 *>(p + 16);
+  return {__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)};
+}
+__device__ __forceinline__ Frag<float> frag_row(const float *p) {
+  const f4 lo = *reinterpret_cast<const f4 *>(p), hi = *reinterpret_cast<const f4 *>(p + 16);
+  return {{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
+}
+
+// Fragment of a column whose contraction index runs over LDS rows: the tile
+// of 32 rows x 16 columns at p (row stride ld).  16-bit elements come through
+// the transposing LDS read: in each group of 16 lanes, lane i names 4
+// elements of row i / 4 and gets column i of the four rows.
+__device__ __forceinline__ Frag<bf16> frag_col(const bf16 *p, int ld, int lane) {
+  const int g = lane >> 4, i = lane & 15;
+  const bf16 *q = p + (4 * g + (i >> 2)) * ld + (i & 3) * 4;
+  const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q));
+  const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + 16 * ld));
+  return {__builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7))};
+}
+__device__ __forceinline__ Frag<float> frag_col(const float *p, int ld, int lane) {
+  const float *q = p + (4 * (lane >> 4)) * ld + (lane & 15);
+  Frag<float> f;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    f.v[r] = q[r * ld];
+    f.v[4 + r] = q[(16 + r) * ld];
+  }
+  return f;
+}
+
+// Float32 values as a sum of N fragments of the operand type.  A bfloat16
+// part leaves at most 2^-8 of what it was given: two parts of P and X leave
+// 2^-16, far below the rounding of a 16-bit output (2^-8 or 2^-11); three
+// parts of what is added to X leave 2^-24, so the float32 state is as exact
+// as one summed from float32 products.
+template <typename T>
+struct Parts;
+template <>
+struct Parts<bf16> {
+  static constexpr int kRead = 2, kAdd = 3;
+};
+template <>
+struct Parts<float> {
+  static constexpr int kRead = 1, kAdd = 1;
+};
+template <int N>
+__device__ __forceinline__ void split(const float *x, Frag<bf16> *f) {
+  float r[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) r[e] = x[e];
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      f[n].v[e] = (bf16)r[e];
+      r[e] -= (float)f[n].v[e];
+    }
+}
+template <int N>
+__device__ __forceinline__ void split(const float *x, Frag<float> *f) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) f[0].v[e] = x[e];
+}
+__device__ __forceinline__ void values(const Frag<bf16> &f, float *x) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = (float)f.v[e];
+}
+__device__ __forceinline__ void values(const Frag<float> &f, float *x) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = f.v[e];
+}
+
+// n rows (of L) of a chunk into LDS, zeros past row n and past column D.
+template <typename T, typename CT, int W, int L>
+__device__ __forceinline__ void stage(CT *lds, const T *src, int64_t st, int D, int n, int col0) {
+  constexpr int ld = W + 16 / sizeof(CT);
+  for (int e = threadIdx.x; e < L * W; e += kThreads) {
+    const int i = e / W, d = e % W;
+    lds[i * ld + d] = i < n && col0 + d < D ? (CT)(float)src[i * st + col0 + d] : (CT)0.f;
+  }
+}
+
+}  // namespace
+
+// One workgroup: one sequence and head, kCols columns of the output, every
+// chunk in turn.  T: the tensors' type; CT: the operands' type (bfloat16 as
+// it is; float32 and float16 in float32: float16 would need its range
+// watched in P and X); OT: the output's; DA: Da rounded up.
+template <typename T, typename CT, typename OT, int DA, int L>
+__global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
+  constexpr int pad = 16 / sizeof(CT);
+  constexpr int lda = DA + pad, ldc = kCols + pad, ldp = L + pad;
+  constexpr int KB = DA / 32;
+  constexpr int NR = Parts<CT>::kRead, NA = Parts<CT>::kAdd;
+  __shared__ alignas(16) CT A[2 * L * lda + L * ldc + NR * L * ldp];
+  __shared__ float dec[L + 1];  // e^{g n}
+  CT *const Bm = A + L * lda;
+  CT *const C = Bm + L * lda;
+  CT *const P = C + L * ldc;
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  const int ct = blockIdx.x % p.ctiles, bh = blockIdx.x / p.ctiles;
+  const int h = bh % p.H, b = bh / p.H;
+  const int c0 = ct * kCols;
+  const int valid = valid_length(p.lengths, b, p.T);
+  const int len = max(valid, 0);
+
+  const float gd = p.log_decay[h];
+  for (int n = threadIdx.x; n <= L; n += kThreads) dec[n] = n ? expf(gd * n) : 1.f;
+
+  const T *a = (const T *)p.a.p + (int64_t)b * p.a.sb + (int64_t)(h / p.a.share) * p.a.sh;
+  const T *bb = (const T *)p.b.p + (int64_t)b * p.b.sb + (int64_t)(h / p.b.share) * p.b.sh;
+  const T *c = (const T *)p.c.p + (int64_t)b * p.c.sb + (int64_t)(h / p.c.share) * p.c.sh;
+  OT *out = (OT *)p.out + ((int64_t)b * p.T * p.H + h) * p.Dc;
+  const int64_t sot = (int64_t)p.H * p.Dc;
+
+  // X: tile k holds rows 16k + 4g + r of column c0 + 16w + lane % 16
+  f4 X[2 * KB];
+  const int xc = c0 + 16 * w + l16;
+  const int64_t xb = (int64_t)bh * p.Da * p.Dc;
+#pragma unroll
+  for (int k = 0; k < 2 * KB; ++k)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * k + 4 * g + r;
+      X[k][r] = p.x_in && row < p.Da && xc < p.Dc
+                    ? p.x_in[xb + (p.x_tr ? (int64_t)xc * p.Da + row : (int64_t)row * p.Dc + xc)]
+                    : 0.f;
+    }
+
+  for (int t0 = 0; t0 < len; t0 += L) {
+    const int n = min(L, len - t0);
+    // backwards: the first row is the last position not yet taken
+    const int64_t first = p.rev ? len - 1 - t0 : t0;
+    const int64_t step = p.rev ? -1 : 1;
+    __syncthreads();
+    stage<T, CT, DA, L>(A, a + first * p.a.st, step * p.a.st, p.Da, n, 0);
+    stage<T, CT, DA, L>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+    stage<T, CT, kCols, L>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+    __syncthreads();
+    if (p.out && w < L / 16) {
+      // P^T: wave w the columns i of 16w.., rows j <= i
+      for (int jt = 0; jt <= w; ++jt) {
+        f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+          acc = mma(frag_row(Bm + (16 * jt + l16) * lda + 32 * kb + 4 * g),
+                    frag_row(A + (16 * w + l16) * lda + 32 * kb + 4 * g), acc);
+        const int i = 16 * w + l16, j = 16 * jt + 4 * g;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          float x = i >= j + r ? acc[r] * (dec[max(i - j - r, 0)] * p.p_scale) : 0.f;
+#pragma unroll
+          for (int s = 0; s < NR; ++s) {
+            P[s * L * ldp + i * ldp + j + r] = (CT)x;
+            x -= (float)(CT)x;
+          }
+        }
+      }
+      // an even number of 16-column tiles is read: zeros above the diagonal
+      if (!(w & 1))
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < NR; ++s)
+            P[s * L * ldp + (16 * w + l16) * ldp + 16 * (w + 1) + 4 * g + r] = (CT)0.f;
+    }
+    __syncthreads();
+    if (p.out) {
+      f4 O[L / 16];
+#pragma unroll
+      for (int it = 0; it < L / 16; ++it) O[it] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = X[2 * kb][r], x[4 + r] = X[2 * kb + 1][r];
+        Frag<CT> xf[NR];
+        split<NR>(x, xf);
+#pragma unroll
+        for (int it = 0; it < L / 16; ++it) {
+          const Frag<CT> af = frag_row(A + (16 * it + l16) * lda + 32 * kb + 4 * g);
+#pragma unroll
+          for (int s = 0; s < NR; ++s) O[it] = mma(xf[s], af, O[it]);
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < L / 16; ++it) {
+        const int i = 16 * it + l16;
+        const float d = dec[i + p.off] * p.x_scale;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[it][r] *= d;
+#pragma unroll
+        for (int jb = 0; jb <= it / 2; ++jb) {
+          const Frag<CT> cf = frag_col(C + 32 * jb * ldc + 16 * w, ldc, lane);
+#pragma unroll
+          for (int s = 0; s < NR; ++s)
+            O[it] = mma(cf, frag_row(P + s * L * ldp + i * ldp + 32 * jb + 4 * g), O[it]);
+        }
+        if (i < n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int col = c0 + 16 * w + 4 * g + r;
+            if (col < p.Dc) out[(first + step * i) * sot + col] = (OT)O[it][r];
+          }
+      }
+    }
+    // X <- e^{g n} X + sum_j e^{g (n - off - j)} b_j c_j^T
+#pragma unroll
+    for (int k = 0; k < 2 * KB; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) X[k][r] *= dec[n];
+#pragma unroll
+    for (int jb = 0; jb < L / 32; ++jb) {
+      float x[8];
+      values(frag_col(C + 32 * jb * ldc + 16 * w, ldc, lane), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = 32 * jb + 4 * g + (e & 3) + (e >> 2) * 16;
+        x[e] *= dec[max(n - p.off - j, 0)] * p.add_scale;
+      }
+      Frag<CT> cf[NA];
+      split<NA>(x, cf);
+#pragma unroll
+      for (int k = 0; k < 2 * KB; ++k) {
+        const Frag<CT> bf = frag_col(Bm + 32 * jb * lda + 16 * k, lda, lane);
+#pragma unroll
+        for (int s = 0; s < NA; ++s) X[k] = mma(bf, cf[s], X[k]);
+      }
+    }
+  }
+
+  if (p.out) {
+    const OT fill = (OT)(valid < 0 ? p.bad : 0.f);
+    for (int64_t e = threadIdx.x; e < (int64_t)(p.T - len) * kCols; e += kThreads) {
+      const int64_t t = len + e / kCols;
+      const int col = c0 + e % kCols;
+      if (col < p.Dc) out[t * sot + col] = fill;
+    }
+  }
+  if (p.x_out) {
+#pragma unroll
+    for (int k = 0; k < 2 * KB; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * k + 4 * g + r;
+        if (row < p.Da && xc < p.Dc)
+          p.x_out[xb + (int64_t)row * p.Dc + xc] = valid >= 0 ? X[k][r] : p.bad;
+      }
+  }
+}
+
+// Sum over the heads that share one: part [B*T][H][D] float32 to out
+// [B*T][H / share][D].
+template <typename T>
+__global__ __launch_bounds__(256) void k_share_sum(const float *part, T *out, int64_t rows, int H,
+                                                   int share, int D) {
+  const int64_t n = rows * (H / share) * D;
+  for (int64_t e = blockIdx.x * (int64_t)256 + threadIdx.x; e < n; e += (int64_t)gridDim.x * 256) {
+    const int64_t rh = e / D;
+    const float *s = part + rh * share * D + e % D;
+    float x = 0.f;
+    for (int i = 0; i < share; ++i) x += s[(int64_t)i * D];
+    out[e] = (T)x;
+  }
+}
+
+// One position: a workgroup per stream and head.  Thread t owns column
+// t % 64 of each 64 and every fourth row.
+template <typename T>
+__global__ __launch_bounds__(256) void k_linattn_step(semicrf_linattn_shape_t s, const T *q,
+                                                      const T *k, const T *v,
+                                                      const float *log_decay,
+                                                      const int32_t *slots, int nslots,
+                                                      float *state, T *o) {
+  __shared__ float qs[256], ks[256], red[4][64];
+  const int b = blockIdx.x / s.H, h = blockIdx.x % s.H;
+  const int slot = slots ? slots[b] : b;
+  T *const ob = o + ((int64_t)b * s.H + h) * s.Dv;
+  if (slot < 0 || slot >= nslots) {
+    for (int c = threadIdx.x; c < s.Dv; c += 256) ob[c] = (T)0.f;
+    return;
+  }
+  const T *qb = q + b * s.q_stride[0] + h / (s.H / s.Hq) * s.q_stride[2];
+  const T *kb = k + b * s.k_stride[0] + h / (s.H / s.Hk) * s.k_stride[2];
+  const T *vb = v + b * s.v_stride[0] + h / (s.H / s.Hv) * s.v_stride[2];
+  if ((int)threadIdx.x < s.Dk) {
+    qs[threadIdx.x] = (float)qb[threadIdx.x];
+    ks[threadIdx.x] = (float)kb[threadIdx.x];
+  }
+  __syncthreads();
+  const float d = expf(log_decay[h]);
+  float *const S = state + ((int64_t)slot * s.H + h) * s.Dk * s.Dv;
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  for (int c0 = 0; c0 < s.Dv; c0 += 64) {
+    const int c = c0 + lane;
+    float acc = 0.f;
+    if (c < s.Dv) {
+      const float vc = (float)vb[c];
+      for (int r = w; r < s.Dk; r += 4) {
+        const float x = d * S[(int64_t)r * s.Dv + c] + ks[r] * vc;
+        S[(int64_t)r * s.Dv + c] = x;
+        acc += qs[r] * x;
+      }
+    }
+    red[w][lane] = acc;
+    __syncthreads();
+    if (w == 0 && c < s.Dv)
+      ob[c] = (T)(s.scale * (red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane]));
+    __syncthreads();
+  }
+}
+
+namespace {
+
+int round_da(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+
+// Chunks of 64 positions; of 32 where float32 operands 256 wide would not
+// leave a compute unit's 160 KB of LDS room for the tiles of 64.
+template <typename T, typename CT, typename OT, int DA>
+semicrf_status_t launch_da(const LaArgs &p, hipStream_t st) {
+  constexpr int L = sizeof(CT) * DA > 512 ? 32 : 64;
+  const int64_t grid = (int64_t)p.B * p.H * p.ctiles;
+  if (grid > 0x7fffffff) return SEMICRF_ERR_SHAPE;
+  k_linattn<T, CT, OT, DA, L><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  return launch_status();
+}
+
+template <typename T, typename CT, typename OT>
+semicrf_status_t launch_t(const LaArgs &p, hipStream_t st) {
+  switch (round_da(p.Da)) {
+    case 32: return launch_da<T, CT, OT, 32>(p, st);
+    case 64: return launch_da<T, CT, OT, 64>(p, st);
+    case 128: return launch_da<T, CT, OT, 128>(p, st);
+    default: return launch_da<T, CT, OT, 256>(p, st);
+  }
+}
+
+// f32_out: the output is float32 whatever the tensors are (parts of the
+// gradient of a shared head).
+semicrf_status_t launch_linattn(const LaArgs &p, int dtype, bool f32_out, hipStream_t st) {
+  switch (dtype) {
+    case SEMICRF_F32: return launch_t<float, float, float>(p, st);
+    case SEMICRF_BF16:
+      return f32_out ? launch_t<bf16, bf16, float>(p, st) : launch_t<bf16, bf16, bf16>(p, st);
+    default:
+      return f32_out ? launch_t<f16, float, float>(p, st) : launch_t<f16, float, f16>(p, st);
+  }
+}
+
+semicrf_status_t check(const semicrf_linattn_shape_t *s) {
+  if (!s) return SEMICRF_ERR_NULL;
+  if (s->B < 1 || s->T < 1 || s->H < 1 || s->Hq < 1 || s->Hk < 1 || s->Hv < 1 || s->Dk < 1 ||
+      s->Dv < 1 || s->H % s->Hq || s->H % s->Hk || s->H % s->Hv)
+    return SEMICRF_ERR_SHAPE;
+  if ((int64_t)s->B * s->H * 4 > 0x7fffffff) return SEMICRF_ERR_SHAPE;
+  if (s->Dk > 256 || s->Dv > 256) return SEMICRF_ERR_UNSUPPORTED;
+  if (!dtype_ok(s->dtype)) return SEMICRF_ERR_ARG;
+  return SEMICRF_OK;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Parts of a shared head's gradient: one float32 row a head.
+size_t share_bytes(const semicrf_linattn_shape_t *s, int heads, int D) {
+  return heads == s->H ? 0 : align256((size_t)s->B * s->T * s->H * D * sizeof(float));
+}
+
+View view(const void *p, const int64_t *st, int share) { return {p, st[0], st[1], st[2], share}; }
+
+semicrf_status_t share_sum(const semicrf_linattn_shape_t *s, const float *part, void *out,
+                           int heads, int D, hipStream_t st) {
+  const int64_t rows = (int64_t)s->B * s->T, n = rows * heads * D;
+  const unsigned grid = (unsigned)(n < 256 * 8192 ? (n + 255) / 256 : 8192);
+  const int share = s->H / heads;
+  switch (s->dtype) {
+    case SEMICRF_F32:
+      k_share_sum<<<grid, 256, 0, st>>>(part, (float *)out, rows, s->H, share, D);
+      break;
+    case SEMICRF_BF16:
+      k_share_sum<<<grid, 256, 0, st>>>(part, (bf16 *)out, rows, s->H, share, D);
+      break;
+    default: k_share_sum<<<grid, 256, 0, st>>>(part, (f16 *)out, rows, s->H, share, D);
+  }
+  return launch_status();
+}
+
+}  // namespace
+
+}  // namespace semicrf
+
+using namespace semicrf;
+
+extern "C" {
+
+semicrf_status_t semicrf_linattn_workspace_size(const semicrf_linattn_shape_t *s, int backward,
+                                                size_t *bytes) {
+  if (!bytes) return SEMICRF_ERR_NULL;
+  const semicrf_status_t e = check(s);
+  if (e != SEMICRF_OK) return e;
+  *bytes = 0;
+  if (backward)
+    *bytes = share_bytes(s, s->Hq, s->Dk) + share_bytes(s, s->Hk, s->Dk) +
+             share_bytes(s, s->Hv, s->Dv);
+  return SEMICRF_OK;
+}
+
+semicrf_status_t semicrf_linattn_fwd(const semicrf_linattn_shape_t *s, const void *q,
+                                     const void *k, const void *v, const float *log_decay,
+                                     const int32_t *lengths, const float *state_in, void *o,
+                                     float *state_out, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+  if (!s || !q || !k || !v || !log_decay || !o) return SEMICRF_ERR_NULL;
+  size_t need;
+  const semicrf_status_t e = semicrf_linattn_workspace_size(s, 0, &need);
+  if (e != SEMICRF_OK) return e;
+  if (need && (!workspace || workspace_bytes < need)) return SEMICRF_ERR_WORKSPACE;
+  (void)hipGetLastError();
+  LaArgs p = {};
+  p.a = view(q, s->q_stride, s->H / s->Hq);
+  p.b = view(k, s->k_stride, s->H / s->Hk);
+  p.c = view(v, s->v_stride, s->H / s->Hv);
+  p.log_decay = log_decay;
+  p.lengths = lengths;
+  p.x_in = state_in;
+  p.x_out = state_out;
+  p.out = o;
+  p.off = 1;
+  p.bad = __builtin_nanf("");
+  p.p_scale = p.x_scale = s->scale;
+  p.add_scale = 1.f;
+  p.B = s->B, p.T = s->T, p.H = s->H, p.Da = s->Dk, p.Dc = s->Dv;
+  p.ctiles = (p.Dc + kCols - 1) / kCols;
+  return launch_linattn(p, s->dtype, false, (hipStream_t)stream);
+}
+
+semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const void *q,
+                                     const void *k, const void *v, const float *log_decay,
+                                     const int32_t *lengths, const float *state_in,
+                                     const void *grad_o, const float *grad_state, void *grad_q,
+                                     void *grad_k, void *grad_v, float *grad_state_in,
+                                     void *workspace, size_t workspace_bytes, void *stream) {
+  if (!s || !q || !k || !v || !log_decay || !grad_o) return SEMICRF_ERR_NULL;
+  size_t need;
+  semicrf_status_t e = semicrf_linattn_workspace_size(s, 1, &need);
+  if (e != SEMICRF_OK) return e;
+  if (need && (!workspace || workspace_bytes < need)) return SEMICRF_ERR_WORKSPACE;
+  (void)hipGetLastError();
+  hipStream_t st = (hipStream_t)stream;
+  char *ws = (char *)workspace;
+  float *pq = (float *)ws;
+  ws += share_bytes(s, s->Hq, s->Dk);
+  float *pk = (float *)ws;
+  ws += share_bytes(s, s->Hk, s->Dk);
+  float *pv = (float *)ws;
+  const View vq = view(q, s->q_stride, s->H / s->Hq), vk = view(k, s->k_stride, s->H / s->Hk),
+             vv = view(v, s->v_stride, s->H / s->Hv);
+  const int64_t row = (int64_t)s->H * s->Dv;
+  const View vg = {grad_o, s->T * row, row, s->Dv, 1};
+  LaArgs p = {};
+  p.log_decay = log_decay;
+  p.lengths = lengths;
+  p.p_scale = s->scale;
+  p.B = s->B, p.T = s->T, p.H = s->H;
+  auto run = [&](View a, View b, View c, int Da, int Dc, void *out, float *part, int heads) {
+    p.a = a, p.b = b, p.c = c, p.Da = Da, p.Dc = Dc;
+    p.ctiles = (Dc + kCols - 1) / kCols;
+    const bool shared = out && heads != s->H;
+    p.out = shared ? part : out;
+    semicrf_status_t r = launch_linattn(p, s->dtype, shared, st);
+    if (r == SEMICRF_OK && shared) r = share_sum(s, part, out, heads, Dc, st);
+    return r;
+  };
+  if (grad_q) {
+    p.x_in = state_in, p.x_tr = 1, p.x_out = nullptr, p.rev = 0, p.off = 1;
+    p.x_scale = s->scale, p.add_scale = 1.f;
+    e = run(vg, vv, vk, s->Dv, s->Dk, grad_q, pq, s->Hq);
+    if (e != SEMICRF_OK) return e;
+  }
+  p.rev = 1, p.off = 0, p.x_scale = 1.f, p.add_scale = s->scale, p.x_in = grad_state;
+  if (grad_k) {
+    p.x_tr = 1, p.x_out = nullptr;
+    e = run(vv, vg, vq, s->Dv, s->Dk, grad_k, pk, s->Hk);
+    if (e != SEMICRF_OK) return e;
+  }
+  if (grad_v || grad_state_in) {
+    p.x_tr = 0, p.x_out = grad_state_in;
+    e = run(vk, vq, vg, s->Dk, s->Dv, grad_v, pv, s->Hv);
+  }
+  return e;
+}
+
+semicrf_status_t semicrf_linattn_step(const semicrf_linattn_shape_t *s, const void *q,
+                                      const void *k, const void *v, const float *log_decay,
+                                      const int32_t *slots, int nslots, float *state, void *o,
+                                      void *stream) {
+  if (!s || !q || !k || !v || !log_decay || !state || !o) return SEMICRF_ERR_NULL;
+  const semicrf_status_t e = check(s);
+  if (e != SEMICRF_OK) return e;
+  if (s->T != 1 || nslots < 1) return SEMICRF_ERR_SHAPE;
+  (void)hipGetLastError();
+  const unsigned grid = (unsigned)s->B * s->H;
+  hipStream_t st = (hipStream_t)stream;
+  switch (s->dtype) {
+    case SEMICRF_F32:
+      k_linattn_step<<<grid, 256, 0, st>>>(*s, (const float *)q, (const float *)k,
+                                           (const float *)v, log_decay, slots, nslots, state,
+                                           (float *)o);
+      break;
+    case SEMICRF_BF16:
+      k_linattn_step<<<grid, 256, 0, st>>>(*s, (const bf16 *)q, (const bf16 *)k, (const bf16 *)v,
+                                           log_decay, slots, nslots, state, (bf16 *)o);
+      break;
+    default:
+      k_linattn_step<<<grid, 256, 0, st>>>(*s, (const f16 *)q, (const f16 *)k, (const f16 *)v,
+                                           log_decay, slots, nslots, state, (f16 *)o);
+  }
+  return launch_status();
+}
+
+}  // extern "C"

@@ -1,0 +1,302 @@
+"""The encoder's operators over libsemicrf.so (the C ABI in
+include/semicrf_encoder.h): linear attention with a decay for each head, its
+single-token form, and group norm with an activation, channels last.
+
+    o = linear_attention(q, k, v, log_decay, lengths=lengths)
+    y = group_norm(x, groups, weight, bias, lengths=lengths, activation="silu")
+    o = linear_attention_step(q, k, v, log_decay, state, slots=slots)
+
+The first two carry gradients (torch.autograd.Function over the library's
+backward entry points); the step moves a pool of states in place.  Tensors
+are CUDA (HIP) tensors, float32, bfloat16 or float16; states, norms' weights
+and decays are float32, lengths and slots int32.  Outputs and workspaces are
+allocated with torch on the input's device and the work is enqueued on
+torch's current stream.  Positions at or past a sequence's length are never
+read and their rows of every output and gradient are 0; a length outside
+[0, T] gives NaN outputs and zero gradients.  There is no CPU fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import binding as bd
+
+EXPORTS = (
+    "semicrf_linattn_workspace_size", "semicrf_linattn_fwd", "semicrf_linattn_bwd",
+    "semicrf_linattn_step", "semicrf_groupnorm_workspace_size", "semicrf_groupnorm_fwd",
+    "semicrf_groupnorm_bwd",
+)
+DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
+MAX_HEAD = 256  # the widest Dk and Dv
+
+
+class _LinattnShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "T", "H", "Hq", "Hk", "Hv", "Dk", "Dv", "dtype")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride")])
+
+
+class _GroupnormShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "T", "C", "G", "dtype", "act")]
+                + [("eps", ctypes.c_float)])
+
+
+_lib = None
+
+
+def load():
+    """The library with the signatures of the encoder's entry points."""
+    global _lib
+    if _lib is None:
+        lib = bd.load()
+        P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+        for name in ("linattn", "groupnorm"):
+            f = getattr(lib, "semicrf_%s_workspace_size" % name)
+            f.argtypes, f.restype = [P, I, ctypes.POINTER(Z)], I
+        lib.semicrf_linattn_fwd.argtypes = [P] * 9 + [P, Z, P]
+        lib.semicrf_linattn_bwd.argtypes = [P] * 13 + [P, Z, P]
+        lib.semicrf_linattn_step.argtypes = [P] * 6 + [I, P, P, P]
+        lib.semicrf_groupnorm_fwd.argtypes = [P] * 7 + [P, Z, P]
+        lib.semicrf_groupnorm_bwd.argtypes = [P] * 10 + [P, Z, P]
+        for name in EXPORTS:
+            getattr(lib, name).restype = I
+        _lib = lib
+    return _lib
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _on:
+    """Makes the tensors' device the current one for the launches inside."""
+
+    def __init__(self, dev):
+        self.dev = dev
+
+    def __enter__(self):
+        self.was = torch.cuda.current_device()
+        if self.was != self.dev.index:
+            torch.cuda.set_device(self.dev)
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.was != self.dev.index:
+            torch.cuda.set_device(self.was)
+
+
+def _call(name, dev, shape, backward, *args):
+    """A library call with the workspace its shape needs (backward None: none)."""
+    lib = load()
+    with _on(dev) as stream:
+        if backward is not None:
+            n = ctypes.c_size_t(0)
+            rc = getattr(lib, name.rsplit("_", 1)[0] + "_workspace_size")(
+                ctypes.byref(shape), backward, ctypes.byref(n))
+            if rc:
+                raise bd.SemiCRFError(rc, name)
+            ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
+            args += (_ptr(ws), n.value)
+        rc = getattr(lib, name)(ctypes.byref(shape), *args, stream)
+    if rc:
+        raise bd.SemiCRFError(rc, name)
+
+
+def _check(name, t, dev, dtype, shape):
+    if t.device != dev or t.dtype != dtype or not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError("%s must be a contiguous %s %s tensor on %s"
+                         % (name, dtype, list(shape), dev))
+
+
+def _check_device(t):
+    if t.device.type != "cuda":
+        raise ValueError("the encoder's operators run on the GPU only; got a %s tensor"
+                         % t.device.type)
+    if t.dtype not in DTYPES:
+        raise ValueError("unsupported type %s (float32, bfloat16 or float16)" % t.dtype)
+
+
+def _rows(t):
+    """t itself if its last dimension is contiguous, else a copy."""
+    return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+
+
+def _linattn_shape(q, k, v, log_decay, scale, T):
+    """Checks q, k, v ([B, T, heads, D] or, for T None, [B, heads, D]) and
+    log_decay; the shape structure and the tensors with contiguous rows."""
+    _check_device(q)
+    dims = 3 if T is None else 4
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dim() != dims or t.device != q.device or t.dtype != q.dtype:
+            raise ValueError("%s must be a [B, %sheads, D] %s tensor on %s"
+                             % (name, "" if T is None else "T, ", q.dtype, q.device))
+        if t.shape[:-2] != q.shape[:-2]:
+            raise ValueError("q, k and v must have the same B%s" % ("" if T is None else " and T"))
+    if k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k must have the same width")
+    if not (1 <= q.shape[-1] <= MAX_HEAD and 1 <= v.shape[-1] <= MAX_HEAD):
+        raise ValueError("heads are 1 to %d wide" % MAX_HEAD)
+    heads = [t.shape[-2] for t in (q, k, v)]
+    H = max(heads)
+    if min(heads) < 1 or any(H % h for h in heads):
+        raise ValueError("the larger number of heads must be a multiple of the others: %s" % heads)
+    if log_decay.requires_grad:
+        raise ValueError("log_decay is a constant of the model: it gets no gradient")
+    _check("log_decay", log_decay, q.device, torch.float32, (H,))
+    q, k, v = _rows(q), _rows(k), _rows(v)
+
+    def strides(t):
+        s = t.stride()
+        return (ctypes.c_int64 * 3)(s[0], s[1] if T is not None else 0, s[-2])
+
+    shape = _LinattnShape(q.shape[0], 1 if T is None else T, H, *heads, q.shape[-1], v.shape[-1],
+                          DTYPES[q.dtype], q.shape[-1] ** -0.5 if scale is None else float(scale),
+                          strides(q), strides(k), strides(v))
+    return shape, q, k, v
+
+
+class LinearAttention(torch.autograd.Function):
+    """o [B, T, H, Dv] and the state after each sequence [B, H, Dk, Dv]."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, state, log_decay, lengths, scale):
+        ctx.scale = scale
+        ctx.save_for_backward(q, k, v, state, log_decay, lengths)
+        ctx.set_materialize_grads(False)
+        shape, q, k, v = _linattn_shape(q, k, v, log_decay, scale, q.shape[1])
+        o = torch.empty((shape.B, shape.T, shape.H, shape.Dv), dtype=q.dtype, device=q.device)
+        last = torch.empty((shape.B, shape.H, shape.Dk, shape.Dv), dtype=torch.float32,
+                           device=q.device)
+        _call("semicrf_linattn_fwd", q.device, shape, 0, _ptr(q), _ptr(k), _ptr(v),
+              _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(o), _ptr(last))
+        return o, last
+
+    @staticmethod
+    def backward(ctx, do, dlast):
+        q, k, v, state, log_decay, lengths = ctx.saved_tensors
+        shape, q, k, v = _linattn_shape(q, k, v, log_decay, ctx.scale, q.shape[1])
+        dev = q.device
+        if do is None:
+            do = torch.zeros((shape.B, shape.T, shape.H, shape.Dv), dtype=q.dtype, device=dev)
+        do = do.contiguous()
+        dlast = None if dlast is None else dlast.contiguous()
+        need = ctx.needs_input_grad
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=dev) if n else None
+                 for t, n in ((q, need[0]), (k, need[1]), (v, need[2]))]
+        dstate = torch.empty_like(state) if state is not None and need[3] else None
+        _call("semicrf_linattn_bwd", dev, shape, 1, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
+              _ptr(lengths), _ptr(state), _ptr(do), _ptr(dlast), *(_ptr(g) for g in grads),
+              _ptr(dstate))
+        return (*grads, dstate, None, None, None)
+
+
+def linear_attention(q, k, v, log_decay, lengths=None, state=None, scale=None,
+                     return_state: bool = False):
+    """Linear attention with a decay for each head, over whole sequences:
+
+        S_t = exp(log_decay_h) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+
+    q, k [B, T, heads, Dk] and v [B, T, heads, Dv] of one type, any strides
+    with contiguous rows; their numbers of heads divide the largest, H, and
+    head h reads head h // (H // heads) of a tensor with fewer (shared
+    heads).  log_decay [H] float32, at most 0, a constant of the model (it
+    gets no gradient).  lengths [B] int32; state [B, H, Dk, Dv] float32, the
+    state before the first position (zeros by default); scale, Dk ** -0.5 by
+    default.  Returns o [B, T, H, Dv] or, with return_state, (o, the state
+    after each sequence's last position).  Gradients flow to q, k, v and
+    state."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, T, heads, D]")
+    shape, *_ = _linattn_shape(q, k, v, log_decay, scale, q.shape[1])
+    if lengths is not None:
+        _check("lengths", lengths, q.device, torch.int32, (shape.B,))
+    if state is not None:
+        _check("state", state, q.device, torch.float32, (shape.B, shape.H, shape.Dk, shape.Dv))
+    if shape.B == 0 or shape.T == 0:
+        o = torch.zeros((shape.B, shape.T, shape.H, shape.Dv), dtype=q.dtype, device=q.device)
+        last = (torch.zeros((shape.B, shape.H, shape.Dk, shape.Dv), device=q.device)
+                if state is None else state.clone())
+    else:
+        o, last = LinearAttention.apply(q, k, v, state, log_decay, lengths, scale)
+    return (o, last) if return_state else o
+
+
+def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
+    """One position of B streams: q, k [B, heads, Dk], v [B, heads, Dv].
+    state [slots, H, Dk, Dv] float32 is a pool; stream b's is state[slots[b]]
+    (slots [B] int32, distinct; stream b's own row b by default) and is moved
+    in place.  A stream whose slot is outside the pool is idle: its row of
+    the result [B, H, Dv] is 0.  No gradients."""
+    shape, q, k, v = _linattn_shape(q, k, v, log_decay, scale, None)
+    if state.dim() != 4 or state.shape[0] < 1:
+        raise ValueError("state must be [slots, H, Dk, Dv] with at least one slot")
+    _check("state", state, q.device, torch.float32,
+           (state.shape[0], shape.H, shape.Dk, shape.Dv))
+    if slots is not None:
+        _check("slots", slots, q.device, torch.int32, (shape.B,))
+    o = torch.empty((shape.B, shape.H, shape.Dv), dtype=q.dtype, device=q.device)
+    if shape.B:
+        _call("semicrf_linattn_step", q.device, shape, None, _ptr(q), _ptr(k), _ptr(v),
+              _ptr(log_decay), _ptr(slots), state.shape[0], _ptr(state), _ptr(o))
+    return o
+
+
+class GroupNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, lengths, groups, eps, act):
+        B, T, C = x.shape
+        shape = _GroupnormShape(B, T, C, groups, DTYPES[x.dtype], act, eps)
+        y = torch.empty_like(x)
+        stats = torch.empty((B, groups, 2), dtype=torch.float32, device=x.device)
+        _call("semicrf_groupnorm_fwd", x.device, shape, 0, _ptr(x), _ptr(weight), _ptr(bias),
+              _ptr(lengths), _ptr(y), _ptr(stats))
+        ctx.shape = shape
+        ctx.save_for_backward(x, weight, bias, lengths, stats)
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, lengths, stats = ctx.saved_tensors
+        dy = dy.contiguous()
+        dx = torch.empty_like(x)
+        dw = torch.empty_like(weight) if weight is not None and ctx.needs_input_grad[1] else None
+        db = torch.empty_like(bias) if bias is not None and ctx.needs_input_grad[2] else None
+        _call("semicrf_groupnorm_bwd", x.device, ctx.shape, 1, _ptr(x), _ptr(weight), _ptr(bias),
+              _ptr(lengths), _ptr(dy), _ptr(stats), _ptr(dx), _ptr(dw), _ptr(db))
+        return dx, dw, db, None, None, None, None
+
+
+def group_norm(x, groups: int, weight=None, bias=None, lengths=None, eps: float = 1e-5,
+               activation: str = "none"):
+    """Group norm of x [B, ..., C] over the positions of a sequence and the
+    C / groups neighbouring channels of a group, then weight and bias ([C]
+    float32, each optional) and the activation ("none", "silu", "gelu" with
+    the error function, "relu").  lengths [B] int32 for x [B, T, C]:
+    statistics over the first lengths[b] positions.  Gradients flow to x,
+    weight and bias.  A norm of each position by itself is that of
+    x.view(B * T, 1, C)."""
+    _check_device(x)
+    if x.dim() < 2 or x.shape[-1] < 1:
+        raise ValueError("x must be [B, ..., C]")
+    C = x.shape[-1]
+    if groups < 1 or C % groups:
+        raise ValueError("%d channels do not divide into %d groups" % (C, groups))
+    if activation not in ACTIVATIONS:
+        raise ValueError("activation must be one of %s" % ", ".join(ACTIVATIONS))
+    if not eps >= 0:
+        raise ValueError("eps must not be negative")
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _check(name, t, x.device, torch.float32, (C,))
+    if lengths is not None:
+        if x.dim() != 3:
+            raise ValueError("lengths go with x [B, T, C]")
+        _check("lengths", lengths, x.device, torch.int32, (x.shape[0],))
+    if x.numel() == 0:
+        return x.clone()
+    y = GroupNorm.apply(x.contiguous().view(x.shape[0], -1, C), weight, bias, lengths, int(groups),
+                        float(eps), ACTIVATIONS[activation])
+    return y.view(x.shape)

@@ -1,0 +1,289 @@
+"""The AdamW step against its definition.
+
+The header gives every operation and its rounding to float32, so the states
+and float32 parameters are compared bit by bit with numpy's float32
+operations in that order, and the 8-bit codes with a search over the 256
+values.  Against the formula in float64: m and v are sums of two products
+(4 e |terms|), the update a quotient of them (12 e of itself), e = 2^-24."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from semi_markov_crf_zero_amd import optim
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+F = np.float32
+E = 2.0 ** -24
+HYPER = dict(lr=3e-3, beta1=0.9, beta2=0.98, eps=1e-8, weight_decay=0.1)
+
+# magnitudes of the 8-bit forms, in order of their codes
+SIGNED = np.array([(m / 8 if e == 0 else 1 + m / 8) * 2.0 ** (max(e, 1) - 7)
+                   for e in range(16) for m in range(8)][:127])
+ROOT = np.array([(m / 16 if e == 0 else 1 + m / 16) * 2.0 ** (max(e, 1) - 7)
+                 for e in range(16) for m in range(16)])
+
+
+def nearest(x, table):
+    """Code of the nearest value, ties to the even code."""
+    i = np.clip(np.searchsorted(table, x), 1, len(table) - 1)
+    lo, hi = x - table[i - 1], table[i] - x
+    return np.where((lo < hi) | ((lo == hi) & (i % 2 == 1)), i - 1, i)
+
+
+def blocks(x):
+    n = -(-len(x) // 256) * 256
+    return np.concatenate([x, np.zeros(n - len(x), x.dtype)]).reshape(-1, 256)
+
+
+def encode(x, table, most):
+    n = len(x)
+    x = blocks(x)
+    top = np.abs(x).max(1, keepdims=True).astype(F)
+    with np.errstate(divide="ignore", over="ignore"):
+        inv = np.where(top > F(2.0 ** -100), (F(1) / top) * F(most), F(0)).astype(F)
+    y = (x * inv).astype(F)
+    code = nearest(np.abs(y).astype(np.float64), table)
+    return code.reshape(-1)[:n], np.signbit(y).reshape(-1)[:n], (top * F(1 / most)).reshape(-1).astype(F)
+
+
+def decode8(code, neg, scale, table):
+    x = blocks(np.where(neg, -table[code], table[code]).astype(F)) * scale[:, None]
+    return x.astype(F).reshape(-1)[:len(code)]
+
+
+def step(p, g, m, v, t, hy, gs=None):
+    """One step in float32, each operation by itself."""
+    b1, b2 = hy["beta1"], hy["beta2"]
+    g = g.astype(F)
+    if gs is not None:
+        g = g * F(gs)
+    m = m * F(b1) + F(1 - b1) * g
+    v = v * F(b2) + (F(1 - b2) * g) * g
+    root = np.sqrt(v)
+    down = root * F(1 / math.sqrt(1 - b2 ** t)) + F(hy["eps"])
+    p = p * F(1 - hy["lr"] * hy["weight_decay"]) - (m / down) * F(hy["lr"] / (1 - b1 ** t))
+    return p.astype(F), m.astype(F), v.astype(F), root.astype(F)
+
+
+def tensors(seed, sizes, dtype, grad, offset=0):
+    """Parameters and gradients, each `offset` elements past an aligned start."""
+    gen = torch.Generator().manual_seed(seed)
+
+    def one(n, dt, std):
+        t = (torch.randn(n, generator=gen) * std).to(dt)
+        d = torch.zeros(n + offset, dtype=dt, device=DEV)[offset:]
+        d.copy_(t)
+        return d
+    return [one(n, TYPES[dtype], 0.5) for n in sizes], [one(n, TYPES[grad], 0.01) for n in sizes]
+
+
+def host(ts):
+    return [t.detach().float().cpu().numpy() for t in ts]
+
+
+SIZES = [1, 3, 255, 256, 257, 4095, 4096, 4097, 0, 20000, 64]
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("dtype,grad", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16"),
+                                        ("bf16", "f32"), ("f16", "f16")])
+def test_states_in_32_bits(dtype, grad, offset):
+    p, g = tensors(1, SIZES, dtype, grad, offset)
+    plan = optim.AdamWPlan(p)
+    P, G = host(p), host(g)
+    M, V = [np.zeros(n, F) for n in SIZES], [np.zeros(n, F) for n in SIZES]
+    for t in range(1, 4):
+        plan.run(g, t, **HYPER)
+        for i in range(len(SIZES)):
+            P[i], M[i], V[i], _ = step(P[i], G[i], M[i], V[i], t, HYPER)
+            if dtype != "f32":
+                P[i] = torch.from_numpy(P[i]).to(TYPES[dtype]).float().numpy()
+        for got, want in ((host(p), P), (host(plan.exp_avg), M), (host(plan.exp_avg_sq), V)):
+            for a, b in zip(got, want):
+                assert np.array_equal(a, b), t
+
+
+@pytest.mark.parametrize("offset", [0, 1])
+@pytest.mark.parametrize("dtype,grad", [("f32", "f32"), ("f32", "bf16"), ("bf16", "bf16")])
+def test_states_in_8_bits(dtype, grad, offset):
+    p, g = tensors(2, SIZES, dtype, grad, offset)
+    plan = optim.AdamWPlan(p, bits=8)
+    P, G = host(p), host(g)
+    M, V = [np.zeros(n, F) for n in SIZES], [np.zeros(n, F) for n in SIZES]
+    for t in range(1, 5):
+        plan.run(g, t, **HYPER)
+        for i, n in enumerate(SIZES):
+            if not n:
+                continue
+            P[i], m, _, root = step(P[i], G[i], M[i], V[i], t, HYPER)
+            if dtype != "f32":
+                P[i] = torch.from_numpy(P[i]).to(TYPES[dtype]).float().numpy()
+            cm, neg, sm = encode(m, SIGNED, 448)
+            cr, _, sr = encode(root, ROOT, 496)
+            M[i] = decode8(cm, neg, sm, SIGNED)
+            r = decode8(cr, np.zeros(n, bool), sr, ROOT)
+            V[i] = (r * r).astype(F)
+            (gm, gsm), (gr, gsr) = plan.exp_avg[i], plan.exp_avg_sq[i]
+            raw = gm.view(torch.uint8).cpu().numpy()
+            assert np.array_equal(raw & 127, cm) and np.array_equal(raw >> 7, neg), (t, n)
+            assert np.array_equal(gr.cpu().numpy(), cr), (t, n)
+            assert np.array_equal(gsm.cpu().numpy(), sm) and np.array_equal(gsr.cpu().numpy(), sr)
+            assert np.array_equal(optim.moment_values(gm, gsm).cpu().numpy(), M[i])
+            assert np.array_equal(optim.moment_values(gr, gsr).cpu().numpy(), V[i])
+            assert np.array_equal(host(p[i:i + 1])[0], P[i]), (t, n)
+
+
+def test_against_the_formula_in_64_bits():
+    p, g = tensors(3, [10000], "f32", "f32")
+    plan = optim.AdamWPlan(p)
+    x, gg = host(p)[0].astype(np.float64), host(g)[0].astype(np.float64)
+    m = v = 0.0
+    for t in range(1, 6):
+        plan.run(g, t, **HYPER)
+        m = 0.9 * m + 0.1 * gg
+        v = 0.98 * v + 0.02 * gg * gg
+        up = HYPER["lr"] * (m / (1 - 0.9 ** t)) / (np.sqrt(v / (1 - 0.98 ** t)) + 1e-8)
+        x = x * (1 - HYPER["lr"] * 0.1) - up
+        # gradients of one sign in every step: no cancellation in m
+        assert np.all(np.abs(host(plan.exp_avg)[0] - m) <= 5 * t * E * np.abs(m))
+        assert np.all(np.abs(host(plan.exp_avg_sq)[0] - v) <= 6 * t * E * v)
+        assert np.all(np.abs(host(p)[0] - x) <= t * E * (4 * np.abs(x) + 40 * np.abs(up) + 0.02))
+
+
+def test_masters_scale_and_missing_gradients():
+    p, g = tensors(4, [500, 300, 700], "bf16", "bf16")
+    masters = [t.float() + 1e-4 for t in p]
+    plan = optim.AdamWPlan(p, masters=masters)
+    P, G, W = host(p), host(g), host(masters)
+    scale = torch.tensor([0.37], device=DEV)
+    plan.run([g[0], None, g[2]], 1, grad_scale=scale, **HYPER)
+    for i in (0, 2):
+        W[i], m, v, _ = step(W[i], G[i], np.zeros_like(W[i]), np.zeros_like(W[i]), 1, HYPER, 0.37)
+        assert np.array_equal(host(masters)[i], W[i])
+        assert np.array_equal(host(p)[i], torch.from_numpy(W[i]).bfloat16().float().numpy())
+        assert np.array_equal(host(plan.exp_avg)[i], m)
+    assert np.array_equal(host(p)[1], P[1]) and not host(plan.exp_avg)[1].any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_many_tensors(bits):
+    """More than one launch holds."""
+    sizes = [1 + (i * 37) % 600 for i in range(1000)]
+    p, g = tensors(5, sizes, "f32", "f32")
+    plan = optim.AdamWPlan(p, bits=bits)
+    P, G = host(p), host(g)
+    g[417] = None
+    plan.run(g, 1, **HYPER)
+    for i in range(1000):
+        if i != 417:
+            P[i] = step(P[i], G[i], np.zeros(sizes[i], F), np.zeros(sizes[i], F), 1, HYPER)[0]
+    for a, b in zip(host(p), P):
+        assert np.array_equal(a, b)
+
+
+def test_non_finite_gradients_stay_where_they_are():
+    for bits in (32, 8):
+        p, g = tensors(6, [1024], "f32", "f32")
+        plan = optim.AdamWPlan(p, bits=bits)
+        g[0][300], g[0][800] = float("nan"), float("inf")
+        plan.run(g, 1, **HYPER)
+        bad = ~host(p)[0].astype(np.float64).__abs__().__lt__(1e30)
+        assert bad[300] and bad[800] and bad.sum() == 2
+        m = plan.exp_avg[0] if bits == 32 else optim.moment_values(*plan.exp_avg[0])
+        fine = np.isfinite(host([m])[0])
+        if bits == 32:
+            assert fine.sum() == 1022
+        else:  # their blocks of 256 and no others
+            assert fine[:256].all() and fine[512:768].all()
+            assert not fine[256:512].any() and not fine[800]
+
+
+def test_states_that_decay_to_nothing():
+    """Blocks whose moments pass below 2^-100 hold zeros, not NaN."""
+    p, g = tensors(7, [512], "f32", "f32")
+    plan = optim.AdamWPlan(p, bits=8)
+    plan.run(g, 1, **HYPER)
+    zero = [torch.zeros_like(g[0])]
+    for t in range(2, 1500):
+        plan.run(zero, t, lr=0.0, beta1=0.9, beta2=0.9, eps=1e-8, weight_decay=0.0)
+    m, v = optim.moment_values(*plan.exp_avg[0]), optim.moment_values(*plan.exp_avg_sq[0])
+    assert (m == 0).all() and plan.exp_avg[0][1].isfinite().all()
+    # v stops at float32's last subnormals (0.9 times 4 of them rounds to 4),
+    # whose root is far above 2^-100
+    assert (v >= 0).all() and (v <= 16 * 2.0 ** -149).all()
+
+
+def test_optimizer_matches_torch_and_resumes():
+    """AdamW as a torch optimizer: torch's own AdamW on the same gradients
+    (the same formula in another order: 64 e of the parameter and the moves)."""
+    torch.manual_seed(0)
+    net = torch.nn.Sequential(torch.nn.Linear(33, 65), torch.nn.Linear(65, 7)).to(DEV)
+    other = torch.nn.Sequential(torch.nn.Linear(33, 65), torch.nn.Linear(65, 7)).to(DEV)
+    other.load_state_dict(net.state_dict())
+    kw = dict(lr=1e-2, betas=(0.9, 0.98), weight_decay=0.05)
+    a, b = optim.AdamW(net.parameters(), **kw), torch.optim.AdamW(other.parameters(), **kw)
+    for i in range(5):
+        for x, y in zip(net.parameters(), other.parameters()):
+            x.grad = torch.randn_like(x)
+            y.grad = x.grad.clone()
+        a.step()
+        b.step()
+    for x, y in zip(net.parameters(), other.parameters()):
+        assert ((x - y).abs() <= 64 * E * (y.abs() + 5e-2)).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_optimizer_state_dict(bits):
+    def make():
+        torch.manual_seed(1)
+        net = torch.nn.Linear(40, 30).to(DEV).bfloat16()
+        return net, optim.AdamW(net.parameters(), lr=1e-2, bits=bits, masters=True)
+
+    def steps(net, opt, lo, hi):
+        for i in range(lo, hi):
+            gen = torch.Generator(device=DEV).manual_seed(i)
+            for p in net.parameters():
+                p.grad = torch.randn(p.shape, device=DEV, generator=gen).bfloat16()
+            opt.step()
+
+    net, opt = make()
+    steps(net, opt, 0, 3)
+    saved = [t.clone() for t in net.parameters()], opt.state_dict()
+    saved = (saved[0], {"state": {k: {n: t.clone() if isinstance(t, torch.Tensor) else t
+                                      for n, t in s.items()} for k, s in saved[1]["state"].items()},
+                        "param_groups": saved[1]["param_groups"]})
+    steps(net, opt, 3, 6)
+    net2, opt2 = make()
+    with torch.no_grad():
+        for p, t in zip(net2.parameters(), saved[0]):
+            p.copy_(t)
+    opt2.load_state_dict(saved[1])
+    steps(net2, opt2, 3, 6)
+    for x, y in zip(net.parameters(), net2.parameters()):
+        assert torch.equal(x, y)
+
+
+def test_refusals():
+    p = torch.zeros(10, device=DEV)
+    for args, kw in ((([p.double()],), {}), (([p[::2]],), {}), (([p],), dict(bits=16)),
+                     (([p],), dict(exp_avg=[])), (([p],), dict(exp_avg=[p[:9]])),
+                     (([p],), dict(masters=[p.half()])),
+                     (([p],), dict(bits=8, exp_avg=[(p.to(torch.uint8), p[:1])])),
+                     (([p],), dict(bits=8, exp_avg_sq=[(p.to(torch.uint8), p[:2])]))):
+        with pytest.raises(ValueError):
+            optim.AdamWPlan(*args, **kw)
+    plan = optim.AdamWPlan([p])
+    for grads, kw in (([], {}), ([p[:9]], {}), ([p.double()], {}), ([p.cpu()], {}),
+                      ([torch.zeros(20, device=DEV)[::2]], {}), ([p], dict(grad_scale=p))):
+        with pytest.raises(ValueError):
+            plan.run(grads, 1, **kw)
+    with pytest.raises(RuntimeError):
+        plan.run([p], 0)
+    with pytest.raises(ValueError):
+        optim.moment_values(torch.zeros(300, dtype=torch.uint8, device=DEV), p[:1])
+    with pytest.raises(ValueError):
+        optim.moment_values(p, p[:1])
