@@ -23,6 +23,14 @@
 // e^{g i'} and adds with e^{g (n-j')}: off = 1 or 0 moves one step of the
 // decay from the reading to the adding side.
 //
+// Long sequences are cut into segments so that a few heads fill the GPU.  A
+// segment's part of X does not depend on what came before: k_linattn_state
+// sums it for each segment from X = 0, k_linattn_scan runs
+//   X before segment s+1 = e^{g n_s} (X before segment s) + part of s
+// over the segments, and k_linattn starts each one from its own X.  X^T is
+// what the transposed pair adds up to, so the four passes need two sets of
+// states: that of (k, v) forwards and that of (q, grad_o) backwards.
+//
 // Positions past the length are loaded as zeros (a select, so NaN there
 // stays out) and their rows of the output are written as 0.
 #include "encoder.h"
@@ -52,7 +60,9 @@ struct LaArgs {
   const float *log_decay;
   const int32_t *lengths;
   const float *x_in;  // [B][H][Da][Dc], or [B][H][Dc][Da] if x_tr; or NULL
-  float *x_out;       // the same layout; or NULL
+  float *x_out;       // [B][H][Da][Dc]; or NULL
+  float *xs;          // [B][H][nseg - 1], as x_in: before segments 1..
+  int nseg, seg;      // segments, positions of one (a multiple of the chunk)
   void *out;          // [B][T][H][Dc] contiguous; or NULL
   int x_tr;
   int rev, off;
@@ -60,6 +70,7 @@ struct LaArgs {
   float p_scale, x_scale, add_scale;  // of P, of A X, of what a chunk adds to X
   int B, T, H, Da, Dc;
   int ctiles;
+  int vec, out_vec;  // 16-byte loads; four elements a store
 };
 
 // A fragment is a lane's part of one operand over a 32-wide stretch of the
@@ -161,7 +172,46 @@ __device__ __forceinline__ void values(const Frag<float> &f, float *x) {
   for (int e = 0; e < 8; ++e) x[e] = f.v[e];
 }
 
-// n rows (of L) of a chunk into LDS, zeros past row n and past column D.
+// A tile of a chunk: L rows of W columns, zeros past row n and past column
+// D.  fetch() issues a thread's 16-byte loads into registers while the chunk
+// before is worked on, put() writes them to LDS.
+template <typename T, typename CT, int W, int L>
+struct Tile {
+  static constexpr int VE = 16 / sizeof(T), per = W / VE, NV = L * per / kThreads;
+  static constexpr int ld = W + 16 / sizeof(CT);
+  Pack<T, VE> r[NV];
+
+  __device__ __forceinline__ void fetch(const T *src, int64_t st, int D, int n, int col0) {
+    const int c = threadIdx.x % per * VE, i0 = threadIdx.x / per;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = i0 + k * (kThreads / per);
+      if (i < n && col0 + c < D) {
+        r[k] = *reinterpret_cast<const Pack<T, VE> *>(src + i * st + col0 + c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) r[k].v[e] = (T)0.f;
+      }
+    }
+  }
+  __device__ __forceinline__ void put(CT *lds) const {
+    const int c = threadIdx.x % per * VE, i0 = threadIdx.x / per;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      Pack<CT, VE> x;
+#pragma unroll
+      for (int e = 0; e < VE; ++e) x.v[e] = (CT)r[k].v[e];
+      CT *to = lds + (i0 + k * (kThreads / per)) * ld + c;
+#pragma unroll
+      for (int e = 0; e < VE; e += 16 / sizeof(CT))
+        *reinterpret_cast<Pack<CT, 16 / sizeof(CT)> *>(to + e) =
+            *reinterpret_cast<const Pack<CT, 16 / sizeof(CT)> *>(x.v + e);
+    }
+  }
+};
+
+// The same without the alignment 16-byte loads need: element by element,
+// straight to LDS.
 template <typename T, typename CT, int W, int L>
 __device__ __forceinline__ void stage(CT *lds, const T *src, int64_t st, int D, int n, int col0) {
   constexpr int ld = W + 16 / sizeof(CT);
@@ -171,10 +221,119 @@ __device__ __forceinline__ void stage(CT *lds, const T *src, int64_t st, int D, 
   }
 }
 
+// X <- e^{g n} X + sum_j e^{g (n - off - j)} b_j c_j^T over a staged chunk:
+// B in rows of lda, this wave's 16 columns of C in rows of ldc.
+template <typename CT, int KB, int L>
+__device__ __forceinline__ void add_chunk(f4 *X, const CT *Bm, const CT *C, const float *dec,
+                                          int n, int off, float scale, int lane) {
+  constexpr int lda = 32 * KB + 16 / sizeof(CT), ldc = kCols + 16 / sizeof(CT);
+  constexpr int NA = Parts<CT>::kAdd;
+  const int g = lane >> 4;
+#pragma unroll
+  for (int k = 0; k < 2 * KB; ++k)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) X[k][r] *= dec[n];
+#pragma unroll
+  for (int jb = 0; jb < L / 32; ++jb) {
+    float x[8];
+    values(frag_col(C + 32 * jb * ldc, ldc, lane), x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int j = 32 * jb + 4 * g + (e & 3) + (e >> 2) * 16;
+      x[e] *= dec[max(n - off - j, 0)] * scale;
+    }
+    Frag<CT> cf[NA];
+    split<NA>(x, cf);
+#pragma unroll
+    for (int k = 0; k < 2 * KB; ++k) {
+      const Frag<CT> bf = frag_col(Bm + 32 * jb * lda + 16 * k, lda, lane);
+#pragma unroll
+      for (int s = 0; s < NA; ++s) X[k] = mma(bf, cf[s], X[k]);
+    }
+  }
+}
+
 }  // namespace
 
-// One workgroup: one sequence and head, kCols columns of the output, every
-// chunk in turn.  T: the tensors' type; CT: the operands' type (bfloat16 as
+// Parts of X: one workgroup per segment but the last, kCols columns.  Writes
+// xs[segment]; a segment past the length leaves zeros.
+template <typename T, typename CT, int DA, int L>
+__global__ __launch_bounds__(kThreads) void k_linattn_state(LaArgs p) {
+  constexpr int pad = 16 / sizeof(CT);
+  constexpr int lda = DA + pad, ldc = kCols + pad, KB = DA / 32;
+  __shared__ alignas(16) CT Bm[L * lda + L * ldc];
+  CT *const C = Bm + L * lda;
+  __shared__ float dec[L + 1];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  const int ct = blockIdx.x % p.ctiles, s0 = blockIdx.x / p.ctiles % (p.nseg - 1);
+  const int bh = blockIdx.x / p.ctiles / (p.nseg - 1);
+  const int h = bh % p.H, b = bh / p.H, c0 = ct * kCols;
+  const int len = max(valid_length(p.lengths, b, p.T), 0);
+  const int lo = s0 * p.seg, hi = min(len, lo + p.seg);
+  const float gd = p.log_decay[h];
+  for (int n = threadIdx.x; n <= L; n += kThreads) dec[n] = n ? expf(gd * n) : 1.f;
+  const T *bb = (const T *)p.b.p + (int64_t)b * p.b.sb + (int64_t)(h / p.b.share) * p.b.sh;
+  const T *c = (const T *)p.c.p + (int64_t)b * p.c.sb + (int64_t)(h / p.c.share) * p.c.sh;
+  f4 X[2 * KB];
+#pragma unroll
+  for (int k = 0; k < 2 * KB; ++k) X[k] = f4{0.f, 0.f, 0.f, 0.f};
+  Tile<T, CT, DA, L> tb;
+  Tile<T, CT, kCols, L> tc;
+  const int64_t step = p.rev ? -1 : 1;
+  auto fetch = [&](int t0) {
+    const int n = min(L, hi - t0);
+    const int64_t first = p.rev ? len - 1 - t0 : t0;
+    tb.fetch(bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+    tc.fetch(c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+  };
+  if (p.vec && lo < hi) fetch(lo);
+  for (int t0 = lo; t0 < hi; t0 += L) {
+    const int n = min(L, hi - t0);
+    const int64_t first = p.rev ? len - 1 - t0 : t0;
+    __syncthreads();
+    if (p.vec) {
+      tb.put(Bm);
+      tc.put(C);
+    } else {
+      stage<T, CT, DA, L>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+      stage<T, CT, kCols, L>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+    }
+    __syncthreads();
+    if (p.vec && t0 + L < hi) fetch(t0 + L);
+    add_chunk<CT, KB, L>(X, Bm, C + 16 * w, dec, n, p.off, p.add_scale, lane);
+  }
+  const int xc = c0 + 16 * w + l16;
+  float *out = p.xs + ((int64_t)bh * (p.nseg - 1) + s0) * p.Da * p.Dc;
+#pragma unroll
+  for (int k = 0; k < 2 * KB; ++k)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * k + 4 * g + r;
+      if (row < p.Da && xc < p.Dc) out[row * p.Dc + xc] = X[k][r];
+    }
+}
+
+// xs[s] from the part of segment s to X before segment s + 1, one element of
+// X a thread.
+__global__ __launch_bounds__(kThreads) void k_linattn_scan(LaArgs p) {
+  const int64_t n = (int64_t)p.Da * p.Dc;
+  const int64_t e = blockIdx.x * (int64_t)kThreads + threadIdx.x;
+  if (e >= (int64_t)p.B * p.H * n) return;
+  const int64_t bh = e / n;
+  const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+  const int len = max(valid_length(p.lengths, b, p.T), 0);
+  float *x = p.xs + bh * (p.nseg - 1) * n + e % n;
+  float acc = p.x_in ? p.x_in[e] : 0.f;
+  const float gd = p.log_decay[h];
+  for (int s = 0; s < p.nseg - 1; ++s) {
+    const int m = min(max(len - s * p.seg, 0), p.seg);
+    acc = (m ? expf(gd * m) : 1.f) * acc + x[s * n];
+    x[s * n] = acc;
+  }
+}
+
+// One workgroup: one segment of one sequence and head, kCols columns of the
+// output, every chunk in turn.  T: the tensors' type; CT: the operands' type (bfloat16 as
 // it is; float32 and float16 in float32: float16 would need its range
 // watched in P and X); OT: the output's; DA: Da rounded up.
 template <typename T, typename CT, typename OT, int DA, int L>
@@ -182,7 +341,7 @@ __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
   constexpr int pad = 16 / sizeof(CT);
   constexpr int lda = DA + pad, ldc = kCols + pad, ldp = L + pad;
   constexpr int KB = DA / 32;
-  constexpr int NR = Parts<CT>::kRead, NA = Parts<CT>::kAdd;
+  constexpr int NR = Parts<CT>::kRead;
   __shared__ alignas(16) CT A[2 * L * lda + L * ldc + NR * L * ldp];
   __shared__ float dec[L + 1];  // e^{g n}
   CT *const Bm = A + L * lda;
@@ -190,11 +349,13 @@ __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
   CT *const P = C + L * ldc;
 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
-  const int ct = blockIdx.x % p.ctiles, bh = blockIdx.x / p.ctiles;
+  const int ct = blockIdx.x % p.ctiles, s0 = blockIdx.x / p.ctiles % p.nseg;
+  const int bh = blockIdx.x / p.ctiles / p.nseg;
   const int h = bh % p.H, b = bh / p.H;
   const int c0 = ct * kCols;
   const int valid = valid_length(p.lengths, b, p.T);
   const int len = max(valid, 0);
+  const int lo = s0 * p.seg, hi = min(len, lo + p.seg);  // of the order taken
 
   const float gd = p.log_decay[h];
   for (int n = threadIdx.x; n <= L; n += kThreads) dec[n] = n ? expf(gd * n) : 1.f;
@@ -209,52 +370,79 @@ __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
   f4 X[2 * KB];
   const int xc = c0 + 16 * w + l16;
   const int64_t xb = (int64_t)bh * p.Da * p.Dc;
+  const float *x0 = s0 ? p.xs + ((int64_t)bh * (p.nseg - 1) + s0 - 1) * p.Da * p.Dc
+                       : p.x_in ? p.x_in + xb : nullptr;
 #pragma unroll
   for (int k = 0; k < 2 * KB; ++k)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * k + 4 * g + r;
-      X[k][r] = p.x_in && row < p.Da && xc < p.Dc
-                    ? p.x_in[xb + (p.x_tr ? (int64_t)xc * p.Da + row : (int64_t)row * p.Dc + xc)]
+      X[k][r] = x0 && row < p.Da && xc < p.Dc
+                    ? x0[p.x_tr ? xc * p.Da + row : row * p.Dc + xc]
                     : 0.f;
     }
 
-  for (int t0 = 0; t0 < len; t0 += L) {
-    const int n = min(L, len - t0);
-    // backwards: the first row is the last position not yet taken
-    const int64_t first = p.rev ? len - 1 - t0 : t0;
-    const int64_t step = p.rev ? -1 : 1;
+  Tile<T, CT, DA, L> ta, tb;
+  Tile<T, CT, kCols, L> tc;
+  // rows of a chunk in the order taken: backwards, row 0 is the last
+  // position not yet taken
+  const int64_t step = p.rev ? -1 : 1;
+  auto at = [&](int t0) { return (int64_t)(p.rev ? len - 1 - t0 : t0); };
+  auto fetch = [&](int t0) {
+    const int n = min(L, hi - t0);
+    const int64_t first = at(t0);
+    ta.fetch(a + first * p.a.st, step * p.a.st, p.Da, n, 0);
+    tb.fetch(bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+    tc.fetch(c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+  };
+  if (p.vec && lo < hi) fetch(lo);
+
+  for (int t0 = lo; t0 < hi; t0 += L) {
+    const int n = min(L, hi - t0);
+    const int64_t first = at(t0);
     __syncthreads();
-    stage<T, CT, DA, L>(A, a + first * p.a.st, step * p.a.st, p.Da, n, 0);
-    stage<T, CT, DA, L>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
-    stage<T, CT, kCols, L>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+    if (p.vec) {
+      ta.put(A);
+      tb.put(Bm);
+      tc.put(C);
+    } else {
+      stage<T, CT, DA, L>(A, a + first * p.a.st, step * p.a.st, p.Da, n, 0);
+      stage<T, CT, DA, L>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+      stage<T, CT, kCols, L>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+    }
     __syncthreads();
-    if (p.out && w < L / 16) {
-      // P^T: wave w the columns i of 16w.., rows j <= i
-      for (int jt = 0; jt <= w; ++jt) {
+    if (p.vec && t0 + L < hi) fetch(t0 + L);
+    if (p.out) {
+      // P, its tiles on and below the diagonal shared out over the waves.  A
+      // tile is computed transposed: a lane then holds four neighbours of a
+      // row of P
+      constexpr int NT = L / 16, tiles = NT * (NT + 1) / 2;
+      for (int tile = w; tile < tiles; tile += kThreads / 64) {
+        const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
+        const int jt = tile - it * (it + 1) / 2;
         f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
           acc = mma(frag_row(Bm + (16 * jt + l16) * lda + 32 * kb + 4 * g),
-                    frag_row(A + (16 * w + l16) * lda + 32 * kb + 4 * g), acc);
-        const int i = 16 * w + l16, j = 16 * jt + 4 * g;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float x = i >= j + r ? acc[r] * (dec[max(i - j - r, 0)] * p.p_scale) : 0.f;
-#pragma unroll
-          for (int s = 0; s < NR; ++s) {
-            P[s * L * ldp + i * ldp + j + r] = (CT)x;
-            x -= (float)(CT)x;
-          }
-        }
-      }
-      // an even number of 16-column tiles is read: zeros above the diagonal
-      if (!(w & 1))
+                    frag_row(A + (16 * it + l16) * lda + 32 * kb + 4 * g), acc);
+        const int i = 16 * it + l16, j = 16 * jt + 4 * g;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
+          acc[r] = i >= j + r ? acc[r] * (dec[max(i - j - r, 0)] * p.p_scale) : 0.f;
 #pragma unroll
-          for (int s = 0; s < NR; ++s)
-            P[s * L * ldp + (16 * w + l16) * ldp + 16 * (w + 1) + 4 * g + r] = (CT)0.f;
+        for (int q = 0; q < NR; ++q) {
+          Pack<CT, 4> x;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            x.v[r] = (CT)acc[r];
+            acc[r] -= (float)x.v[r];
+          }
+          *reinterpret_cast<Pack<CT, 4> *>(P + q * L * ldp + i * ldp + j) = x;
+          // P is read 32 columns at a time: zeros right of an odd diagonal tile
+          if (it == jt && !(it & 1))
+            *reinterpret_cast<Pack<CT, 4> *>(P + q * L * ldp + i * ldp + j + 16) = Pack<CT, 4>{};
+        }
+      }
     }
     __syncthreads();
     if (p.out) {
@@ -288,48 +476,36 @@ __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
           for (int s = 0; s < NR; ++s)
             O[it] = mma(cf, frag_row(P + s * L * ldp + i * ldp + 32 * jb + 4 * g), O[it]);
         }
-        if (i < n)
+        const int col = c0 + 16 * w + 4 * g;
+        if (i < n && col < p.Dc) {
+          OT *to = out + (first + step * i) * sot + col;
+          if (p.out_vec) {
+            Pack<OT, 4> x;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int col = c0 + 16 * w + 4 * g + r;
-            if (col < p.Dc) out[(first + step * i) * sot + col] = (OT)O[it][r];
+            for (int r = 0; r < 4; ++r) x.v[r] = (OT)O[it][r];
+            *reinterpret_cast<Pack<OT, 4> *>(to) = x;
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (col + r < p.Dc) to[r] = (OT)O[it][r];
           }
+        }
       }
     }
-    // X <- e^{g n} X + sum_j e^{g (n - off - j)} b_j c_j^T
-#pragma unroll
-    for (int k = 0; k < 2 * KB; ++k)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) X[k][r] *= dec[n];
-#pragma unroll
-    for (int jb = 0; jb < L / 32; ++jb) {
-      float x[8];
-      values(frag_col(C + 32 * jb * ldc + 16 * w, ldc, lane), x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = 32 * jb + 4 * g + (e & 3) + (e >> 2) * 16;
-        x[e] *= dec[max(n - p.off - j, 0)] * p.add_scale;
-      }
-      Frag<CT> cf[NA];
-      split<NA>(x, cf);
-#pragma unroll
-      for (int k = 0; k < 2 * KB; ++k) {
-        const Frag<CT> bf = frag_col(Bm + 32 * jb * lda + 16 * k, lda, lane);
-#pragma unroll
-        for (int s = 0; s < NA; ++s) X[k] = mma(bf, cf[s], X[k]);
-      }
-    }
+    add_chunk<CT, KB, L>(X, Bm, C + 16 * w, dec, n, p.off, p.add_scale, lane);
   }
 
   if (p.out) {
     const OT fill = (OT)(valid < 0 ? p.bad : 0.f);
-    for (int64_t e = threadIdx.x; e < (int64_t)(p.T - len) * kCols; e += kThreads) {
-      const int64_t t = len + e / kCols;
+    const int f0 = max(len, lo), f1 = min((int64_t)p.T, (int64_t)lo + p.seg);
+    for (int64_t e = threadIdx.x; e < (int64_t)(f1 - f0) * kCols; e += kThreads) {
+      const int64_t t = f0 + e / kCols;
       const int col = c0 + e % kCols;
       if (col < p.Dc) out[t * sot + col] = fill;
     }
   }
-  if (p.x_out) {
+  // the segment that holds the last valid position (the first, if none)
+  if (p.x_out && hi == len && (lo < len || s0 == 0)) {
 #pragma unroll
     for (int k = 0; k < 2 * KB; ++k)
 #pragma unroll
@@ -408,35 +584,86 @@ int round_da(int D) { return D <= 32 ? 32 : D <= 64 ? 64 : D <= 128 ? 128 : 256;
 
 // Chunks of 64 positions; of 32 where float32 operands 256 wide would not
 // leave a compute unit's 160 KB of LDS room for the tiles of 64.
+template <typename CT, int DA>
+constexpr int chunk_of() {
+  return sizeof(CT) * DA > 512 ? 32 : 64;
+}
+
 template <typename T, typename CT, typename OT, int DA>
-semicrf_status_t launch_da(const LaArgs &p, hipStream_t st) {
-  constexpr int L = sizeof(CT) * DA > 512 ? 32 : 64;
-  const int64_t grid = (int64_t)p.B * p.H * p.ctiles;
-  if (grid > 0x7fffffff) return SEMICRF_ERR_SHAPE;
-  k_linattn<T, CT, OT, DA, L><<<(unsigned)grid, kThreads, 0, st>>>(p);
+semicrf_status_t launch_da(const LaArgs &p, bool states, hipStream_t st) {
+  constexpr int L = chunk_of<CT, DA>();
+  if (states) {
+    const int64_t grid = (int64_t)p.B * p.H * (p.nseg - 1) * p.ctiles;
+    k_linattn_state<T, CT, DA, L><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  } else {
+    const int64_t grid = (int64_t)p.B * p.H * p.nseg * p.ctiles;
+    k_linattn<T, CT, OT, DA, L><<<(unsigned)grid, kThreads, 0, st>>>(p);
+  }
   return launch_status();
 }
 
 template <typename T, typename CT, typename OT>
-semicrf_status_t launch_t(const LaArgs &p, hipStream_t st) {
+semicrf_status_t launch_t(const LaArgs &p, bool states, hipStream_t st) {
   switch (round_da(p.Da)) {
-    case 32: return launch_da<T, CT, OT, 32>(p, st);
-    case 64: return launch_da<T, CT, OT, 64>(p, st);
-    case 128: return launch_da<T, CT, OT, 128>(p, st);
-    default: return launch_da<T, CT, OT, 256>(p, st);
+    case 32: return launch_da<T, CT, OT, 32>(p, states, st);
+    case 64: return launch_da<T, CT, OT, 64>(p, states, st);
+    case 128: return launch_da<T, CT, OT, 128>(p, states, st);
+    default: return launch_da<T, CT, OT, 256>(p, states, st);
   }
 }
 
-// f32_out: the output is float32 whatever the tensors are (parts of the
-// gradient of a shared head).
-semicrf_status_t launch_linattn(const LaArgs &p, int dtype, bool f32_out, hipStream_t st) {
+// Whether every row of a tensor is a whole number of aligned 16-byte pieces.
+bool aligned(const View &v, int D, int dtype) {
+  const int e = 16 / elem_size(dtype);
+  return (uintptr_t)v.p % 16 == 0 && D % e == 0 && v.sb % e == 0 && v.st % e == 0 &&
+         v.sh % e == 0;
+}
+
+// The pass over the chunks.  f32_out: the output is float32 whatever the
+// tensors are (parts of the gradient of a shared head).
+semicrf_status_t launch_linattn(LaArgs p, int dtype, bool f32_out, hipStream_t st) {
+  p.vec = aligned(p.a, p.Da, dtype) && aligned(p.b, p.Da, dtype) && aligned(p.c, p.Dc, dtype);
+  p.out_vec = p.Dc % 4 == 0 && (uintptr_t)p.out % (4 * (f32_out ? 4 : elem_size(dtype))) == 0;
   switch (dtype) {
-    case SEMICRF_F32: return launch_t<float, float, float>(p, st);
+    case SEMICRF_F32: return launch_t<float, float, float>(p, false, st);
     case SEMICRF_BF16:
-      return f32_out ? launch_t<bf16, bf16, float>(p, st) : launch_t<bf16, bf16, bf16>(p, st);
+      return f32_out ? launch_t<bf16, bf16, float>(p, false, st)
+                     : launch_t<bf16, bf16, bf16>(p, false, st);
     default:
-      return f32_out ? launch_t<f16, float, float>(p, st) : launch_t<f16, float, f16>(p, st);
+      return f32_out ? launch_t<f16, float, float>(p, false, st)
+                     : launch_t<f16, float, f16>(p, false, st);
   }
+}
+
+// The segments' states of a pair (b, c) in p.xs.
+semicrf_status_t launch_states(LaArgs p, int dtype, hipStream_t st) {
+  if (p.nseg < 2) return SEMICRF_OK;
+  p.vec = aligned(p.b, p.Da, dtype) && aligned(p.c, p.Dc, dtype);
+  semicrf_status_t e = dtype == SEMICRF_F32    ? launch_t<float, float, float>(p, true, st)
+                       : dtype == SEMICRF_BF16 ? launch_t<bf16, bf16, bf16>(p, true, st)
+                                               : launch_t<f16, float, f16>(p, true, st);
+  if (e != SEMICRF_OK) return e;
+  const int64_t n = (int64_t)p.B * p.H * p.Da * p.Dc;
+  k_linattn_scan<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
+  return launch_status();
+}
+
+// Segments: enough for kFill workgroups, each of four chunks at least.
+constexpr int kFill = 1024;
+void segments(const semicrf_linattn_shape_t *s, int *nseg, int *seg) {
+  const int64_t heads = (int64_t)s->B * s->H, chunks = (s->T + 63) / 64;
+  int64_t n = (kFill + heads - 1) / heads;
+  if (n > chunks / 4) n = chunks / 4;
+  if (n < 1) n = 1;
+  const int64_t per = (chunks + n - 1) / n;
+  *seg = (int)(per * 64);
+  *nseg = (int)((chunks + per - 1) / per);
+}
+
+size_t state_bytes(const semicrf_linattn_shape_t *s) {
+  int nseg, seg;
+  segments(s, &nseg, &seg);
+  return ((size_t)s->B * s->H * (nseg - 1) * s->Dk * s->Dv * sizeof(float) + 255) / 256 * 256;
 }
 
 semicrf_status_t check(const semicrf_linattn_shape_t *s) {
@@ -444,7 +671,9 @@ semicrf_status_t check(const semicrf_linattn_shape_t *s) {
   if (s->B < 1 || s->T < 1 || s->H < 1 || s->Hq < 1 || s->Hk < 1 || s->Hv < 1 || s->Dk < 1 ||
       s->Dv < 1 || s->H % s->Hq || s->H % s->Hk || s->H % s->Hv)
     return SEMICRF_ERR_SHAPE;
-  if ((int64_t)s->B * s->H * 4 > 0x7fffffff) return SEMICRF_ERR_SHAPE;
+  // a grid counts sequences, heads, four column tiles and the segments, which
+  // are few where those are many; a state's elements over 256 threads
+  if (s->T > 1 << 30 || (int64_t)s->B * s->H * 1024 > 0x7fffffff) return SEMICRF_ERR_SHAPE;
   if (s->Dk > 256 || s->Dv > 256) return SEMICRF_ERR_UNSUPPORTED;
   if (!dtype_ok(s->dtype)) return SEMICRF_ERR_ARG;
   return SEMICRF_OK;
@@ -489,9 +718,9 @@ semicrf_status_t semicrf_linattn_workspace_size(const semicrf_linattn_shape_t *s
   if (!bytes) return SEMICRF_ERR_NULL;
   const semicrf_status_t e = check(s);
   if (e != SEMICRF_OK) return e;
-  *bytes = 0;
+  *bytes = state_bytes(s);
   if (backward)
-    *bytes = share_bytes(s, s->Hq, s->Dk) + share_bytes(s, s->Hk, s->Dk) +
+    *bytes += share_bytes(s, s->Hq, s->Dk) + share_bytes(s, s->Hk, s->Dk) +
              share_bytes(s, s->Hv, s->Dv);
   return SEMICRF_OK;
 }
@@ -522,7 +751,10 @@ semicrf_status_t semicrf_linattn_fwd(const semicrf_linattn_shape_t *s, const voi
   p.add_scale = 1.f;
   p.B = s->B, p.T = s->T, p.H = s->H, p.Da = s->Dk, p.Dc = s->Dv;
   p.ctiles = (p.Dc + kCols - 1) / kCols;
-  return launch_linattn(p, s->dtype, false, (hipStream_t)stream);
+  p.xs = (float *)workspace;
+  segments(s, &p.nseg, &p.seg);
+  const semicrf_status_t r = launch_states(p, s->dtype, (hipStream_t)stream);
+  return r == SEMICRF_OK ? launch_linattn(p, s->dtype, false, (hipStream_t)stream) : r;
 }
 
 semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const void *q,
@@ -539,6 +771,8 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
   (void)hipGetLastError();
   hipStream_t st = (hipStream_t)stream;
   char *ws = (char *)workspace;
+  float *xs = (float *)ws;
+  ws += state_bytes(s);
   float *pq = (float *)ws;
   ws += share_bytes(s, s->Hq, s->Dk);
   float *pk = (float *)ws;
@@ -553,30 +787,45 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
   p.lengths = lengths;
   p.p_scale = s->scale;
   p.B = s->B, p.T = s->T, p.H = s->H;
-  auto run = [&](View a, View b, View c, int Da, int Dc, void *out, float *part, int heads) {
+  p.xs = xs;
+  segments(s, &p.nseg, &p.seg);
+  auto set = [&](View a, View b, View c, int Da, int Dc) {
     p.a = a, p.b = b, p.c = c, p.Da = Da, p.Dc = Dc;
     p.ctiles = (Dc + kCols - 1) / kCols;
+  };
+  auto run = [&](void *out, float *part, int heads) {
     const bool shared = out && heads != s->H;
     p.out = shared ? part : out;
     semicrf_status_t r = launch_linattn(p, s->dtype, shared, st);
-    if (r == SEMICRF_OK && shared) r = share_sum(s, part, out, heads, Dc, st);
+    if (r == SEMICRF_OK && shared) r = share_sum(s, part, out, heads, p.Dc, st);
     return r;
   };
   if (grad_q) {
-    p.x_in = state_in, p.x_tr = 1, p.x_out = nullptr, p.rev = 0, p.off = 1;
+    p.x_in = state_in, p.rev = 0, p.off = 1;
     p.x_scale = s->scale, p.add_scale = 1.f;
-    e = run(vg, vv, vk, s->Dv, s->Dk, grad_q, pq, s->Hq);
+    set(vq, vk, vv, s->Dk, s->Dv);
+    e = launch_states(p, s->dtype, st);
+    if (e != SEMICRF_OK) return e;
+    p.x_tr = 1;
+    set(vg, vv, vk, s->Dv, s->Dk);
+    e = run(grad_q, pq, s->Hq);
     if (e != SEMICRF_OK) return e;
   }
-  p.rev = 1, p.off = 0, p.x_scale = 1.f, p.add_scale = s->scale, p.x_in = grad_state;
-  if (grad_k) {
-    p.x_tr = 1, p.x_out = nullptr;
-    e = run(vv, vg, vq, s->Dv, s->Dk, grad_k, pk, s->Hk);
+  p.rev = 1, p.off = 0, p.x_scale = 1.f, p.add_scale = s->scale, p.x_in = grad_state, p.x_tr = 0;
+  if (grad_k || grad_v || grad_state_in) {
+    set(vk, vq, vg, s->Dk, s->Dv);
+    e = launch_states(p, s->dtype, st);
     if (e != SEMICRF_OK) return e;
   }
   if (grad_v || grad_state_in) {
-    p.x_tr = 0, p.x_out = grad_state_in;
-    e = run(vk, vq, vg, s->Dk, s->Dv, grad_v, pv, s->Hv);
+    p.x_out = grad_state_in;
+    e = run(grad_v, pv, s->Hv);
+    if (e != SEMICRF_OK) return e;
+  }
+  if (grad_k) {
+    p.x_tr = 1, p.x_out = nullptr;
+    set(vv, vg, vq, s->Dv, s->Dk);
+    e = run(grad_k, pk, s->Hk);
   }
   return e;
 }
