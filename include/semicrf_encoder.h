@@ -42,6 +42,10 @@ enum { SEMICRF_ACT_NONE = 0, SEMICRF_ACT_SILU = 1, SEMICRF_ACT_GELU = 2, SEMICRF
  * everything before the position itself.  g is a constant of the model: it
  * gets no gradient.
  *
+ * Non-finite inputs are not checked: one at a valid position may reach any
+ * row of its sequence and head (positions are worked on in blocks, whose
+ * masked products are zeros times what they multiply).
+ *
  * Layout.  q, k [B][T][Hq or Hk][Dk], v [B][T][Hv][Dv] of one type (F32,
  * BF16 or F16) with the element strides given for B, T and heads; the last
  * dimension is contiguous.  H is a multiple of Hq, Hk and Hv: head h reads

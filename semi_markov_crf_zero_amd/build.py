@@ -33,12 +33,17 @@ COMMON = [
     "-I" + os.path.join(ROOT, "include"), "-I" + CSRC,
     "-Wall", "-Wno-unused-result",
 ]
+# Matrix instructions that accumulate in the vector registers they are read
+# from: linattn.hip's accumulators are operands of the next product, and
+# without this a tenth of its loop copies them from and to the accumulation
+# registers.
+EXTRA = {"linattn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def _compile(src: str, asm: bool) -> str:
     obj = os.path.join(BUILD, os.path.basename(os.path.dirname(src)) + "_" +
                        os.path.basename(src) + ".o")
-    cmd = [HIPCC] + COMMON + ["-c", src, "-o", obj]
+    cmd = [HIPCC] + COMMON + EXTRA.get(os.path.basename(src), []) + ["-c", src, "-o", obj]
     if asm:
         cmd += ["--save-temps"]
     r = subprocess.run(cmd, cwd=BUILD, capture_output=True, text=True)

@@ -40,10 +40,16 @@ namespace semicrf {
 namespace {
 
 typedef f32x4_t f4;
+typedef float f2 __attribute__((ext_vector_type(2)));
+typedef __bf16 b2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef s4 __attribute__((address_space(3))) lds_s4;
 
+typedef unsigned u4 __attribute__((ext_vector_type(4)));
+
+constexpr int kRange = 0x7fffffff;      // bytes a buffer descriptor reaches
+constexpr int kRawBuffer = 0x00027000;  // its last word: raw 32-bit data
 constexpr int kThreads = 256;  // four waves, 16 output columns each
 constexpr int kCols = 64;      // output columns of a workgroup
 
@@ -70,7 +76,6 @@ struct LaArgs {
   float p_scale, x_scale, add_scale;  // of P, of A X, of what a chunk adds to X
   int B, T, H, Da, Dc;
   int ctiles;
-  int vec, out_vec;  // 16-byte loads; four elements a store
 };
 
 // A fragment is a lane's part of one operand over a 32-wide stretch of the
@@ -145,23 +150,42 @@ template <>
 struct Parts<float> {
   static constexpr int kRead = 1, kAdd = 1;
 };
+// Two neighbours at a time: one instruction rounds a pair.
 template <int N>
 __device__ __forceinline__ void split(const float *x, Frag<bf16> *f) {
-  float r[8];
+  f2 r[4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) r[e] = x[e];
+  for (int e = 0; e < 4; ++e) r[e] = f2{x[2 * e], x[2 * e + 1]};
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      f[n].v[e] = (bf16)r[e];
-      r[e] -= (float)f[n].v[e];
+    for (int e = 0; e < 4; ++e) {
+      const b2 y = __builtin_convertvector(r[e], b2);
+      f[n].v[2 * e] = y[0];
+      f[n].v[2 * e + 1] = y[1];
+      r[e] -= __builtin_convertvector(y, f2);
     }
 }
 template <int N>
 __device__ __forceinline__ void split(const float *x, Frag<float> *f) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) f[0].v[e] = x[e];
+}
+// Four float32 values rounded to the type; x keeps what is left of them.
+__device__ __forceinline__ void part4(f4 &x, Pack<bf16, 4> &y) {
+  const f2 lo = {x[0], x[1]}, hi = {x[2], x[3]};
+  const b2 a = __builtin_convertvector(lo, b2), b = __builtin_convertvector(hi, b2);
+  const f2 ra = lo - __builtin_convertvector(a, f2), rb = hi - __builtin_convertvector(b, f2);
+  x = f4{ra[0], ra[1], rb[0], rb[1]};
+  y = {{a[0], a[1], b[0], b[1]}};
+}
+template <typename T>
+__device__ __forceinline__ void part4(f4 &x, Pack<T, 4> &y) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    y.v[r] = (T)x[r];
+    x[r] -= (float)y.v[r];
+  }
 }
 __device__ __forceinline__ void values(const Frag<bf16> &f, float *x) {
 #pragma unroll
@@ -174,33 +198,37 @@ __device__ __forceinline__ void values(const Frag<float> &f, float *x) {
 
 // A tile of a chunk: L rows of W columns, zeros past row n and past column
 // D.  fetch() issues a thread's 16-byte loads into registers while the chunk
-// before is worked on, put() writes them to LDS.
+// before is worked on, put() writes them to LDS.  The loads go through a
+// buffer descriptor whose range a row that is not wanted lies past, so it
+// reads 0 without a branch, whatever memory holds there.
 template <typename T, typename CT, int W, int L>
 struct Tile {
   static constexpr int VE = 16 / sizeof(T), per = W / VE, NV = L * per / kThreads;
   static constexpr int ld = W + 16 / sizeof(CT);
-  Pack<T, VE> r[NV];
+  u4 r[NV];
 
-  __device__ __forceinline__ void fetch(const T *src, int64_t st, int D, int n, int col0) {
+  // row i of the tile is row `row0 + step * i` (step +-1) from src, rows st
+  // elements apart
+  __device__ __forceinline__ void fetch(const T *src, int st, int D, int n, int row0, int step,
+                                        int col0) {
     const int c = threadIdx.x % per * VE, i0 = threadIdx.x / per;
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src, 0, kRange, kRawBuffer);
+    const bool col = col0 + c < D;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = i0 + k * (kThreads / per);
-      if (i < n && col0 + c < D) {
-        r[k] = *reinterpret_cast<const Pack<T, VE> *>(src + i * st + col0 + c);
-      } else {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) r[k].v[e] = (T)0.f;
-      }
+      const int at = ((row0 + step * i) * st + col0 + c) * (int)sizeof(T);
+      r[k] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, i < n && col ? at : -1, 0, 0);
     }
   }
   __device__ __forceinline__ void put(CT *lds) const {
     const int c = threadIdx.x % per * VE, i0 = threadIdx.x / per;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
+      const Pack<T, VE> y = __builtin_bit_cast(Pack<T, VE>, r[k]);
       Pack<CT, VE> x;
 #pragma unroll
-      for (int e = 0; e < VE; ++e) x.v[e] = (CT)r[k].v[e];
+      for (int e = 0; e < VE; ++e) x.v[e] = (CT)y.v[e];
       CT *to = lds + (i0 + k * (kThreads / per)) * ld + c;
 #pragma unroll
       for (int e = 0; e < VE; e += 16 / sizeof(CT))
@@ -221,27 +249,44 @@ __device__ __forceinline__ void stage(CT *lds, const T *src, int64_t st, int D, 
   }
 }
 
+// The decays a workgroup uses, with the pass's factors in them; entries of
+// negative powers are 0, so masked places need no branch.
+template <int L>
+struct Decays {
+  float x[L + 1];       // e^{g n}: of X over n positions
+  float p[2 * L];       // p_scale e^{g (n - L)}: of P
+  float read[L];        // x_scale e^{g (i + off)}: of X read by position i
+  float add[2 * L + 1]; // add_scale e^{g (n - L)}: of what a position adds to X
+
+  __device__ __forceinline__ void fill(const LaArgs &a, float g) {
+    auto e = [&](int n) { return n < 0 ? 0.f : n ? expf(g * n) : 1.f; };
+    for (int n = threadIdx.x; n < 2 * L + 1; n += kThreads) {
+      add[n] = a.add_scale * e(n - L);
+      if (n <= L) x[n] = e(n);
+      if (n < 2 * L) p[n] = a.p_scale * e(n - L);
+      if (n < L) read[n] = a.x_scale * e(n + a.off);
+    }
+  }
+};
+
 // X <- e^{g n} X + sum_j e^{g (n - off - j)} b_j c_j^T over a staged chunk:
-// B in rows of lda, this wave's 16 columns of C in rows of ldc.
+// B in rows of lda, this wave's 16 columns of C in fragments.
 template <typename CT, int KB, int L>
-__device__ __forceinline__ void add_chunk(f4 *X, const CT *Bm, const CT *C, const float *dec,
-                                          int n, int off, float scale, int lane) {
-  constexpr int lda = 32 * KB + 16 / sizeof(CT), ldc = kCols + 16 / sizeof(CT);
+__device__ __forceinline__ void add_chunk(f4 *X, const CT *Bm, const Frag<CT> *C,
+                                          const Decays<L> &dec, int n, int off, int lane) {
+  constexpr int lda = 32 * KB + 16 / sizeof(CT);
   constexpr int NA = Parts<CT>::kAdd;
-  const int g = lane >> 4;
+  const float *add = dec.add + L + n - off - 4 * (lane >> 4);
 #pragma unroll
   for (int k = 0; k < 2 * KB; ++k)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) X[k][r] *= dec[n];
+    for (int r = 0; r < 4; ++r) X[k][r] *= dec.x[n];
 #pragma unroll
   for (int jb = 0; jb < L / 32; ++jb) {
     float x[8];
-    values(frag_col(C + 32 * jb * ldc, ldc, lane), x);
+    values(C[jb], x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int j = 32 * jb + 4 * g + (e & 3) + (e >> 2) * 16;
-      x[e] *= dec[max(n - off - j, 0)] * scale;
-    }
+    for (int e = 0; e < 8; ++e) x[e] *= add[-(32 * jb + (e & 3) + (e >> 2) * 16)];
     Frag<CT> cf[NA];
     split<NA>(x, cf);
 #pragma unroll
@@ -257,21 +302,20 @@ __device__ __forceinline__ void add_chunk(f4 *X, const CT *Bm, const CT *C, cons
 
 // Parts of X: one workgroup per segment but the last, kCols columns.  Writes
 // xs[segment]; a segment past the length leaves zeros.
-template <typename T, typename CT, int DA, int L>
+template <typename T, typename CT, int DA, int L, bool VEC>
 __global__ __launch_bounds__(kThreads) void k_linattn_state(LaArgs p) {
   constexpr int pad = 16 / sizeof(CT);
   constexpr int lda = DA + pad, ldc = kCols + pad, KB = DA / 32;
   __shared__ alignas(16) CT Bm[L * lda + L * ldc];
   CT *const C = Bm + L * lda;
-  __shared__ float dec[L + 1];
+  __shared__ Decays<L> dec;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int ct = blockIdx.x % p.ctiles, s0 = blockIdx.x / p.ctiles % (p.nseg - 1);
   const int bh = blockIdx.x / p.ctiles / (p.nseg - 1);
   const int h = bh % p.H, b = bh / p.H, c0 = ct * kCols;
   const int len = max(valid_length(p.lengths, b, p.T), 0);
   const int lo = s0 * p.seg, hi = min(len, lo + p.seg);
-  const float gd = p.log_decay[h];
-  for (int n = threadIdx.x; n <= L; n += kThreads) dec[n] = n ? expf(gd * n) : 1.f;
+  dec.fill(p, p.log_decay[h]);
   const T *bb = (const T *)p.b.p + (int64_t)b * p.b.sb + (int64_t)(h / p.b.share) * p.b.sh;
   const T *c = (const T *)p.c.p + (int64_t)b * p.c.sb + (int64_t)(h / p.c.share) * p.c.sh;
   f4 X[2 * KB];
@@ -279,28 +323,32 @@ __global__ __launch_bounds__(kThreads) void k_linattn_state(LaArgs p) {
   for (int k = 0; k < 2 * KB; ++k) X[k] = f4{0.f, 0.f, 0.f, 0.f};
   Tile<T, CT, DA, L> tb;
   Tile<T, CT, kCols, L> tc;
-  const int64_t step = p.rev ? -1 : 1;
+  // rows of a chunk in the order taken; `base` is the lowest position
+  const int step = p.rev ? -1 : 1;
   auto fetch = [&](int t0) {
-    const int n = min(L, hi - t0);
-    const int64_t first = p.rev ? len - 1 - t0 : t0;
-    tb.fetch(bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
-    tc.fetch(c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+    const int n = min(L, hi - t0), row0 = p.rev ? n - 1 : 0;
+    const int64_t base = p.rev ? len - t0 - n : t0;
+    tb.fetch(bb + base * p.b.st, (int)p.b.st, p.Da, n, row0, step, 0);
+    tc.fetch(c + base * p.c.st, (int)p.c.st, p.Dc, n, row0, step, c0);
   };
-  if (p.vec && lo < hi) fetch(lo);
+  if (VEC && lo < hi) fetch(lo);
   for (int t0 = lo; t0 < hi; t0 += L) {
     const int n = min(L, hi - t0);
-    const int64_t first = p.rev ? len - 1 - t0 : t0;
     __syncthreads();
-    if (p.vec) {
+    if (VEC) {
       tb.put(Bm);
       tc.put(C);
     } else {
+      const int64_t first = p.rev ? len - 1 - t0 : t0;
       stage<T, CT, DA, L>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
       stage<T, CT, kCols, L>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
     }
     __syncthreads();
-    if (p.vec && t0 + L < hi) fetch(t0 + L);
-    add_chunk<CT, KB, L>(X, Bm, C + 16 * w, dec, n, p.off, p.add_scale, lane);
+    if (VEC && t0 + L < hi) fetch(t0 + L);
+    Frag<CT> cf[L / 32];
+#pragma unroll
+    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col(C + 32 * jb * ldc + 16 * w, ldc, lane);
+    add_chunk<CT, KB, L>(X, Bm, cf, dec, n, p.off, lane);
   }
   const int xc = c0 + 16 * w + l16;
   float *out = p.xs + ((int64_t)bh * (p.nseg - 1) + s0) * p.Da * p.Dc;
@@ -324,11 +372,18 @@ __global__ __launch_bounds__(kThreads) void k_linattn_scan(LaArgs p) {
   const int len = max(valid_length(p.lengths, b, p.T), 0);
   float *x = p.xs + bh * (p.nseg - 1) * n + e % n;
   float acc = p.x_in ? p.x_in[e] : 0.f;
-  const float gd = p.log_decay[h];
-  for (int s = 0; s < p.nseg - 1; ++s) {
-    const int m = min(max(len - s * p.seg, 0), p.seg);
-    acc = (m ? expf(gd * m) : 1.f) * acc + x[s * n];
-    x[s * n] = acc;
+  const float gd = p.log_decay[h], whole = expf(gd * p.seg);
+  // eight loads at a time: the sum is a chain, the loads are not
+  for (int s0 = 0; s0 < p.nseg - 1; s0 += 8) {
+    float part[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[k] = s0 + k < p.nseg - 1 ? x[(s0 + k) * n] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int s = s0 + k, m = min(max(len - s * p.seg, 0), p.seg);
+      acc = (m == p.seg ? whole : m ? expf(gd * m) : 1.f) * acc + part[k];
+      if (s < p.nseg - 1) x[s * n] = acc;
+    }
   }
 }
 
@@ -336,14 +391,14 @@ __global__ __launch_bounds__(kThreads) void k_linattn_scan(LaArgs p) {
 // output, every chunk in turn.  T: the tensors' type; CT: the operands' type (bfloat16 as
 // it is; float32 and float16 in float32: float16 would need its range
 // watched in P and X); OT: the output's; DA: Da rounded up.
-template <typename T, typename CT, typename OT, int DA, int L>
+template <typename T, typename CT, typename OT, int DA, int L, bool VEC>
 __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
   constexpr int pad = 16 / sizeof(CT);
   constexpr int lda = DA + pad, ldc = kCols + pad, ldp = L + pad;
   constexpr int KB = DA / 32;
   constexpr int NR = Parts<CT>::kRead;
   __shared__ alignas(16) CT A[2 * L * lda + L * ldc + NR * L * ldp];
-  __shared__ float dec[L + 1];  // e^{g n}
+  __shared__ Decays<L> dec;
   CT *const Bm = A + L * lda;
   CT *const C = Bm + L * lda;
   CT *const P = C + L * ldc;
@@ -357,8 +412,7 @@ __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
   const int len = max(valid, 0);
   const int lo = s0 * p.seg, hi = min(len, lo + p.seg);  // of the order taken
 
-  const float gd = p.log_decay[h];
-  for (int n = threadIdx.x; n <= L; n += kThreads) dec[n] = n ? expf(gd * n) : 1.f;
+  dec.fill(p, p.log_decay[h]);
 
   const T *a = (const T *)p.a.p + (int64_t)b * p.a.sb + (int64_t)(h / p.a.share) * p.a.sh;
   const T *bb = (const T *)p.b.p + (int64_t)b * p.b.sb + (int64_t)(h / p.b.share) * p.b.sh;
@@ -366,89 +420,100 @@ __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
   OT *out = (OT *)p.out + ((int64_t)b * p.T * p.H + h) * p.Dc;
   const int64_t sot = (int64_t)p.H * p.Dc;
 
-  // X: tile k holds rows 16k + 4g + r of column c0 + 16w + lane % 16
+  // X: tile k holds rows 16k + 4g + r of column c0 + 16w + lane % 16.  All
+  // loads at once, through a descriptor that reads 0 past the state
   f4 X[2 * KB];
   const int xc = c0 + 16 * w + l16;
   const int64_t xb = (int64_t)bh * p.Da * p.Dc;
   const float *x0 = s0 ? p.xs + ((int64_t)bh * (p.nseg - 1) + s0 - 1) * p.Da * p.Dc
                        : p.x_in ? p.x_in + xb : nullptr;
+  const auto xr = __builtin_amdgcn_make_buffer_rsrc((void *)x0, 0, x0 ? kRange : 0, kRawBuffer);
+  const int xrow = p.x_tr ? 1 : p.Dc, xcol = p.x_tr ? p.Da : 1;
 #pragma unroll
   for (int k = 0; k < 2 * KB; ++k)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * k + 4 * g + r;
-      X[k][r] = x0 && row < p.Da && xc < p.Dc
-                    ? x0[p.x_tr ? xc * p.Da + row : row * p.Dc + xc]
-                    : 0.f;
+      const int at = 4 * (row * xrow + xc * xcol);
+      X[k][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                              xr, row < p.Da && xc < p.Dc ? at : -1, 0, 0));
     }
 
   Tile<T, CT, DA, L> ta, tb;
   Tile<T, CT, kCols, L> tc;
   // rows of a chunk in the order taken: backwards, row 0 is the last
-  // position not yet taken
-  const int64_t step = p.rev ? -1 : 1;
-  auto at = [&](int t0) { return (int64_t)(p.rev ? len - 1 - t0 : t0); };
+  // position not yet taken; `base` is the lowest position
+  const int step = p.rev ? -1 : 1;
   auto fetch = [&](int t0) {
-    const int n = min(L, hi - t0);
-    const int64_t first = at(t0);
-    ta.fetch(a + first * p.a.st, step * p.a.st, p.Da, n, 0);
-    tb.fetch(bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
-    tc.fetch(c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+    const int n = min(L, hi - t0), row0 = p.rev ? n - 1 : 0;
+    const int64_t base = p.rev ? len - t0 - n : t0;
+    ta.fetch(a + base * p.a.st, (int)p.a.st, p.Da, n, row0, step, 0);
+    tb.fetch(bb + base * p.b.st, (int)p.b.st, p.Da, n, row0, step, 0);
+    tc.fetch(c + base * p.c.st, (int)p.c.st, p.Dc, n, row0, step, c0);
   };
-  if (p.vec && lo < hi) fetch(lo);
-
-  for (int t0 = lo; t0 < hi; t0 += L) {
-    const int n = min(L, hi - t0);
-    const int64_t first = at(t0);
-    __syncthreads();
-    if (p.vec) {
+  auto stage_chunk = [&](int t0) {
+    if (VEC) {
       ta.put(A);
       tb.put(Bm);
       tc.put(C);
     } else {
+      const int n = min(L, hi - t0);
+      const int64_t first = p.rev ? len - 1 - t0 : t0;
       stage<T, CT, DA, L>(A, a + first * p.a.st, step * p.a.st, p.Da, n, 0);
       stage<T, CT, DA, L>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
       stage<T, CT, kCols, L>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
     }
+  };
+  if (lo < hi) {
+    if (VEC) fetch(lo);
+    stage_chunk(lo);
+  }
+
+  // Two barriers a chunk: one when its tiles and one when P is in LDS.
+  // Everything that reads the tiles comes before the second, so the next
+  // chunk's tiles follow it at once.
+  constexpr int NT = L / 16;
+  for (int t0 = lo; t0 < hi; t0 += L) {
+    const int n = min(L, hi - t0);
     __syncthreads();
-    if (p.vec && t0 + L < hi) fetch(t0 + L);
+    if (VEC && t0 + L < hi) fetch(t0 + L);
+    Frag<CT> cf[L / 32];
+#pragma unroll
+    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col(C + 32 * jb * ldc + 16 * w, ldc, lane);
+    f4 O[NT];
     if (p.out) {
-      // P, its tiles on and below the diagonal shared out over the waves.  A
+      // P: wave w its rows 16w.., the tiles up to the diagonal and, as P is
+      // read 32 columns at a time, the one beside it (zeros, by the table).  A
       // tile is computed transposed: a lane then holds four neighbours of a
       // row of P
-      constexpr int NT = L / 16, tiles = NT * (NT + 1) / 2;
-      for (int tile = w; tile < tiles; tile += kThreads / 64) {
-        const int it = tile < 1 ? 0 : tile < 3 ? 1 : tile < 6 ? 2 : 3;
-        const int jt = tile - it * (it + 1) / 2;
-        f4 acc = {0.f, 0.f, 0.f, 0.f};
+      if (w < NT) {
+        Frag<CT> af[KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
-          acc = mma(frag_row(Bm + (16 * jt + l16) * lda + 32 * kb + 4 * g),
-                    frag_row(A + (16 * it + l16) * lda + 32 * kb + 4 * g), acc);
-        const int i = 16 * it + l16, j = 16 * jt + 4 * g;
+          af[kb] = frag_row(A + (16 * w + l16) * lda + 32 * kb + 4 * g);
+        const int i = 16 * w + l16;
+        const float *dp = dec.p + L + i - 4 * g;
+        CT *to = P + i * ldp + 4 * g;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[r] = i >= j + r ? acc[r] * (dec[max(i - j - r, 0)] * p.p_scale) : 0.f;
+        for (int jt = 0; jt < NT; ++jt) {
+          if (jt > (w | 1)) break;
+          f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < NR; ++q) {
-          Pack<CT, 4> x;
+          for (int kb = 0; kb < KB; ++kb)
+            acc = mma(frag_row(Bm + (16 * jt + l16) * lda + 32 * kb + 4 * g), af[kb], acc);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x.v[r] = (CT)acc[r];
-            acc[r] -= (float)x.v[r];
+          for (int r = 0; r < 4; ++r) acc[r] *= dp[-(16 * jt + r)];
+#pragma unroll
+          for (int q = 0; q < NR; ++q) {
+            Pack<CT, 4> x;
+            part4(acc, x);
+            *reinterpret_cast<Pack<CT, 4> *>(to + q * L * ldp + 16 * jt) = x;
           }
-          *reinterpret_cast<Pack<CT, 4> *>(P + q * L * ldp + i * ldp + j) = x;
-          // P is read 32 columns at a time: zeros right of an odd diagonal tile
-          if (it == jt && !(it & 1))
-            *reinterpret_cast<Pack<CT, 4> *>(P + q * L * ldp + i * ldp + j + 16) = Pack<CT, 4>{};
         }
       }
-    }
-    __syncthreads();
-    if (p.out) {
-      f4 O[L / 16];
+      // what X gives to each position
 #pragma unroll
-      for (int it = 0; it < L / 16; ++it) O[it] = f4{0.f, 0.f, 0.f, 0.f};
+      for (int it = 0; it < NT; ++it) O[it] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
         float x[8];
@@ -457,32 +522,37 @@ __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
         Frag<CT> xf[NR];
         split<NR>(x, xf);
 #pragma unroll
-        for (int it = 0; it < L / 16; ++it) {
+        for (int it = 0; it < NT; ++it) {
           const Frag<CT> af = frag_row(A + (16 * it + l16) * lda + 32 * kb + 4 * g);
 #pragma unroll
-          for (int s = 0; s < NR; ++s) O[it] = mma(xf[s], af, O[it]);
+          for (int q = 0; q < NR; ++q) O[it] = mma(xf[q], af, O[it]);
         }
       }
 #pragma unroll
-      for (int it = 0; it < L / 16; ++it) {
-        const int i = 16 * it + l16;
-        const float d = dec[i + p.off] * p.x_scale;
+      for (int it = 0; it < NT; ++it) {
+        const float d = dec.read[16 * it + l16];
 #pragma unroll
         for (int r = 0; r < 4; ++r) O[it][r] *= d;
+      }
+    }
+    add_chunk<CT, KB, L>(X, Bm, cf, dec, n, p.off, lane);
+    __syncthreads();
+    if (p.out) {
+      const int64_t first = p.rev ? len - 1 - t0 : t0;
+      const int col = c0 + 16 * w + 4 * g;
 #pragma unroll
-        for (int jb = 0; jb <= it / 2; ++jb) {
-          const Frag<CT> cf = frag_col(C + 32 * jb * ldc + 16 * w, ldc, lane);
+      for (int it = 0; it < NT; ++it) {
+        const int i = 16 * it + l16;
 #pragma unroll
-          for (int s = 0; s < NR; ++s)
-            O[it] = mma(cf, frag_row(P + s * L * ldp + i * ldp + 32 * jb + 4 * g), O[it]);
-        }
-        const int col = c0 + 16 * w + 4 * g;
+        for (int jb = 0; jb <= it / 2; ++jb)
+#pragma unroll
+          for (int q = 0; q < NR; ++q)
+            O[it] = mma(cf[jb], frag_row(P + q * L * ldp + i * ldp + 32 * jb + 4 * g), O[it]);
         if (i < n && col < p.Dc) {
           OT *to = out + (first + step * i) * sot + col;
-          if (p.out_vec) {
+          if (VEC) {
             Pack<OT, 4> x;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) x.v[r] = (OT)O[it][r];
+            part4(O[it], x);
             *reinterpret_cast<Pack<OT, 4> *>(to) = x;
           } else {
 #pragma unroll
@@ -492,7 +562,7 @@ __global__ __launch_bounds__(kThreads) void k_linattn(LaArgs p) {
         }
       }
     }
-    add_chunk<CT, KB, L>(X, Bm, C + 16 * w, dec, n, p.off, p.add_scale, lane);
+    if (t0 + L < hi) stage_chunk(t0 + L);
   }
 
   if (p.out) {
@@ -589,59 +659,65 @@ constexpr int chunk_of() {
   return sizeof(CT) * DA > 512 ? 32 : 64;
 }
 
-template <typename T, typename CT, typename OT, int DA>
+template <typename T, typename CT, typename OT, int DA, bool VEC>
 semicrf_status_t launch_da(const LaArgs &p, bool states, hipStream_t st) {
   constexpr int L = chunk_of<CT, DA>();
   if (states) {
     const int64_t grid = (int64_t)p.B * p.H * (p.nseg - 1) * p.ctiles;
-    k_linattn_state<T, CT, DA, L><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    k_linattn_state<T, CT, DA, L, VEC><<<(unsigned)grid, kThreads, 0, st>>>(p);
   } else {
     const int64_t grid = (int64_t)p.B * p.H * p.nseg * p.ctiles;
-    k_linattn<T, CT, OT, DA, L><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    k_linattn<T, CT, OT, DA, L, VEC><<<(unsigned)grid, kThreads, 0, st>>>(p);
   }
   return launch_status();
 }
 
-template <typename T, typename CT, typename OT>
-semicrf_status_t launch_t(const LaArgs &p, bool states, hipStream_t st) {
+template <typename T, typename CT, typename OT, bool VEC>
+semicrf_status_t launch_v(const LaArgs &p, bool states, hipStream_t st) {
   switch (round_da(p.Da)) {
-    case 32: return launch_da<T, CT, OT, 32>(p, states, st);
-    case 64: return launch_da<T, CT, OT, 64>(p, states, st);
-    case 128: return launch_da<T, CT, OT, 128>(p, states, st);
-    default: return launch_da<T, CT, OT, 256>(p, states, st);
+    case 32: return launch_da<T, CT, OT, 32, VEC>(p, states, st);
+    case 64: return launch_da<T, CT, OT, 64, VEC>(p, states, st);
+    case 128: return launch_da<T, CT, OT, 128, VEC>(p, states, st);
+    default: return launch_da<T, CT, OT, 256, VEC>(p, states, st);
   }
 }
 
-// Whether every row of a tensor is a whole number of aligned 16-byte pieces.
+// Whether every row of a tensor is a whole number of aligned 16-byte pieces,
+// and a chunk of rows within reach of a buffer descriptor.
 bool aligned(const View &v, int D, int dtype) {
-  const int e = 16 / elem_size(dtype);
+  const int size = elem_size(dtype), e = 16 / size;
   return (uintptr_t)v.p % 16 == 0 && D % e == 0 && v.sb % e == 0 && v.st % e == 0 &&
-         v.sh % e == 0;
+         v.sh % e == 0 && v.st >= 0 && (v.st * 64 + 256) * size < kRange;
+}
+
+template <typename T, typename CT, typename OT>
+semicrf_status_t launch_t(const LaArgs &p, bool vec, bool states, hipStream_t st) {
+  return vec ? launch_v<T, CT, OT, true>(p, states, st) : launch_v<T, CT, OT, false>(p, states, st);
 }
 
 // The pass over the chunks.  f32_out: the output is float32 whatever the
 // tensors are (parts of the gradient of a shared head).
-semicrf_status_t launch_linattn(LaArgs p, int dtype, bool f32_out, hipStream_t st) {
-  p.vec = aligned(p.a, p.Da, dtype) && aligned(p.b, p.Da, dtype) && aligned(p.c, p.Dc, dtype);
-  p.out_vec = p.Dc % 4 == 0 && (uintptr_t)p.out % (4 * (f32_out ? 4 : elem_size(dtype))) == 0;
+semicrf_status_t launch_linattn(const LaArgs &p, int dtype, bool f32_out, hipStream_t st) {
+  const bool vec = aligned(p.a, p.Da, dtype) && aligned(p.b, p.Da, dtype) &&
+                   aligned(p.c, p.Dc, dtype) && (uintptr_t)p.out % 16 == 0;
   switch (dtype) {
-    case SEMICRF_F32: return launch_t<float, float, float>(p, false, st);
+    case SEMICRF_F32: return launch_t<float, float, float>(p, vec, false, st);
     case SEMICRF_BF16:
-      return f32_out ? launch_t<bf16, bf16, float>(p, false, st)
-                     : launch_t<bf16, bf16, bf16>(p, false, st);
+      return f32_out ? launch_t<bf16, bf16, float>(p, vec, false, st)
+                     : launch_t<bf16, bf16, bf16>(p, vec, false, st);
     default:
-      return f32_out ? launch_t<f16, float, float>(p, false, st)
-                     : launch_t<f16, float, f16>(p, false, st);
+      return f32_out ? launch_t<f16, float, float>(p, vec, false, st)
+                     : launch_t<f16, float, f16>(p, vec, false, st);
   }
 }
 
 // The segments' states of a pair (b, c) in p.xs.
-semicrf_status_t launch_states(LaArgs p, int dtype, hipStream_t st) {
+semicrf_status_t launch_states(const LaArgs &p, int dtype, hipStream_t st) {
   if (p.nseg < 2) return SEMICRF_OK;
-  p.vec = aligned(p.b, p.Da, dtype) && aligned(p.c, p.Dc, dtype);
-  semicrf_status_t e = dtype == SEMICRF_F32    ? launch_t<float, float, float>(p, true, st)
-                       : dtype == SEMICRF_BF16 ? launch_t<bf16, bf16, bf16>(p, true, st)
-                                               : launch_t<f16, float, f16>(p, true, st);
+  const bool vec = aligned(p.b, p.Da, dtype) && aligned(p.c, p.Dc, dtype);
+  semicrf_status_t e = dtype == SEMICRF_F32    ? launch_t<float, float, float>(p, vec, true, st)
+                       : dtype == SEMICRF_BF16 ? launch_t<bf16, bf16, bf16>(p, vec, true, st)
+                                               : launch_t<f16, float, f16>(p, vec, true, st);
   if (e != SEMICRF_OK) return e;
   const int64_t n = (int64_t)p.B * p.H * p.Da * p.Dc;
   k_linattn_scan<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, st>>>(p);
