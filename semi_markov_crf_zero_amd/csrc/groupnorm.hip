@@ -12,6 +12,10 @@
 // leave one partial per channel vector; a small kernel adds them in a fixed
 // order in float64, and the last pass reads x again and writes the result.
 //
+// Short sequences (a norm of each position by itself above all) take another
+// way: a workgroup holds NS whole sequences, a stretch of memory without
+// gaps, in LDS, so x is read once, whatever C and the groups are.
+//
 // Sums.  mean and var come from sums of (x - pivot) and its square in
 // float64, the pivot the group's first element: the subtraction takes the
 // common offset out before anything is squared.
@@ -215,25 +219,17 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, 
   }
 }
 
-// One wave per sequence and group: the channels' sums over the slabs, and
-// mean(d), mean(d h) of the group.
-__global__ __launch_bounds__(64) void k_gn_bwd_group(GnArgs p, const float2 *part, double2 *sums,
-                                                     float2 *coef) {
+// One wave per sequence and group: mean(d), mean(d h) of the group.
+__global__ __launch_bounds__(64) void k_gn_bwd_group(GnArgs p, const float2 *part, float2 *coef) {
   const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
   const int len = valid_length(p.lengths, b, p.T);
   double m1 = 0, m2 = 0;
-  for (int c = threadIdx.x; c < p.Cg; c += 64) {
-    const int ch = g * p.Cg + c;
-    double a1 = 0, a2 = 0;
-    for (int s = 0; s < p.slabs; ++s) {
-      const float2 d = part[((int64_t)b * p.slabs + s) * p.C + ch];
-      a1 += d.x;
-      a2 += d.y;
-    }
-    sums[(int64_t)b * p.C + ch] = make_double2(a1, a2);
+  for (int e = threadIdx.x; e < p.slabs * p.Cg; e += 64) {
+    const int ch = g * p.Cg + e % p.Cg;
+    const float2 d = part[((int64_t)b * p.slabs + e / p.Cg) * p.C + ch];
     const double w = p.weight ? p.weight[ch] : 1.0;
-    m1 += w * a1;
-    m2 += w * a2;
+    m1 += w * d.x;
+    m2 += w * d.y;
   }
   for (int o = 32; o; o >>= 1) {
     m1 += __shfl_xor(m1, o);
@@ -245,28 +241,50 @@ __global__ __launch_bounds__(64) void k_gn_bwd_group(GnArgs p, const float2 *par
   }
 }
 
-// One workgroup per 64 channels: the sums over the batch.
-__global__ __launch_bounds__(256) void k_gn_bwd_params(GnArgs p, const double2 *sums, float *dw,
-                                                       float *db) {
+// The parameters' gradients: rows of partials [n][C] added in float64, 64
+// channels and n / splits rows a workgroup; then the splits.
+__global__ __launch_bounds__(256) void k_gn_bwd_params(int C, int64_t n, int splits,
+                                                       const float2 *part, double2 *sums,
+                                                       float *dw, float *db) {
   __shared__ double2 red[256];
-  const int ch = blockIdx.x * 64 + threadIdx.x % 64, q = threadIdx.x / 64;
+  const int tiles = (C + 63) / 64, s = blockIdx.x / tiles;
+  const int ch = blockIdx.x % tiles * 64 + threadIdx.x % 64, q = threadIdx.x / 64;
+  const int64_t r0 = n * s / splits, r1 = n * (s + 1) / splits;
   double a1 = 0, a2 = 0;
-  if (ch < p.C)
-    for (int b = q; b < p.B; b += 4) {
-      const double2 d = sums[(int64_t)b * p.C + ch];
+  if (ch < C)
+#pragma unroll 8
+    for (int64_t r = r0 + q; r < r1; r += 4) {
+      const float2 d = part[r * C + ch];
       a1 += d.x;
       a2 += d.y;
     }
   red[threadIdx.x] = make_double2(a1, a2);
   __syncthreads();
-  if (q == 0 && ch < p.C) {
+  if (q == 0 && ch < C) {
     for (int k = 1; k < 4; ++k) {
       a1 += red[k * 64 + threadIdx.x].x;
       a2 += red[k * 64 + threadIdx.x].y;
     }
-    if (db) db[ch] = (float)a1;
-    if (dw) dw[ch] = (float)a2;
+    if (splits > 1) {
+      sums[(int64_t)s * C + ch] = make_double2(a1, a2);
+    } else {
+      if (db) db[ch] = (float)a1;
+      if (dw) dw[ch] = (float)a2;
+    }
   }
+}
+__global__ __launch_bounds__(64) void k_gn_bwd_params_sum(int C, int splits, const double2 *sums,
+                                                          float *dw, float *db) {
+  const int ch = blockIdx.x * 64 + threadIdx.x;
+  if (ch >= C) return;
+  double a1 = 0, a2 = 0;
+#pragma unroll 8
+  for (int s = 0; s < splits; ++s) {
+    a1 += sums[(int64_t)s * C + ch].x;
+    a2 += sums[(int64_t)s * C + ch].y;
+  }
+  if (db) db[ch] = (float)a1;
+  if (dw) dw[ch] = (float)a2;
 }
 
 template <typename T, int V, int ACT>
@@ -308,6 +326,212 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GnArgs p, const T *x,
       for (int i = 0; i < V; ++i) d.v[i] = (T)0.f;
     }
     *reinterpret_cast<Pack<T, V> *>(dx + base + (int64_t)t * p.C) = d;
+  }
+}
+
+// ---- short sequences -------------------------------------------------------
+
+namespace {
+
+// x / d for x < 2^16 and 1 <= d < 2^16: the high word of x times
+// ceil(2^32 / d); 2^32 itself stands as 0.
+__device__ __forceinline__ int div_small(int x, uint32_t m) {
+  return m ? (int)__umulhi((uint32_t)x, m) : x;
+}
+
+struct SmallArgs {
+  GnArgs g;
+  int ns, TC;             // sequences of a workgroup, elements of one
+  uint32_t mTC, mC, mCg;  // for div_small
+};
+
+// Walks through consecutive elements of a workgroup's stretch: sequence,
+// position, channel and group.
+struct Walk {
+  int s, t, c, g, in_g;
+  __device__ __forceinline__ Walk(const SmallArgs &p, int e) {
+    s = div_small(e, p.mTC);
+    const int r = e - s * p.TC;
+    t = div_small(r, p.mC);
+    c = r - t * p.g.C;
+    g = div_small(c, p.mCg);
+    in_g = c - g * p.g.Cg;
+  }
+  __device__ __forceinline__ void next(const SmallArgs &p) {
+    ++c;
+    if (++in_g == p.g.Cg) in_g = 0, ++g;
+    if (c == p.g.C) {
+      c = g = 0;
+      if (++t == p.g.T) t = 0, ++s;
+    }
+  }
+};
+
+constexpr int kTeam = 8;  // lanes that sum one group
+
+__device__ __forceinline__ double team_sum(double x) {
+#pragma unroll
+  for (int o = kTeam / 2; o; o >>= 1) x += __shfl_xor(x, o);
+  return x;
+}
+
+// LDS: n floats of data (twice backwards), weight and bias, a pair a group.
+__device__ __forceinline__ void load_params(const GnArgs &p, float *w, float *b) {
+  for (int c = threadIdx.x; c < p.C; c += kThreads) {
+    w[c] = p.weight ? p.weight[c] : 1.f;
+    b[c] = p.bias ? p.bias[c] : 0.f;
+  }
+}
+
+}  // namespace
+
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(kThreads) void k_gn_small(SmallArgs p, const T *x, T *y,
+                                                       float *stats) {
+  extern __shared__ float lds[];
+  const int most = p.ns * p.TC;
+  float *xs = lds, *w = xs + (most + 1) / 2 * 2, *bi = w + p.g.C, *st = bi + p.g.C;
+  const int b0 = blockIdx.x * p.ns, ns = min(p.ns, p.g.B - b0), n = ns * p.TC;
+  x += (int64_t)b0 * p.TC;
+  y += (int64_t)b0 * p.TC;
+  load_params(p.g, w, bi);
+  for (int e = threadIdx.x * V; e < n; e += kThreads * V) {
+    const Pack<T, V> d = *reinterpret_cast<const Pack<T, V> *>(x + e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) xs[e + i] = (float)d.v[i];
+  }
+  __syncthreads();
+  const int lane = threadIdx.x % kTeam;
+  for (int pair = threadIdx.x / kTeam; pair < ns * p.g.G; pair += kThreads / kTeam) {
+    const int s = pair / p.g.G, g = pair % p.g.G;
+    const int len = valid_length(p.g.lengths, b0 + s, p.g.T), m = max(len, 0) * p.g.Cg;
+    const float *u = xs + s * p.TC + g * p.g.Cg;
+    double sum = 0, sq = 0;
+    for (int j = lane; j < m; j += kTeam) {
+      const int t = div_small(j, p.mCg);
+      sum += u[t * p.g.C + j - t * p.g.Cg];
+    }
+    const double mean = team_sum(sum) / max(m, 1);
+    for (int j = lane; j < m; j += kTeam) {
+      const int t = div_small(j, p.mCg);
+      const double d = u[t * p.g.C + j - t * p.g.Cg] - mean;
+      sq += d * d;
+    }
+    const double var = team_sum(sq) / max(m, 1);
+    if (lane == 0) {
+      const float none = len < 0 ? __builtin_nanf("") : 0.f;
+      const float a = m ? (float)mean : none;
+      const float r = m ? (float)(1.0 / sqrt(var + (double)p.g.eps)) : none;
+      st[2 * pair] = a;
+      st[2 * pair + 1] = r;
+      stats[2 * ((int64_t)b0 * p.g.G + pair)] = a;
+      stats[2 * ((int64_t)b0 * p.g.G + pair) + 1] = r;
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x * V; e < n; e += kThreads * V) {
+    Walk k(p, e);
+    Pack<T, V> d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int len = valid_length(p.g.lengths, b0 + k.s, p.g.T);
+      const float2 a = *reinterpret_cast<const float2 *>(st + 2 * (k.s * p.g.G + k.g));
+      const float v = act<ACT>((xs[e + i] - a.x) * a.y * w[k.c] + bi[k.c]);
+      d.v[i] = (T)(k.t < len ? v : len < 0 ? __builtin_nanf("") : 0.f);
+      k.next(p);
+    }
+    *reinterpret_cast<Pack<T, V> *>(y + e) = d;
+  }
+}
+
+// dx, and the workgroup's sums of dz and dz h per channel: part[workgroup][C].
+template <typename T, int V, int ACT>
+__global__ __launch_bounds__(kThreads) void k_gn_small_bwd(SmallArgs p, const T *x, const T *dy,
+                                                           const float *stats, T *dx,
+                                                           float2 *part) {
+  extern __shared__ float lds[];
+  const int most = p.ns * p.TC;
+  float *hs = lds, *dz = hs + most, *w = dz + most, *bi = w + p.g.C, *st = bi + p.g.C;
+  __shared__ double2 red[kThreads];
+  const int b0 = blockIdx.x * p.ns, ns = min(p.ns, p.g.B - b0), n = ns * p.TC;
+  x += (int64_t)b0 * p.TC;
+  dy += (int64_t)b0 * p.TC;
+  dx += (int64_t)b0 * p.TC;
+  stats += 2 * (int64_t)b0 * p.g.G;
+  load_params(p.g, w, bi);
+  __syncthreads();
+  for (int e = threadIdx.x * V; e < n; e += kThreads * V) {
+    const Pack<T, V> d = *reinterpret_cast<const Pack<T, V> *>(x + e);
+    const Pack<T, V> q = *reinterpret_cast<const Pack<T, V> *>(dy + e);
+    Walk k(p, e);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int len = valid_length(p.g.lengths, b0 + k.s, p.g.T);
+      const float2 a = *reinterpret_cast<const float2 *>(stats + 2 * (k.s * p.g.G + k.g));
+      const float h = ((float)d.v[i] - a.x) * a.y;
+      const bool in = k.t < len;
+      hs[e + i] = in ? h : 0.f;
+      dz[e + i] = in ? (float)q.v[i] * act_slope<ACT>(h * w[k.c] + bi[k.c]) : 0.f;
+      k.next(p);
+    }
+  }
+  __syncthreads();
+  const int lane = threadIdx.x % kTeam;
+  for (int pair = threadIdx.x / kTeam; pair < ns * p.g.G; pair += kThreads / kTeam) {
+    const int s = pair / p.g.G, g = pair % p.g.G;
+    const int m = max(valid_length(p.g.lengths, b0 + s, p.g.T), 0) * p.g.Cg;
+    const int at = s * p.TC + g * p.g.Cg;
+    double m1 = 0, m2 = 0;
+    for (int j = lane; j < m; j += kTeam) {
+      const int t = div_small(j, p.mCg), c = j - t * p.g.Cg;
+      const float d = dz[at + t * p.g.C + c] * w[g * p.g.Cg + c];
+      m1 += d;
+      m2 += (double)d * hs[at + t * p.g.C + c];
+    }
+    m1 = team_sum(m1) / max(m, 1);
+    m2 = team_sum(m2) / max(m, 1);
+    if (lane == 0) {
+      st[2 * pair] = (float)m1;
+      st[2 * pair + 1] = (float)m2;
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x * V; e < n; e += kThreads * V) {
+    Walk k(p, e);
+    Pack<T, V> d;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float2 a = *reinterpret_cast<const float2 *>(st + 2 * (k.s * p.g.G + k.g));
+      const float rstd = stats[2 * (k.s * p.g.G + k.g) + 1];
+      const bool in = k.t < valid_length(p.g.lengths, b0 + k.s, p.g.T);
+      d.v[i] = (T)(in ? rstd * (dz[e + i] * w[k.c] - a.x - hs[e + i] * a.y) : 0.f);
+      k.next(p);
+    }
+    *reinterpret_cast<Pack<T, V> *>(dx + e) = d;
+  }
+  if (!part) return;
+  // the channels' sums over the rows: as many row groups as there are threads
+  const int rows = ns * p.g.T, groups = max(1, min(kThreads / p.g.C, rows));
+  for (int c0 = 0; c0 < p.g.C; c0 += kThreads) {
+    const int c = c0 + (p.g.C < kThreads ? threadIdx.x % p.g.C : threadIdx.x);
+    const int q = p.g.C < kThreads ? threadIdx.x / p.g.C : 0;
+    double a1 = 0, a2 = 0;
+    if (c < p.g.C && q < groups)
+      for (int r = q; r < rows; r += groups) {
+        const float d = dz[r * p.g.C + c];
+        a1 += d;
+        a2 += (double)d * hs[r * p.g.C + c];
+      }
+    red[threadIdx.x] = make_double2(a1, a2);
+    __syncthreads();
+    if (c < p.g.C && q == 0) {
+      for (int k = 1; k < groups; ++k) {
+        a1 += red[k * p.g.C + c].x;
+        a2 += red[k * p.g.C + c].y;
+      }
+      part[(int64_t)blockIdx.x * p.g.C + c] = make_float2((float)a1, (float)a2);
+    }
+    __syncthreads();
   }
 }
 
@@ -358,8 +582,63 @@ GnArgs args(const semicrf_groupnorm_shape_t *s, int V) {
   return p;
 }
 
+// Short sequences go NS at a time through LDS: about kStretch elements a
+// workgroup, NS a power of two so that a stretch is a whole number of
+// vectors; where 64 KB of LDS hold what the backward pass keeps of one.
+constexpr int kStretch = 4096;
+uint32_t magic(int d) { return d == 1 ? 0 : (uint32_t)(((1ull << 32) + d - 1) / d); }
+SmallArgs small_args(const semicrf_groupnorm_shape_t *s) {
+  SmallArgs p = {};
+  p.g = args(s, 1);
+  p.TC = s->T * s->C;
+  p.ns = 1;
+  while (2 * p.ns * p.TC <= kStretch && p.ns < s->B) p.ns *= 2;
+  p.mTC = magic(p.TC);
+  p.mC = magic(s->C);
+  p.mCg = magic(p.g.Cg);
+  return p;
+}
+// LDS of a short-sequence workgroup with `arrays` copies of its data.
+size_t small_lds(const SmallArgs &p, int arrays) {
+  return sizeof(float) * ((size_t)arrays * p.ns * p.TC + 2 * (size_t)p.g.C +
+                          2 * (size_t)p.ns * p.g.G + 2);
+}
+bool small_path(const semicrf_groupnorm_shape_t *s) {
+  return (int64_t)s->T * s->C <= 2 * kStretch &&
+         small_lds(small_args(s), 2) + kThreads * sizeof(double2) <= 65536;
+}
+int64_t small_blocks(const semicrf_groupnorm_shape_t *s) {
+  const int ns = small_args(s).ns;
+  return (s->B + ns - 1) / ns;
+}
+// Elements a thread moves at once there: groups do not matter, only whole
+// aligned pieces of a stretch.
+int small_width(const semicrf_groupnorm_shape_t *s, const void *const *ptrs, int n) {
+  const int size = elem_size(s->dtype), stretch = small_args(s).ns * s->T * s->C;
+  int V = 16 / size;
+  while (V > 1 && (stretch % V || (int64_t)s->B * s->T * s->C % V)) V /= 2;
+  for (int i = 0; i < n; ++i)
+    while (V > 1 && (uintptr_t)ptrs[i] % (V * size)) V /= 2;
+  return V;
+}
+
+// Rows of partials of the parameters' gradients, and how many workgroups of
+// k_gn_bwd_params share them: 64 rows each at least, 64 at most.
+int param_splits(int64_t rows) {
+  const int64_t n = rows / 64;
+  return n < 1 ? 1 : n > 64 ? 64 : (int)n;
+}
+size_t param_bytes(const semicrf_groupnorm_shape_t *s, int64_t rows) {
+  const int n = param_splits(rows);
+  return n > 1 ? align256((size_t)n * s->C * sizeof(double2)) : 0;
+}
+
 // Workspace for the narrowest vectors (the widest partials).
 size_t need(const semicrf_groupnorm_shape_t *s, int backward) {
+  if (small_path(s)) {
+    const int64_t rows = small_blocks(s);
+    return backward ? align256((size_t)rows * s->C * sizeof(float2)) + param_bytes(s, rows) : 0;
+  }
   size_t n = 0;
   for (int V = 1; V <= 8; V *= 2) {
     if ((s->C / s->G) % V) break;
@@ -367,8 +646,7 @@ size_t need(const semicrf_groupnorm_shape_t *s, int backward) {
     size_t m;
     if (backward)
       m = align256((size_t)p.B * p.slabs * p.C * sizeof(float2)) +
-          align256((size_t)p.B * p.C * sizeof(double2)) +
-          align256((size_t)p.B * p.G * sizeof(float2));
+          param_bytes(s, (int64_t)p.B * p.slabs) + align256((size_t)p.B * p.G * sizeof(float2));
     else
       m = align256((size_t)p.B * p.slabs * p.cv * sizeof(double2));
     if (m > n) n = m;
@@ -386,21 +664,30 @@ semicrf_status_t run_fwd(const GnArgs &p, const void *x, void *y, float *stats, 
   return launch_status();
 }
 
+// part [rows][C] to dw and db.
+void run_params(int C, int64_t rows, const float2 *part, double2 *sums, float *dw, float *db,
+                hipStream_t st) {
+  if (!dw && !db) return;
+  const int splits = param_splits(rows), tiles = (C + 63) / 64;
+  k_gn_bwd_params<<<(unsigned)(tiles * splits), 256, 0, st>>>(C, rows, splits, part, sums, dw, db);
+  if (splits > 1) k_gn_bwd_params_sum<<<tiles, 64, 0, st>>>(C, splits, sums, dw, db);
+}
+
 template <typename T, int V, int ACT>
 semicrf_status_t run_bwd(const GnArgs &p, const void *x, const void *dy, const float *stats,
-                         void *dx, float *dw, float *db, void *ws, hipStream_t st) {
+                         void *dx, float *dw, float *db, void *ws, size_t sums_bytes,
+                         hipStream_t st) {
   const unsigned grid = (unsigned)p.B * p.slabs * p.tiles;
   char *w = (char *)ws;
   float2 *part = (float2 *)w;
   w += align256((size_t)p.B * p.slabs * p.C * sizeof(float2));
   double2 *sums = (double2 *)w;
-  w += align256((size_t)p.B * p.C * sizeof(double2));
-  float2 *coef = (float2 *)w;
+  float2 *coef = (float2 *)(w + sums_bytes);
   k_gn_bwd_sums<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats, part);
-  k_gn_bwd_group<<<(unsigned)p.B * p.G, 64, 0, st>>>(p, part, sums, coef);
-  if (dw || db) k_gn_bwd_params<<<(p.C + 63) / 64, 256, 0, st>>>(p, sums, dw, db);
+  k_gn_bwd_group<<<(unsigned)p.B * p.G, 64, 0, st>>>(p, part, coef);
   k_gn_bwd_apply<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats, coef,
                                                        (T *)dx);
+  run_params(p.C, (int64_t)p.B * p.slabs, part, sums, dw, db, st);
   return launch_status();
 }
 
@@ -432,6 +719,7 @@ semicrf_status_t dispatch(int dtype, int V, int act, F f) {
 
 struct Fwd {
   GnArgs p;
+  SmallArgs small;  // ns 0: the long way
   const void *x;
   void *y;
   float *stats;
@@ -439,12 +727,18 @@ struct Fwd {
   hipStream_t st;
   template <typename T, int V, int ACT>
   semicrf_status_t run() {
-    return run_fwd<T, V, ACT>(p, x, y, stats, ws, st);
+    if (!small.ns) return run_fwd<T, V, ACT>(p, x, y, stats, ws, st);
+    const unsigned grid = (unsigned)((small.g.B + small.ns - 1) / small.ns);
+    k_gn_small<T, V, ACT><<<grid, kThreads, small_lds(small, 1), st>>>(small, (const T *)x,
+                                                                       (T *)y, stats);
+    return launch_status();
   }
 };
 
 struct Bwd {
   GnArgs p;
+  SmallArgs small;
+  size_t sums_bytes;
   const void *x, *dy;
   const float *stats;
   void *dx;
@@ -453,7 +747,15 @@ struct Bwd {
   hipStream_t st;
   template <typename T, int V, int ACT>
   semicrf_status_t run() {
-    return run_bwd<T, V, ACT>(p, x, dy, stats, dx, dw, db, ws, st);
+    if (!small.ns)
+      return run_bwd<T, V, ACT>(p, x, dy, stats, dx, dw, db, ws, sums_bytes, st);
+    const unsigned grid = (unsigned)((small.g.B + small.ns - 1) / small.ns);
+    float2 *part = dw || db ? (float2 *)ws : nullptr;
+    k_gn_small_bwd<T, V, ACT><<<grid, kThreads, small_lds(small, 2), st>>>(
+        small, (const T *)x, (const T *)dy, stats, (T *)dx, part);
+    double2 *sums = (double2 *)((char *)ws + align256((size_t)grid * small.g.C * sizeof(float2)));
+    run_params(small.g.C, grid, part, sums, dw, db, st);
+    return launch_status();
   }
 };
 
@@ -481,12 +783,17 @@ semicrf_status_t semicrf_groupnorm_fwd(const semicrf_groupnorm_shape_t *s, const
   if (!s || !x || !y || !stats) return SEMICRF_ERR_NULL;
   const semicrf_status_t e = check(s);
   if (e != SEMICRF_OK) return e;
-  if (!workspace || workspace_bytes < need(s, 0)) return SEMICRF_ERR_WORKSPACE;
+  const size_t bytes = need(s, 0);
+  if (bytes && (!workspace || workspace_bytes < bytes)) return SEMICRF_ERR_WORKSPACE;
   (void)hipGetLastError();
   const void *ptrs[] = {x, y};
-  const int V = vector_width(s, ptrs, 2);
-  Fwd f = {args(s, V), x, y, stats, workspace, (hipStream_t)stream};
-  f.p.lengths = lengths, f.p.weight = weight, f.p.bias = bias;
+  const bool small = small_path(s);
+  const int V = small ? small_width(s, ptrs, 2) : vector_width(s, ptrs, 2);
+  Fwd f = {args(s, small ? 1 : V), {}, x, y, stats, workspace, (hipStream_t)stream};
+  if (small) f.small = small_args(s);
+  f.p.lengths = f.small.g.lengths = lengths;
+  f.p.weight = f.small.g.weight = weight;
+  f.p.bias = f.small.g.bias = bias;
   return dispatch(s->dtype, V, s->act, f);
 }
 
@@ -499,13 +806,19 @@ semicrf_status_t semicrf_groupnorm_bwd(const semicrf_groupnorm_shape_t *s, const
   if (!s || !x || !grad_y || !stats || !grad_x) return SEMICRF_ERR_NULL;
   const semicrf_status_t e = check(s);
   if (e != SEMICRF_OK) return e;
-  if (!workspace || workspace_bytes < need(s, 1)) return SEMICRF_ERR_WORKSPACE;
+  const size_t bytes = need(s, 1);
+  if (bytes && (!workspace || workspace_bytes < bytes)) return SEMICRF_ERR_WORKSPACE;
   (void)hipGetLastError();
   const void *ptrs[] = {x, grad_y, grad_x};
-  const int V = vector_width(s, ptrs, 3);
-  Bwd f = {args(s, V), x, grad_y, stats, grad_x, grad_weight, grad_bias, workspace,
+  const bool small = small_path(s);
+  const int V = small ? small_width(s, ptrs, 3) : vector_width(s, ptrs, 3);
+  Bwd f = {args(s, small ? 1 : V), {}, 0, x, grad_y, stats, grad_x, grad_weight, grad_bias, workspace,
            (hipStream_t)stream};
-  f.p.lengths = lengths, f.p.weight = weight, f.p.bias = bias;
+  if (small) f.small = small_args(s);
+  f.sums_bytes = param_bytes(s, (int64_t)f.p.B * f.p.slabs);
+  f.p.lengths = f.small.g.lengths = lengths;
+  f.p.weight = f.small.g.weight = weight;
+  f.p.bias = f.small.g.bias = bias;
   return dispatch(s->dtype, V, s->act, f);
 }
 
