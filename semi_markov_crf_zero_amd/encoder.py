@@ -18,6 +18,7 @@ read and their rows of every output and gradient are 0; a length outside
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -71,38 +72,31 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-class _on:
-    """Makes the tensors' device the current one for the launches inside."""
-
-    def __init__(self, dev):
-        self.dev = dev
-
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.was != self.dev.index:
-            torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.was != self.dev.index:
-            torch.cuda.set_device(self.was)
+def launch(fn, dev, *args):
+    """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
+    was = torch._C._cuda_getDevice()
+    if was == dev.index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(was))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        raise bd.SemiCRFError(rc, fn.__name__)
 
 
-def _call(name, dev, shape, backward, *args):
-    """A library call with the workspace its shape needs (backward None: none)."""
-    lib = load()
-    with _on(dev) as stream:
-        if backward is not None:
-            n = ctypes.c_size_t(0)
-            rc = getattr(lib, name.rsplit("_", 1)[0] + "_workspace_size")(
-                ctypes.byref(shape), backward, ctypes.byref(n))
-            if rc:
-                raise bd.SemiCRFError(rc, name)
-            ws = torch.empty(n.value, dtype=torch.uint8, device=dev) if n.value else None
-            args += (_ptr(ws), n.value)
-        rc = getattr(lib, name)(ctypes.byref(shape), *args, stream)
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name, kind, fields, backward):
+    """Workspace of a shape (a tuple of the structure's fields)."""
+    n = ctypes.c_size_t(0)
+    rc = getattr(load(), name)(ctypes.byref(kind(*fields)), backward, ctypes.byref(n))
     if rc:
         raise bd.SemiCRFError(rc, name)
+    return n.value
+
+
+def _workspace(name, kind, fields, backward, dev):
+    n = _workspace_bytes(name, kind, fields, backward)
+    return (torch.empty(n, dtype=torch.uint8, device=dev) if n else None), n
 
 
 def _check(name, t, dev, dtype, shape):
@@ -124,73 +118,77 @@ def _rows(t):
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
-def _linattn_shape(q, k, v, log_decay, scale, T):
-    """Checks q, k, v ([B, T, heads, D] or, for T None, [B, heads, D]) and
-    log_decay; the shape structure and the tensors with contiguous rows."""
+def _linattn_check(q, k, v, log_decay, step):
+    """Checks q, k, v ([B, T, heads, D], or [B, heads, D] for a step) and
+    log_decay; B, T, H, Hq, Hk, Hv, Dk, Dv, dtype."""
     _check_device(q)
-    dims = 3 if T is None else 4
+    dev, dtype, lead = q.device, q.dtype, q.shape[:-2]
     for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != dims or t.device != q.device or t.dtype != q.dtype:
+        if t.dim() != (3 if step else 4) or t.device != dev or t.dtype != dtype:
             raise ValueError("%s must be a [B, %sheads, D] %s tensor on %s"
-                             % (name, "" if T is None else "T, ", q.dtype, q.device))
-        if t.shape[:-2] != q.shape[:-2]:
-            raise ValueError("q, k and v must have the same B%s" % ("" if T is None else " and T"))
-    if k.shape[-1] != q.shape[-1]:
+                             % (name, "" if step else "T, ", dtype, dev))
+        if t.shape[:-2] != lead:
+            raise ValueError("q, k and v must have the same B%s" % ("" if step else " and T"))
+    (Hq, Dk), (Hk, Dk2), (Hv, Dv) = q.shape[-2:], k.shape[-2:], v.shape[-2:]
+    if Dk2 != Dk:
         raise ValueError("q and k must have the same width")
-    if not (1 <= q.shape[-1] <= MAX_HEAD and 1 <= v.shape[-1] <= MAX_HEAD):
+    if not (1 <= Dk <= MAX_HEAD and 1 <= Dv <= MAX_HEAD):
         raise ValueError("heads are 1 to %d wide" % MAX_HEAD)
-    heads = [t.shape[-2] for t in (q, k, v)]
-    H = max(heads)
-    if min(heads) < 1 or any(H % h for h in heads):
-        raise ValueError("the larger number of heads must be a multiple of the others: %s" % heads)
+    H = max(Hq, Hk, Hv)
+    if min(Hq, Hk, Hv) < 1 or H % Hq or H % Hk or H % Hv:
+        raise ValueError("the larger number of heads must be a multiple of the others: %s"
+                         % [Hq, Hk, Hv])
     if log_decay.requires_grad:
         raise ValueError("log_decay is a constant of the model: it gets no gradient")
-    _check("log_decay", log_decay, q.device, torch.float32, (H,))
-    q, k, v = _rows(q), _rows(k), _rows(v)
+    _check("log_decay", log_decay, dev, torch.float32, (H,))
+    return lead[0], 1 if step else lead[1], H, Hq, Hk, Hv, Dk, Dv, DTYPES[dtype]
 
-    def strides(t):
-        s = t.stride()
-        return (ctypes.c_int64 * 3)(s[0], s[1] if T is not None else 0, s[-2])
 
-    shape = _LinattnShape(q.shape[0], 1 if T is None else T, H, *heads, q.shape[-1], v.shape[-1],
-                          DTYPES[q.dtype], q.shape[-1] ** -0.5 if scale is None else float(scale),
-                          strides(q), strides(k), strides(v))
-    return shape, q, k, v
+def _strides(t):
+    s = t.stride()
+    return (s[0], s[1] if len(s) == 4 else 0, s[-2])
 
 
 class LinearAttention(torch.autograd.Function):
-    """o [B, T, H, Dv] and the state after each sequence [B, H, Dk, Dv]."""
+    """o [B, T, H, Dv] and the state after each sequence [B, H, Dk, Dv]; dims
+    is what _linattn_check gives."""
 
     @staticmethod
-    def forward(ctx, q, k, v, state, log_decay, lengths, scale):
-        ctx.scale = scale
+    def forward(ctx, q, k, v, state, log_decay, lengths, dims, scale):
         ctx.save_for_backward(q, k, v, state, log_decay, lengths)
         ctx.set_materialize_grads(False)
-        shape, q, k, v = _linattn_shape(q, k, v, log_decay, scale, q.shape[1])
-        o = torch.empty((shape.B, shape.T, shape.H, shape.Dv), dtype=q.dtype, device=q.device)
-        last = torch.empty((shape.B, shape.H, shape.Dk, shape.Dv), dtype=torch.float32,
-                           device=q.device)
-        _call("semicrf_linattn_fwd", q.device, shape, 0, _ptr(q), _ptr(k), _ptr(v),
-              _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(o), _ptr(last))
+        ctx.dims, ctx.scale = dims, scale
+        B, T, H, _, _, _, Dk, Dv, _ = dims
+        q, k, v = _rows(q), _rows(k), _rows(v)
+        dev = q.device
+        fields = (*dims, scale, _strides(q), _strides(k), _strides(v))
+        o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
+        last = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+        ws, n = _workspace("semicrf_linattn_workspace_size", _LinattnShape, fields, 0, dev)
+        launch(load().semicrf_linattn_fwd, dev, ctypes.byref(_LinattnShape(*fields)), _ptr(q),
+               _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(o), _ptr(last),
+               _ptr(ws), n)
         return o, last
 
     @staticmethod
     def backward(ctx, do, dlast):
         q, k, v, state, log_decay, lengths = ctx.saved_tensors
-        shape, q, k, v = _linattn_shape(q, k, v, log_decay, ctx.scale, q.shape[1])
-        dev = q.device
+        B, T, H, _, _, _, _, Dv, _ = ctx.dims
+        need, dev = ctx.needs_input_grad, q.device
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=dev) if n else None
+                      for t, n in ((q, need[0]), (k, need[1]), (v, need[2])))
+        dstate = torch.empty_like(state) if state is not None and need[3] else None
+        q, k, v = _rows(q), _rows(k), _rows(v)
+        fields = (*ctx.dims, ctx.scale, _strides(q), _strides(k), _strides(v))
         if do is None:
-            do = torch.zeros((shape.B, shape.T, shape.H, shape.Dv), dtype=q.dtype, device=dev)
+            do = torch.zeros((B, T, H, Dv), dtype=q.dtype, device=dev)
         do = do.contiguous()
         dlast = None if dlast is None else dlast.contiguous()
-        need = ctx.needs_input_grad
-        grads = [torch.empty(t.shape, dtype=t.dtype, device=dev) if n else None
-                 for t, n in ((q, need[0]), (k, need[1]), (v, need[2]))]
-        dstate = torch.empty_like(state) if state is not None and need[3] else None
-        _call("semicrf_linattn_bwd", dev, shape, 1, _ptr(q), _ptr(k), _ptr(v), _ptr(log_decay),
-              _ptr(lengths), _ptr(state), _ptr(do), _ptr(dlast), *(_ptr(g) for g in grads),
-              _ptr(dstate))
-        return (*grads, dstate, None, None, None)
+        ws, n = _workspace("semicrf_linattn_workspace_size", _LinattnShape, fields, 1, dev)
+        launch(load().semicrf_linattn_bwd, dev, ctypes.byref(_LinattnShape(*fields)), _ptr(q),
+               _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(do),
+               _ptr(dlast), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dstate), _ptr(ws), n)
+        return dq, dk, dv, dstate, None, None, None, None
 
 
 def linear_attention(q, k, v, log_decay, lengths=None, state=None, scale=None,
@@ -208,19 +206,18 @@ def linear_attention(q, k, v, log_decay, lengths=None, state=None, scale=None,
     default.  Returns o [B, T, H, Dv] or, with return_state, (o, the state
     after each sequence's last position).  Gradients flow to q, k, v and
     state."""
-    if q.dim() != 4:
-        raise ValueError("q must be [B, T, heads, D]")
-    shape, *_ = _linattn_shape(q, k, v, log_decay, scale, q.shape[1])
+    dims = _linattn_check(q, k, v, log_decay, False)
+    B, T, H, _, _, _, Dk, Dv, _ = dims
     if lengths is not None:
-        _check("lengths", lengths, q.device, torch.int32, (shape.B,))
+        _check("lengths", lengths, q.device, torch.int32, (B,))
     if state is not None:
-        _check("state", state, q.device, torch.float32, (shape.B, shape.H, shape.Dk, shape.Dv))
-    if shape.B == 0 or shape.T == 0:
-        o = torch.zeros((shape.B, shape.T, shape.H, shape.Dv), dtype=q.dtype, device=q.device)
-        last = (torch.zeros((shape.B, shape.H, shape.Dk, shape.Dv), device=q.device)
-                if state is None else state.clone())
+        _check("state", state, q.device, torch.float32, (B, H, Dk, Dv))
+    if B == 0 or T == 0:
+        o = torch.zeros((B, T, H, Dv), dtype=q.dtype, device=q.device)
+        last = torch.zeros((B, H, Dk, Dv), device=q.device) if state is None else state.clone()
     else:
-        o, last = LinearAttention.apply(q, k, v, state, log_decay, lengths, scale)
+        o, last = LinearAttention.apply(q, k, v, state, log_decay, lengths, dims,
+                                        Dk ** -0.5 if scale is None else float(scale))
     return (o, last) if return_state else o
 
 
@@ -230,17 +227,22 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     (slots [B] int32, distinct; stream b's own row b by default) and is moved
     in place.  A stream whose slot is outside the pool is idle: its row of
     the result [B, H, Dv] is 0.  No gradients."""
-    shape, q, k, v = _linattn_shape(q, k, v, log_decay, scale, None)
+    dims = _linattn_check(q, k, v, log_decay, True)
+    B, _, H, _, _, _, Dk, Dv, _ = dims
+    dev = q.device
     if state.dim() != 4 or state.shape[0] < 1:
         raise ValueError("state must be [slots, H, Dk, Dv] with at least one slot")
-    _check("state", state, q.device, torch.float32,
-           (state.shape[0], shape.H, shape.Dk, shape.Dv))
+    N = state.shape[0]
+    _check("state", state, dev, torch.float32, (N, H, Dk, Dv))
     if slots is not None:
-        _check("slots", slots, q.device, torch.int32, (shape.B,))
-    o = torch.empty((shape.B, shape.H, shape.Dv), dtype=q.dtype, device=q.device)
-    if shape.B:
-        _call("semicrf_linattn_step", q.device, shape, None, _ptr(q), _ptr(k), _ptr(v),
-              _ptr(log_decay), _ptr(slots), state.shape[0], _ptr(state), _ptr(o))
+        _check("slots", slots, dev, torch.int32, (B,))
+    o = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
+    if B:
+        q, k, v = _rows(q), _rows(k), _rows(v)
+        shape = _LinattnShape(*dims, Dk ** -0.5 if scale is None else scale, _strides(q),
+                              _strides(k), _strides(v))
+        launch(load().semicrf_linattn_step, dev, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
+               _ptr(log_decay), _ptr(slots), N, _ptr(state), _ptr(o))
     return o
 
 
@@ -248,24 +250,28 @@ class GroupNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, lengths, groups, eps, act):
         B, T, C = x.shape
-        shape = _GroupnormShape(B, T, C, groups, DTYPES[x.dtype], act, eps)
+        dev = x.device
+        ctx.fields = fields = (B, T, C, groups, DTYPES[x.dtype], act, eps)
         y = torch.empty_like(x)
-        stats = torch.empty((B, groups, 2), dtype=torch.float32, device=x.device)
-        _call("semicrf_groupnorm_fwd", x.device, shape, 0, _ptr(x), _ptr(weight), _ptr(bias),
-              _ptr(lengths), _ptr(y), _ptr(stats))
-        ctx.shape = shape
+        stats = torch.empty((B, groups, 2), dtype=torch.float32, device=dev)
+        ws, n = _workspace("semicrf_groupnorm_workspace_size", _GroupnormShape, fields, 0, dev)
+        launch(load().semicrf_groupnorm_fwd, dev, ctypes.byref(_GroupnormShape(*fields)), _ptr(x),
+               _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(y), _ptr(stats), _ptr(ws), n)
         ctx.save_for_backward(x, weight, bias, lengths, stats)
         return y
 
     @staticmethod
     def backward(ctx, dy):
         x, weight, bias, lengths, stats = ctx.saved_tensors
+        need, dev = ctx.needs_input_grad, x.device
         dy = dy.contiguous()
         dx = torch.empty_like(x)
-        dw = torch.empty_like(weight) if weight is not None and ctx.needs_input_grad[1] else None
-        db = torch.empty_like(bias) if bias is not None and ctx.needs_input_grad[2] else None
-        _call("semicrf_groupnorm_bwd", x.device, ctx.shape, 1, _ptr(x), _ptr(weight), _ptr(bias),
-              _ptr(lengths), _ptr(dy), _ptr(stats), _ptr(dx), _ptr(dw), _ptr(db))
+        dw = torch.empty_like(weight) if need[1] else None
+        db = torch.empty_like(bias) if need[2] else None
+        ws, n = _workspace("semicrf_groupnorm_workspace_size", _GroupnormShape, ctx.fields, 1, dev)
+        launch(load().semicrf_groupnorm_bwd, dev, ctypes.byref(_GroupnormShape(*ctx.fields)),
+               _ptr(x), _ptr(weight), _ptr(bias), _ptr(lengths), _ptr(dy), _ptr(stats), _ptr(dx),
+               _ptr(dw), _ptr(db), _ptr(ws), n)
         return dx, dw, db, None, None, None, None
 
 
@@ -297,6 +303,9 @@ def group_norm(x, groups: int, weight=None, bias=None, lengths=None, eps: float 
         _check("lengths", lengths, x.device, torch.int32, (x.shape[0],))
     if x.numel() == 0:
         return x.clone()
-    y = GroupNorm.apply(x.contiguous().view(x.shape[0], -1, C), weight, bias, lengths, int(groups),
-                        float(eps), ACTIVATIONS[activation])
-    return y.view(x.shape)
+    flat = x.contiguous()
+    if x.dim() != 3:
+        flat = flat.view(x.shape[0], -1, C)
+    y = GroupNorm.apply(flat, weight, bias, lengths, int(groups), float(eps),
+                        ACTIVATIONS[activation])
+    return y if x.dim() == 3 else y.view(x.shape)

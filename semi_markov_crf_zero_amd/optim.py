@@ -14,16 +14,23 @@ optional.
 from __future__ import annotations
 
 import ctypes
+import operator
+from array import array
 
 import torch
 
 from . import binding as bd
-from .encoder import DTYPES, _on
+from .encoder import DTYPES, launch
 
 EXPORTS = ("semicrf_adamw_table_size", "semicrf_adamw_table", "semicrf_adamw_step",
            "semicrf_adamw_values")
 BLOCK = 256  # elements that share one scale of an 8-bit state
 MOMENT_TYPES = {torch.float8_e4m3fn: 0, torch.uint8: 1}  # codes of m; of the root of v
+
+
+_is_none, _dtype = (lambda g: g is None), operator.attrgetter("dtype")
+_numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
+_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
 
 class _Tensor(ctypes.Structure):
@@ -44,7 +51,7 @@ def load():
                          ctypes.c_size_t)
         lib.semicrf_adamw_table_size.argtypes = [P, I, I, ctypes.POINTER(Z)]
         lib.semicrf_adamw_table.argtypes = [P, I, I, P, Z]
-        lib.semicrf_adamw_step.argtypes = [P, P, P, P, I, I, L, D, D, D, D, D, P, P]
+        lib.semicrf_adamw_step.argtypes = [P, P, P, ctypes.c_char_p, I, I, L, D, D, D, D, D, P, P]
         lib.semicrf_adamw_values.argtypes = [P, P, L, I, P, P]
         for name in EXPORTS:
             getattr(lib, name).restype = I
@@ -63,11 +70,8 @@ def moment_values(codes, scale):
         raise ValueError("scale must hold one float32 for each %d codes, on their device" % BLOCK)
     out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
     if codes.numel():
-        with _on(codes.device) as stream:
-            rc = load().semicrf_adamw_values(codes.data_ptr(), scale.data_ptr(), codes.numel(),
-                                             MOMENT_TYPES[codes.dtype], out.data_ptr(), stream)
-        if rc:
-            raise bd.SemiCRFError(rc, "semicrf_adamw_values")
+        launch(load().semicrf_adamw_values, codes.device, codes.data_ptr(), scale.data_ptr(),
+               codes.numel(), MOMENT_TYPES[codes.dtype], out.data_ptr())
     return out
 
 
@@ -157,7 +161,7 @@ class AdamWPlan:
         if rc:
             raise bd.SemiCRFError(rc, "semicrf_adamw_table")
         self.table = self.host.to(self.dev)
-        self._grads, self._types = (ctypes.c_void_p * n)(), (ctypes.c_uint8 * n)()
+        self._host, self._device = self.host.data_ptr(), self.table.data_ptr()
 
     def run(self, grads, step: int, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
             eps: float = 1e-8, weight_decay: float = 1e-2, grad_scale=None):
@@ -168,26 +172,30 @@ class AdamWPlan:
         coefficient, an inverse loss scale), read on the device."""
         if len(grads) != len(self.params):
             raise ValueError("need one gradient for each of the %d parameters" % len(self.params))
-        at, types = self._grads, self._types
-        for i, g in enumerate(grads):
-            if g is None:
-                at[i] = None
-                continue
-            if (g.dtype not in DTYPES or g.numel() != self.numels[i] or g.device != self.dev
-                    or not g.is_contiguous()):
-                raise ValueError("gradient %d must be a contiguous float32, bfloat16 or float16 "
-                                 "tensor of %d elements on %s" % (i, self.numels[i], self.dev))
-            at[i], types[i] = g.data_ptr(), DTYPES[g.dtype]
+        there, numels = grads, self.numels
+        if any(map(_is_none, grads)):
+            there = [g for g in grads if g is not None]
+            numels = [n for n, g in zip(numels, grads) if g is not None]
+        dtypes = list(map(_dtype, there))
+        if not (set(dtypes) <= DTYPES.keys() and list(map(_numel, there)) == numels
+                and set(map(_get_device, there)) <= {self.dev.index}
+                and all(map(_is_contiguous, there))):
+            raise ValueError("gradients must be contiguous float32, bfloat16 or float16 tensors of "
+                             "their parameters' sizes on %s" % self.dev)
+        at, types = array("Q", map(_data_ptr, there)), bytes(map(DTYPES.get, dtypes))
+        if there is not grads:
+            full, kinds, it = array("Q"), bytearray(), iter(zip(at, types))
+            for g in grads:
+                a, k = (0, 0) if g is None else next(it)
+                full.append(a)
+                kinds.append(k)
+            at, types = full, bytes(kinds)
         if grad_scale is not None and (grad_scale.device != self.dev or grad_scale.numel() != 1
                                        or grad_scale.dtype != torch.float32):
             raise ValueError("grad_scale must be one float32 on %s" % self.dev)
-        with _on(self.dev) as stream:
-            rc = load().semicrf_adamw_step(
-                self.host.data_ptr(), self.table.data_ptr(), at, types, len(grads), self.bits, int(step),
-                lr, beta1, beta2, eps, weight_decay,
-                None if grad_scale is None else grad_scale.data_ptr(), stream)
-        if rc:
-            raise bd.SemiCRFError(rc, "semicrf_adamw_step")
+        launch(load().semicrf_adamw_step, self.dev, self._host, self._device, at.buffer_info()[0],
+               types, len(grads), self.bits, int(step), lr, beta1, beta2, eps, weight_decay,
+               None if grad_scale is None else grad_scale.data_ptr())
 
 
 class AdamW(torch.optim.Optimizer):

@@ -145,13 +145,13 @@ def test_adamw_table(lib):
 
 
 def test_adamw_step_arguments(lib):
-    P, g, t = FAKE, (ctypes.c_void_p * 1)(0x1000), (ctypes.c_uint8 * 1)(0)
+    P, g, t = FAKE, (ctypes.c_void_p * 1)(0x1000), bytes(1)
     ok = dict(host=P, dev=P, g=g, t=t, count=1, bits=32, step=1, lr=1e-3, b1=0.9, b2=0.999,
               eps=1e-8, wd=0.0)
     for kw, code in ((dict(host=None), 1), (dict(dev=None), 1), (dict(g=None), 1),
                      (dict(t=None), 1), (dict(count=0), 2), (dict(bits=4), 6), (dict(step=0), 6),
                      (dict(b1=1.0), 6), (dict(b2=-0.1), 6), (dict(eps=-1.0), 6),
-                     (dict(t=(ctypes.c_uint8 * 1)(7)), 6)):
+                     (dict(t=bytes([7])), 6)):
         a = dict(ok, **kw)
         assert lib.semicrf_adamw_step(*a.values(), None, None) == code, kw
     assert lib.semicrf_adamw_values(P, P, 0, 0, P, None) == 2
