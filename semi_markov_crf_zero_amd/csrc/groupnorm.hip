@@ -40,9 +40,15 @@ struct GnArgs {
   const float *weight, *bias;
 };
 
+// 1 / (1 + e^-z) from the hardware's base-2 exponential and reciprocal, each
+// within an ulp: the exponent's rounding adds |z| 2^-24 of e^-z.
+__device__ __forceinline__ float sigmoid(float z) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896341f));
+}
+
 template <int ACT>
 __device__ __forceinline__ float act(float z) {
-  if (ACT == SEMICRF_ACT_SILU) return z / (1.f + expf(-z));
+  if (ACT == SEMICRF_ACT_SILU) return z * sigmoid(z);
   if (ACT == SEMICRF_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
   if (ACT == SEMICRF_ACT_RELU) return z > 0.f ? z : z == z ? 0.f : z;
   return z;
@@ -51,15 +57,33 @@ __device__ __forceinline__ float act(float z) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {
   if (ACT == SEMICRF_ACT_SILU) {
-    const float e = 1.f / (1.f + expf(-z));
+    const float e = sigmoid(z);
     return e * (1.f + z * (1.f - e));
   }
   if (ACT == SEMICRF_ACT_GELU)
     return 0.5f * (1.f + erff(z * 0.70710678118654752f)) +
-           z * expf(-0.5f * z * z) * 0.39894228040143268f;
+           z * __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f) * 0.39894228040143268f;
   if (ACT == SEMICRF_ACT_RELU) return z > 0.f ? 1.f : 0.f;
   return 1.f;
 }
+
+// What a thread needs of its channels: they lie in one group.
+template <int V>
+struct Channels {
+  float mean, rstd, w[V], b[V];
+  __device__ __forceinline__ Channels(const GnArgs &p, const float *stats, int64_t seq, int ch) {
+    const int64_t bg = seq * p.G + ch / p.Cg;
+    mean = stats[2 * bg];
+    rstd = stats[2 * bg + 1];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[i] = p.weight ? p.weight[ch + i] : 1.f;
+      b[i] = p.bias ? p.bias[ch + i] : 0.f;
+    }
+  }
+};
+
+constexpr int kUnroll = 4;  // positions a thread has loads in flight for
 
 }  // namespace
 
@@ -77,15 +101,25 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnArgs p, const T *x, doub
     const T *row = x + (int64_t)b * p.T * p.C;
     const float pivot = (float)row[v * V / p.Cg * p.Cg];
     row += (int64_t)v * V;
-    for (int t = s * p.slab + r; t < t1; t += p.rows) {
-      const Pack<T, V> d = *reinterpret_cast<const Pack<T, V> *>(row + (int64_t)t * p.C);
+    auto one = [&](const Pack<T, V> &d) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const double e = (float)d.v[i] - pivot;
         sum += e;
         sq += e * e;
       }
+    };
+    int t = s * p.slab + r;
+    for (; t + (kUnroll - 1) * p.rows < t1; t += kUnroll * p.rows) {
+      Pack<T, V> d[kUnroll];
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k)
+        d[k] = *reinterpret_cast<const Pack<T, V> *>(row + (int64_t)(t + k * p.rows) * p.C);
+#pragma unroll
+      for (int k = 0; k < kUnroll; ++k) one(d[k]);
     }
+    for (; t < t1; t += p.rows)
+      one(*reinterpret_cast<const Pack<T, V> *>(row + (int64_t)t * p.C));
   }
   red[threadIdx.x] = make_double2(sum, sq);
   __syncthreads();
@@ -98,23 +132,40 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnArgs p, const T *x, doub
   }
 }
 
-// One wave per sequence and group: mean and 1/sqrt(var + eps).
+// Sum of two values over the workgroup, in a fixed order; all threads get it.
+__device__ __forceinline__ double2 block_sum(double a, double b) {
+  __shared__ double2 red[kThreads / 64];
+  for (int o = 32; o; o >>= 1) {
+    a += __shfl_xor(a, o);
+    b += __shfl_xor(b, o);
+  }
+  if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = make_double2(a, b);
+  __syncthreads();
+  double2 s = red[0];
+  for (int k = 1; k < kThreads / 64; ++k) {
+    s.x += red[k].x;
+    s.y += red[k].y;
+  }
+  return s;
+}
+
+// One workgroup per sequence and group: mean and 1/sqrt(var + eps).
 template <typename T>
-__global__ __launch_bounds__(64) void k_gn_stats(GnArgs p, int V, const T *x, const double2 *part,
+__global__ __launch_bounds__(kThreads) void k_gn_stats(GnArgs p, int V, const T *x, const double2 *part,
                                                  float *stats) {
   const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
   const int vg = p.Cg / V;  // channel vectors of a group
   const int len = valid_length(p.lengths, b, p.T);
   double sum = 0, sq = 0;
-  for (int e = threadIdx.x; e < p.slabs * vg; e += 64) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e < p.slabs * vg; e += kThreads) {
     const double2 d = part[((int64_t)b * p.slabs + e / vg) * p.cv + g * vg + e % vg];
     sum += d.x;
     sq += d.y;
   }
-  for (int o = 32; o; o >>= 1) {
-    sum += __shfl_xor(sum, o);
-    sq += __shfl_xor(sq, o);
-  }
+  const double2 all = block_sum(sum, sq);
+  sum = all.x;
+  sq = all.y;
   if (threadIdx.x == 0) {
     float mean = 0.f, rstd = 0.f;
     if (len > 0) {
@@ -140,30 +191,29 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GnArgs p, const T *x, con
   const int valid = valid_length(p.lengths, b, p.T);
   const int t1 = min(p.T, (s + 1) * p.slab), len = min(t1, max(valid, 0));
   const float fill = valid < 0 ? __builtin_nanf("") : 0.f;
-  float mean[V], rstd[V], w[V], bi[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int ch = v * V + i;
-    const float *st = stats + 2 * ((int64_t)b * p.G + ch / p.Cg);
-    mean[i] = st[0];
-    rstd[i] = st[1];
-    w[i] = p.weight ? p.weight[ch] : 1.f;
-    bi[i] = p.bias ? p.bias[ch] : 0.f;
-  }
+  const Channels<V> u(p, stats, b, v * V);
   const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
-  for (int t = s * p.slab + r; t < t1; t += p.rows) {
-    Pack<T, V> d;
-    if (t < len) {
-      d = *reinterpret_cast<const Pack<T, V> *>(x + base + (int64_t)t * p.C);
+  auto one = [&](int t, Pack<T, V> d) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        d.v[i] = (T)act<ACT>(((float)d.v[i] - mean[i]) * rstd[i] * w[i] + bi[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) d.v[i] = (T)fill;
-    }
+    for (int i = 0; i < V; ++i)
+      d.v[i] = (T)act<ACT>(((float)d.v[i] - u.mean) * u.rstd * u.w[i] + u.b[i]);
     *reinterpret_cast<Pack<T, V> *>(y + base + (int64_t)t * p.C) = d;
+  };
+  int t = s * p.slab + r;
+  for (; t + (kUnroll - 1) * p.rows < len; t += kUnroll * p.rows) {
+    Pack<T, V> d[kUnroll];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k)
+      d[k] = *reinterpret_cast<const Pack<T, V> *>(x + base + (int64_t)(t + k * p.rows) * p.C);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) one(t + k * p.rows, d[k]);
   }
+  for (; t < len; t += p.rows)
+    one(t, *reinterpret_cast<const Pack<T, V> *>(x + base + (int64_t)t * p.C));
+  Pack<T, V> none;
+#pragma unroll
+  for (int i = 0; i < V; ++i) none.v[i] = (T)fill;
+  for (; t < t1; t += p.rows) *reinterpret_cast<Pack<T, V> *>(y + base + (int64_t)t * p.C) = none;
 }
 
 // Partial sums of dz and dz h per channel: part[b][slab][C].
@@ -180,27 +230,33 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, 
 #pragma unroll
   for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.f;
   if (r < p.rows && v < p.cv) {
-    float mean[V], rstd[V], w[V], bi[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int ch = v * V + i;
-      const float *st = stats + 2 * ((int64_t)b * p.G + ch / p.Cg);
-      mean[i] = st[0];
-      rstd[i] = st[1];
-      w[i] = p.weight ? p.weight[ch] : 1.f;
-      bi[i] = p.bias ? p.bias[ch] : 0.f;
-    }
+    const Channels<V> u(p, stats, b, v * V);
     const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
-    for (int t = s * p.slab + r; t < t1; t += p.rows) {
-      const Pack<T, V> d = *reinterpret_cast<const Pack<T, V> *>(x + base + (int64_t)t * p.C);
-      const Pack<T, V> e = *reinterpret_cast<const Pack<T, V> *>(dy + base + (int64_t)t * p.C);
+    auto one = [&](const Pack<T, V> &d, const Pack<T, V> &e) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float h = ((float)d.v[i] - mean[i]) * rstd[i];
-        const float dz = (float)e.v[i] * act_slope<ACT>(h * w[i] + bi[i]);
+        const float h = ((float)d.v[i] - u.mean) * u.rstd;
+        const float dz = (float)e.v[i] * act_slope<ACT>(h * u.w[i] + u.b[i]);
         s1[i] += dz;
         s2[i] += dz * h;
       }
+    };
+    int t = s * p.slab + r;
+    for (; t + p.rows < t1; t += 2 * p.rows) {
+      Pack<T, V> d[2], e[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int64_t at = base + (int64_t)(t + k * p.rows) * p.C;
+        d[k] = *reinterpret_cast<const Pack<T, V> *>(x + at);
+        e[k] = *reinterpret_cast<const Pack<T, V> *>(dy + at);
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) one(d[k], e[k]);
+    }
+    for (; t < t1; t += p.rows) {
+      const int64_t at = base + (int64_t)t * p.C;
+      one(*reinterpret_cast<const Pack<T, V> *>(x + at),
+          *reinterpret_cast<const Pack<T, V> *>(dy + at));
     }
   }
 #pragma unroll
@@ -219,25 +275,23 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, 
   }
 }
 
-// One wave per sequence and group: mean(d), mean(d h) of the group.
-__global__ __launch_bounds__(64) void k_gn_bwd_group(GnArgs p, const float2 *part, float2 *coef) {
+// One workgroup per sequence and group: mean(d), mean(d h) of the group.
+__global__ __launch_bounds__(kThreads) void k_gn_bwd_group(GnArgs p, const float2 *part, float2 *coef) {
   const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
   const int len = valid_length(p.lengths, b, p.T);
   double m1 = 0, m2 = 0;
-  for (int e = threadIdx.x; e < p.slabs * p.Cg; e += 64) {
+#pragma unroll 4
+  for (int e = threadIdx.x; e < p.slabs * p.Cg; e += kThreads) {
     const int ch = g * p.Cg + e % p.Cg;
     const float2 d = part[((int64_t)b * p.slabs + e / p.Cg) * p.C + ch];
     const double w = p.weight ? p.weight[ch] : 1.0;
     m1 += w * d.x;
     m2 += w * d.y;
   }
-  for (int o = 32; o; o >>= 1) {
-    m1 += __shfl_xor(m1, o);
-    m2 += __shfl_xor(m2, o);
-  }
+  const double2 all = block_sum(m1, m2);
   if (threadIdx.x == 0) {
     const double n = (double)max(len, 1) * p.Cg;
-    coef[(int64_t)b * p.G + g] = make_float2((float)(m1 / n), (float)(m2 / n));
+    coef[(int64_t)b * p.G + g] = make_float2((float)(all.x / n), (float)(all.y / n));
   }
 }
 
@@ -297,36 +351,39 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GnArgs p, const T *x,
   if (r >= p.rows || v >= p.cv) return;
   const int t1 = min(p.T, (s + 1) * p.slab);
   const int len = min(t1, max(valid_length(p.lengths, b, p.T), 0));
-  float mean[V], rstd[V], w[V], bi[V], m1[V], m2[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int ch = v * V + i;
-    const int64_t bg = (int64_t)b * p.G + ch / p.Cg;
-    mean[i] = stats[2 * bg];
-    rstd[i] = stats[2 * bg + 1];
-    m1[i] = coef[bg].x;
-    m2[i] = coef[bg].y;
-    w[i] = p.weight ? p.weight[ch] : 1.f;
-    bi[i] = p.bias ? p.bias[ch] : 0.f;
-  }
+  const Channels<V> u(p, stats, b, v * V);
+  const float2 m = coef[(int64_t)b * p.G + v * V / p.Cg];
   const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
-  for (int t = s * p.slab + r; t < t1; t += p.rows) {
-    Pack<T, V> d;
-    if (t < len) {
-      d = *reinterpret_cast<const Pack<T, V> *>(x + base + (int64_t)t * p.C);
-      const Pack<T, V> e = *reinterpret_cast<const Pack<T, V> *>(dy + base + (int64_t)t * p.C);
+  auto one = [&](int t, Pack<T, V> d, const Pack<T, V> &e) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float h = ((float)d.v[i] - mean[i]) * rstd[i];
-        const float dh = (float)e.v[i] * act_slope<ACT>(h * w[i] + bi[i]) * w[i];
-        d.v[i] = (T)(rstd[i] * (dh - m1[i] - h * m2[i]));
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) d.v[i] = (T)0.f;
+    for (int i = 0; i < V; ++i) {
+      const float h = ((float)d.v[i] - u.mean) * u.rstd;
+      const float dh = (float)e.v[i] * act_slope<ACT>(h * u.w[i] + u.b[i]) * u.w[i];
+      d.v[i] = (T)(u.rstd * (dh - m.x - h * m.y));
     }
     *reinterpret_cast<Pack<T, V> *>(dx + base + (int64_t)t * p.C) = d;
+  };
+  int t = s * p.slab + r;
+  for (; t + p.rows < len; t += 2 * p.rows) {
+    Pack<T, V> d[2], e[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t at = base + (int64_t)(t + k * p.rows) * p.C;
+      d[k] = *reinterpret_cast<const Pack<T, V> *>(x + at);
+      e[k] = *reinterpret_cast<const Pack<T, V> *>(dy + at);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) one(t + k * p.rows, d[k], e[k]);
   }
+  for (; t < len; t += p.rows) {
+    const int64_t at = base + (int64_t)t * p.C;
+    one(t, *reinterpret_cast<const Pack<T, V> *>(x + at),
+        *reinterpret_cast<const Pack<T, V> *>(dy + at));
+  }
+  Pack<T, V> none;
+#pragma unroll
+  for (int i = 0; i < V; ++i) none.v[i] = (T)0.f;
+  for (; t < t1; t += p.rows) *reinterpret_cast<Pack<T, V> *>(dx + base + (int64_t)t * p.C) = none;
 }
 
 // ---- short sequences -------------------------------------------------------
@@ -570,9 +627,9 @@ GnArgs args(const semicrf_groupnorm_shape_t *s, int V) {
   p.tiles = (p.cv + p.cvt - 1) / p.cvt;
   p.rows = kThreads / p.cvt;
   // slabs: enough workgroups to fill the GPU several times over, but no
-  // shorter than four positions a thread
+  // shorter than eight positions a thread
   const int64_t tiles = (int64_t)s->B * p.tiles;
-  const int64_t most = (s->T + 4 * p.rows - 1) / (4 * p.rows);
+  const int64_t most = (s->T + 8 * p.rows - 1) / (8 * p.rows);
   int64_t slabs = (2048 + tiles - 1) / tiles;
   if (slabs > most) slabs = most;
   if (slabs < 1) slabs = 1;
@@ -659,7 +716,7 @@ semicrf_status_t run_fwd(const GnArgs &p, const void *x, void *y, float *stats, 
                          hipStream_t st) {
   const unsigned grid = (unsigned)p.B * p.slabs * p.tiles;
   k_gn_sums<T, V><<<grid, kThreads, 0, st>>>(p, (const T *)x, (double2 *)ws);
-  k_gn_stats<T><<<(unsigned)p.B * p.G, 64, 0, st>>>(p, V, (const T *)x, (const double2 *)ws, stats);
+  k_gn_stats<T><<<(unsigned)p.B * p.G, kThreads, 0, st>>>(p, V, (const T *)x, (const double2 *)ws, stats);
   k_gn_apply<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, stats, (T *)y);
   return launch_status();
 }
@@ -684,7 +741,7 @@ semicrf_status_t run_bwd(const GnArgs &p, const void *x, const void *dy, const f
   double2 *sums = (double2 *)w;
   float2 *coef = (float2 *)(w + sums_bytes);
   k_gn_bwd_sums<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats, part);
-  k_gn_bwd_group<<<(unsigned)p.B * p.G, 64, 0, st>>>(p, part, coef);
+  k_gn_bwd_group<<<(unsigned)p.B * p.G, kThreads, 0, st>>>(p, part, coef);
   k_gn_bwd_apply<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats, coef,
                                                        (T *)dx);
   run_params(p.C, (int64_t)p.B * p.slabs, part, sums, dw, db, st);
