@@ -34,10 +34,11 @@ COMMON = [
     "-Wall", "-Wno-unused-result",
 ]
 # Matrix instructions that accumulate in the vector registers they are read
-# from: linattn.hip's accumulators are operands of the next product, and
+# from: linear attention's accumulators are operands of the next product, and
 # without this a tenth of its loop copies them from and to the accumulation
 # registers.
-EXTRA = {"linattn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+EXTRA = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+         for f in ("linattn_f32.hip", "linattn_bf16.hip", "linattn_f16.hip")}
 
 
 def _compile(src: str, asm: bool) -> str:
@@ -60,7 +61,7 @@ def _link(objs, lib):
     os.replace(tmp, lib)
 
 
-def build(asm: bool = False, jobs: int = 4) -> str:
+def build(asm: bool = False, jobs: int = 8) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     probes = sorted(glob.glob(os.path.join(PROBE, "*.hip")))
