@@ -166,15 +166,42 @@ semicrf_status_t launch_states(const LaArgs &p, int dtype, hipStream_t st) {
   return launch_status();
 }
 
-// Segments: enough for kFill workgroups, each of four chunks at least.
-constexpr int kFill = 1024;
+// Workgroups of the chunk kernel a compute unit holds.
+int resident(int Da, int Dc, int dtype) {
+  const bool f32 = dtype != SEMICRF_BF16;
+  const int DA = Da <= 128 ? (Da + 31) / 32 * 32 : 256, L = linattn_chunk(f32);
+  const int NW = DA > 128 ? 4 : linattn_waves(Dc, true), e = f32 ? 4 : 2, pad = 16 / e;
+  const int lds = e * L * (2 * (DA + pad) + 16 * NW + pad + (f32 ? 1 : 2) * (L + pad)) +
+                  4 * (6 * L + 2);
+  const int by_lds = (int)(163840 / lds), by_waves = 4 * linattn_occupancy(DA, NW) / NW;
+  const int n = by_lds < by_waves ? by_lds : by_waves;
+  return n < 1 ? 1 : n;
+}
+
+// Segments.  A chunk takes a workgroup about 3 us where it has a compute unit
+// to itself and 1 us more for each that shares it (bfloat16, 64 wide); with
+// segments the states' pass adds about 0.45 of that and two launches 10 us.
+// The number that this puts first, of those that give every compute unit 1,
+// 2, ... workgroups over up to two rounds; four chunks at least in each.
 void segments(const semicrf_linattn_shape_t *s, int *nseg, int *seg) {
-  const int64_t heads = (int64_t)s->B * s->H, chunks = (s->T + 63) / 64;
-  int64_t n = (kFill + heads - 1) / heads;
-  if (n > chunks / 4) n = chunks / 4;
-  if (n < 1) n = 1;
-  const int64_t per = (chunks + n - 1) / n;
-  *seg = (int)(per * 64);
+  const int r1 = resident(s->Dk, s->Dv, s->dtype), r2 = resident(s->Dv, s->Dk, s->dtype);
+  const int res = r1 < r2 ? r1 : r2, L = 64;
+  const int64_t heads = (int64_t)s->B * s->H, chunks = (s->T + L - 1) / L;
+  int64_t best_n = 1;
+  double best = 0;
+  for (int k = 0; k <= 2 * res; ++k) {
+    int64_t n = k ? 256 * k / heads : 1;
+    if (n > chunks / 4) n = chunks / 4;
+    if (n < 1) n = 1;
+    const int64_t per = (chunks + n - 1) / n, slots = 256 * res;
+    n = (chunks + per - 1) / per;
+    const int64_t full = heads * n / slots, left = heads * n % slots;
+    double us = (double)per * (full * (2 + res) + (left ? 2 + (left + 255) / 256 : 0));
+    if (n > 1) us = 1.45 * us + 10;
+    if (!k || us < best) best = us, best_n = n;
+  }
+  const int64_t per = (chunks + best_n - 1) / best_n;
+  *seg = (int)(per * L);
   *nseg = (int)((chunks + per - 1) / per);
 }
 

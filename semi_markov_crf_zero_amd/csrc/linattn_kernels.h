@@ -32,6 +32,22 @@ struct LaArgs {
   int ctiles;
 };
 
+// Positions of a chunk.  The products inside a chunk grow with it, the reading
+// and updating of X shrink: 64 for bfloat16 operands; 32 for float32 ones,
+// whose matrix rate is a sixteenth and whose tiles of 64 would leave a
+// compute unit room for one workgroup.
+__host__ __device__ constexpr int linattn_chunk(bool f32_operands) { return f32_operands ? 32 : 64; }
+
+// Waves of a workgroup: one for 16 columns of the output.
+inline int linattn_waves(int Dc, bool vec) {
+  const int w = (Dc + 15) / 16;
+  return !vec ? 4 : w <= 2 ? 2 : w <= 6 ? w : 8;
+}
+// Waves a SIMD is to hold (what the registers are rationed to).
+__host__ __device__ constexpr int linattn_occupancy(int DA, int NW) {
+  return DA <= 64 || (DA <= 96 && NW >= 4) ? 3 : DA <= 128 ? 2 : 1;
+}
+
 // Widths of a launch: Da up to DA (a multiple of 32), NW waves for 16 NW
 // columns of Dc.  vec: 16-byte loads; f32_out: float32 output whatever the
 // tensors are; states: k_linattn_state instead of k_linattn.
@@ -345,7 +361,8 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
 // it is; float32 and float16 in float32: float16 would need its range
 // watched in P and X); OT: the output's; DA: Da rounded up.
 template <typename T, typename CT, typename OT, int DA, int NW, int L, bool VEC>
-__global__ __launch_bounds__(64 * NW) void k_linattn(LaArgs p) {
+__global__ __launch_bounds__(64 * NW)
+    __attribute__((amdgpu_waves_per_eu(linattn_occupancy(DA, NW)))) void k_linattn(LaArgs p) {
   constexpr int pad = 16 / sizeof(CT);
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
   constexpr int lda = DA + pad, ldc = kCols + pad, ldp = L + pad;
@@ -544,16 +561,9 @@ __global__ __launch_bounds__(64 * NW) void k_linattn(LaArgs p) {
 
 namespace {
 
-// Chunks of 64 positions; of 32 where float32 operands 256 wide would not
-// leave a compute unit's 160 KB of LDS room for the tiles of 64.
-template <typename CT, int DA>
-constexpr int chunk_of() {
-  return sizeof(CT) * DA > 512 ? 32 : 64;
-}
-
 template <typename T, typename CT, typename OT, int DA, int NW, bool VEC>
 semicrf_status_t launch_one(LaArgs p, bool states, hipStream_t st) {
-  constexpr int L = chunk_of<CT, DA>();
+  constexpr int L = linattn_chunk(sizeof(CT) == 4);
   p.ctiles = (p.Dc + 16 * NW - 1) / (16 * NW);
   const int64_t grid = (int64_t)p.B * p.H * (states ? p.nseg - 1 : p.nseg) * p.ctiles;
   if (grid > 0x7fffffff) return SEMICRF_ERR_SHAPE;
@@ -566,8 +576,7 @@ semicrf_status_t launch_one(LaArgs p, bool states, hipStream_t st) {
 
 template <typename T, typename CT, typename OT, int DA>
 semicrf_status_t launch_nw(const LaArgs &p, bool states, hipStream_t st) {
-  switch ((p.Dc + 15) / 16) {
-    case 1:
+  switch (linattn_waves(p.Dc, true)) {
     case 2: return launch_one<T, CT, OT, DA, 2, true>(p, states, st);
     case 3: return launch_one<T, CT, OT, DA, 3, true>(p, states, st);
     case 4: return launch_one<T, CT, OT, DA, 4, true>(p, states, st);
