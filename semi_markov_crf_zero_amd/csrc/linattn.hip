@@ -168,12 +168,12 @@ semicrf_status_t launch_states(const LaArgs &p, int dtype, hipStream_t st) {
 
 // Workgroups of the chunk kernel a compute unit holds.
 int resident(int Da, int Dc, int dtype) {
-  const bool f32 = dtype != SEMICRF_BF16;
-  const int DA = Da <= 128 ? (Da + 31) / 32 * 32 : 256, L = linattn_chunk(f32);
-  const int NW = DA > 128 ? 4 : linattn_waves(Dc, true), e = f32 ? 4 : 2, pad = 16 / e;
-  const int lds = e * L * (2 * (DA + pad) + 16 * NW + pad + (f32 ? 1 : 2) * (L + pad)) +
-                  4 * (6 * L + 2);
-  const int by_lds = (int)(163840 / lds), by_waves = 4 * linattn_occupancy(DA, NW) / NW;
+  const int NP = linattn_parts(dtype), NR = NP == 3 ? 3 : 2, L = linattn_chunk(NP);
+  const int DA = Da <= 128 ? (Da + 31) / 32 * 32 : 256;
+  const int NW = DA > 128 ? 4 : linattn_waves(Dc, true);
+  const int lds = 2 * L * (NP * (2 * (DA + 8) + 16 * NW + 8) + NR * (L + 8)) + 4 * (6 * L + 2);
+  const int by_lds = (int)(163840 / lds), occ = linattn_occupancy(DA, NW);
+  const int by_waves = NW < 4 ? 4 * occ / NW : occ / ((NW + 3) / 4);
   const int n = by_lds < by_waves ? by_lds : by_waves;
   return n < 1 ? 1 : n;
 }

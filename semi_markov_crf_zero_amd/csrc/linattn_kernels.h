@@ -32,20 +32,34 @@ struct LaArgs {
   int ctiles;
 };
 
+// Operands.  The matrix cores multiply bfloat16 sixteen times as fast as
+// float32, and a float32 is a sum of three bfloat16 parts (8 bits each), a
+// float16 of two: so every operand is held in NP parts, and a product of two
+// sums keeps the pairs of parts (i, j) whose share is above the last part's
+// (i + j < the number of parts).
+//   inputs       1, 2 or 3 parts: exact
+//   P and X      2 parts for 16-bit tensors (2^-16, far below the rounding of
+//                the output, 2^-8 or 2^-11), 3 for float32 (2^-24)
+//   what is added to X   3 parts always: X is float32 whatever the tensors are
+// Float32 at 64 columns: 6 products of 16 cycles in the place of 8 of 32.
+__host__ __device__ constexpr int linattn_parts(int dtype) {
+  return dtype == SEMICRF_F32 ? 3 : dtype == SEMICRF_F16 ? 2 : 1;
+}
 // Positions of a chunk.  The products inside a chunk grow with it, the reading
-// and updating of X shrink: 64 for bfloat16 operands; 32 for float32 ones,
-// whose matrix rate is a sixteenth and whose tiles of 64 would leave a
-// compute unit room for one workgroup.
-__host__ __device__ constexpr int linattn_chunk(bool f32_operands) { return f32_operands ? 32 : 64; }
+// and updating of X shrink: 64; 32 where more parts than one would leave a
+// compute unit's LDS room for one workgroup.
+__host__ __device__ constexpr int linattn_chunk(int parts) { return parts > 1 ? 32 : 64; }
 
 // Waves of a workgroup: one for 16 columns of the output.
 inline int linattn_waves(int Dc, bool vec) {
   const int w = (Dc + 15) / 16;
   return !vec ? 4 : w <= 2 ? 2 : w <= 6 ? w : 8;
 }
-// Waves a SIMD is to hold (what the registers are rationed to).
+// Waves a SIMD is to hold (what the registers are rationed to).  The waves of
+// a workgroup are dealt to the four SIMDs from the first one on, so one of
+// five to eight waves needs two places there: four places hold two of them.
 __host__ __device__ constexpr int linattn_occupancy(int DA, int NW) {
-  return DA <= 64 || (DA <= 96 && NW >= 4) ? 3 : DA <= 128 ? 2 : 1;
+  return DA <= 64 ? (NW <= 4 ? 3 : 4) : DA <= 128 ? 2 : 1;
 }
 
 // Widths of a launch: Da up to DA (a multiple of 32), NW waves for 16 NW
@@ -74,131 +88,100 @@ constexpr int kRawBuffer = 0x00027000;  // its last word: raw 32-bit data
 
 // A fragment is a lane's part of one operand over a 32-wide stretch of the
 // contraction: indices {4g + r} and {16 + 4g + r} (g = lane / 16, r < 4) of
-// row or column lane % 16.  That is how two neighbouring 16x16 accumulator
-// tiles hold their rows, so X goes from accumulators to operands in place.
-template <typename T>
-struct Frag;
-template <>
-struct Frag<bf16> {
-  bf8 v;
-};
-template <>
-struct Frag<float> {
-  float v[8];
+// row or column lane % 16, in N parts.  That is how two neighbouring 16x16
+// accumulator tiles hold their rows, so X goes from accumulators to operands
+// in place.
+template <int N>
+struct Frag {
+  bf8 v[N];
 };
 
-__device__ __forceinline__ f4 mma(const Frag<bf16> &a, const Frag<bf16> &b, f4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
-}
-__device__ __forceinline__ f4 mma(const Frag<float> &a, const Frag<float> &b, f4 c) {
+// c + a b, the pairs of parts (i, j) with i + j < K.
+template <int K, int N, int M>
+__device__ __forceinline__ f4 mma(const Frag<N> &a, const Frag<M> &b, f4 c) {
 #pragma unroll
-  for (int r = 0; r < 8; ++r) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[r], b.v[r], c, 0, 0, 0);
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < M; ++j)
+      if (i + j < K) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[j], c, 0, 0, 0);
   return c;
 }
 
-// Fragment of a row whose contraction index is contiguous: p at index 4g.
-__device__ __forceinline__ Frag<bf16> frag_row(const bf16 *p) {
+// Fragment of a row whose contraction index is contiguous: p at index 4g; the
+// parts lie `plane` apart.
+template <int N>
+__device__ __forceinline__ Frag<N> frag_row(const bf16 *p, int plane) {
   typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
-  const bf4 lo = *reinterpret_cast<const bf4 *>(p), hi = *reinterpret_cast<const bf4 *>(p + 16);
-  return {__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7)};
-}
-__device__ __forceinline__ Frag<float> frag_row(const float *p) {
-  const f4 lo = *reinterpret_cast<const f4 *>(p), hi = *reinterpret_cast<const f4 *>(p + 16);
-  return {{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]}};
-}
-
-// Fragment of a column whose contraction index runs over LDS rows: the tile
-// of 32 rows x 16 columns at p (row stride ld).  16-bit elements come through
-// the transposing LDS read: in each group of 16 lanes, lane i names 4
-// elements of row i / 4 and gets column i of the four rows.
-__device__ __forceinline__ Frag<bf16> frag_col(const bf16 *p, int ld, int lane) {
-  const int g = lane >> 4, i = lane & 15;
-  const bf16 *q = p + (4 * g + (i >> 2)) * ld + (i & 3) * 4;
-  const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q));
-  const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + 16 * ld));
-  return {__builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7))};
-}
-__device__ __forceinline__ Frag<float> frag_col(const float *p, int ld, int lane) {
-  const float *q = p + (4 * (lane >> 4)) * ld + (lane & 15);
-  Frag<float> f;
+  Frag<N> f;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    f.v[r] = q[r * ld];
-    f.v[4 + r] = q[(16 + r) * ld];
+  for (int i = 0; i < N; ++i) {
+    const bf4 lo = *reinterpret_cast<const bf4 *>(p + i * plane);
+    const bf4 hi = *reinterpret_cast<const bf4 *>(p + i * plane + 16);
+    f.v[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
   return f;
 }
 
-// Float32 values as a sum of N fragments of the operand type.  A bfloat16
-// part leaves at most 2^-8 of what it was given: two parts of P and X leave
-// 2^-16, far below the rounding of a 16-bit output (2^-8 or 2^-11); three
-// parts of what is added to X leave 2^-24, so the float32 state is as exact
-// as one summed from float32 products.
-template <typename T>
-struct Parts;
-template <>
-struct Parts<bf16> {
-  static constexpr int kRead = 2, kAdd = 3;
-};
-template <>
-struct Parts<float> {
-  static constexpr int kRead = 1, kAdd = 1;
-};
-// Two neighbours at a time: one instruction rounds a pair.
+// Fragment of a column whose contraction index runs over LDS rows: the tile
+// of 32 rows x 16 columns at p (row stride ld), through the transposing LDS
+// read: in each group of 16 lanes, lane i names 4 elements of row i / 4 and
+// gets column i of the four rows.
 template <int N>
-__device__ __forceinline__ void split(const float *x, Frag<bf16> *f) {
-  f2 r[4];
+__device__ __forceinline__ Frag<N> frag_col(const bf16 *p, int plane, int ld, int lane) {
+  const bf16 *q = p + (4 * (lane >> 4) + ((lane & 15) >> 2)) * ld + (lane & 3) * 4;
+  Frag<N> f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) r[e] = f2{x[2 * e], x[2 * e + 1]};
-#pragma unroll
-  for (int n = 0; n < N; ++n)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const b2 y = __builtin_convertvector(r[e], b2);
-      f[n].v[2 * e] = y[0];
-      f[n].v[2 * e + 1] = y[1];
-      r[e] -= __builtin_convertvector(y, f2);
-    }
-}
-template <int N>
-__device__ __forceinline__ void split(const float *x, Frag<float> *f) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) f[0].v[e] = x[e];
-}
-// Four float32 values rounded to the type; x keeps what is left of them.
-__device__ __forceinline__ void part4(f4 &x, Pack<bf16, 4> &y) {
-  const f2 lo = {x[0], x[1]}, hi = {x[2], x[3]};
-  const b2 a = __builtin_convertvector(lo, b2), b = __builtin_convertvector(hi, b2);
-  const f2 ra = lo - __builtin_convertvector(a, f2), rb = hi - __builtin_convertvector(b, f2);
-  x = f4{ra[0], ra[1], rb[0], rb[1]};
-  y = {{a[0], a[1], b[0], b[1]}};
-}
-template <typename T>
-__device__ __forceinline__ void part4(f4 &x, Pack<T, 4> &y) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-    y.v[r] = (T)x[r];
-    x[r] -= (float)y.v[r];
+  for (int i = 0; i < N; ++i) {
+    const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + i * plane));
+    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + i * plane + 16 * ld));
+    f.v[i] = __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
-}
-__device__ __forceinline__ void values(const Frag<bf16> &f, float *x) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = (float)f.v[e];
-}
-__device__ __forceinline__ void values(const Frag<float> &f, float *x) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = f.v[e];
+  return f;
 }
 
-// A tile of a chunk: L rows of W columns, zeros past row n and past column
-// D.  fetch() issues a thread's 16-byte loads into registers while the chunk
-// before is worked on, put() writes them to LDS.  The loads go through a
+// Two float32 rounded to bfloat16; x keeps what is left.  One instruction
+// rounds a pair.
+__device__ __forceinline__ b2 part2(f2 &x) {
+  const b2 y = __builtin_convertvector(x, b2);
+  x -= __builtin_convertvector(y, f2);
+  return y;
+}
+template <int N>
+__device__ __forceinline__ Frag<N> split(const float *x) {
+  Frag<N> f;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    f2 r = {x[e], x[e + 1]};
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const b2 y = part2(r);
+      f.v[n][e] = y[0];
+      f.v[n][e + 1] = y[1];
+    }
+  }
+  return f;
+}
+template <int N>
+__device__ __forceinline__ void values(const Frag<N> &f, float *x) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = (float)f.v[N - 1][e];
+#pragma unroll
+    for (int n = N - 2; n >= 0; --n) x[e] += (float)f.v[n][e];
+  }
+}
+
+constexpr int kPad = 8;  // elements after a row in LDS: its banks start 4 further on
+
+// A tile of a chunk: L rows of W columns in N parts, zeros past row n and past
+// column D.  fetch() issues a thread's 16-byte loads into registers while the
+// chunk before is worked on, put() writes them to LDS.  The loads go through a
 // buffer descriptor whose range a row that is not wanted lies past, so it
 // reads 0 without a branch, whatever memory holds there.
-template <typename T, typename CT, int W, int L, int NT>
+template <typename T, int N, int W, int L, int NT>
 struct Tile {
   static constexpr int VE = 16 / sizeof(T), per = W / VE, all = L * per, NV = (all + NT - 1) / NT;
-  static constexpr int ld = W + 16 / sizeof(CT);
+  static constexpr int ld = W + kPad, plane = L * ld;
   u4 r[NV];
 
   // row i of the tile is row `row0 + step * i` (step +-1) from src, rows st
@@ -213,32 +196,49 @@ struct Tile {
       r[k] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, i < n && c < D ? at : -1, 0, 0);
     }
   }
-  __device__ __forceinline__ void put(CT *lds) const {
+  __device__ __forceinline__ void put(bf16 *lds) const {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int e = threadIdx.x + k * NT, i = e / per, c = e % per * VE;
       if (all % NT && e >= all) break;
-      const Pack<T, VE> y = __builtin_bit_cast(Pack<T, VE>, r[k]);
-      Pack<CT, VE> x;
+      bf16 *to = lds + i * ld + c;
+      if (N == 1) {
+        *reinterpret_cast<u4 *>(to) = r[k];
+      } else {
+        const Pack<T, VE> y = __builtin_bit_cast(Pack<T, VE>, r[k]);
+        Pack<bf16, VE> x[N];
 #pragma unroll
-      for (int q = 0; q < VE; ++q) x.v[q] = (CT)y.v[q];
-      CT *to = lds + i * ld + c;
+        for (int q = 0; q < VE; q += 2) {
+          f2 v = {(float)y.v[q], (float)y.v[q + 1]};
 #pragma unroll
-      for (int q = 0; q < VE; q += 16 / sizeof(CT))
-        *reinterpret_cast<Pack<CT, 16 / sizeof(CT)> *>(to + q) =
-            *reinterpret_cast<const Pack<CT, 16 / sizeof(CT)> *>(x.v + q);
+          for (int m = 0; m < N; ++m) {
+            const b2 z = part2(v);
+            x[m].v[q] = z[0];
+            x[m].v[q + 1] = z[1];
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < N; ++m) *reinterpret_cast<Pack<bf16, VE> *>(to + m * plane) = x[m];
+      }
     }
   }
 };
 
 // The same without the alignment 16-byte loads need: element by element,
 // straight to LDS.
-template <typename T, typename CT, int W, int L, int NT>
-__device__ __forceinline__ void stage(CT *lds, const T *src, int64_t st, int D, int n, int col0) {
-  constexpr int ld = W + 16 / sizeof(CT);
+template <typename T, int N, int W, int L, int NT>
+__device__ __forceinline__ void stage(bf16 *lds, const T *src, int64_t st, int D, int n,
+                                      int col0) {
+  constexpr int ld = W + kPad, plane = L * ld;
   for (int e = threadIdx.x; e < L * W; e += NT) {
     const int i = e / W, d = e % W;
-    lds[i * ld + d] = i < n && col0 + d < D ? (CT)(float)src[i * st + col0 + d] : (CT)0.f;
+    float x = i < n && col0 + d < D ? (float)src[i * st + col0 + d] : 0.f;
+#pragma unroll
+    for (int m = 0; m < N; ++m) {
+      const bf16 y = (bf16)x;
+      lds[m * plane + i * ld + d] = y;
+      x -= (float)y;
+    }
   }
 }
 
@@ -264,11 +264,10 @@ struct Decays {
 
 // X <- e^{g n} X + sum_j e^{g (n - off - j)} b_j c_j^T over a staged chunk:
 // B in rows of lda, this wave's 16 columns of C in fragments.
-template <typename CT, int KB, int L>
-__device__ __forceinline__ void add_chunk(f4 *X, const CT *Bm, const Frag<CT> *C,
+template <int NP, int KB, int L>
+__device__ __forceinline__ void add_chunk(f4 *X, const bf16 *Bm, const Frag<NP> *C,
                                           const Decays<L> &dec, int n, int off, int lane) {
-  constexpr int lda = 32 * KB + 16 / sizeof(CT);
-  constexpr int NA = Parts<CT>::kAdd;
+  constexpr int lda = 32 * KB + kPad;
   const float *add = dec.add + L + n - off - 4 * (lane >> 4);
 #pragma unroll
   for (int k = 0; k < 2 * KB; ++k)
@@ -280,29 +279,23 @@ __device__ __forceinline__ void add_chunk(f4 *X, const CT *Bm, const Frag<CT> *C
     values(C[jb], x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] *= add[-(32 * jb + (e & 3) + (e >> 2) * 16)];
-    Frag<CT> cf[NA];
-    split<NA>(x, cf);
+    const Frag<3> cf = split<3>(x);
 #pragma unroll
-    for (int k = 0; k < 2 * KB; ++k) {
-      const Frag<CT> bf = frag_col(Bm + 32 * jb * lda + 16 * k, lda, lane);
-#pragma unroll
-      for (int s = 0; s < NA; ++s) X[k] = mma(bf, cf[s], X[k]);
-    }
+    for (int k = 0; k < 2 * KB; ++k)
+      X[k] = mma<3>(frag_col<NP>(Bm + 32 * jb * lda + 16 * k, L * lda, lda, lane), cf, X[k]);
   }
 }
 
 }  // namespace
 
 // Parts of X: one workgroup of NW waves per segment but the last, 16 NW
-// columns.  Writes
-// xs[segment]; a segment past the length leaves zeros.
-template <typename T, typename CT, int DA, int NW, int L, bool VEC>
+// columns.  Writes xs[segment]; a segment past the length leaves zeros.
+template <typename T, int NP, int DA, int NW, int L, bool VEC>
 __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
-  constexpr int pad = 16 / sizeof(CT);
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
-  constexpr int lda = DA + pad, ldc = kCols + pad, KB = DA / 32;
-  __shared__ alignas(16) CT Bm[L * lda + L * ldc];
-  CT *const C = Bm + L * lda;
+  constexpr int lda = DA + kPad, ldc = kCols + kPad, KB = DA / 32;
+  __shared__ alignas(16) bf16 Bm[NP * L * (lda + ldc)];
+  bf16 *const C = Bm + NP * L * lda;
   __shared__ Decays<L> dec;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int ct = blockIdx.x % p.ctiles, s0 = blockIdx.x / p.ctiles % (p.nseg - 1);
@@ -316,8 +309,8 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
   f4 X[2 * KB];
 #pragma unroll
   for (int k = 0; k < 2 * KB; ++k) X[k] = f4{0.f, 0.f, 0.f, 0.f};
-  Tile<T, CT, DA, L, kThreads> tb;
-  Tile<T, CT, kCols, L, kThreads> tc;
+  Tile<T, NP, DA, L, kThreads> tb;
+  Tile<T, NP, kCols, L, kThreads> tc;
   // rows of a chunk in the order taken; `base` is the lowest position
   const int step = p.rev ? -1 : 1;
   auto fetch = [&](int t0) {
@@ -335,15 +328,15 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
       tc.put(C);
     } else {
       const int64_t first = p.rev ? len - 1 - t0 : t0;
-      stage<T, CT, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
-      stage<T, CT, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+      stage<T, NP, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+      stage<T, NP, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
     }
     __syncthreads();
     if (VEC && t0 + L < hi) fetch(t0 + L);
-    Frag<CT> cf[L / 32];
+    Frag<NP> cf[L / 32];
 #pragma unroll
-    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col(C + 32 * jb * ldc + 16 * w, ldc, lane);
-    add_chunk<CT, KB, L>(X, Bm, cf, dec, n, p.off, lane);
+    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col<NP>(C + 32 * jb * ldc + 16 * w, L * ldc, ldc, lane);
+    add_chunk<NP, KB, L>(X, Bm, cf, dec, n, p.off, lane);
   }
   const int xc = c0 + 16 * w + l16;
   float *out = p.xs + ((int64_t)bh * (p.nseg - 1) + s0) * p.Da * p.Dc;
@@ -360,19 +353,18 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
 // columns of the output, every chunk in turn.  T: the tensors' type; CT: the operands' type (bfloat16 as
 // it is; float32 and float16 in float32: float16 would need its range
 // watched in P and X); OT: the output's; DA: Da rounded up.
-template <typename T, typename CT, typename OT, int DA, int NW, int L, bool VEC>
+template <typename T, int NP, typename OT, int DA, int NW, int L, bool VEC>
 __global__ __launch_bounds__(64 * NW)
     __attribute__((amdgpu_waves_per_eu(linattn_occupancy(DA, NW)))) void k_linattn(LaArgs p) {
-  constexpr int pad = 16 / sizeof(CT);
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
-  constexpr int lda = DA + pad, ldc = kCols + pad, ldp = L + pad;
+  constexpr int lda = DA + kPad, ldc = kCols + kPad, ldp = L + kPad;
   constexpr int KB = DA / 32;
-  constexpr int NR = Parts<CT>::kRead;
-  __shared__ alignas(16) CT A[2 * L * lda + L * ldc + NR * L * ldp];
+  constexpr int NR = NP == 3 ? 3 : 2;  // parts of P and X
+  __shared__ alignas(16) bf16 A[L * (NP * (2 * lda + ldc) + NR * ldp)];
+  bf16 *const Bm = A + NP * L * lda;
+  bf16 *const C = Bm + NP * L * lda;
+  bf16 *const P = C + NP * L * ldc;
   __shared__ Decays<L> dec;
-  CT *const Bm = A + L * lda;
-  CT *const C = Bm + L * lda;
-  CT *const P = C + L * ldc;
 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int ct = blockIdx.x % p.ctiles, s0 = blockIdx.x / p.ctiles % p.nseg;
@@ -410,8 +402,8 @@ __global__ __launch_bounds__(64 * NW)
                                               xr, row < p.Da && xc < p.Dc ? at : -1, 0, 0));
     }
 
-  Tile<T, CT, DA, L, kThreads> ta, tb;
-  Tile<T, CT, kCols, L, kThreads> tc;
+  Tile<T, NP, DA, L, kThreads> ta, tb;
+  Tile<T, NP, kCols, L, kThreads> tc;
   // rows of a chunk in the order taken: backwards, row 0 is the last
   // position not yet taken; `base` is the lowest position
   const int step = p.rev ? -1 : 1;
@@ -430,9 +422,9 @@ __global__ __launch_bounds__(64 * NW)
     } else {
       const int n = min(L, hi - t0);
       const int64_t first = p.rev ? len - 1 - t0 : t0;
-      stage<T, CT, DA, L, kThreads>(A, a + first * p.a.st, step * p.a.st, p.Da, n, 0);
-      stage<T, CT, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
-      stage<T, CT, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+      stage<T, NP, DA, L, kThreads>(A, a + first * p.a.st, step * p.a.st, p.Da, n, 0);
+      stage<T, NP, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+      stage<T, NP, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
     }
   };
   if (lo < hi) {
@@ -448,9 +440,9 @@ __global__ __launch_bounds__(64 * NW)
     const int n = min(L, hi - t0);
     __syncthreads();
     if (VEC && t0 + L < hi) fetch(t0 + L);
-    Frag<CT> cf[L / 32];
+    Frag<NP> cf[L / 32];
 #pragma unroll
-    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col(C + 32 * jb * ldc + 16 * w, ldc, lane);
+    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col<NP>(C + 32 * jb * ldc + 16 * w, L * ldc, ldc, lane);
     f4 O[NT];
     if (p.out) {
       // P: wave w its rows 16w.., the tiles up to the diagonal and, as P is
@@ -459,27 +451,28 @@ __global__ __launch_bounds__(64 * NW)
       // row of P
 #pragma unroll
       for (int it = w; it < NT; it += NW) {
-        Frag<CT> af[KB];
+        Frag<NP> af[KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
-          af[kb] = frag_row(A + (16 * it + l16) * lda + 32 * kb + 4 * g);
+          af[kb] = frag_row<NP>(A + (16 * it + l16) * lda + 32 * kb + 4 * g, L * lda);
         const int i = 16 * it + l16;
         const float *dp = dec.p + L + i - 4 * g;
-        CT *to = P + i * ldp + 4 * g;
+        bf16 *to = P + i * ldp + 4 * g;
 #pragma unroll
         for (int jt = 0; jt < NT; ++jt) {
           if (jt > (it | 1)) break;
           f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
-            acc = mma(frag_row(Bm + (16 * jt + l16) * lda + 32 * kb + 4 * g), af[kb], acc);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[r] *= dp[-(16 * jt + r)];
+            acc = mma<3>(frag_row<NP>(Bm + (16 * jt + l16) * lda + 32 * kb + 4 * g, L * lda),
+                         af[kb], acc);
+          f2 lo = {acc[0] * dp[-16 * jt], acc[1] * dp[-16 * jt - 1]};
+          f2 hi = {acc[2] * dp[-16 * jt - 2], acc[3] * dp[-16 * jt - 3]};
 #pragma unroll
           for (int q = 0; q < NR; ++q) {
-            Pack<CT, 4> x;
-            part4(acc, x);
-            *reinterpret_cast<Pack<CT, 4> *>(to + q * L * ldp + 16 * jt) = x;
+            const b2 x = part2(lo), y = part2(hi);
+            *reinterpret_cast<Pack<bf16, 4> *>(to + q * L * ldp + 16 * jt) =
+                Pack<bf16, 4>{{x[0], x[1], y[0], y[1]}};
           }
         }
       }
@@ -491,14 +484,11 @@ __global__ __launch_bounds__(64 * NW)
         float x[8];
 #pragma unroll
         for (int r = 0; r < 4; ++r) x[r] = X[2 * kb][r], x[4 + r] = X[2 * kb + 1][r];
-        Frag<CT> xf[NR];
-        split<NR>(x, xf);
+        const Frag<NR> xf = split<NR>(x);
 #pragma unroll
-        for (int it = 0; it < NT; ++it) {
-          const Frag<CT> af = frag_row(A + (16 * it + l16) * lda + 32 * kb + 4 * g);
-#pragma unroll
-          for (int q = 0; q < NR; ++q) O[it] = mma(xf[q], af, O[it]);
-        }
+        for (int it = 0; it < NT; ++it)
+          O[it] = mma<NR>(
+              xf, frag_row<NP>(A + (16 * it + l16) * lda + 32 * kb + 4 * g, L * lda), O[it]);
       }
 #pragma unroll
       for (int it = 0; it < NT; ++it) {
@@ -507,7 +497,7 @@ __global__ __launch_bounds__(64 * NW)
         for (int r = 0; r < 4; ++r) O[it][r] *= d;
       }
     }
-    add_chunk<CT, KB, L>(X, Bm, cf, dec, n, p.off, lane);
+    add_chunk<NP, KB, L>(X, Bm, cf, dec, n, p.off, lane);
     __syncthreads();
     if (p.out) {
       const int64_t first = p.rev ? len - 1 - t0 : t0;
@@ -517,14 +507,13 @@ __global__ __launch_bounds__(64 * NW)
         const int i = 16 * it + l16;
 #pragma unroll
         for (int jb = 0; jb <= it / 2; ++jb)
-#pragma unroll
-          for (int q = 0; q < NR; ++q)
-            O[it] = mma(cf[jb], frag_row(P + q * L * ldp + i * ldp + 32 * jb + 4 * g), O[it]);
+          O[it] = mma<NR>(cf[jb], frag_row<NR>(P + i * ldp + 32 * jb + 4 * g, L * ldp), O[it]);
         if (i < n && col < p.Dc) {
           OT *to = out + (first + step * i) * sot + col;
           if (VEC) {
             Pack<OT, 4> x;
-            part4(O[it], x);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x.v[r] = (OT)O[it][r];
             *reinterpret_cast<Pack<OT, 4> *>(to) = x;
           } else {
 #pragma unroll
@@ -561,28 +550,28 @@ __global__ __launch_bounds__(64 * NW)
 
 namespace {
 
-template <typename T, typename CT, typename OT, int DA, int NW, bool VEC>
+template <typename T, int NP, typename OT, int DA, int NW, bool VEC>
 semicrf_status_t launch_one(LaArgs p, bool states, hipStream_t st) {
-  constexpr int L = linattn_chunk(sizeof(CT) == 4);
+  constexpr int L = linattn_chunk(NP);
   p.ctiles = (p.Dc + 16 * NW - 1) / (16 * NW);
   const int64_t grid = (int64_t)p.B * p.H * (states ? p.nseg - 1 : p.nseg) * p.ctiles;
   if (grid > 0x7fffffff) return SEMICRF_ERR_SHAPE;
   if (states)
-    k_linattn_state<T, CT, DA, NW, L, VEC><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
+    k_linattn_state<T, NP, DA, NW, L, VEC><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
   else
-    k_linattn<T, CT, OT, DA, NW, L, VEC><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
+    k_linattn<T, NP, OT, DA, NW, L, VEC><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
   return launch_status();
 }
 
-template <typename T, typename CT, typename OT, int DA>
+template <typename T, int NP, typename OT, int DA>
 semicrf_status_t launch_nw(const LaArgs &p, bool states, hipStream_t st) {
   switch (linattn_waves(p.Dc, true)) {
-    case 2: return launch_one<T, CT, OT, DA, 2, true>(p, states, st);
-    case 3: return launch_one<T, CT, OT, DA, 3, true>(p, states, st);
-    case 4: return launch_one<T, CT, OT, DA, 4, true>(p, states, st);
-    case 5: return launch_one<T, CT, OT, DA, 5, true>(p, states, st);
-    case 6: return launch_one<T, CT, OT, DA, 6, true>(p, states, st);
-    default: return launch_one<T, CT, OT, DA, 8, true>(p, states, st);
+    case 2: return launch_one<T, NP, OT, DA, 2, true>(p, states, st);
+    case 3: return launch_one<T, NP, OT, DA, 3, true>(p, states, st);
+    case 4: return launch_one<T, NP, OT, DA, 4, true>(p, states, st);
+    case 5: return launch_one<T, NP, OT, DA, 5, true>(p, states, st);
+    case 6: return launch_one<T, NP, OT, DA, 6, true>(p, states, st);
+    default: return launch_one<T, NP, OT, DA, 8, true>(p, states, st);
   }
 }
 
@@ -591,16 +580,16 @@ semicrf_status_t launch_nw(const LaArgs &p, bool states, hipStream_t st) {
 // would leave a lane 256 registers, and X alone takes 64.
 // Without aligned rows the loads are by element and cost more than padding:
 // two widths serve.
-template <typename T, typename CT, typename OT>
+template <typename T, int NP, typename OT>
 semicrf_status_t launch_type(const LaArgs &p, bool vec, bool states, hipStream_t st) {
   if (!vec)
-    return p.Da <= 64 ? launch_one<T, CT, OT, 64, 4, false>(p, states, st)
-                      : launch_one<T, CT, OT, 256, 4, false>(p, states, st);
-  if (p.Da <= 32) return launch_nw<T, CT, OT, 32>(p, states, st);
-  if (p.Da <= 64) return launch_nw<T, CT, OT, 64>(p, states, st);
-  if (p.Da <= 96) return launch_nw<T, CT, OT, 96>(p, states, st);
-  if (p.Da <= 128) return launch_nw<T, CT, OT, 128>(p, states, st);
-  return launch_one<T, CT, OT, 256, 4, true>(p, states, st);
+    return p.Da <= 64 ? launch_one<T, NP, OT, 64, 4, false>(p, states, st)
+                      : launch_one<T, NP, OT, 256, 4, false>(p, states, st);
+  if (p.Da <= 32) return launch_nw<T, NP, OT, 32>(p, states, st);
+  if (p.Da <= 64) return launch_nw<T, NP, OT, 64>(p, states, st);
+  if (p.Da <= 96) return launch_nw<T, NP, OT, 96>(p, states, st);
+  if (p.Da <= 128) return launch_nw<T, NP, OT, 128>(p, states, st);
+  return launch_one<T, NP, OT, 256, 4, true>(p, states, st);
 }
 
 }  // namespace
