@@ -171,7 +171,7 @@ int resident(int Da, int Dc, int dtype) {
   const int NP = linattn_parts(dtype), NR = NP == 3 ? 3 : 2, L = linattn_chunk(NP);
   const int DA = Da <= 128 ? (Da + 31) / 32 * 32 : 256;
   const int NW = DA > 128 ? 4 : linattn_waves(Dc, true);
-  const int lds = 2 * L * (NP * (2 * (DA + 8) + 16 * NW + 8) + NR * (L + 8)) + 4 * (6 * L + 2);
+  const int lds = 2 * L * (NP * (2 * DA + 4 + 16 * NW + 16) + NR * (L + 4)) + 4 * (6 * L + 2);
   const int by_lds = (int)(163840 / lds), occ = linattn_occupancy(DA, NW);
   const int by_waves = NW < 4 ? 4 * occ / NW : occ / ((NW + 3) / 4);
   const int n = by_lds < by_waves ? by_lds : by_waves;

@@ -107,33 +107,62 @@ __device__ __forceinline__ f4 mma(const Frag<N> &a, const Frag<M> &b, f4 c) {
   return c;
 }
 
-// Fragment of a row whose contraction index is contiguous: p at index 4g; the
-// parts lie `plane` apart.
-template <int N>
-__device__ __forceinline__ Frag<N> frag_row(const bf16 *p, int plane) {
+// Tiles in LDS, by what is read of them.  A phase of an 8-byte read serves 16
+// lanes from 32 banks: a fragment of rows asks for one 8-byte unit of 16 rows
+// (A, P), the transposing read of columns for 4 units of 4 rows (C), both of
+// B.  16 different bank pairs each time: rows an odd number of units apart;
+// rows 4 or 12 units (mod 16) apart; for both, the units of a row exchanged
+// by an XOR with a number that the row gives.  The first two leave one address
+// and constant offsets, the XOR a handful of addresses, so only B has it.
+template <int W>
+struct ByRow {
+  static constexpr int row = W + 4;
+  __device__ static __forceinline__ int at(int r, int u) { return r * row + 4 * u; }
+};
+template <int W>
+struct ByColumn {
+  static constexpr int row = W % 32 == 16 ? W : W + 16;
+  __device__ static __forceinline__ int at(int r, int u) { return r * row + 4 * u; }
+};
+template <int W>
+struct ByBoth {
+  static constexpr int row = W;
+  __device__ static __forceinline__ int at(int r, int u) {
+    const int key = W % 64 == 0 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r & 2) << 1) | ((r >> 2) & 3);
+    return r * row + 4 * (u ^ key);
+  }
+};
+
+// Fragment of row row0 + lane % 16 (row0 a multiple of 16), contraction
+// indices 32 kb..; the parts lie `plane` apart.
+template <int N, typename Lay>
+__device__ __forceinline__ Frag<N> frag_row(const bf16 *t, int plane, int row0, int kb, int lane) {
   typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+  const int r = lane & 15, u = 8 * kb + (lane >> 4);
+  const bf16 *lo = t + row0 * Lay::row + Lay::at(r, u);
+  const bf16 *hi = t + row0 * Lay::row + Lay::at(r, u + 4);
   Frag<N> f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const bf4 lo = *reinterpret_cast<const bf4 *>(p + i * plane);
-    const bf4 hi = *reinterpret_cast<const bf4 *>(p + i * plane + 16);
-    f.v[i] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
+  for (int i = 0; i < N; ++i)
+    f.v[i] = __builtin_shufflevector(*reinterpret_cast<const bf4 *>(lo + i * plane),
+                                     *reinterpret_cast<const bf4 *>(hi + i * plane), 0, 1, 2, 3, 4,
+                                     5, 6, 7);
   return f;
 }
 
-// Fragment of a column whose contraction index runs over LDS rows: the tile
-// of 32 rows x 16 columns at p (row stride ld), through the transposing LDS
-// read: in each group of 16 lanes, lane i names 4 elements of row i / 4 and
-// gets column i of the four rows.
-template <int N>
-__device__ __forceinline__ Frag<N> frag_col(const bf16 *p, int plane, int ld, int lane) {
-  const bf16 *q = p + (4 * (lane >> 4) + ((lane & 15) >> 2)) * ld + (lane & 3) * 4;
+// Fragment of column 16 ct + lane % 16 whose contraction index runs over the
+// 32 rows from row0, through the transposing LDS read: in each group of 16
+// lanes, lane i names 4 elements of row i / 4 and gets column i of the four
+// rows.
+template <int N, typename Lay>
+__device__ __forceinline__ Frag<N> frag_col(const bf16 *t, int plane, int row0, int ct, int lane) {
+  const int r = 4 * (lane >> 4) + ((lane & 15) >> 2), u = 4 * ct + (lane & 3);
+  const bf16 *q = t + row0 * Lay::row + Lay::at(r, u);
   Frag<N> f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + i * plane));
-    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + i * plane + 16 * ld));
+    const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(q + i * plane + 16 * Lay::row));
     f.v[i] = __builtin_bit_cast(bf8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   }
   return f;
@@ -171,17 +200,15 @@ __device__ __forceinline__ void values(const Frag<N> &f, float *x) {
   }
 }
 
-constexpr int kPad = 8;  // elements after a row in LDS: its banks start 4 further on
-
 // A tile of a chunk: L rows of W columns in N parts, zeros past row n and past
 // column D.  fetch() issues a thread's 16-byte loads into registers while the
 // chunk before is worked on, put() writes them to LDS.  The loads go through a
 // buffer descriptor whose range a row that is not wanted lies past, so it
 // reads 0 without a branch, whatever memory holds there.
-template <typename T, int N, int W, int L, int NT>
+template <typename T, int N, typename Lay, int W, int L, int NT>
 struct Tile {
   static constexpr int VE = 16 / sizeof(T), per = W / VE, all = L * per, NV = (all + NT - 1) / NT;
-  static constexpr int ld = W + kPad, plane = L * ld;
+  static constexpr int plane = L * Lay::row;
   u4 r[NV];
 
   // row i of the tile is row `row0 + step * i` (step +-1) from src, rows st
@@ -201,24 +228,22 @@ struct Tile {
     for (int k = 0; k < NV; ++k) {
       const int e = threadIdx.x + k * NT, i = e / per, c = e % per * VE;
       if (all % NT && e >= all) break;
-      bf16 *to = lds + i * ld + c;
-      if (N == 1) {
-        *reinterpret_cast<u4 *>(to) = r[k];
-      } else {
-        const Pack<T, VE> y = __builtin_bit_cast(Pack<T, VE>, r[k]);
-        Pack<bf16, VE> x[N];
+      const Pack<T, VE> y = __builtin_bit_cast(Pack<T, VE>, r[k]);
 #pragma unroll
-        for (int q = 0; q < VE; q += 2) {
-          f2 v = {(float)y.v[q], (float)y.v[q + 1]};
+      for (int q = 0; q < VE; q += 4) {
+        bf16 *to = lds + Lay::at(i, (c + q) / 4);
+        f2 lo = {(float)y.v[q], (float)y.v[q + 1]}, hi = {(float)y.v[q + 2], (float)y.v[q + 3]};
 #pragma unroll
-          for (int m = 0; m < N; ++m) {
-            const b2 z = part2(v);
-            x[m].v[q] = z[0];
-            x[m].v[q + 1] = z[1];
+        for (int m = 0; m < N; ++m) {
+          Pack<bf16, 4> x;
+          if constexpr (N == 1) {
+            x = {{y.v[q], y.v[q + 1], y.v[q + 2], y.v[q + 3]}};
+          } else {
+            const b2 a = part2(lo), b = part2(hi);
+            x = {{a[0], a[1], b[0], b[1]}};
           }
+          *reinterpret_cast<Pack<bf16, 4> *>(to + m * plane) = x;
         }
-#pragma unroll
-        for (int m = 0; m < N; ++m) *reinterpret_cast<Pack<bf16, VE> *>(to + m * plane) = x[m];
       }
     }
   }
@@ -226,17 +251,17 @@ struct Tile {
 
 // The same without the alignment 16-byte loads need: element by element,
 // straight to LDS.
-template <typename T, int N, int W, int L, int NT>
+template <typename T, int N, typename Lay, int W, int L, int NT>
 __device__ __forceinline__ void stage(bf16 *lds, const T *src, int64_t st, int D, int n,
                                       int col0) {
-  constexpr int ld = W + kPad, plane = L * ld;
+  constexpr int plane = L * Lay::row;
   for (int e = threadIdx.x; e < L * W; e += NT) {
     const int i = e / W, d = e % W;
     float x = i < n && col0 + d < D ? (float)src[i * st + col0 + d] : 0.f;
 #pragma unroll
     for (int m = 0; m < N; ++m) {
       const bf16 y = (bf16)x;
-      lds[m * plane + i * ld + d] = y;
+      lds[m * plane + Lay::at(i, d / 4) + d % 4] = y;
       x -= (float)y;
     }
   }
@@ -263,11 +288,11 @@ struct Decays {
 };
 
 // X <- e^{g n} X + sum_j e^{g (n - off - j)} b_j c_j^T over a staged chunk:
-// B in rows of lda, this wave's 16 columns of C in fragments.
+// B from LDS, this wave's 16 columns of C in fragments.
 template <int NP, int KB, int L>
 __device__ __forceinline__ void add_chunk(f4 *X, const bf16 *Bm, const Frag<NP> *C,
                                           const Decays<L> &dec, int n, int off, int lane) {
-  constexpr int lda = 32 * KB + kPad;
+  constexpr int DA = 32 * KB;
   const float *add = dec.add + L + n - off - 4 * (lane >> 4);
 #pragma unroll
   for (int k = 0; k < 2 * KB; ++k)
@@ -282,7 +307,7 @@ __device__ __forceinline__ void add_chunk(f4 *X, const bf16 *Bm, const Frag<NP> 
     const Frag<3> cf = split<3>(x);
 #pragma unroll
     for (int k = 0; k < 2 * KB; ++k)
-      X[k] = mma<3>(frag_col<NP>(Bm + 32 * jb * lda + 16 * k, L * lda, lda, lane), cf, X[k]);
+      X[k] = mma<3>(frag_col<NP, ByBoth<DA>>(Bm, L * DA, 32 * jb, k, lane), cf, X[k]);
   }
 }
 
@@ -293,9 +318,11 @@ __device__ __forceinline__ void add_chunk(f4 *X, const bf16 *Bm, const Frag<NP> 
 template <typename T, int NP, int DA, int NW, int L, bool VEC>
 __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
-  constexpr int lda = DA + kPad, ldc = kCols + kPad, KB = DA / 32;
-  __shared__ alignas(16) bf16 Bm[NP * L * (lda + ldc)];
-  bf16 *const C = Bm + NP * L * lda;
+  constexpr int KB = DA / 32;
+  typedef ByBoth<DA> LB;
+  typedef ByColumn<kCols> LC;
+  __shared__ alignas(16) bf16 Bm[NP * L * (DA + LC::row)];
+  bf16 *const C = Bm + NP * L * DA;
   __shared__ Decays<L> dec;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int ct = blockIdx.x % p.ctiles, s0 = blockIdx.x / p.ctiles % (p.nseg - 1);
@@ -309,8 +336,8 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
   f4 X[2 * KB];
 #pragma unroll
   for (int k = 0; k < 2 * KB; ++k) X[k] = f4{0.f, 0.f, 0.f, 0.f};
-  Tile<T, NP, DA, L, kThreads> tb;
-  Tile<T, NP, kCols, L, kThreads> tc;
+  Tile<T, NP, LB, DA, L, kThreads> tb;
+  Tile<T, NP, LC, kCols, L, kThreads> tc;
   // rows of a chunk in the order taken; `base` is the lowest position
   const int step = p.rev ? -1 : 1;
   auto fetch = [&](int t0) {
@@ -328,14 +355,14 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
       tc.put(C);
     } else {
       const int64_t first = p.rev ? len - 1 - t0 : t0;
-      stage<T, NP, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
-      stage<T, NP, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+      stage<T, NP, LB, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+      stage<T, NP, LC, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
     }
     __syncthreads();
     if (VEC && t0 + L < hi) fetch(t0 + L);
     Frag<NP> cf[L / 32];
 #pragma unroll
-    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col<NP>(C + 32 * jb * ldc + 16 * w, L * ldc, ldc, lane);
+    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col<NP, LC>(C, L * LC::row, 32 * jb, w, lane);
     add_chunk<NP, KB, L>(X, Bm, cf, dec, n, p.off, lane);
   }
   const int xc = c0 + 16 * w + l16;
@@ -357,13 +384,16 @@ template <typename T, int NP, typename OT, int DA, int NW, int L, bool VEC>
 __global__ __launch_bounds__(64 * NW)
     __attribute__((amdgpu_waves_per_eu(linattn_occupancy(DA, NW)))) void k_linattn(LaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
-  constexpr int lda = DA + kPad, ldc = kCols + kPad, ldp = L + kPad;
   constexpr int KB = DA / 32;
   constexpr int NR = NP == 3 ? 3 : 2;  // parts of P and X
-  __shared__ alignas(16) bf16 A[L * (NP * (2 * lda + ldc) + NR * ldp)];
-  bf16 *const Bm = A + NP * L * lda;
-  bf16 *const C = Bm + NP * L * lda;
-  bf16 *const P = C + NP * L * ldc;
+  typedef ByRow<DA> LA;
+  typedef ByBoth<DA> LB;
+  typedef ByColumn<kCols> LC;
+  typedef ByRow<L> LP;
+  __shared__ alignas(16) bf16 A[L * (NP * (LA::row + DA + LC::row) + NR * LP::row)];
+  bf16 *const Bm = A + NP * L * LA::row;
+  bf16 *const C = Bm + NP * L * DA;
+  bf16 *const P = C + NP * L * LC::row;
   __shared__ Decays<L> dec;
 
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
@@ -402,8 +432,9 @@ __global__ __launch_bounds__(64 * NW)
                                               xr, row < p.Da && xc < p.Dc ? at : -1, 0, 0));
     }
 
-  Tile<T, NP, DA, L, kThreads> ta, tb;
-  Tile<T, NP, kCols, L, kThreads> tc;
+  Tile<T, NP, LA, DA, L, kThreads> ta;
+  Tile<T, NP, LB, DA, L, kThreads> tb;
+  Tile<T, NP, LC, kCols, L, kThreads> tc;
   // rows of a chunk in the order taken: backwards, row 0 is the last
   // position not yet taken; `base` is the lowest position
   const int step = p.rev ? -1 : 1;
@@ -422,9 +453,9 @@ __global__ __launch_bounds__(64 * NW)
     } else {
       const int n = min(L, hi - t0);
       const int64_t first = p.rev ? len - 1 - t0 : t0;
-      stage<T, NP, DA, L, kThreads>(A, a + first * p.a.st, step * p.a.st, p.Da, n, 0);
-      stage<T, NP, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
-      stage<T, NP, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
+      stage<T, NP, LA, DA, L, kThreads>(A, a + first * p.a.st, step * p.a.st, p.Da, n, 0);
+      stage<T, NP, LB, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
+      stage<T, NP, LC, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
     }
   };
   if (lo < hi) {
@@ -442,7 +473,7 @@ __global__ __launch_bounds__(64 * NW)
     if (VEC && t0 + L < hi) fetch(t0 + L);
     Frag<NP> cf[L / 32];
 #pragma unroll
-    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col<NP>(C + 32 * jb * ldc + 16 * w, L * ldc, ldc, lane);
+    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col<NP, LC>(C, L * LC::row, 32 * jb, w, lane);
     f4 O[NT];
     if (p.out) {
       // P: wave w its rows 16w.., the tiles up to the diagonal and, as P is
@@ -454,24 +485,22 @@ __global__ __launch_bounds__(64 * NW)
         Frag<NP> af[KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
-          af[kb] = frag_row<NP>(A + (16 * it + l16) * lda + 32 * kb + 4 * g, L * lda);
+          af[kb] = frag_row<NP, LA>(A, L * LA::row, 16 * it, kb, lane);
         const int i = 16 * it + l16;
         const float *dp = dec.p + L + i - 4 * g;
-        bf16 *to = P + i * ldp + 4 * g;
 #pragma unroll
         for (int jt = 0; jt < NT; ++jt) {
           if (jt > (it | 1)) break;
           f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
-            acc = mma<3>(frag_row<NP>(Bm + (16 * jt + l16) * lda + 32 * kb + 4 * g, L * lda),
-                         af[kb], acc);
+            acc = mma<3>(frag_row<NP, LB>(Bm, L * DA, 16 * jt, kb, lane), af[kb], acc);
           f2 lo = {acc[0] * dp[-16 * jt], acc[1] * dp[-16 * jt - 1]};
           f2 hi = {acc[2] * dp[-16 * jt - 2], acc[3] * dp[-16 * jt - 3]};
 #pragma unroll
           for (int q = 0; q < NR; ++q) {
             const b2 x = part2(lo), y = part2(hi);
-            *reinterpret_cast<Pack<bf16, 4> *>(to + q * L * ldp + 16 * jt) =
+            *reinterpret_cast<Pack<bf16, 4> *>(P + q * L * LP::row + LP::at(i, 4 * jt + g)) =
                 Pack<bf16, 4>{{x[0], x[1], y[0], y[1]}};
           }
         }
@@ -487,8 +516,7 @@ __global__ __launch_bounds__(64 * NW)
         const Frag<NR> xf = split<NR>(x);
 #pragma unroll
         for (int it = 0; it < NT; ++it)
-          O[it] = mma<NR>(
-              xf, frag_row<NP>(A + (16 * it + l16) * lda + 32 * kb + 4 * g, L * lda), O[it]);
+          O[it] = mma<NR>(xf, frag_row<NP, LA>(A, L * LA::row, 16 * it, kb, lane), O[it]);
       }
 #pragma unroll
       for (int it = 0; it < NT; ++it) {
@@ -507,7 +535,7 @@ __global__ __launch_bounds__(64 * NW)
         const int i = 16 * it + l16;
 #pragma unroll
         for (int jb = 0; jb <= it / 2; ++jb)
-          O[it] = mma<NR>(cf[jb], frag_row<NR>(P + i * ldp + 32 * jb + 4 * g, L * ldp), O[it]);
+          O[it] = mma<NR>(cf[jb], frag_row<NR, LP>(P, L * LP::row, 16 * it, jb, lane), O[it]);
         if (i < n && col < p.Dc) {
           OT *to = out + (first + step * i) * sot + col;
           if (VEC) {
