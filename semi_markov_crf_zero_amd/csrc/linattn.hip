@@ -82,15 +82,18 @@ __global__ __launch_bounds__(256) void k_share_sum(const float *part, T *out, in
   }
 }
 
-// One position: a workgroup per stream and head.  Thread t owns column
-// t % 64 of each 64 and every fourth row.
-template <typename T>
+// One position: a workgroup per stream and head.  The state is read and
+// written once, V neighbouring columns and kStepRows rows of a thread in
+// flight; thread t takes column group t % tpr of rows t / tpr, + groups, ...
+constexpr int kStepRows = 8;
+template <typename T, int V>
 __global__ __launch_bounds__(256) void k_linattn_step(semicrf_linattn_shape_t s, const T *q,
                                                       const T *k, const T *v,
                                                       const float *log_decay,
                                                       const int32_t *slots, int nslots,
                                                       float *state, T *o) {
-  __shared__ float qs[256], ks[256], red[4][64];
+  __shared__ float qs[256], ks[256];
+  __shared__ Pack<float, V> red[256];
   const int b = blockIdx.x / s.H, h = blockIdx.x % s.H;
   const int slot = slots ? slots[b] : b;
   T *const ob = o + ((int64_t)b * s.H + h) * s.Dv;
@@ -98,33 +101,57 @@ __global__ __launch_bounds__(256) void k_linattn_step(semicrf_linattn_shape_t s,
     for (int c = threadIdx.x; c < s.Dv; c += 256) ob[c] = (T)0.f;
     return;
   }
-  const T *qb = q + b * s.q_stride[0] + h / (s.H / s.Hq) * s.q_stride[2];
-  const T *kb = k + b * s.k_stride[0] + h / (s.H / s.Hk) * s.k_stride[2];
   const T *vb = v + b * s.v_stride[0] + h / (s.H / s.Hv) * s.v_stride[2];
+  float *const S = state + ((int64_t)slot * s.H + h) * s.Dk * s.Dv;
+  const int tpr = s.Dv / V, groups = 256 / tpr;
+  const int c = threadIdx.x % tpr * V, r0 = threadIdx.x / tpr;
+  const bool on = r0 < groups;
+  Pack<float, V> x[kStepRows];
+  auto load = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < kStepRows; ++i)
+      if (r + i * groups < s.Dk)
+        x[i] = *reinterpret_cast<const Pack<float, V> *>(S + (r + i * groups) * s.Dv + c);
+  };
+  if (on) load(r0);
   if ((int)threadIdx.x < s.Dk) {
-    qs[threadIdx.x] = (float)qb[threadIdx.x];
-    ks[threadIdx.x] = (float)kb[threadIdx.x];
+    qs[threadIdx.x] =
+        (float)q[b * s.q_stride[0] + h / (s.H / s.Hq) * s.q_stride[2] + threadIdx.x] * s.scale;
+    ks[threadIdx.x] = (float)k[b * s.k_stride[0] + h / (s.H / s.Hk) * s.k_stride[2] + threadIdx.x];
+  }
+  const float d = expf(log_decay[h]);
+  float vc[V];
+  Pack<float, V> acc;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    vc[i] = on ? (float)vb[c + i] : 0.f;
+    acc.v[i] = 0.f;
   }
   __syncthreads();
-  const float d = expf(log_decay[h]);
-  float *const S = state + ((int64_t)slot * s.H + h) * s.Dk * s.Dv;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  for (int c0 = 0; c0 < s.Dv; c0 += 64) {
-    const int c = c0 + lane;
-    float acc = 0.f;
-    if (c < s.Dv) {
-      const float vc = (float)vb[c];
-      for (int r = w; r < s.Dk; r += 4) {
-        const float x = d * S[(int64_t)r * s.Dv + c] + ks[r] * vc;
-        S[(int64_t)r * s.Dv + c] = x;
-        acc += qs[r] * x;
+  if (on)
+    for (int r = r0; r < s.Dk; r += kStepRows * groups) {
+      if (r != r0) load(r);
+#pragma unroll
+      for (int i = 0; i < kStepRows; ++i) {
+        const int row = r + i * groups;
+        if (row < s.Dk) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            x[i].v[e] = d * x[i].v[e] + ks[row] * vc[e];
+            acc.v[e] += qs[row] * x[i].v[e];
+          }
+          *reinterpret_cast<Pack<float, V> *>(S + row * s.Dv + c) = x[i];
+        }
       }
     }
-    red[w][lane] = acc;
-    __syncthreads();
-    if (w == 0 && c < s.Dv)
-      ob[c] = (T)(s.scale * (red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane]));
-    __syncthreads();
+  red[threadIdx.x] = acc;
+  __syncthreads();
+  if (r0 == 0) {
+    for (int g = 1; g < groups; ++g)
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc.v[e] += red[g * tpr + threadIdx.x].v[e];
+#pragma unroll
+    for (int e = 0; e < V; ++e) ob[c + e] = (T)acc.v[e];
   }
 }
 
@@ -209,6 +236,21 @@ size_t state_bytes(const semicrf_linattn_shape_t *s) {
   int nseg, seg;
   segments(s, &nseg, &seg);
   return ((size_t)s->B * s->H * (nseg - 1) * s->Dk * s->Dv * sizeof(float) + 255) / 256 * 256;
+}
+
+template <typename T>
+semicrf_status_t launch_step(const semicrf_linattn_shape_t &s, const void *q, const void *k,
+                             const void *v, const float *log_decay, const int32_t *slots,
+                             int nslots, float *state, void *o, void *stream) {
+  const unsigned grid = (unsigned)s.B * s.H;
+  hipStream_t st = (hipStream_t)stream;
+  if (s.Dv % 4 == 0 && (uintptr_t)state % 16 == 0)
+    k_linattn_step<T, 4><<<grid, 256, 0, st>>>(s, (const T *)q, (const T *)k, (const T *)v,
+                                               log_decay, slots, nslots, state, (T *)o);
+  else
+    k_linattn_step<T, 1><<<grid, 256, 0, st>>>(s, (const T *)q, (const T *)k, (const T *)v,
+                                               log_decay, slots, nslots, state, (T *)o);
+  return launch_status();
 }
 
 semicrf_status_t check(const semicrf_linattn_shape_t *s) {
@@ -382,23 +424,13 @@ semicrf_status_t semicrf_linattn_step(const semicrf_linattn_shape_t *s, const vo
   if (e != SEMICRF_OK) return e;
   if (s->T != 1 || nslots < 1) return SEMICRF_ERR_SHAPE;
   (void)hipGetLastError();
-  const unsigned grid = (unsigned)s->B * s->H;
-  hipStream_t st = (hipStream_t)stream;
   switch (s->dtype) {
     case SEMICRF_F32:
-      k_linattn_step<<<grid, 256, 0, st>>>(*s, (const float *)q, (const float *)k,
-                                           (const float *)v, log_decay, slots, nslots, state,
-                                           (float *)o);
-      break;
+      return launch_step<float>(*s, q, k, v, log_decay, slots, nslots, state, o, stream);
     case SEMICRF_BF16:
-      k_linattn_step<<<grid, 256, 0, st>>>(*s, (const bf16 *)q, (const bf16 *)k, (const bf16 *)v,
-                                           log_decay, slots, nslots, state, (bf16 *)o);
-      break;
-    default:
-      k_linattn_step<<<grid, 256, 0, st>>>(*s, (const f16 *)q, (const f16 *)k, (const f16 *)v,
-                                           log_decay, slots, nslots, state, (f16 *)o);
+      return launch_step<bf16>(*s, q, k, v, log_decay, slots, nslots, state, o, stream);
+    default: return launch_step<f16>(*s, q, k, v, log_decay, slots, nslots, state, o, stream);
   }
-  return launch_status();
 }
 
 }  // extern "C"
