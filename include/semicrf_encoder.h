@@ -65,7 +65,9 @@ typedef struct {
     int64_t q_stride[3], k_stride[3], v_stride[3]; /* B, T, head; in elements */
 } semicrf_linattn_shape_t;
 
-/* Bytes of workspace of semicrf_linattn_fwd (backward = 0) or _bwd (1). */
+/* Bytes of workspace of semicrf_linattn_fwd (backward = 0) or _bwd (1).  The
+ * forward call leaves the states before its segments there (none for short
+ * sequences: 0 bytes). */
 semicrf_status_t semicrf_linattn_workspace_size(const semicrf_linattn_shape_t *shape, int backward,
                                                 size_t *bytes);
 
@@ -80,13 +82,15 @@ semicrf_status_t semicrf_linattn_fwd(const semicrf_linattn_shape_t *shape, const
  *   G_t = exp(g) G_{t+1} + scale q_t grad_o_t^T,   G after the last position
  *   = grad_state (or 0), dL/dstate_in = exp(g) G_0,
  *   grad_q_t = scale S_t grad_o_t,  grad_k_t = G_t v_t,  grad_v_t = G_t^T k_t.
- * lengths, state_in, grad_state and each output may be NULL (skipped). */
+ * lengths, state_in, grad_state and each output may be NULL (skipped).
+ * states: the forward call's workspace as that call left it (same shape, k,
+ * v, log_decay, lengths and state_in), or NULL to compute it again. */
 semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *shape, const void *q,
                                      const void *k, const void *v, const float *log_decay,
                                      const int32_t *lengths, const float *state_in,
-                                     const void *grad_o, const float *grad_state, void *grad_q,
-                                     void *grad_k, void *grad_v, float *grad_state_in,
-                                     void *workspace, size_t workspace_bytes, void *stream);
+                                     const void *states, const void *grad_o,
+                                     const float *grad_state, void *grad_q, void *grad_k,
+                                     void *grad_v, float *grad_state_in, void *workspace, size_t workspace_bytes, void *stream);
 
 /* One position of B streams (shape.T = 1; the T strides are not used):
  * stream b's state, state[slots[b]] [H][Dk][Dv] of a pool of `nslots`, is

@@ -346,9 +346,9 @@ semicrf_status_t semicrf_linattn_fwd(const semicrf_linattn_shape_t *s, const voi
 semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const void *q,
                                      const void *k, const void *v, const float *log_decay,
                                      const int32_t *lengths, const float *state_in,
-                                     const void *grad_o, const float *grad_state, void *grad_q,
-                                     void *grad_k, void *grad_v, float *grad_state_in,
-                                     void *workspace, size_t workspace_bytes, void *stream) {
+                                     const void *states, const void *grad_o,
+                                     const float *grad_state, void *grad_q, void *grad_k,
+                                     void *grad_v, float *grad_state_in, void *workspace, size_t workspace_bytes, void *stream) {
   if (!s || !q || !k || !v || !log_decay || !grad_o) return SEMICRF_ERR_NULL;
   size_t need;
   semicrf_status_t e = semicrf_linattn_workspace_size(s, 1, &need);
@@ -389,13 +389,18 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
     p.x_in = state_in, p.rev = 0, p.off = 1;
     p.x_scale = s->scale, p.add_scale = 1.f;
     set(vq, vk, vv, s->Dk, s->Dv);
-    e = launch_states(p, s->dtype, st);
-    if (e != SEMICRF_OK) return e;
+    if (states) {
+      p.xs = (float *)states;  // read only
+    } else {
+      e = launch_states(p, s->dtype, st);
+      if (e != SEMICRF_OK) return e;
+    }
     p.x_tr = 1;
     set(vg, vv, vk, s->Dv, s->Dk);
     e = run(grad_q, pq, s->Hq);
     if (e != SEMICRF_OK) return e;
   }
+  p.xs = xs;
   p.rev = 1, p.off = 0, p.x_scale = 1.f, p.add_scale = s->scale, p.x_in = grad_state, p.x_tr = 0;
   if (grad_k || grad_v || grad_state_in) {
     set(vk, vq, vg, s->Dk, s->Dv);

@@ -330,7 +330,6 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
   const int h = bh % p.H, b = bh / p.H, c0 = ct * kCols;
   const int len = max(valid_length(p.lengths, b, p.T), 0);
   const int lo = s0 * p.seg, hi = min(len, lo + p.seg);
-  dec.fill(p, p.log_decay[h]);
   const T *bb = (const T *)p.b.p + (int64_t)b * p.b.sb + (int64_t)(h / p.b.share) * p.b.sh;
   const T *c = (const T *)p.c.p + (int64_t)b * p.c.sb + (int64_t)(h / p.c.share) * p.c.sh;
   f4 X[2 * KB];
@@ -347,6 +346,7 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
     tc.fetch(c + base * p.c.st, (int)p.c.st, p.Dc, n, row0, step, c0);
   };
   if (VEC && lo < hi) fetch(lo);
+  dec.fill(p, p.log_decay[h]);
   for (int t0 = lo; t0 < hi; t0 += L) {
     const int n = min(L, hi - t0);
     __syncthreads();
@@ -405,32 +405,12 @@ __global__ __launch_bounds__(64 * NW)
   const int len = max(valid, 0);
   const int lo = s0 * p.seg, hi = min(len, lo + p.seg);  // of the order taken
 
-  dec.fill(p, p.log_decay[h]);
 
   const T *a = (const T *)p.a.p + (int64_t)b * p.a.sb + (int64_t)(h / p.a.share) * p.a.sh;
   const T *bb = (const T *)p.b.p + (int64_t)b * p.b.sb + (int64_t)(h / p.b.share) * p.b.sh;
   const T *c = (const T *)p.c.p + (int64_t)b * p.c.sb + (int64_t)(h / p.c.share) * p.c.sh;
   OT *out = (OT *)p.out + ((int64_t)b * p.T * p.H + h) * p.Dc;
   const int64_t sot = (int64_t)p.H * p.Dc;
-
-  // X: tile k holds rows 16k + 4g + r of column c0 + 16w + lane % 16.  All
-  // loads at once, through a descriptor that reads 0 past the state
-  f4 X[2 * KB];
-  const int xc = c0 + 16 * w + l16;
-  const int64_t xb = (int64_t)bh * p.Da * p.Dc;
-  const float *x0 = s0 ? p.xs + ((int64_t)bh * (p.nseg - 1) + s0 - 1) * p.Da * p.Dc
-                       : p.x_in ? p.x_in + xb : nullptr;
-  const auto xr = __builtin_amdgcn_make_buffer_rsrc((void *)x0, 0, x0 ? kRange : 0, kRawBuffer);
-  const int xrow = p.x_tr ? 1 : p.Dc, xcol = p.x_tr ? p.Da : 1;
-#pragma unroll
-  for (int k = 0; k < 2 * KB; ++k)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int row = 16 * k + 4 * g + r;
-      const int at = 4 * (row * xrow + xc * xcol);
-      X[k][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
-                                              xr, row < p.Da && xc < p.Dc ? at : -1, 0, 0));
-    }
 
   Tile<T, NP, LA, DA, L, kThreads> ta;
   Tile<T, NP, LB, DA, L, kThreads> tb;
@@ -458,10 +438,29 @@ __global__ __launch_bounds__(64 * NW)
       stage<T, NP, LC, kCols, L, kThreads>(C, c + first * p.c.st, step * p.c.st, p.Dc, n, c0);
     }
   };
-  if (lo < hi) {
-    if (VEC) fetch(lo);
-    stage_chunk(lo);
-  }
+  if (VEC && lo < hi) fetch(lo);
+
+  // X: tile k holds rows 16k + 4g + r of column c0 + 16w + lane % 16.  All
+  // loads at once, through a descriptor that reads 0 past the state
+  f4 X[2 * KB];
+  const int xc = c0 + 16 * w + l16;
+  const int64_t xb = (int64_t)bh * p.Da * p.Dc;
+  const float *x0 = s0 ? p.xs + ((int64_t)bh * (p.nseg - 1) + s0 - 1) * p.Da * p.Dc
+                       : p.x_in ? p.x_in + xb : nullptr;
+  const auto xr = __builtin_amdgcn_make_buffer_rsrc((void *)x0, 0, x0 ? kRange : 0, kRawBuffer);
+  const int xrow = p.x_tr ? 1 : p.Dc, xcol = p.x_tr ? p.Da : 1;
+#pragma unroll
+  for (int k = 0; k < 2 * KB; ++k)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * k + 4 * g + r;
+      const int at = 4 * (row * xrow + xc * xcol);
+      X[k][r] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                              xr, row < p.Da && xc < p.Dc ? at : -1, 0, 0));
+    }
+
+  dec.fill(p, p.log_decay[h]);
+  if (lo < hi) stage_chunk(lo);
 
   // Two barriers a chunk: one when its tiles and one when P is in LDS.
   // Everything that reads the tiles comes before the second, so the next

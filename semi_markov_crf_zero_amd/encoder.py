@@ -58,7 +58,7 @@ def load():
             f = getattr(lib, "semicrf_%s_workspace_size" % name)
             f.argtypes, f.restype = [P, I, ctypes.POINTER(Z)], I
         lib.semicrf_linattn_fwd.argtypes = [P] * 9 + [P, Z, P]
-        lib.semicrf_linattn_bwd.argtypes = [P] * 13 + [P, Z, P]
+        lib.semicrf_linattn_bwd.argtypes = [P] * 14 + [P, Z, P]
         lib.semicrf_linattn_step.argtypes = [P] * 6 + [I, P, P, P]
         lib.semicrf_groupnorm_fwd.argtypes = [P] * 7 + [P, Z, P]
         lib.semicrf_groupnorm_bwd.argtypes = [P] * 10 + [P, Z, P]
@@ -155,9 +155,9 @@ class LinearAttention(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, q, k, v, state, log_decay, lengths, dims, scale):
-        ctx.save_for_backward(q, k, v, state, log_decay, lengths)
         ctx.set_materialize_grads(False)
         ctx.dims, ctx.scale = dims, scale
+        saved = q, k, v, state, log_decay, lengths
         B, T, H, _, _, _, Dk, Dv, _ = dims
         q, k, v = _rows(q), _rows(k), _rows(v)
         dev = q.device
@@ -168,11 +168,12 @@ class LinearAttention(torch.autograd.Function):
         launch(load().semicrf_linattn_fwd, dev, ctypes.byref(_LinattnShape(*fields)), _ptr(q),
                _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(o), _ptr(last),
                _ptr(ws), n)
+        ctx.save_for_backward(*saved, ws)
         return o, last
 
     @staticmethod
     def backward(ctx, do, dlast):
-        q, k, v, state, log_decay, lengths = ctx.saved_tensors
+        q, k, v, state, log_decay, lengths, states = ctx.saved_tensors
         B, T, H, _, _, _, _, Dv, _ = ctx.dims
         need, dev = ctx.needs_input_grad, q.device
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=dev) if n else None
@@ -186,8 +187,8 @@ class LinearAttention(torch.autograd.Function):
         dlast = None if dlast is None else dlast.contiguous()
         ws, n = _workspace("semicrf_linattn_workspace_size", _LinattnShape, fields, 1, dev)
         launch(load().semicrf_linattn_bwd, dev, ctypes.byref(_LinattnShape(*fields)), _ptr(q),
-               _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(do),
-               _ptr(dlast), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dstate), _ptr(ws), n)
+               _ptr(k), _ptr(v), _ptr(log_decay), _ptr(lengths), _ptr(state), _ptr(states),
+               _ptr(do), _ptr(dlast), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dstate), _ptr(ws), n)
         return dq, dk, dv, dstate, None, None, None, None
 
 

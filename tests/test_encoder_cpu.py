@@ -50,8 +50,8 @@ def test_linattn_shapes_refused(lib, kw, code):
     P = FAKE
     assert lib.semicrf_linattn_fwd(ctypes.byref(s), P, P, P, P, None, None, P, None, P, 1 << 40,
                                    None) == code
-    assert lib.semicrf_linattn_bwd(ctypes.byref(s), P, P, P, P, None, None, P, None, P, P, P, None,
-                                   P, 1 << 40, None) == code
+    assert lib.semicrf_linattn_bwd(ctypes.byref(s), P, P, P, P, None, None, None, P, None, P, P, P,
+                                   None, P, 1 << 40, None) == code
 
 
 def test_linattn_null_and_workspace(lib):
@@ -65,10 +65,10 @@ def test_linattn_null_and_workspace(lib):
         a = [P, P, P, P, None, None, P, None]
         a[i] = None
         assert lib.semicrf_linattn_fwd(r, *a, P, 1 << 40, None) == 1
-        b = [P, P, P, P, None, None, P, None, P, P, P, None]
-        b[i] = None
+        b = [P, P, P, P, None, None, None, P, None, P, P, P, None]
+        b[i if i < 4 else 7] = None
         assert lib.semicrf_linattn_bwd(r, *b, P, 1 << 40, None) == 1
-    b = [P, P, P, P, None, None, P, None, P, P, P, None]
+    b = [P, P, P, P, None, None, None, P, None, P, P, P, None]
     assert lib.semicrf_linattn_bwd(r, *b, P, n.value - 1, None) == 4
     assert lib.semicrf_linattn_bwd(r, *b, None, n.value, None) == 4
     assert lib.semicrf_linattn_step(r, P, P, P, P, None, 4, P, P, None) == 2  # T is not 1

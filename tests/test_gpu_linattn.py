@@ -414,3 +414,28 @@ def test_refusals():
                      ((x, x, x, g, s.transpose(2, 3)), {})):
         with pytest.raises(ValueError):
             encoder.linear_attention_step(*args, **kw)
+
+
+def test_backward_without_the_forward_call():
+    """semicrf_linattn_bwd with no states left by a forward call computes them."""
+    import ctypes
+    t = draw(17, 1, 3000, (2, 2, 2), 32, 48, "bf16", True)
+    d = {n: x.to(DEV) for n, x in t.items()}
+    for n in ("q", "k", "v", "state"):
+        d[n].requires_grad_(True)
+    o, last = encoder.linear_attention(d["q"], d["k"], d["v"], d["g"], state=d["state"],
+                                       return_state=True)
+    want = torch.autograd.grad((o, last), [d[n] for n in ("q", "k", "v", "state")],
+                               (d["do"], d["ds"]))
+    fields = (1, 3000, 2, 2, 2, 2, 32, 48, 1, 32 ** -0.5,
+              *(d[n].stride()[:3] for n in ("q", "k", "v")))
+    ws, n = encoder._workspace("semicrf_linattn_workspace_size", encoder._LinattnShape, fields, 1,
+                               o.device)
+    got = [torch.empty_like(x) for x in want]
+    encoder.launch(encoder.load().semicrf_linattn_bwd, o.device,
+                   ctypes.byref(encoder._LinattnShape(*fields)),
+                   *(d[n].data_ptr() for n in ("q", "k", "v", "g")), None, d["state"].data_ptr(),
+                   None, d["do"].data_ptr(), d["ds"].data_ptr(), *(x.data_ptr() for x in got),
+                   ws.data_ptr(), n)
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
