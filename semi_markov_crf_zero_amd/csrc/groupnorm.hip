@@ -67,19 +67,26 @@ __device__ __forceinline__ float act_slope(float z) {
   return 1.f;
 }
 
-// What a thread needs of its channels: they lie in one group.
-template <int V>
+// What a thread needs of its V channels: ONE group holds them all, or each
+// has its own statistics.
+template <int V, bool ONE>
 struct Channels {
-  float mean, rstd, w[V], b[V];
+  float mean[ONE ? 1 : V], rstd[ONE ? 1 : V], w[V], b[V];
   __device__ __forceinline__ Channels(const GnArgs &p, const float *stats, int64_t seq, int ch) {
-    const int64_t bg = seq * p.G + ch / p.Cg;
-    mean = stats[2 * bg];
-    rstd = stats[2 * bg + 1];
+#pragma unroll
+    for (int i = 0; i < (ONE ? 1 : V); ++i) {
+      const int64_t bg = seq * p.G + (ch + i) / p.Cg;
+      mean[i] = stats[2 * bg];
+      rstd[i] = stats[2 * bg + 1];
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       w[i] = p.weight ? p.weight[ch + i] : 1.f;
       b[i] = p.bias ? p.bias[ch + i] : 0.f;
     }
+  }
+  __device__ __forceinline__ float h(float x, int i) const {
+    return (x - mean[ONE ? 0 : i]) * rstd[ONE ? 0 : i];
   }
 };
 
@@ -87,26 +94,31 @@ constexpr int kUnroll = 4;  // positions a thread has loads in flight for
 
 }  // namespace
 
-// Partial sums of x - pivot and its square: part[b][slab][channel vector].
-template <typename T, int V>
+// Partial sums of x - pivot and its square, one pair for a vector of channels
+// or, where groups part it, for each: part[b][slab][pairs].
+template <typename T, int V, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_sums(GnArgs p, const T *x, double2 *part) {
+  constexpr int N = ONE ? 1 : V;
   __shared__ double2 red[kThreads];
   const int b = blockIdx.x / (p.slabs * p.tiles), s = blockIdx.x / p.tiles % p.slabs;
   const int c = threadIdx.x % p.cvt, r = threadIdx.x / p.cvt;
   const int v = blockIdx.x % p.tiles * p.cvt + c;
   const int len = max(valid_length(p.lengths, b, p.T), 0);
   const int t1 = min(len, (s + 1) * p.slab);
-  double sum = 0, sq = 0;
+  double sum[N] = {}, sq[N] = {};
   if (r < p.rows && v < p.cv && len > 0) {
     const T *row = x + (int64_t)b * p.T * p.C;
-    const float pivot = (float)row[v * V / p.Cg * p.Cg];
+    float pivot[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) pivot[i] = (float)row[(v * V + i) / p.Cg * p.Cg];
     row += (int64_t)v * V;
     auto one = [&](const Pack<T, V> &d) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const double e = (float)d.v[i] - pivot;
-        sum += e;
-        sq += e * e;
+        const int k = ONE ? 0 : i;
+        const double e = (float)d.v[i] - pivot[k];
+        sum[k] += e;
+        sq[k] += e * e;
       }
     };
     int t = s * p.slab + r;
@@ -121,14 +133,19 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnArgs p, const T *x, doub
     for (; t < t1; t += p.rows)
       one(*reinterpret_cast<const Pack<T, V> *>(row + (int64_t)t * p.C));
   }
-  red[threadIdx.x] = make_double2(sum, sq);
-  __syncthreads();
-  if (r == 0 && v < p.cv) {
-    for (int k = 1; k < p.rows; ++k) {
-      sum += red[k * p.cvt + c].x;
-      sq += red[k * p.cvt + c].y;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i) __syncthreads();
+    red[threadIdx.x] = make_double2(sum[i], sq[i]);
+    __syncthreads();
+    if (r == 0 && v < p.cv) {
+      double a1 = sum[i], a2 = sq[i];
+      for (int k = 1; k < p.rows; ++k) {
+        a1 += red[k * p.cvt + c].x;
+        a2 += red[k * p.cvt + c].y;
+      }
+      part[((int64_t)b * p.slabs + s) * p.cv * N + v * N + i] = make_double2(a1, a2);
     }
-    part[((int64_t)b * p.slabs + s) * p.cv + v] = make_double2(sum, sq);
   }
 }
 
@@ -151,15 +168,15 @@ __device__ __forceinline__ double2 block_sum(double a, double b) {
 
 // One workgroup per sequence and group: mean and 1/sqrt(var + eps).
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_gn_stats(GnArgs p, int V, const T *x, const double2 *part,
+__global__ __launch_bounds__(kThreads) void k_gn_stats(GnArgs p, int pairs, const T *x, const double2 *part,
                                                  float *stats) {
   const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
-  const int vg = p.Cg / V;  // channel vectors of a group
+  const int vg = pairs / p.G;  // pairs of a group
   const int len = valid_length(p.lengths, b, p.T);
   double sum = 0, sq = 0;
 #pragma unroll 4
   for (int e = threadIdx.x; e < p.slabs * vg; e += kThreads) {
-    const double2 d = part[((int64_t)b * p.slabs + e / vg) * p.cv + g * vg + e % vg];
+    const double2 d = part[((int64_t)b * p.slabs + e / vg) * pairs + g * vg + e % vg];
     sum += d.x;
     sq += d.y;
   }
@@ -181,7 +198,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_stats(GnArgs p, int V, const T 
   }
 }
 
-template <typename T, int V, int ACT>
+template <typename T, int V, int ACT, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_apply(GnArgs p, const T *x, const float *stats,
                                                        T *y) {
   const int b = blockIdx.x / (p.slabs * p.tiles), s = blockIdx.x / p.tiles % p.slabs;
@@ -191,12 +208,12 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GnArgs p, const T *x, con
   const int valid = valid_length(p.lengths, b, p.T);
   const int t1 = min(p.T, (s + 1) * p.slab), len = min(t1, max(valid, 0));
   const float fill = valid < 0 ? __builtin_nanf("") : 0.f;
-  const Channels<V> u(p, stats, b, v * V);
+  const Channels<V, ONE> u(p, stats, b, v * V);
   const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
   auto one = [&](int t, Pack<T, V> d) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      d.v[i] = (T)act<ACT>(((float)d.v[i] - u.mean) * u.rstd * u.w[i] + u.b[i]);
+      d.v[i] = (T)act<ACT>(u.h((float)d.v[i], i) * u.w[i] + u.b[i]);
     *reinterpret_cast<Pack<T, V> *>(y + base + (int64_t)t * p.C) = d;
   };
   int t = s * p.slab + r;
@@ -217,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply(GnArgs p, const T *x, con
 }
 
 // Partial sums of dz and dz h per channel: part[b][slab][C].
-template <typename T, int V, int ACT>
+template <typename T, int V, int ACT, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, const T *dy,
                                                           const float *stats, float2 *part) {
   __shared__ float2 red[kThreads * V];
@@ -230,12 +247,12 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, 
 #pragma unroll
   for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.f;
   if (r < p.rows && v < p.cv) {
-    const Channels<V> u(p, stats, b, v * V);
+    const Channels<V, ONE> u(p, stats, b, v * V);
     const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
     auto one = [&](const Pack<T, V> &d, const Pack<T, V> &e) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float h = ((float)d.v[i] - u.mean) * u.rstd;
+        const float h = u.h((float)d.v[i], i);
         const float dz = (float)e.v[i] * act_slope<ACT>(h * u.w[i] + u.b[i]);
         s1[i] += dz;
         s2[i] += dz * h;
@@ -295,29 +312,35 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_group(GnArgs p, const float
   }
 }
 
-// The parameters' gradients: rows of partials [n][C] added in float64, 64
+// The parameters' gradients: rows of partials [n][C] added in float64, 16
 // channels and n / splits rows a workgroup; then the splits.
-__global__ __launch_bounds__(256) void k_gn_bwd_params(int C, int64_t n, int splits,
-                                                       const float2 *part, double2 *sums,
-                                                       float *dw, float *db) {
-  __shared__ double2 red[256];
-  const int tiles = (C + 63) / 64, s = blockIdx.x / tiles;
-  const int ch = blockIdx.x % tiles * 64 + threadIdx.x % 64, q = threadIdx.x / 64;
+constexpr int kParamThreads = 1024;
+__global__ __launch_bounds__(kParamThreads) void k_gn_bwd_params(int C, int64_t n, int splits,
+                                                                 const float2 *part, double2 *sums,
+                                                                 float *dw, float *db) {
+  __shared__ double2 red[kParamThreads / 4];
+  const int tiles = (C + 15) / 16, s = blockIdx.x / tiles;
+  const int ch = blockIdx.x % tiles * 16 + threadIdx.x % 16, q = threadIdx.x / 16;
   const int64_t r0 = n * s / splits, r1 = n * (s + 1) / splits;
   double a1 = 0, a2 = 0;
   if (ch < C)
 #pragma unroll 8
-    for (int64_t r = r0 + q; r < r1; r += 4) {
+    for (int64_t r = r0 + q; r < r1; r += kParamThreads / 16) {
       const float2 d = part[r * C + ch];
       a1 += d.x;
       a2 += d.y;
     }
-  red[threadIdx.x] = make_double2(a1, a2);
+  for (int o = 16; o < 64; o <<= 1) {
+    a1 += __shfl_xor(a1, o);
+    a2 += __shfl_xor(a2, o);
+  }
+  if (threadIdx.x % 64 < 16) red[threadIdx.x / 64 * 16 + threadIdx.x % 16] = make_double2(a1, a2);
   __syncthreads();
-  if (q == 0 && ch < C) {
-    for (int k = 1; k < 4; ++k) {
-      a1 += red[k * 64 + threadIdx.x].x;
-      a2 += red[k * 64 + threadIdx.x].y;
+  if (threadIdx.x < 16 && ch < C) {
+    a1 = a2 = 0;
+    for (int k = 0; k < kParamThreads / 64; ++k) {
+      a1 += red[k * 16 + threadIdx.x].x;
+      a2 += red[k * 16 + threadIdx.x].y;
     }
     if (splits > 1) {
       sums[(int64_t)s * C + ch] = make_double2(a1, a2);
@@ -341,7 +364,7 @@ __global__ __launch_bounds__(64) void k_gn_bwd_params_sum(int C, int splits, con
   if (dw) dw[ch] = (float)a2;
 }
 
-template <typename T, int V, int ACT>
+template <typename T, int V, int ACT, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GnArgs p, const T *x, const T *dy,
                                                            const float *stats, const float2 *coef,
                                                            T *dx) {
@@ -351,15 +374,18 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_apply(GnArgs p, const T *x,
   if (r >= p.rows || v >= p.cv) return;
   const int t1 = min(p.T, (s + 1) * p.slab);
   const int len = min(t1, max(valid_length(p.lengths, b, p.T), 0));
-  const Channels<V> u(p, stats, b, v * V);
-  const float2 m = coef[(int64_t)b * p.G + v * V / p.Cg];
+  const Channels<V, ONE> u(p, stats, b, v * V);
+  float2 m[ONE ? 1 : V];
+#pragma unroll
+  for (int i = 0; i < (ONE ? 1 : V); ++i) m[i] = coef[(int64_t)b * p.G + (v * V + i) / p.Cg];
   const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
   auto one = [&](int t, Pack<T, V> d, const Pack<T, V> &e) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float h = ((float)d.v[i] - u.mean) * u.rstd;
+      const float h = u.h((float)d.v[i], i);
       const float dh = (float)e.v[i] * act_slope<ACT>(h * u.w[i] + u.b[i]) * u.w[i];
-      d.v[i] = (T)(u.rstd * (dh - m.x - h * m.y));
+      const int k = ONE ? 0 : i;
+      d.v[i] = (T)(u.rstd[k] * (dh - m[k].x - h * m[k].y));
     }
     *reinterpret_cast<Pack<T, V> *>(dx + base + (int64_t)t * p.C) = d;
   };
@@ -609,11 +635,11 @@ semicrf_status_t check(const semicrf_groupnorm_shape_t *s) {
 }
 
 // Channels of a thread: 16 bytes of them, or the largest power of two below
-// that divides a group and that every pointer is aligned for.
+// that divides a row and that every pointer is aligned for.
 int vector_width(const semicrf_groupnorm_shape_t *s, const void *const *ptrs, int n) {
-  const int size = elem_size(s->dtype), Cg = s->C / s->G;
+  const int size = elem_size(s->dtype);
   int V = 16 / size;
-  while (V > 1 && Cg % V) V /= 2;
+  while (V > 1 && s->C % V) V /= 2;
   for (int i = 0; i < n; ++i)
     while (V > 1 && (uintptr_t)ptrs[i] % (V * size)) V /= 2;
   return V;
@@ -679,11 +705,13 @@ int small_width(const semicrf_groupnorm_shape_t *s, const void *const *ptrs, int
   return V;
 }
 
-// Rows of partials of the parameters' gradients, and how many workgroups of
-// k_gn_bwd_params share them: 64 rows each at least, 64 at most.
+// Workgroups that share the rows of partials of the parameters' gradients: one
+// up to 4096 rows (eight of its loops of eight loads: about 5 us, as much as
+// the second launch that more of them need), 64 at most.
 int param_splits(int64_t rows) {
-  const int64_t n = rows / 64;
-  return n < 1 ? 1 : n > 64 ? 64 : (int)n;
+  if (rows <= 4096) return 1;
+  const int64_t n = rows / 2048;
+  return n > 64 ? 64 : (int)n;
 }
 size_t param_bytes(const semicrf_groupnorm_shape_t *s, int64_t rows) {
   const int n = param_splits(rows);
@@ -698,26 +726,28 @@ size_t need(const semicrf_groupnorm_shape_t *s, int backward) {
   }
   size_t n = 0;
   for (int V = 1; V <= 8; V *= 2) {
-    if ((s->C / s->G) % V) break;
+    if (s->C % V) break;
     const GnArgs p = args(s, V);
+    const int pairs = (s->C / s->G) % V ? p.C : p.cv;
     size_t m;
     if (backward)
       m = align256((size_t)p.B * p.slabs * p.C * sizeof(float2)) +
           param_bytes(s, (int64_t)p.B * p.slabs) + align256((size_t)p.B * p.G * sizeof(float2));
     else
-      m = align256((size_t)p.B * p.slabs * p.cv * sizeof(double2));
+      m = align256((size_t)p.B * p.slabs * pairs * sizeof(double2));
     if (m > n) n = m;
   }
   return n;
 }
 
-template <typename T, int V, int ACT>
+template <typename T, int V, int ACT, bool ONE>
 semicrf_status_t run_fwd(const GnArgs &p, const void *x, void *y, float *stats, void *ws,
                          hipStream_t st) {
   const unsigned grid = (unsigned)p.B * p.slabs * p.tiles;
-  k_gn_sums<T, V><<<grid, kThreads, 0, st>>>(p, (const T *)x, (double2 *)ws);
-  k_gn_stats<T><<<(unsigned)p.B * p.G, kThreads, 0, st>>>(p, V, (const T *)x, (const double2 *)ws, stats);
-  k_gn_apply<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, stats, (T *)y);
+  k_gn_sums<T, V, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, (double2 *)ws);
+  k_gn_stats<T><<<(unsigned)p.B * p.G, kThreads, 0, st>>>(p, ONE ? p.cv : p.C, (const T *)x,
+                                                         (const double2 *)ws, stats);
+  k_gn_apply<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, stats, (T *)y);
   return launch_status();
 }
 
@@ -725,12 +755,12 @@ semicrf_status_t run_fwd(const GnArgs &p, const void *x, void *y, float *stats, 
 void run_params(int C, int64_t rows, const float2 *part, double2 *sums, float *dw, float *db,
                 hipStream_t st) {
   if (!dw && !db) return;
-  const int splits = param_splits(rows), tiles = (C + 63) / 64;
-  k_gn_bwd_params<<<(unsigned)(tiles * splits), 256, 0, st>>>(C, rows, splits, part, sums, dw, db);
-  if (splits > 1) k_gn_bwd_params_sum<<<tiles, 64, 0, st>>>(C, splits, sums, dw, db);
+  const int splits = param_splits(rows), tiles = (C + 15) / 16;
+  k_gn_bwd_params<<<(unsigned)(tiles * splits), kParamThreads, 0, st>>>(C, rows, splits, part, sums, dw, db);
+  if (splits > 1) k_gn_bwd_params_sum<<<(C + 63) / 64, 64, 0, st>>>(C, splits, sums, dw, db);
 }
 
-template <typename T, int V, int ACT>
+template <typename T, int V, int ACT, bool ONE>
 semicrf_status_t run_bwd(const GnArgs &p, const void *x, const void *dy, const float *stats,
                          void *dx, float *dw, float *db, void *ws, size_t sums_bytes,
                          hipStream_t st) {
@@ -740,10 +770,11 @@ semicrf_status_t run_bwd(const GnArgs &p, const void *x, const void *dy, const f
   w += align256((size_t)p.B * p.slabs * p.C * sizeof(float2));
   double2 *sums = (double2 *)w;
   float2 *coef = (float2 *)(w + sums_bytes);
-  k_gn_bwd_sums<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats, part);
+  k_gn_bwd_sums<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats,
+                                                           part);
   k_gn_bwd_group<<<(unsigned)p.B * p.G, kThreads, 0, st>>>(p, part, coef);
-  k_gn_bwd_apply<T, V, ACT><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats, coef,
-                                                       (T *)dx);
+  k_gn_bwd_apply<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats,
+                                                            coef, (T *)dx);
   run_params(p.C, (int64_t)p.B * p.slabs, part, sums, dw, db, st);
   return launch_status();
 }
@@ -784,7 +815,9 @@ struct Fwd {
   hipStream_t st;
   template <typename T, int V, int ACT>
   semicrf_status_t run() {
-    if (!small.ns) return run_fwd<T, V, ACT>(p, x, y, stats, ws, st);
+    if (!small.ns)
+      return p.Cg % V ? run_fwd<T, V, ACT, V == 1>(p, x, y, stats, ws, st)
+                      : run_fwd<T, V, ACT, true>(p, x, y, stats, ws, st);
     const unsigned grid = (unsigned)((small.g.B + small.ns - 1) / small.ns);
     k_gn_small<T, V, ACT><<<grid, kThreads, small_lds(small, 1), st>>>(small, (const T *)x,
                                                                        (T *)y, stats);
@@ -805,7 +838,8 @@ struct Bwd {
   template <typename T, int V, int ACT>
   semicrf_status_t run() {
     if (!small.ns)
-      return run_bwd<T, V, ACT>(p, x, dy, stats, dx, dw, db, ws, sums_bytes, st);
+      return p.Cg % V ? run_bwd<T, V, ACT, V == 1>(p, x, dy, stats, dx, dw, db, ws, sums_bytes, st)
+                      : run_bwd<T, V, ACT, true>(p, x, dy, stats, dx, dw, db, ws, sums_bytes, st);
     const unsigned grid = (unsigned)((small.g.B + small.ns - 1) / small.ns);
     float2 *part = dw || db ? (float2 *)ws : nullptr;
     k_gn_small_bwd<T, V, ACT><<<grid, kThreads, small_lds(small, 2), st>>>(

@@ -255,3 +255,15 @@ def test_empty_and_refusals():
                      ((x[:, None], 2), dict(lengths=torch.zeros(2, dtype=torch.int32, device=DEV)))):
         with pytest.raises(ValueError):
             encoder.group_norm(*args, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("C,G", [(96, 32), (24, 24), (40, 8), (12, 1), (50, 2), (72, 8)])
+def test_vectors_that_groups_part(C, G, dtype):
+    """Long sequences whose groups are not whole vectors of channels."""
+    compare(2, 1500, C, G, dtype, lengths=[1500, 901], poison=True, seed=C)
+
+
+def test_many_rows_of_partials():
+    """Parameters' gradients over more workgroups than one reduction takes."""
+    compare(9000, 1, 520, 8, "bf16", name="none", seed=21)
