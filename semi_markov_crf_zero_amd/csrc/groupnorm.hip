@@ -35,6 +35,7 @@ struct GnArgs {
   int rows;   // positions a workgroup takes at once = kThreads / cvt
   int slab;   // positions of one workgroup
   int slabs;  // of a sequence
+  int lanes;  // threads that sum one group's partials
   float eps;
   const int32_t *lengths;
   const float *weight, *bias;
@@ -149,13 +150,15 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnArgs p, const T *x, doub
   }
 }
 
-// Sum of two values over the workgroup, in a fixed order; all threads get it.
-__device__ __forceinline__ double2 block_sum(double a, double b) {
-  __shared__ double2 red[kThreads / 64];
-  for (int o = 32; o; o >>= 1) {
+// Sums of two values over teams of `lanes` neighbouring threads (a power of
+// two up to 64, or the whole workgroup), in a fixed order; all of them get it.
+__device__ __forceinline__ double2 team_sum(double a, double b, int lanes) {
+  for (int o = (lanes < 64 ? lanes : 64) / 2; o; o >>= 1) {
     a += __shfl_xor(a, o);
     b += __shfl_xor(b, o);
   }
+  if (lanes <= 64) return make_double2(a, b);
+  __shared__ double2 red[kThreads / 64];
   if (threadIdx.x % 64 == 0) red[threadIdx.x / 64] = make_double2(a, b);
   __syncthreads();
   double2 s = red[0];
@@ -166,36 +169,38 @@ __device__ __forceinline__ double2 block_sum(double a, double b) {
   return s;
 }
 
-// One workgroup per sequence and group: mean and 1/sqrt(var + eps).
+// mean and 1/sqrt(var + eps) from the sums of x - pivot and its square over m
+// values; 0, 0 of nothing, NaN of a length that is none (m < 0).
+__device__ __forceinline__ float2 stats_of(double2 sum, int64_t m, float pivot, float eps) {
+  if (m <= 0) {
+    const float x = m < 0 ? __builtin_nanf("") : 0.f;
+    return make_float2(x, x);
+  }
+  const double n = 1.0 / (double)m, mean = sum.x * n, var = sum.y * n - mean * mean;
+  const double v = (var > 0 ? var : var == var ? 0.0 : var) + (double)eps;
+  return make_float2((float)(pivot + mean), 1.f / sqrtf((float)v));
+}
+
+// A team of p.lanes threads per sequence and group: its statistics.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void k_gn_stats(GnArgs p, int pairs, const T *x, const double2 *part,
-                                                 float *stats) {
-  const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
+__global__ __launch_bounds__(kThreads) void k_gn_stats(GnArgs p, int pairs, const T *x,
+                                                       const double2 *part, float *stats) {
+  const int64_t bg = blockIdx.x * (int64_t)(kThreads / p.lanes) + threadIdx.x / p.lanes;
+  const int b = (int)(bg / p.G), g = (int)(bg % p.G), lane = threadIdx.x % p.lanes;
+  if (b >= p.B) return;
   const int vg = pairs / p.G;  // pairs of a group
   const int len = valid_length(p.lengths, b, p.T);
   double sum = 0, sq = 0;
 #pragma unroll 4
-  for (int e = threadIdx.x; e < p.slabs * vg; e += kThreads) {
+  for (int e = lane; e < p.slabs * vg; e += p.lanes) {
     const double2 d = part[((int64_t)b * p.slabs + e / vg) * pairs + g * vg + e % vg];
     sum += d.x;
     sq += d.y;
   }
-  const double2 all = block_sum(sum, sq);
-  sum = all.x;
-  sq = all.y;
-  if (threadIdx.x == 0) {
-    float mean = 0.f, rstd = 0.f;
-    if (len > 0) {
-      const double n = (double)len * p.Cg, m = sum / n;
-      mean = (float)((double)(float)x[(int64_t)b * p.T * p.C + g * p.Cg] + m);
-      const double var = sq / n - m * m;
-      rstd = (float)(1.0 / sqrt((var > 0 ? var : var == var ? 0.0 : var) + (double)p.eps));
-    } else if (len < 0) {
-      mean = rstd = __builtin_nanf("");
-    }
-    stats[2 * ((int64_t)b * p.G + g)] = mean;
-    stats[2 * ((int64_t)b * p.G + g) + 1] = rstd;
-  }
+  const double2 all = team_sum(sum, sq, p.lanes);
+  if (lane == 0)
+    reinterpret_cast<float2 *>(stats)[bg] =
+        stats_of(all, (int64_t)len * p.Cg, (float)x[(int64_t)b * p.T * p.C + g * p.Cg], p.eps);
 }
 
 template <typename T, int V, int ACT, bool ONE>
@@ -292,23 +297,26 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, 
   }
 }
 
-// One workgroup per sequence and group: mean(d), mean(d h) of the group.
-__global__ __launch_bounds__(kThreads) void k_gn_bwd_group(GnArgs p, const float2 *part, float2 *coef) {
-  const int b = blockIdx.x / p.G, g = blockIdx.x % p.G;
+// A team of p.lanes threads per sequence and group: its mean(d), mean(d h).
+__global__ __launch_bounds__(kThreads) void k_gn_bwd_group(GnArgs p, const float2 *part,
+                                                           float2 *coef) {
+  const int64_t bg = blockIdx.x * (int64_t)(kThreads / p.lanes) + threadIdx.x / p.lanes;
+  const int b = (int)(bg / p.G), g = (int)(bg % p.G), lane = threadIdx.x % p.lanes;
+  if (b >= p.B) return;
   const int len = valid_length(p.lengths, b, p.T);
   double m1 = 0, m2 = 0;
 #pragma unroll 4
-  for (int e = threadIdx.x; e < p.slabs * p.Cg; e += kThreads) {
+  for (int e = lane; e < p.slabs * p.Cg; e += p.lanes) {
     const int ch = g * p.Cg + e % p.Cg;
     const float2 d = part[((int64_t)b * p.slabs + e / p.Cg) * p.C + ch];
     const double w = p.weight ? p.weight[ch] : 1.0;
     m1 += w * d.x;
     m2 += w * d.y;
   }
-  const double2 all = block_sum(m1, m2);
-  if (threadIdx.x == 0) {
-    const double n = (double)max(len, 1) * p.Cg;
-    coef[(int64_t)b * p.G + g] = make_float2((float)(all.x / n), (float)(all.y / n));
+  const double2 all = team_sum(m1, m2, p.lanes);
+  if (lane == 0) {
+    const double n = 1.0 / ((double)max(len, 1) * p.Cg);
+    coef[bg] = make_float2((float)(all.x * n), (float)(all.y * n));
   }
 }
 
@@ -450,14 +458,6 @@ struct Walk {
   }
 };
 
-constexpr int kTeam = 8;  // lanes that sum one group
-
-__device__ __forceinline__ double team_sum(double x) {
-#pragma unroll
-  for (int o = kTeam / 2; o; o >>= 1) x += __shfl_xor(x, o);
-  return x;
-}
-
 // LDS: n floats of data (twice backwards), weight and bias, a pair a group.
 __device__ __forceinline__ void load_params(const GnArgs &p, float *w, float *b) {
   for (int c = threadIdx.x; c < p.C; c += kThreads) {
@@ -484,31 +484,24 @@ __global__ __launch_bounds__(kThreads) void k_gn_small(SmallArgs p, const T *x, 
     for (int i = 0; i < V; ++i) xs[e + i] = (float)d.v[i];
   }
   __syncthreads();
-  const int lane = threadIdx.x % kTeam;
-  for (int pair = threadIdx.x / kTeam; pair < ns * p.g.G; pair += kThreads / kTeam) {
+  const int lanes = p.g.lanes, lane = threadIdx.x % lanes;
+  for (int pair = threadIdx.x / lanes; pair < ns * p.g.G; pair += kThreads / lanes) {
     const int s = pair / p.g.G, g = pair % p.g.G;
-    const int len = valid_length(p.g.lengths, b0 + s, p.g.T), m = max(len, 0) * p.g.Cg;
+    const int len = valid_length(p.g.lengths, b0 + s, p.g.T), m = len * p.g.Cg;
     const float *u = xs + s * p.TC + g * p.g.Cg;
+    const float pivot = u[0];
     double sum = 0, sq = 0;
-    for (int j = lane; j < m; j += kTeam) {
-      const int t = div_small(j, p.mCg);
-      sum += u[t * p.g.C + j - t * p.g.Cg];
-    }
-    const double mean = team_sum(sum) / max(m, 1);
-    for (int j = lane; j < m; j += kTeam) {
-      const int t = div_small(j, p.mCg);
-      const double d = u[t * p.g.C + j - t * p.g.Cg] - mean;
+    for (int j = lane; j < m; j += lanes) {
+      const int t = p.g.T == 1 ? 0 : div_small(j, p.mCg);
+      const double d = u[t * p.g.C + j - t * p.g.Cg] - pivot;
+      sum += d;
       sq += d * d;
     }
-    const double var = team_sum(sq) / max(m, 1);
+    const double2 all = team_sum(sum, sq, lanes);
     if (lane == 0) {
-      const float none = len < 0 ? __builtin_nanf("") : 0.f;
-      const float a = m ? (float)mean : none;
-      const float r = m ? (float)(1.0 / sqrt(var + (double)p.g.eps)) : none;
-      st[2 * pair] = a;
-      st[2 * pair + 1] = r;
-      stats[2 * ((int64_t)b0 * p.g.G + pair)] = a;
-      stats[2 * ((int64_t)b0 * p.g.G + pair) + 1] = r;
+      const float2 a = stats_of(all, m, pivot, p.g.eps);
+      reinterpret_cast<float2 *>(st)[pair] = a;
+      reinterpret_cast<float2 *>(stats)[(int64_t)b0 * p.g.G + pair] = a;
     }
   }
   __syncthreads();
@@ -559,23 +552,23 @@ __global__ __launch_bounds__(kThreads) void k_gn_small_bwd(SmallArgs p, const T 
     }
   }
   __syncthreads();
-  const int lane = threadIdx.x % kTeam;
-  for (int pair = threadIdx.x / kTeam; pair < ns * p.g.G; pair += kThreads / kTeam) {
+  const int lanes = p.g.lanes, lane = threadIdx.x % lanes;
+  for (int pair = threadIdx.x / lanes; pair < ns * p.g.G; pair += kThreads / lanes) {
     const int s = pair / p.g.G, g = pair % p.g.G;
     const int m = max(valid_length(p.g.lengths, b0 + s, p.g.T), 0) * p.g.Cg;
     const int at = s * p.TC + g * p.g.Cg;
     double m1 = 0, m2 = 0;
-    for (int j = lane; j < m; j += kTeam) {
-      const int t = div_small(j, p.mCg), c = j - t * p.g.Cg;
+    for (int j = lane; j < m; j += lanes) {
+      const int t = p.g.T == 1 ? 0 : div_small(j, p.mCg), c = j - t * p.g.Cg;
       const float d = dz[at + t * p.g.C + c] * w[g * p.g.Cg + c];
       m1 += d;
       m2 += (double)d * hs[at + t * p.g.C + c];
     }
-    m1 = team_sum(m1) / max(m, 1);
-    m2 = team_sum(m2) / max(m, 1);
+    const double2 all = team_sum(m1, m2, lanes);
     if (lane == 0) {
-      st[2 * pair] = (float)m1;
-      st[2 * pair + 1] = (float)m2;
+      const float n = 1.f / (float)max(m, 1);
+      st[2 * pair] = (float)all.x * n;
+      st[2 * pair + 1] = (float)all.y * n;
     }
   }
   __syncthreads();
@@ -665,6 +658,18 @@ GnArgs args(const semicrf_groupnorm_shape_t *s, int V) {
   return p;
 }
 
+// Threads that sum `entries` values: about four each, 64 at most, or the
+// workgroup for many.
+int team(int64_t entries) {
+  int n = 1;
+  while (n < 64 && 4 * n < entries) n *= 2;
+  return entries > 4096 ? kThreads : n;
+}
+unsigned team_grid(const GnArgs &p) {
+  const int64_t teams = kThreads / p.lanes;
+  return (unsigned)(((int64_t)p.B * p.G + teams - 1) / teams);
+}
+
 // Short sequences go NS at a time through LDS: about kStretch elements a
 // workgroup, NS a power of two so that a stretch is a whole number of
 // vectors; where 64 KB of LDS hold what the backward pass keeps of one.
@@ -679,6 +684,10 @@ SmallArgs small_args(const semicrf_groupnorm_shape_t *s) {
   p.mTC = magic(p.TC);
   p.mC = magic(s->C);
   p.mCg = magic(p.g.Cg);
+  // a team for each group; wider ones where the groups are few
+  const int n = team((int64_t)s->T * p.g.Cg);
+  p.g.lanes = n > 64 ? 64 : n;
+  while (p.g.lanes < 64 && 2 * p.g.lanes * p.ns * s->G <= kThreads) p.g.lanes *= 2;
   return p;
 }
 // LDS of a short-sequence workgroup with `arrays` copies of its data.
@@ -741,11 +750,12 @@ size_t need(const semicrf_groupnorm_shape_t *s, int backward) {
 }
 
 template <typename T, int V, int ACT, bool ONE>
-semicrf_status_t run_fwd(const GnArgs &p, const void *x, void *y, float *stats, void *ws,
+semicrf_status_t run_fwd(GnArgs p, const void *x, void *y, float *stats, void *ws,
                          hipStream_t st) {
   const unsigned grid = (unsigned)p.B * p.slabs * p.tiles;
   k_gn_sums<T, V, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, (double2 *)ws);
-  k_gn_stats<T><<<(unsigned)p.B * p.G, kThreads, 0, st>>>(p, ONE ? p.cv : p.C, (const T *)x,
+  p.lanes = team((int64_t)p.slabs * (ONE ? p.cv : p.C) / p.G);
+  k_gn_stats<T><<<team_grid(p), kThreads, 0, st>>>(p, ONE ? p.cv : p.C, (const T *)x,
                                                          (const double2 *)ws, stats);
   k_gn_apply<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, stats, (T *)y);
   return launch_status();
@@ -761,7 +771,7 @@ void run_params(int C, int64_t rows, const float2 *part, double2 *sums, float *d
 }
 
 template <typename T, int V, int ACT, bool ONE>
-semicrf_status_t run_bwd(const GnArgs &p, const void *x, const void *dy, const float *stats,
+semicrf_status_t run_bwd(GnArgs p, const void *x, const void *dy, const float *stats,
                          void *dx, float *dw, float *db, void *ws, size_t sums_bytes,
                          hipStream_t st) {
   const unsigned grid = (unsigned)p.B * p.slabs * p.tiles;
@@ -772,7 +782,8 @@ semicrf_status_t run_bwd(const GnArgs &p, const void *x, const void *dy, const f
   float2 *coef = (float2 *)(w + sums_bytes);
   k_gn_bwd_sums<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats,
                                                            part);
-  k_gn_bwd_group<<<(unsigned)p.B * p.G, kThreads, 0, st>>>(p, part, coef);
+  p.lanes = team((int64_t)p.slabs * p.Cg);
+  k_gn_bwd_group<<<team_grid(p), kThreads, 0, st>>>(p, part, coef);
   k_gn_bwd_apply<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats,
                                                             coef, (T *)dx);
   run_params(p.C, (int64_t)p.B * p.slabs, part, sums, dw, db, st);
