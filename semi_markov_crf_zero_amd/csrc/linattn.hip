@@ -51,18 +51,28 @@ __global__ __launch_bounds__(kThreads) void k_linattn_scan(LaArgs p) {
   const int b = (int)(bh / p.H), h = (int)(bh % p.H);
   const int len = max(valid_length(p.lengths, b, p.T), 0);
   float *x = p.xs + bh * (p.nseg - 1) * n + e % n;
-  float acc = p.x_in ? p.x_in[e] : 0.f;
-  const float gd = p.log_decay[h], whole = expf(gd * p.seg);
-  // eight loads at a time: the sum is a chain, the loads are not
-  for (int s0 = 0; s0 < p.nseg - 1; s0 += 8) {
-    float part[8];
+  // in float64: the same factor again and again (see Decays)
+  double acc = p.x_in ? p.x_in[e] : 0.f;
+  const double gd = p.log_decay[h], whole = exp(gd * p.seg);
+  const int full = len / p.seg, left = len % p.seg;  // segments; positions of the one after
+  const double rest = left ? exp(gd * left) : 1.0;
+  // sixteen loads at a time, the next ones on their way: the sum is a chain,
+  // the loads are not (past the end the last one again)
+  constexpr int N = 16;
+  const int last = p.nseg - 2;
+  float part[N], next[N];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) part[k] = s0 + k < p.nseg - 1 ? x[(s0 + k) * n] : 0.f;
+  for (int k = 0; k < N; ++k) next[k] = x[min(k, last) * n];
+  for (int s0 = 0; s0 <= last; s0 += N) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int s = s0 + k, m = min(max(len - s * p.seg, 0), p.seg);
-      acc = (m == p.seg ? whole : m ? expf(gd * m) : 1.f) * acc + part[k];
-      if (s < p.nseg - 1) x[s * n] = acc;
+    for (int k = 0; k < N; ++k) part[k] = next[k];
+#pragma unroll
+    for (int k = 0; k < N; ++k) next[k] = x[min(s0 + N + k, last) * n];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int s = s0 + k;
+      acc = (s < full ? whole : s == full ? rest : 1.0) * acc + part[k];
+      if (s <= last) x[s * n] = (float)acc;
     }
   }
 }
@@ -198,7 +208,7 @@ int resident(int Da, int Dc, int dtype) {
   const int NP = linattn_parts(dtype), NR = NP == 3 ? 3 : 2, L = linattn_chunk(NP);
   const int DA = Da <= 128 ? (Da + 31) / 32 * 32 : 256;
   const int NW = DA > 128 ? 4 : linattn_waves(Dc, true);
-  const int lds = 2 * L * (NP * (2 * DA + 4 + 16 * NW + 16) + NR * (L + 4)) + 4 * (6 * L + 2);
+  const int lds = 2 * L * (NP * (2 * DA + 4 + 16 * NW + 16) + NR * (L + 4)) + 4 * (7 * L + 3);
   const int by_lds = (int)(163840 / lds), occ = linattn_occupancy(DA, NW);
   const int by_waves = NW < 4 ? 4 * occ / NW : occ / ((NW + 3) / 4);
   const int n = by_lds < by_waves ? by_lds : by_waves;

@@ -267,22 +267,31 @@ __device__ __forceinline__ void stage(bf16 *lds, const T *src, int64_t st, int D
   }
 }
 
-// The decays a workgroup uses, with the pass's factors in them; entries of
-// negative powers are 0, so masked places need no branch.
+// The decays a workgroup uses, with the pass's factors in them, from float64
+// exponentials; entries of negative powers are 0, so masked places need no
+// branch.  X is multiplied by e^{g n} once a chunk, thousands of times in a
+// long sequence: there e^{g n} is a sum of two float32, or its own rounding,
+// the same every time, would add up.
 template <int L>
 struct Decays {
-  float x[L + 1];       // e^{g n}: of X over n positions
-  float p[2 * L];       // p_scale e^{g (n - L)}: of P
-  float read[L];        // x_scale e^{g (i + off)}: of X read by position i
-  float add[2 * L + 1]; // add_scale e^{g (n - L)}: of what a position adds to X
+  float x[L + 1], x_low[L + 1];  // e^{g n}: of X over n positions
+  float p[2 * L];                // p_scale e^{g (n - L)}: of P
+  float read[L];                 // x_scale e^{g (i + off)}: of X read by position i
+  float add[2 * L + 1];          // add_scale e^{g (n - L)}: of what a position adds to X
 
+  // all threads of the workgroup; the caller's next barrier ends it
   __device__ __forceinline__ void fill(const LaArgs &a, float g) {
-    auto e = [&](int n) { return n < 0 ? 0.f : n ? expf(g * n) : 1.f; };
+    for (int n = threadIdx.x; n <= L; n += blockDim.x) {
+      const double e = n ? exp((double)g * n) : 1.0;
+      x[n] = (float)e;
+      x_low[n] = (float)(e - (double)(float)e);
+    }
+    __syncthreads();
     for (int n = threadIdx.x; n < 2 * L + 1; n += blockDim.x) {
-      add[n] = a.add_scale * e(n - L);
-      if (n <= L) x[n] = e(n);
-      if (n < 2 * L) p[n] = a.p_scale * e(n - L);
-      if (n < L) read[n] = a.x_scale * e(n + a.off);
+      const float e = n < L ? 0.f : x[n - L];
+      add[n] = a.add_scale * e;
+      if (n < 2 * L) p[n] = a.p_scale * e;
+      if (n < L) read[n] = a.x_scale * x[n + a.off];
     }
   }
 };
@@ -294,10 +303,11 @@ __device__ __forceinline__ void add_chunk(f4 *X, const bf16 *Bm, const Frag<NP> 
                                           const Decays<L> &dec, int n, int off, int lane) {
   constexpr int DA = 32 * KB;
   const float *add = dec.add + L + n - off - 4 * (lane >> 4);
+  const float all = dec.x[n], low = dec.x_low[n];
 #pragma unroll
   for (int k = 0; k < 2 * KB; ++k)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) X[k][r] *= dec.x[n];
+    for (int r = 0; r < 4; ++r) X[k][r] = fmaf(X[k][r], low, X[k][r] * all);
 #pragma unroll
   for (int jb = 0; jb < L / 32; ++jb) {
     float x[8];

@@ -439,3 +439,19 @@ def test_backward_without_the_forward_call():
                    ws.data_ptr(), n)
     for g, w in zip(got, want):
         assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H", [(1 << 18, 1), (40000, 160)])
+def test_slow_decays_over_long_sequences(T, H, dtype):
+    """k = v = 1: every element of the state is sum_j e^{g j}, a closed form.
+    Each chunk (and segment) rounds it once, without a sign: 4 sqrt(n) 2^-24 of
+    it for the n roundings; e^{g 64} used as one float32 would put its own
+    rounding in thousands of times with one sign.  T = 40000 over 160 heads is
+    one segment or few."""
+    g = float(np.float32(-1.5 / T))
+    k = torch.ones((1, T, H, 16), dtype=TYPES[dtype], device=DEV)
+    _, last = encoder.linear_attention(k, k, k, torch.full((H,), g, device=DEV), return_state=True)
+    want = np.expm1(g * T) / np.expm1(g)
+    off = np.abs(last.cpu().double().numpy() / want - 1).max()
+    assert off <= 4 * np.sqrt(T / 32 + 64) * 2.0 ** -24, off
