@@ -663,7 +663,7 @@ GnArgs args(const semicrf_groupnorm_shape_t *s, int V) {
 int team(int64_t entries) {
   int n = 1;
   while (n < 64 && 4 * n < entries) n *= 2;
-  return entries > 4096 ? kThreads : n;
+  return entries > 256 ? kThreads : n;
 }
 unsigned team_grid(const GnArgs &p) {
   const int64_t teams = kThreads / p.lanes;
