@@ -81,6 +81,17 @@ typedef s4 __attribute__((address_space(3))) lds_s4;
 
 typedef unsigned u4 __attribute__((ext_vector_type(4)));
 
+// A lane's number as something new to the compiler: what follows from it is
+// then computed again in every chunk instead of being kept in registers all
+// along.  For the shapes that are short of them (workgroups of more than four
+// waves have 128 a lane): the load of a spilled register would wait for every
+// tile on its way.
+template <int DA, int NW>
+__device__ __forceinline__ int fresh(int lane) {
+  if (NW > 4 || DA > 96) asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 constexpr int kRange = 0x7fffffff;      // bytes a buffer descriptor reaches
 constexpr int kRawBuffer = 0x00027000;  // its last word: raw 32-bit data
 
@@ -213,20 +224,20 @@ struct Tile {
 
   // row i of the tile is row `row0 + step * i` (step +-1) from src, rows st
   // elements apart
-  __device__ __forceinline__ void fetch(const T *src, int st, int D, int n, int row0, int step,
-                                        int col0) {
+  __device__ __forceinline__ void fetch(int tid, const T *src, int st, int D, int n, int row0,
+                                        int step, int col0) {
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)src, 0, kRange, kRawBuffer);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int e = threadIdx.x + k * NT, i = e / per, c = col0 + e % per * VE;
+      const int e = tid + k * NT, i = e / per, c = col0 + e % per * VE;
       const int at = ((row0 + step * i) * st + c) * (int)sizeof(T);
       r[k] = __builtin_amdgcn_raw_buffer_load_b128(rsrc, i < n && c < D ? at : -1, 0, 0);
     }
   }
-  __device__ __forceinline__ void put(bf16 *lds) const {
+  __device__ __forceinline__ void put(int tid, bf16 *lds) const {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int e = threadIdx.x + k * NT, i = e / per, c = e % per * VE;
+      const int e = tid + k * NT, i = e / per, c = e % per * VE;
       if (all % NT && e >= all) break;
       const Pack<T, VE> y = __builtin_bit_cast(Pack<T, VE>, r[k]);
 #pragma unroll
@@ -352,8 +363,8 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
   auto fetch = [&](int t0) {
     const int n = min(L, hi - t0), row0 = p.rev ? n - 1 : 0;
     const int64_t base = p.rev ? len - t0 - n : t0;
-    tb.fetch(bb + base * p.b.st, (int)p.b.st, p.Da, n, row0, step, 0);
-    tc.fetch(c + base * p.c.st, (int)p.c.st, p.Dc, n, row0, step, c0);
+    tb.fetch(threadIdx.x, bb + base * p.b.st, (int)p.b.st, p.Da, n, row0, step, 0);
+    tc.fetch(threadIdx.x, c + base * p.c.st, (int)p.c.st, p.Dc, n, row0, step, c0);
   };
   if (VEC && lo < hi) fetch(lo);
   dec.fill(p, p.log_decay[h]);
@@ -361,8 +372,8 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
     const int n = min(L, hi - t0);
     __syncthreads();
     if (VEC) {
-      tb.put(Bm);
-      tc.put(C);
+      tb.put(threadIdx.x, Bm);
+      tc.put(threadIdx.x, C);
     } else {
       const int64_t first = p.rev ? len - 1 - t0 : t0;
       stage<T, NP, LB, DA, L, kThreads>(Bm, bb + first * p.b.st, step * p.b.st, p.Da, n, 0);
@@ -429,17 +440,19 @@ __global__ __launch_bounds__(64 * NW)
   // position not yet taken; `base` is the lowest position
   const int step = p.rev ? -1 : 1;
   auto fetch = [&](int t0) {
+    const int tid = fresh<DA, NW>(threadIdx.x);
     const int n = min(L, hi - t0), row0 = p.rev ? n - 1 : 0;
     const int64_t base = p.rev ? len - t0 - n : t0;
-    ta.fetch(a + base * p.a.st, (int)p.a.st, p.Da, n, row0, step, 0);
-    tb.fetch(bb + base * p.b.st, (int)p.b.st, p.Da, n, row0, step, 0);
-    tc.fetch(c + base * p.c.st, (int)p.c.st, p.Dc, n, row0, step, c0);
+    ta.fetch(tid, a + base * p.a.st, (int)p.a.st, p.Da, n, row0, step, 0);
+    tb.fetch(tid, bb + base * p.b.st, (int)p.b.st, p.Da, n, row0, step, 0);
+    tc.fetch(tid, c + base * p.c.st, (int)p.c.st, p.Dc, n, row0, step, c0);
   };
   auto stage_chunk = [&](int t0) {
     if (VEC) {
-      ta.put(A);
-      tb.put(Bm);
-      tc.put(C);
+      const int tid = fresh<DA, NW>(threadIdx.x);
+      ta.put(tid, A);
+      tb.put(tid, Bm);
+      tc.put(tid, C);
     } else {
       const int n = min(L, hi - t0);
       const int64_t first = p.rev ? len - 1 - t0 : t0;
@@ -479,31 +492,31 @@ __global__ __launch_bounds__(64 * NW)
   for (int t0 = lo; t0 < hi; t0 += L) {
     const int n = min(L, hi - t0);
     __syncthreads();
+    const int ln = fresh<DA, NW>(lane), g = ln >> 4, l16 = ln & 15;
     if (VEC && t0 + L < hi) fetch(t0 + L);
     Frag<NP> cf[L / 32];
 #pragma unroll
-    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col<NP, LC>(C, L * LC::row, 32 * jb, w, lane);
+    for (int jb = 0; jb < L / 32; ++jb) cf[jb] = frag_col<NP, LC>(C, L * LC::row, 32 * jb, w, ln);
     f4 O[NT];
     if (p.out) {
       // P: wave w its rows 16w.., the tiles up to the diagonal and, as P is
       // read 32 columns at a time, the one beside it (zeros, by the table).  A
       // tile is computed transposed: a lane then holds four neighbours of a
       // row of P
-#pragma unroll
       for (int it = w; it < NT; it += NW) {
         Frag<NP> af[KB];
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
-          af[kb] = frag_row<NP, LA>(A, L * LA::row, 16 * it, kb, lane);
+          af[kb] = frag_row<NP, LA>(A, L * LA::row, 16 * it, kb, ln);
         const int i = 16 * it + l16;
         const float *dp = dec.p + L + i - 4 * g;
 #pragma unroll
         for (int jt = 0; jt < NT; ++jt) {
-          if (jt > (it | 1)) break;
+          if (jt > (it | 1)) continue;
           f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
-            acc = mma<3>(frag_row<NP, LB>(Bm, L * DA, 16 * jt, kb, lane), af[kb], acc);
+            acc = mma<3>(frag_row<NP, LB>(Bm, L * DA, 16 * jt, kb, ln), af[kb], acc);
           f2 lo = {acc[0] * dp[-16 * jt], acc[1] * dp[-16 * jt - 1]};
           f2 hi = {acc[2] * dp[-16 * jt - 2], acc[3] * dp[-16 * jt - 3]};
 #pragma unroll
@@ -525,7 +538,7 @@ __global__ __launch_bounds__(64 * NW)
         const Frag<NR> xf = split<NR>(x);
 #pragma unroll
         for (int it = 0; it < NT; ++it)
-          O[it] = mma<NR>(xf, frag_row<NP, LA>(A, L * LA::row, 16 * it, kb, lane), O[it]);
+          O[it] = mma<NR>(xf, frag_row<NP, LA>(A, L * LA::row, 16 * it, kb, ln), O[it]);
       }
 #pragma unroll
       for (int it = 0; it < NT; ++it) {
@@ -534,7 +547,7 @@ __global__ __launch_bounds__(64 * NW)
         for (int r = 0; r < 4; ++r) O[it][r] *= d;
       }
     }
-    add_chunk<NP, KB, L>(X, Bm, cf, dec, n, p.off, lane);
+    add_chunk<NP, KB, L>(X, Bm, cf, dec, n, p.off, ln);
     __syncthreads();
     if (p.out) {
       const int64_t first = p.rev ? len - 1 - t0 : t0;
@@ -544,7 +557,7 @@ __global__ __launch_bounds__(64 * NW)
         const int i = 16 * it + l16;
 #pragma unroll
         for (int jb = 0; jb <= it / 2; ++jb)
-          O[it] = mma<NR>(cf[jb], frag_row<NR, LP>(P, L * LP::row, 16 * it, jb, lane), O[it]);
+          O[it] = mma<NR>(cf[jb], frag_row<NR, LP>(P, L * LP::row, 16 * it, jb, ln), O[it]);
         if (i < n && col < p.Dc) {
           OT *to = out + (first + step * i) * sot + col;
           if (VEC) {
