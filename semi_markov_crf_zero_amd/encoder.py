@@ -122,14 +122,20 @@ def _linattn_check(q, k, v, log_decay, step):
     """Checks q, k, v ([B, T, heads, D], or [B, heads, D] for a step) and
     log_decay; B, T, H, Hq, Hk, Hv, Dk, Dv, dtype."""
     _check_device(q)
-    dev, dtype, lead = q.device, q.dtype, q.shape[:-2]
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dim() != (3 if step else 4) or t.device != dev or t.dtype != dtype:
+    dev, dtype = q.device, q.dtype
+    dims = 3 if step else 4
+    for name, t in (("k", k), ("v", v), ("q", q)):
+        if t.dim() != dims or t.dtype != dtype or t.device != dev:
             raise ValueError("%s must be a [B, %sheads, D] %s tensor on %s"
                              % (name, "" if step else "T, ", dtype, dev))
-        if t.shape[:-2] != lead:
-            raise ValueError("q, k and v must have the same B%s" % ("" if step else " and T"))
-    (Hq, Dk), (Hk, Dk2), (Hv, Dv) = q.shape[-2:], k.shape[-2:], v.shape[-2:]
+    if step:
+        (B, Hq, Dk), (Bk, Hk, Dk2), (Bv, Hv, Dv), T = q.shape, k.shape, v.shape, 1
+    else:
+        (B, T, Hq, Dk), (Bk, Tk, Hk, Dk2), (Bv, Tv, Hv, Dv) = q.shape, k.shape, v.shape
+        if Tk != T or Tv != T:
+            raise ValueError("q, k and v must have the same T")
+    if Bk != B or Bv != B:
+        raise ValueError("q, k and v must have the same B")
     if Dk2 != Dk:
         raise ValueError("q and k must have the same width")
     if not (1 <= Dk <= MAX_HEAD and 1 <= Dv <= MAX_HEAD):
@@ -141,7 +147,7 @@ def _linattn_check(q, k, v, log_decay, step):
     if log_decay.requires_grad:
         raise ValueError("log_decay is a constant of the model: it gets no gradient")
     _check("log_decay", log_decay, dev, torch.float32, (H,))
-    return lead[0], 1 if step else lead[1], H, Hq, Hk, Hv, Dk, Dv, DTYPES[dtype]
+    return B, T, H, Hq, Hk, Hv, Dk, Dv, DTYPES[dtype]
 
 
 def _strides(t):

@@ -28,7 +28,7 @@ BLOCK = 256  # elements that share one scale of an 8-bit state
 MOMENT_TYPES = {torch.float8_e4m3fn: 0, torch.uint8: 1}  # codes of m; of the root of v
 
 
-_is_none, _dtype = (lambda g: g is None), operator.attrgetter("dtype")
+_dtype = operator.attrgetter("dtype")
 _numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
 _get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
@@ -162,6 +162,7 @@ class AdamWPlan:
             raise bd.SemiCRFError(rc, "semicrf_adamw_table")
         self.table = self.host.to(self.dev)
         self._host, self._device = self.host.data_ptr(), self.table.data_ptr()
+        self._dtypes = [], b""
 
     def run(self, grads, step: int, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
             eps: float = 1e-8, weight_decay: float = 1e-2, grad_scale=None):
@@ -173,16 +174,22 @@ class AdamWPlan:
         if len(grads) != len(self.params):
             raise ValueError("need one gradient for each of the %d parameters" % len(self.params))
         there, numels = grads, self.numels
-        if any(map(_is_none, grads)):
+        try:
+            dtypes = list(map(_dtype, grads))
+        except AttributeError:  # None among them
             there = [g for g in grads if g is not None]
             numels = [n for n, g in zip(numels, grads) if g is not None]
-        dtypes = list(map(_dtype, there))
-        if not (set(dtypes) <= DTYPES.keys() and list(map(_numel, there)) == numels
+            dtypes = list(map(_dtype, there))
+        if dtypes != self._dtypes[0]:  # the types' codes, worked out once for a list of types
+            if not set(dtypes) <= DTYPES.keys():
+                raise ValueError("gradients must be float32, bfloat16 or float16")
+            self._dtypes = dtypes, bytes(map(DTYPES.get, dtypes))
+        if not (list(map(_numel, there)) == numels
                 and set(map(_get_device, there)) <= {self.dev.index}
                 and all(map(_is_contiguous, there))):
-            raise ValueError("gradients must be contiguous float32, bfloat16 or float16 tensors of "
-                             "their parameters' sizes on %s" % self.dev)
-        at, types = array("Q", map(_data_ptr, there)), bytes(map(DTYPES.get, dtypes))
+            raise ValueError("gradients must be contiguous tensors of their parameters' sizes on %s"
+                             % self.dev)
+        at, types = array("Q", map(_data_ptr, there)), self._dtypes[1]
         if there is not grads:
             full, kinds, it = array("Q"), bytearray(), iter(zip(at, types))
             for g in grads:
