@@ -7,6 +7,12 @@
 // order the header gives, so the codes of an 8-bit state do not depend on
 // how a compiler fuses them.
 //
+// Bound by HBM: 28 bytes a parameter in 32 bits; in 8 bits with float32
+// parameters and bfloat16 gradients 14, and a state's 256 values, their scale
+// and their largest magnitude stay in one wave's registers, so a step is one
+// pass.  Measured: 80 million parameters in 8 bits, 205 us at best (5.4 TB/s);
+// 1.5 million in 120 tensors in 32 bits, 10 us.
+//
 // One launch covers up to kGrads tensors: a workgroup finds its tensor in
 // the table's map and steps SEMICRF_ADAMW_BLOCK elements of it.  The
 // gradients' addresses, new in every step of a training loop, come with the

@@ -12,6 +12,15 @@
 // leave one partial per channel vector; a small kernel adds them in a fixed
 // order in float64, and the last pass reads x again and writes the result.
 //
+// Bound by HBM: a forward pass reads x twice and writes y, a backward pass
+// reads x and dy twice and writes dx; what the first pass left in the caches
+// serves the second in part.  Measured: 2^20 positions of 64 channels in
+// float32, sums 62 us (4.3 TB/s), result 87 us (6.2 TB/s of reads and writes);
+// 16 sequences of 4096 positions (three quarters of them valid) of 256
+// channels in bfloat16 with SiLU, forward 7 + 4 + 15 us, backward 20 + 4 + 22 +
+// 4 us.  Fewer than eight positions a thread cost more in their channels'
+// parameters than they give (result 21 us at four, 15 at eight, 14.5 at 16).
+//
 // Short sequences (a norm of each position by itself above all) take another
 // way: a workgroup holds NS whole sequences, a stretch of memory without
 // gaps, in LDS, so x is read once, whatever C and the groups are.
@@ -520,6 +529,9 @@ __device__ __forceinline__ void load_params(const GnArgs &p, float *w, float *b)
 
 }  // namespace
 
+// 16384 positions of 250 channels in 10 groups, float32: 17 us forward, 25
+// backward (2 and 3 times 16 MB moved: 2 TB/s); the walk over channels and the
+// teams' sums in LDS are what remains.
 template <typename T, int V, int ACT>
 __global__ __launch_bounds__(kThreads) void k_gn_small(SmallArgs p, const T *x, T *y,
                                                        float *stats) {
@@ -711,7 +723,7 @@ GnArgs args(const semicrf_groupnorm_shape_t *s, int V) {
 }
 
 // Threads that sum `entries` values: about four each, 64 at most, or the
-// workgroup for many.
+// workgroup for many (4096 of them: 12 us with 64 threads, 6 with 256).
 int team(int64_t entries) {
   int n = 1;
   while (n < 64 && 4 * n < entries) n *= 2;

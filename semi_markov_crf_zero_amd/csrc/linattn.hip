@@ -31,6 +31,10 @@
 // what the transposed pair adds up to, so the four passes need two sets of
 // states: that of (k, v) forwards and that of (q, grad_o) backwards.
 //
+// The states' pass reads b and c once more, 3.2 GB in the place of 2.15 over
+// 2^20 positions of 4 heads.  Without it a head would be one workgroup: 4 of
+// 256 compute units, 389 ms in the place of 0.70.
+//
 // Positions past the length are loaded as zeros (a select, so NaN there
 // stays out) and their rows of the output are written as 0.
 #include "linattn_kernels.h"
@@ -42,7 +46,8 @@ constexpr int kThreads = 256;
 }
 
 // xs[s] from the part of segment s to X before segment s + 1, one element of
-// X a thread.
+// X a thread.  191 segments of 4 heads of 64 x 64: 24 us, the latency of twelve
+// rounds of sixteen loads.
 __global__ __launch_bounds__(kThreads) void k_linattn_scan(LaArgs p) {
   const int64_t n = (int64_t)p.Da * p.Dc;
   const int64_t e = blockIdx.x * (int64_t)kThreads + threadIdx.x;
@@ -78,7 +83,8 @@ __global__ __launch_bounds__(kThreads) void k_linattn_scan(LaArgs p) {
 }
 
 // Sum over the heads that share one: part [B*T][H][D] float32 to out
-// [B*T][H / share][D].
+// [B*T][H / share][D].  A fixed order, no atomics; 100002 positions of four heads
+// of 40 to two: 25 us.
 template <typename T>
 __global__ __launch_bounds__(256) void k_share_sum(const float *part, T *out, int64_t rows, int H,
                                                    int share, int D) {
@@ -92,8 +98,9 @@ __global__ __launch_bounds__(256) void k_share_sum(const float *part, T *out, in
   }
 }
 
-// One position: a workgroup per stream and head.  The state is read and
-// written once, V neighbouring columns and kStepRows rows of a thread in
+// One position: a workgroup per stream and head.  Bound by the state's bytes:
+// 256 streams of 16 heads of 128 x 128, 537 MB, 114 us, 4.8 TB/s; 4 streams of
+// 4 heads of 64 x 64 4.8 us, a launch.  The state is read and written once, V neighbouring columns and kStepRows rows of a thread in
 // flight; thread t takes column group t % tpr of rows t / tpr, + groups, ...
 constexpr int kStepRows = 8;
 template <typename T, int V>
