@@ -7,7 +7,7 @@ single-token form, and group norm with an activation, channels last.
     o = linear_attention_step(q, k, v, log_decay, state, slots=slots)
 
 The first two carry gradients (torch.autograd.Function over the library's
-backward entry points); the step moves a pool of states in place.  Tensors
+backward entry points; a gradient of a gradient is refused); the step moves a pool of states in place.  Tensors
 are CUDA (HIP) tensors, float32, bfloat16 or float16; states, norms' weights
 and decays are float32, lengths and slots int32.  Outputs and workspaces are
 allocated with torch on the input's device and the work is enqueued on
@@ -21,6 +21,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as bd
 
@@ -178,6 +179,7 @@ class LinearAttention(torch.autograd.Function):
         return o, last
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, do, dlast):
         q, k, v, state, log_decay, lengths, states = ctx.saved_tensors
         B, T, H, _, _, _, _, Dv, _ = ctx.dims
@@ -268,6 +270,7 @@ class GroupNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, weight, bias, lengths, stats = ctx.saved_tensors
         need, dev = ctx.needs_input_grad, x.device

@@ -267,3 +267,12 @@ def test_vectors_that_groups_part(C, G, dtype):
 def test_many_rows_of_partials():
     """Parameters' gradients over more workgroups than one reduction takes."""
     compare(9000, 1, 520, 8, "bf16", name="none", seed=21)
+
+
+def test_second_derivatives_are_refused():
+    """A penalty on a gradient would lack the terms through the operator."""
+    x = torch.randn((2, 5, 8), device=DEV, requires_grad=True)
+    y = encoder.group_norm(x, 2, activation="silu")
+    dx, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.square().sum().backward()

@@ -455,3 +455,16 @@ def test_slow_decays_over_long_sequences(T, H, dtype):
     want = np.expm1(g * T) / np.expm1(g)
     off = np.abs(last.cpu().double().numpy() / want - 1).max()
     assert off <= 4 * np.sqrt(T / 32 + 64) * 2.0 ** -24, off
+
+
+def test_second_derivatives_are_refused():
+    """A penalty on a gradient would lack the terms through the operator."""
+    q, k, v = (torch.randn((1, 5, 2, 4), device=DEV, requires_grad=True) for _ in range(3))
+    g = torch.full((2,), -0.1, device=DEV)
+    o = encoder.linear_attention(q, k, v, g)
+    grads = torch.autograd.grad(o.square().sum(), (q, k, v), create_graph=True)
+    first = torch.autograd.grad(encoder.linear_attention(q, k, v, g).square().sum(), (q, k, v))
+    for a, b in zip(grads, first):
+        assert torch.equal(a, b)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        sum(t.square().sum() for t in grads).backward()
