@@ -22,6 +22,7 @@ import functools
 
 import torch
 from torch.autograd.function import once_differentiable
+from torch.autograd.graph import increment_version
 
 from . import binding as bd
 
@@ -252,6 +253,7 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
                               _strides(k), _strides(v))
         launch(load().semicrf_linattn_step, dev, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
                _ptr(log_decay), _ptr(slots), N, _ptr(state), _ptr(o))
+        increment_version(state)  # a backward pass that saved the old states must fail
     return o
 
 

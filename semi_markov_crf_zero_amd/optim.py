@@ -18,6 +18,7 @@ import operator
 from array import array
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import binding as bd
 from .encoder import DTYPES, launch
@@ -173,12 +174,13 @@ class AdamWPlan:
         coefficient, an inverse loss scale), read on the device."""
         if len(grads) != len(self.params):
             raise ValueError("need one gradient for each of the %d parameters" % len(self.params))
-        there, numels = grads, self.numels
+        there, numels, moved = grads, self.numels, self.params
         try:
             dtypes = list(map(_dtype, grads))
         except AttributeError:  # None among them
             there = [g for g in grads if g is not None]
             numels = [n for n, g in zip(numels, grads) if g is not None]
+            moved = [p for p, g in zip(moved, grads) if g is not None]
             dtypes = list(map(_dtype, there))
         if dtypes != self._dtypes[0]:  # the types' codes, worked out once for a list of types
             if not set(dtypes) <= DTYPES.keys():
@@ -203,6 +205,7 @@ class AdamWPlan:
         launch(load().semicrf_adamw_step, self.dev, self._host, self._device, at.buffer_info()[0],
                types, len(grads), self.bits, int(step), lr, beta1, beta2, eps, weight_decay,
                None if grad_scale is None else grad_scale.data_ptr())
+        increment_version(moved)  # a backward pass that saved the old values must fail
 
 
 class AdamW(torch.optim.Optimizer):

@@ -287,3 +287,17 @@ def test_refusals():
         optim.moment_values(torch.zeros(300, dtype=torch.uint8, device=DEV), p[:1])
     with pytest.raises(ValueError):
         optim.moment_values(p, p[:1])
+
+
+def test_a_step_is_seen_by_autograd():
+    """A backward pass over weights that a step has moved since must not run;
+    one over weights without a gradient may."""
+    a, b = (torch.nn.Parameter(torch.ones(4, device=DEV)) for _ in range(2))
+    opt = optim.AdamW([a, b])
+    x = torch.ones(4, device=DEV, requires_grad=True)
+    over_a, over_b = (x * a).sum(), (x * b).sum()
+    a.grad = torch.ones_like(a)
+    opt.step()
+    over_b.backward()
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        over_a.backward()

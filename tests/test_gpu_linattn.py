@@ -468,3 +468,15 @@ def test_second_derivatives_are_refused():
         assert torch.equal(a, b)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         sum(t.square().sum() for t in grads).backward()
+
+
+def test_a_step_is_seen_by_autograd():
+    """A backward pass over states that a step has moved since must not run."""
+    q, k, v = (torch.randn((1, 5, 2, 4), device=DEV, requires_grad=True) for _ in range(3))
+    g = torch.full((2,), -0.1, device=DEV)
+    pool = torch.zeros((1, 2, 4, 4), device=DEV)
+    o = encoder.linear_attention(q, k, v, g, state=pool)
+    with torch.no_grad():
+        encoder.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], g, pool)
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        o.sum().backward()
