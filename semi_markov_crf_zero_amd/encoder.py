@@ -34,6 +34,7 @@ EXPORTS = (
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
 MAX_HEAD = 256  # the widest Dk and Dv
+MAX_SIZE = 2 ** 31 - 1  # of a dimension: the library's int
 
 
 class _LinattnShape(ctypes.Structure):
@@ -89,6 +90,8 @@ def launch(fn, dev, *args):
 @functools.lru_cache(maxsize=1024)
 def _workspace_bytes(name, kind, fields, backward):
     """Workspace of a shape (a tuple of the structure's fields)."""
+    if max(f for f in fields if isinstance(f, int)) > MAX_SIZE:
+        raise ValueError("sizes are at most %d" % MAX_SIZE)
     n = ctypes.c_size_t(0)
     rc = getattr(load(), name)(ctypes.byref(kind(*fields)), backward, ctypes.byref(n))
     if rc:
@@ -223,8 +226,9 @@ def linear_attention(q, k, v, log_decay, lengths=None, state=None, scale=None,
     if state is not None:
         _check("state", state, q.device, torch.float32, (B, H, Dk, Dv))
     if B == 0 or T == 0:
-        o = torch.zeros((B, T, H, Dv), dtype=q.dtype, device=q.device)
-        last = torch.zeros((B, H, Dk, Dv), device=q.device) if state is None else state.clone()
+        none = q.sum() + k.sum() + v.sum()  # 0, and part of the graph
+        o = none.expand(B, T, H, Dv).clone()
+        last = none.float().expand(B, H, Dk, Dv).clone() if state is None else state.clone()
     else:
         o, last = LinearAttention.apply(q, k, v, state, log_decay, lengths, dims,
                                         Dk ** -0.5 if scale is None else float(scale))
@@ -240,8 +244,8 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     dims = _linattn_check(q, k, v, log_decay, True)
     B, _, H, _, _, _, Dk, Dv, _ = dims
     dev = q.device
-    if state.dim() != 4 or state.shape[0] < 1:
-        raise ValueError("state must be [slots, H, Dk, Dv] with at least one slot")
+    if state.dim() != 4 or not 1 <= state.shape[0] <= MAX_SIZE:
+        raise ValueError("state must be [slots, H, Dk, Dv] with 1 to %d slots" % MAX_SIZE)
     N = state.shape[0]
     _check("state", state, dev, torch.float32, (N, H, Dk, Dv))
     if slots is not None:
@@ -314,7 +318,10 @@ def group_norm(x, groups: int, weight=None, bias=None, lengths=None, eps: float 
             raise ValueError("lengths go with x [B, T, C]")
         _check("lengths", lengths, x.device, torch.int32, (x.shape[0],))
     if x.numel() == 0:
-        return x.clone()
+        y = x.clone()
+        for t in (weight, bias):  # gradients of 0
+            y = y if t is None else y * t.to(x.dtype)
+        return y
     flat = x.contiguous()
     if x.dim() != 3:
         flat = flat.view(x.shape[0], -1, C)

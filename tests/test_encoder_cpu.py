@@ -178,3 +178,10 @@ def test_python_refuses_cpu_tensors():
     with pytest.raises(ValueError):
         optim.moment_values(torch.zeros(4, dtype=torch.uint8), torch.zeros(1))
     assert bd.STATUS[4] == "SEMICRF_ERR_WORKSPACE"
+
+
+def test_python_refuses_sizes_past_the_library_s():
+    """ctypes would cut a size past 31 bits without a word."""
+    with pytest.raises(ValueError, match="sizes"):
+        encoder._workspace_bytes("semicrf_groupnorm_workspace_size", encoder._GroupnormShape,
+                                 (2 ** 32 + 1, 1, 8, 2, 0, 0, 1e-5), 0)

@@ -276,3 +276,14 @@ def test_second_derivatives_are_refused():
     dx, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         dx.square().sum().backward()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("shape", [(0, 5, 8), (2, 0, 8)])
+def test_empty_calls_carry_gradients(shape, dtype):
+    x = torch.zeros(shape, device=DEV, dtype=TYPES[dtype])
+    w, b = (torch.ones(8, device=DEV, requires_grad=True) for _ in range(2))
+    y = encoder.group_norm(x, 2, w, b, activation="silu")
+    assert y.shape == shape and y.dtype == x.dtype
+    y.float().sum().backward()
+    assert torch.equal(w.grad, torch.zeros_like(w)) and torch.equal(b.grad, torch.zeros_like(b))

@@ -480,3 +480,16 @@ def test_a_step_is_seen_by_autograd():
         encoder.linear_attention_step(q[:, 0], k[:, 0], v[:, 0], g, pool)
     with pytest.raises(RuntimeError, match="inplace operation"):
         o.sum().backward()
+
+
+def test_empty_calls_carry_gradients():
+    g = torch.zeros(2, device=DEV)
+    q = torch.zeros((2, 0, 2, 8), device=DEV, dtype=torch.bfloat16, requires_grad=True)
+    o, last = encoder.linear_attention(q, q, q, g, return_state=True)
+    assert o.shape == (2, 0, 2, 8) and last.shape == (2, 2, 8, 8) and not last.any()
+    assert o.dtype == torch.bfloat16 and last.dtype == torch.float32
+    (o.float().sum() + last.sum()).backward()
+    assert q.grad.shape == q.shape
+    s = torch.ones((2, 2, 8, 8), device=DEV, requires_grad=True)
+    encoder.linear_attention(q, q, q, g, state=s, return_state=True)[1].sum().backward()
+    assert torch.equal(s.grad, torch.ones_like(s))
