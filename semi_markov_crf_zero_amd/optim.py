@@ -107,6 +107,9 @@ class AdamWPlan:
                     or not p.is_contiguous()):
                 raise ValueError("parameters must be contiguous float32, bfloat16 or float16 "
                                  "tensors on one GPU")
+        at = [p.data_ptr() for p in self.params if p.numel()]
+        if len(set(at)) != len(at):
+            raise ValueError("a parameter is there twice: two steps would race for it")
         self.masters = list(masters) if masters is not None else [None] * n
         for p, t in zip(self.params, self.masters):
             if t is not None:
@@ -221,6 +224,10 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError("states are held in 32 bits or in 8")
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
                                       weight_decay=weight_decay, bits=bits, masters=masters))
+        self._plans = {}
+
+    def __setstate__(self, state):  # a copy, or from a file: plans are made anew
+        super().__setstate__(state)
         self._plans = {}
 
     def _plan(self, i, group):

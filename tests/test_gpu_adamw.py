@@ -5,6 +5,7 @@ and float32 parameters are compared bit by bit with numpy's float32
 operations in that order, and the 8-bit codes with a search over the 256
 values.  Against the formula in float64: m and v are sums of two products
 (4 e |terms|), the update a quotient of them (12 e of itself), e = 2^-24."""
+import copy
 import math
 
 import numpy as np
@@ -301,3 +302,28 @@ def test_a_step_is_seen_by_autograd():
     over_b.backward()
     with pytest.raises(RuntimeError, match="inplace operation"):
         over_a.backward()
+
+
+def test_a_parameter_twice():
+    p = torch.ones(300, device=DEV)
+    with pytest.raises(ValueError, match="twice"):
+        optim.AdamWPlan([p, p.view(30, 10)])
+    optim.AdamWPlan([p, torch.empty(0, device=DEV), torch.empty(0, device=DEV)])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_copied_optimizer_steps(bits):
+    """A deep copy of a model's parameters with their optimizer goes on as
+    the original does."""
+    p = torch.nn.Parameter(torch.linspace(-1, 1, 300, device=DEV))
+    opt = optim.AdamW([p], bits=bits)
+    p.grad = torch.linspace(2, -1, 300, device=DEV)
+    opt.step()
+    other = copy.deepcopy(opt)
+    twin, = other.param_groups[0]["params"]
+    assert twin.data_ptr() != p.data_ptr()
+    twin.grad = p.grad.clone()
+    opt.step()
+    after = p.detach().clone()
+    other.step()
+    assert torch.equal(twin, after) and torch.equal(p, after)
