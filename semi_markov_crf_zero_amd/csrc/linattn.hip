@@ -136,7 +136,10 @@ __global__ __launch_bounds__(256) void k_linattn_step(semicrf_linattn_shape_t s,
         (float)q[b * s.q_stride[0] + h / (s.H / s.Hq) * s.q_stride[2] + threadIdx.x] * s.scale;
     ks[threadIdx.x] = (float)k[b * s.k_stride[0] + h / (s.H / s.Hk) * s.k_stride[2] + threadIdx.x];
   }
-  const float d = expf(log_decay[h]);
+  // the decay in two floats: one would put its own rounding into a state that
+  // lives for thousands of steps at each of them, always with the same sign
+  const double decay = exp((double)log_decay[h]);
+  const float d = (float)decay, dl = (float)(decay - d);
   float vc[V];
   Pack<float, V> acc;
 #pragma unroll
@@ -154,7 +157,9 @@ __global__ __launch_bounds__(256) void k_linattn_step(semicrf_linattn_shape_t s,
         if (row < s.Dk) {
 #pragma unroll
           for (int e = 0; e < V; ++e) {
-            x[i].v[e] = d * x[i].v[e] + ks[row] * vc[e];
+            const float y = x[i].v[e];
+            const float add = fmaf(ks[row], vc[e], fabsf(y) < INFINITY ? dl * y : 0.f);
+            x[i].v[e] = fmaf(d, y, add);
             acc.v[e] += qs[row] * x[i].v[e];
           }
           *reinterpret_cast<Pack<float, V> *>(S + row * s.Dv + c) = x[i];

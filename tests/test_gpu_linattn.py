@@ -8,6 +8,8 @@ decays e^{g n} (their exponents |g n| up to about 30 where a term still
 counts): (Dk + 160 + T/16) 2^-24 size.  bfloat16 and float16 inputs are
 exact; the working values keep at least 16 bits (2^-16 size), and the output
 rounds once more, by 2^-8 or 2^-11 of itself (float16: by 2^-25 near 0)."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -493,3 +495,24 @@ def test_empty_calls_carry_gradients():
     s = torch.ones((2, 2, 8, 8), device=DEV, requires_grad=True)
     encoder.linear_attention(q, q, q, g, state=s, return_state=True)[1].sum().backward()
     assert torch.equal(s.grad, torch.ones_like(s))
+
+
+def test_slow_decays_over_many_steps():
+    """A state that is only read: S_n = e^{g n} S_0.  A step rounds it twice at
+    most, by 2^-24 of it, without a sign over the 64 elements and 12 decays: 6
+    sqrt(2 n) 2^-24 of it.  e^g used as one float32, up to 2^-25 off, would
+    add up to n 2^-25, 7 times that at n = 5000.  An infinite element stays
+    infinite."""
+    n, H = 5000, 12
+    g = torch.tensor([-1.0 / (700 + 100 * i) for i in range(H)])
+    s0 = 1 + torch.rand((1, H, 8, 8), generator=torch.Generator().manual_seed(3))
+    q = torch.zeros((1, H, 8), device=DEV)
+    state, gd = s0.to(DEV), g.to(DEV)
+    for _ in range(n):
+        encoder.linear_attention_step(q, q, q, gd, state)
+    want = np.exp(g.double().numpy() * n)[None, :, None, None] * s0.double().numpy()
+    off = np.abs(state.cpu().double().numpy() / want - 1).max()
+    assert off <= 6 * np.sqrt(2 * n) * 2.0 ** -24, off
+    state[0, 0, 0, 0] = math.inf
+    encoder.linear_attention_step(q, q, q, gd, state)
+    assert state[0, 0, 0, 0] == math.inf
