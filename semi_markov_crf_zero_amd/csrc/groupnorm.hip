@@ -27,7 +27,9 @@
 //
 // Sums.  mean and var come from sums of (x - pivot) and its square in
 // float64, the pivot the group's first element: the subtraction takes the
-// common offset out before anything is squared.
+// common offset out before anything is squared.  It is one in float64 too: where
+// the first element is far from the others, a float32 difference would lose
+// the same part of each of them.
 #include "encoder.h"
 
 namespace semicrf {
@@ -127,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnArgs p, const T *x, doub
   double sum[N] = {}, sq[N] = {};
   if (r < p.rows && v < p.cv && len > 0) {
     const T *row = x + (int64_t)b * p.T * p.C;
-    float pivot[N];
+    double pivot[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) pivot[i] = (float)row[(v * V + i) / p.Cg * p.Cg];
     row += (int64_t)v * V;
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_sums(GnArgs p, const T *x, doub
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const int k = ONE ? 0 : i;
-        const double e = (float)d.v[i] - pivot[k];
+        const double e = (double)(float)d.v[i] - pivot[k];
         sum[k] += e;
         sq[k] += e * e;
       }
@@ -189,14 +191,14 @@ __device__ __forceinline__ double2 team_sum(double a, double b, int lanes) {
 
 // mean and 1/sqrt(var + eps) from the sums of x - pivot and its square over m
 // values; 0, 0 of nothing, NaN of a length that is none (m < 0).
-__device__ __forceinline__ float2 stats_of(double2 sum, int64_t m, float pivot, float eps) {
+__device__ __forceinline__ float2 stats_of(double2 sum, int64_t m, double pivot, float eps) {
   if (m <= 0) {
     const float x = m < 0 ? __builtin_nanf("") : 0.f;
     return make_float2(x, x);
   }
   const double n = 1.0 / (double)m, mean = sum.x * n, var = sum.y * n - mean * mean;
   const double v = (var > 0 ? var : var == var ? 0.0 : var) + (double)eps;
-  return make_float2((float)(pivot + mean), 1.f / sqrtf((float)v));
+  return make_float2((float)(pivot + mean), (float)(1.0 / sqrt(v)));  // v may pass float32's range
 }
 
 // A team of p.lanes threads per sequence and group: its statistics.
@@ -553,7 +555,7 @@ __global__ __launch_bounds__(kThreads) void k_gn_small(SmallArgs p, const T *x, 
     const int s = pair / p.g.G, g = pair % p.g.G;
     const int len = valid_length(p.g.lengths, b0 + s, p.g.T), m = len * p.g.Cg;
     const float *u = xs + s * p.TC + g * p.g.Cg;
-    const float pivot = u[0];
+    const double pivot = u[0];
     double sum = 0, sq = 0;
     for (int j = lane; j < m; j += lanes) {
       const int t = p.g.T == 1 ? 0 : div_small(j, p.mCg);

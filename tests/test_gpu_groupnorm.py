@@ -287,3 +287,21 @@ def test_empty_calls_carry_gradients(shape, dtype):
     assert y.shape == shape and y.dtype == x.dtype
     y.float().sum().backward()
     assert torch.equal(w.grad, torch.zeros_like(w)) and torch.equal(b.grad, torch.zeros_like(b))
+
+
+@pytest.mark.parametrize("B,T,C,G", [(1, 65536, 16, 1), (1, 30000, 30, 3), (300, 1, 512, 1)])
+def test_a_first_element_far_from_the_others(B, T, C, G):
+    """The others, 0.02 to 0.025, are less than half of the first one's last
+    place: a float32 difference from it would be the same for all of them,
+    and move the mean by 0.02 where the deviation is 10^6 / sqrt(n)."""
+    x = 0.02 + 0.005 * torch.rand((B, T, C), generator=torch.Generator().manual_seed(4))
+    x[:, 0, ::C // G] = 1e6
+    want, tol = reference(x.double().numpy(), np.ones(C), np.zeros(C), [T] * B, G, 1e-5, "none")
+    y = encoder.group_norm(x.to(DEV), G).cpu().double().numpy()
+    assert np.all(np.abs(y - want["y"]) <= tol["y"] + E * np.abs(want["y"]))
+
+
+@pytest.mark.parametrize("T,C,G", [(900, 64, 8), (2, 64, 8)])
+@pytest.mark.parametrize("spread", [1e25, 1e-25])
+def test_variances_past_float32(T, C, G, spread):
+    compare(2, T, C, G, "f32", name="none", spread=spread, eps=0.0, seed=14)
