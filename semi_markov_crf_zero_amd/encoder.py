@@ -160,6 +160,17 @@ def _strides(t):
     return (s[0], s[1] if len(s) == 4 else 0, s[-2])
 
 
+def _once(backward):
+    """once_differentiable, which turns gradients off around each call, only
+    where they are on (create_graph)."""
+    refusing = once_differentiable(backward)
+
+    @functools.wraps(backward)
+    def call(ctx, *grads):
+        return (refusing if torch.is_grad_enabled() else backward)(ctx, *grads)
+    return call
+
+
 class LinearAttention(torch.autograd.Function):
     """o [B, T, H, Dv] and the state after each sequence [B, H, Dk, Dv]; dims
     is what _linattn_check gives."""
@@ -183,7 +194,7 @@ class LinearAttention(torch.autograd.Function):
         return o, last
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, do, dlast):
         q, k, v, state, log_decay, lengths, states = ctx.saved_tensors
         B, T, H, _, _, _, _, Dv, _ = ctx.dims
@@ -276,7 +287,7 @@ class GroupNorm(torch.autograd.Function):
         return y
 
     @staticmethod
-    @once_differentiable
+    @_once
     def backward(ctx, dy):
         x, weight, bias, lengths, stats = ctx.saved_tensors
         need, dev = ctx.needs_input_grad, x.device
