@@ -17,7 +17,7 @@
 // serves the second in part.  Measured: 2^20 positions of 64 channels in
 // float32, sums 62 us (4.3 TB/s), result 87 us (6.2 TB/s of reads and writes);
 // 16 sequences of 4096 positions (three quarters of them valid) of 256
-// channels in bfloat16 with SiLU, forward 7 + 4 + 15 us, backward 20 + 4 + 22 +
+// channels in bfloat16 with SiLU, forward 8 + 4 + 15 us, backward 20 + 4 + 22 +
 // 4 us.  Fewer than eight positions a thread cost more in their channels'
 // parameters than they give (result 21 us at four, 15 at eight, 14.5 at 16).
 //
@@ -531,7 +531,7 @@ __device__ __forceinline__ void load_params(const GnArgs &p, float *w, float *b)
 
 }  // namespace
 
-// 16384 positions of 250 channels in 10 groups, float32: 17 us forward, 25
+// 16384 positions of 250 channels in 10 groups, float32: 18 us forward, 25
 // backward (2 and 3 times 16 MB moved: 2 TB/s); the walk over channels and the
 // teams' sums in LDS are what remains.
 template <typename T, int V, int ACT>

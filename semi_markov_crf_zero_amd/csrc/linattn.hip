@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256) void k_share_sum(const float *part, T *out, in
 
 // One position: a workgroup per stream and head.  Bound by the state's bytes:
 // 256 streams of 16 heads of 128 x 128, 537 MB, 114 us, 4.8 TB/s; 4 streams of
-// 4 heads of 64 x 64 4.8 us, a launch.  The state is read and written once, V neighbouring columns and kStepRows rows of a thread in
+// 4 heads of 64 x 64 5.1 us, a launch.  The state is read and written once, V neighbouring columns and kStepRows rows of a thread in
 // flight; thread t takes column group t % tpr of rows t / tpr, + groups, ...
 constexpr int kStepRows = 8;
 template <typename T, int V>
