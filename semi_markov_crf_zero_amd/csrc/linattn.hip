@@ -100,8 +100,9 @@ __global__ __launch_bounds__(256) void k_share_sum(const float *part, T *out, in
 
 // One position: a workgroup per stream and head.  Bound by the state's bytes:
 // 256 streams of 16 heads of 128 x 128, 537 MB, 114 us, 4.8 TB/s; 4 streams of
-// 4 heads of 64 x 64 5.1 us, a launch.  The state is read and written once, V neighbouring columns and kStepRows rows of a thread in
-// flight; thread t takes column group t % tpr of rows t / tpr, + groups, ...
+// 4 heads of 64 x 64 5.1 us, a launch.  The state is read and written once, V
+// neighbouring columns and kStepRows rows of a thread in flight; thread t takes
+// column group t % tpr of rows t / tpr, + groups, ...
 constexpr int kStepRows = 8;
 template <typename T, int V>
 __global__ __launch_bounds__(256) void k_linattn_step(semicrf_linattn_shape_t s, const T *q,
@@ -370,7 +371,8 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
                                      const int32_t *lengths, const float *state_in,
                                      const void *states, const void *grad_o,
                                      const float *grad_state, void *grad_q, void *grad_k,
-                                     void *grad_v, float *grad_state_in, void *workspace, size_t workspace_bytes, void *stream) {
+                                     void *grad_v, float *grad_state_in, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
   if (!s || !q || !k || !v || !log_decay || !grad_o) return SEMICRF_ERR_NULL;
   size_t need;
   semicrf_status_t e = semicrf_linattn_workspace_size(s, 1, &need);
