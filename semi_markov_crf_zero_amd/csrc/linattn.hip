@@ -33,7 +33,7 @@
 //
 // The states' pass reads b and c once more, 3.2 GB in the place of 2.15 over
 // 2^20 positions of 4 heads.  Without it a head would be one workgroup: 4 of
-// 256 compute units, 389 ms in the place of 0.70.
+// 256 compute units, 389 ms in the place of 0.73.
 //
 // Positions past the length are loaded as zeros (a select, so NaN there
 // stays out) and their rows of the output are written as 0.
@@ -218,10 +218,11 @@ semicrf_status_t launch_states(const LaArgs &p, int dtype, hipStream_t st) {
 
 // Workgroups of the chunk kernel a compute unit holds.
 int resident(int Da, int Dc, int dtype) {
-  const int NP = linattn_parts(dtype), NR = NP == 3 ? 3 : 2, L = linattn_chunk(NP);
+  const int NP = linattn_parts(dtype), NR = 3, L = linattn_chunk(NP);
   const int DA = Da <= 128 ? (Da + 31) / 32 * 32 : 256;
   const int NW = DA > 128 ? 4 : linattn_waves(Dc, true);
-  const int lds = 2 * L * (NP * (2 * DA + 4 + 16 * NW + 16) + NR * (L + 4)) + 4 * (7 * L + 3);
+  const int P = NP == 1 ? L : L + 4;  // a row of a part of P
+  const int lds = 2 * L * (NP * (2 * DA + 4 + 16 * NW + 16) + NR * P) + 4 * (7 * L + 3);
   const int by_lds = (int)(163840 / lds), occ = linattn_occupancy(DA, NW);
   const int by_waves = NW < 4 ? 4 * occ / NW : occ / ((NW + 3) / 4);
   const int n = by_lds < by_waves ? by_lds : by_waves;

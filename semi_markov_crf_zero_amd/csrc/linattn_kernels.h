@@ -3,6 +3,8 @@
 // what they compute).
 #pragma once
 
+#include <type_traits>
+
 #include "encoder.h"
 
 namespace semicrf {
@@ -38,9 +40,11 @@ struct LaArgs {
 // sums keeps the pairs of parts (i, j) whose share is above the last part's
 // (i + j < the number of parts).
 //   inputs       1, 2 or 3 parts: exact
-//   P and X      2 parts for 16-bit tensors (2^-16, far below the rounding of
-//                the output, 2^-8 or 2^-11), 3 for float32 (2^-24)
-//   what is added to X   3 parts always: X is float32 whatever the tensors are
+//   P and X, and what is added to X   3 parts (2^-24): they are float32 whatever
+//                the tensors are.  Two parts for 16-bit tensors would lose what
+//                is left where terms cancel, for 3 to 8 % of the time (32
+//                sequences of 512 positions of 4 heads of 64 + 64 27 us in the
+//                place of 29, 2^20 positions 701 in the place of 726)
 // Float32 at 64 columns: 6 products of 16 cycles in the place of 8 of 32.
 __host__ __device__ constexpr int linattn_parts(int dtype) {
   return dtype == SEMICRF_F32 ? 3 : dtype == SEMICRF_F16 ? 2 : 1;
@@ -404,7 +408,7 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
 // reads them as operands in place; P goes through LDS, as every wave needs all
 // of it.  At 64 x 64 in bfloat16 a chunk of 64 positions is 24 KB read and 8
 // written against about 1000 matrix cycles, 1600 LDS cycles and 500 vector
-// instructions a wave: three workgroups a compute unit (46 KB of LDS, 157
+// instructions a wave: three workgroups a compute unit (54 KB of LDS, 161
 // registers) leave HBM as the bound.  Measured, 2^20 positions of 4 heads:
 // 471 us at best, 4.6 TB/s of 2.15 GB read and written (a large copy: 5.1);
 // matrix cores busy 27 %, vector units 48 %, LDS 52 % (10 % conflicts).  In
@@ -415,11 +419,13 @@ __global__ __launch_bounds__(64 * NW)
     __attribute__((amdgpu_waves_per_eu(linattn_occupancy(DA, NW)))) void k_linattn(LaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
   constexpr int KB = DA / 32;
-  constexpr int NR = NP == 3 ? 3 : 2;  // parts of P and X
+  constexpr int NR = 3;  // parts of P and X
   typedef ByRow<DA> LA;
   typedef ByBoth<DA> LB;
   typedef ByColumn<kCols> LC;
-  typedef ByRow<L> LP;
+  // without padding where that lets a compute unit hold a workgroup more; with
+  // it where the addresses of the other would take registers that are short
+  typedef std::conditional_t<NP == 1, ByBoth<L>, ByRow<L>> LP;
   __shared__ alignas(16) bf16 A[L * (NP * (LA::row + DA + LC::row) + NR * LP::row)];
   bf16 *const Bm = A + NP * L * LA::row;
   bf16 *const C = Bm + NP * L * DA;

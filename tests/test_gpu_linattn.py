@@ -516,3 +516,54 @@ def test_slow_decays_over_many_steps():
     state[0, 0, 0, 0] = math.inf
     encoder.linear_attention_step(q, q, q, gd, state)
     assert state[0, 0, 0, 0] == math.inf
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_what_is_left_where_terms_cancel(dtype):
+    """a = 1 + 2^-9 + 2^-18 and b = 1 + 2^-9 are neighbours to 16 bits, and
+    float32 knows them apart.  They meet as elements of a state and as products
+    of two rows, for every output; with g = 0 and a scale of 1 every other
+    operation is exact.  A handful of roundings of values up to 2: 8 * 2^-24."""
+    a, b, left, bar8 = 1 + 2.0 ** -9 + 2.0 ** -18, 1 + 2.0 ** -9, 2.0 ** -18, 8 * 2.0 ** -24
+    g = torch.zeros(1, device=DEV)
+
+    def call(q, k, v, state):
+        t = [x.clone().to(TYPES[dtype]).requires_grad_(True) for x in (q, k, v)]
+        return t, encoder.linear_attention(*t, g, state=state, scale=1.0, return_state=True)
+
+    def near(x, want):
+        assert abs(x.item() - want) <= bar8, (x.item(), want)
+
+    def rows(T, **at):  # [1, T, 1, 32], rows t0.. as given
+        x = torch.zeros((1, T, 1, 32), device=DEV)
+        for t, row in at.items():
+            x[0, int(t[1:]), 0, :3] = torch.tensor(row, device=DEV)
+        return x
+
+    # elements of a state: S = G = [[a, b], [b, a]], rows (1, -1)
+    S = torch.zeros((1, 1, 32, 32), device=DEV)
+    S[0, 0, :2, :2] = torch.tensor([[a, b], [b, a]], device=DEV)
+    one, none = rows(1, t0=[1.0, -1.0, 0.0]), rows(1)
+    (q, _, _), (o, _) = call(one, none, none, S)
+    near(o[0, 0, 0, 0], left)
+    dq, = torch.autograd.grad(o, q, one.to(o.dtype))
+    near(dq[0, 0, 0, 0], left)
+    (_, k, v), (_, last) = call(none, one, one, None)
+    dk, dv = torch.autograd.grad(last, (k, v), S)
+    near(dk[0, 0, 0, 0], left)
+    near(dv[0, 0, 0, 0], left)
+
+    # products of rows
+    ones, minus = [1.0, 1.0, 1.0], [-1.0, -1.0, -1.0]
+    far, near_ = [1.0, 2.0 ** -9, 2.0 ** -18], [1.0, 2.0 ** -9, 0.0]
+    _, (o, _) = call(rows(3, t2=ones), rows(3, t0=far, t1=near_), rows(3, t0=ones, t1=minus), None)
+    near(o[0, 2, 0, 0], left)
+    (q, _, _), (o, _) = call(rows(3), rows(3, t0=ones, t1=minus), rows(3, t0=far, t1=near_), None)
+    dq, = torch.autograd.grad(o, q, rows(3, t2=ones).to(o.dtype))
+    near(dq[0, 2, 0, 0], left)
+    (_, k, _), (o, _) = call(rows(3, t1=ones, t2=minus), rows(3), rows(3, t0=ones), None)
+    dk, = torch.autograd.grad(o, k, rows(3, t1=far, t2=near_).to(o.dtype))
+    near(dk[0, 0, 0, 0], left)
+    (_, _, v), (o, _) = call(rows(3, t1=far, t2=near_), rows(3, t0=ones), rows(3), None)
+    dv, = torch.autograd.grad(o, v, rows(3, t1=ones, t2=minus).to(o.dtype))
+    near(dv[0, 0, 0, 0], left)
