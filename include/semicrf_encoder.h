@@ -109,7 +109,12 @@ semicrf_status_t semicrf_linattn_step(const semicrf_linattn_shape_t *shape, cons
  *   y = act(h * weight[c] + bias[c])      (weight, bias [C] float32 or NULL)
  * y [B][T][C] in x's type.  stats [B][G][2] float32 (mean, 1/sqrt(var+eps))
  * is written by the forward pass and read by the backward pass; 0, 0 for an
- * empty sequence. */
+ * empty sequence.
+ *
+ * B, T, C <= 2^30, and a launch has at most 2^32 - 1 threads, 256 of them for
+ * each sequence and each 256 vectors of its channels (16 bytes, or what the
+ * alignment allows), up to 64 for a sequence and group; where a sequence is
+ * short (T * C <= 4096), 256 for 4096 elements.  SEMICRF_ERR_SHAPE past that. */
 typedef struct {
     int B, T, C, G;
     int dtype;

@@ -685,8 +685,7 @@ semicrf_status_t check(const semicrf_groupnorm_shape_t *s) {
   if (!s) return SEMICRF_ERR_NULL;
   if (s->B < 1 || s->T < 1 || s->C < 1 || s->G < 1 || s->C % s->G)
     return SEMICRF_ERR_SHAPE;
-  // the grid counts sequences times groups, and times the tiles of a row
-  if (s->T > 1 << 30 || (int64_t)s->B * (s->C + 4096) > 0x7fffffff) return SEMICRF_ERR_SHAPE;
+  if (s->B > 1 << 30 || s->T > 1 << 30 || s->C > 1 << 30) return SEMICRF_ERR_SHAPE;
   if (!dtype_ok(s->dtype) || s->act < SEMICRF_ACT_NONE || s->act > SEMICRF_ACT_RELU ||
       !(s->eps >= 0.f))
     return SEMICRF_ERR_ARG;
@@ -725,11 +724,12 @@ GnArgs args(const semicrf_groupnorm_shape_t *s, int V) {
 }
 
 // Threads that sum `entries` values: about four each, 64 at most, or the
-// workgroup for many (4096 of them: 12 us with 64 threads, 6 with 256).
-int team(int64_t entries) {
+// workgroup for many (4096 of them: 12 us with 64 threads, 6 with 256) of few
+// groups: a million groups fill the GPU with a wave each.
+int team(int64_t entries, int64_t groups) {
   int n = 1;
   while (n < 64 && 4 * n < entries) n *= 2;
-  return entries > 256 ? kThreads : n;
+  return entries > 256 && groups < 1 << 20 ? kThreads : n;
 }
 unsigned team_grid(const GnArgs &p) {
   const int64_t teams = kThreads / p.lanes;
@@ -751,7 +751,7 @@ SmallArgs small_args(const semicrf_groupnorm_shape_t *s) {
   p.mC = magic(s->C);
   p.mCg = magic(p.g.Cg);
   // a team for each group; wider ones where the groups are few
-  const int n = team((int64_t)s->T * p.g.Cg);
+  const int n = team((int64_t)s->T * p.g.Cg, (int64_t)s->B * s->G);
   p.g.lanes = n > 64 ? 64 : n;
   while (p.g.lanes < 64 && 2 * p.g.lanes * p.ns * s->G <= kThreads) p.g.lanes *= 2;
   return p;
@@ -767,7 +767,7 @@ bool small_path(const semicrf_groupnorm_shape_t *s) {
 }
 int64_t small_blocks(const semicrf_groupnorm_shape_t *s) {
   const int ns = small_args(s).ns;
-  return (s->B + ns - 1) / ns;
+  return ((int64_t)s->B + ns - 1) / ns;
 }
 // Elements a thread moves at once there: groups do not matter, only whole
 // aligned pieces of a stretch.
@@ -791,6 +791,24 @@ int param_splits(int64_t rows) {
 size_t param_bytes(const semicrf_groupnorm_shape_t *s, int64_t rows) {
   const int n = param_splits(rows);
   return n > 1 ? align256((size_t)n * s->C * sizeof(double2)) : 0;
+}
+
+// Whether the launches with vectors of V channels are within a grid's 2^32 - 1
+// threads.
+bool fits(const semicrf_groupnorm_shape_t *s, int V) {
+  constexpr int64_t most = 0xffffffff;
+  int64_t rows;
+  if (small_path(s)) {
+    rows = small_blocks(s);
+    if (rows * kThreads > most) return false;
+  } else {
+    const GnArgs p = args(s, V);
+    rows = (int64_t)p.B * p.slabs;
+    if (rows * p.tiles * kThreads > most) return false;
+    const int64_t groups = (int64_t)p.B * p.G;
+    if (groups * team((int64_t)p.slabs * p.Cg, groups) + kThreads > most) return false;
+  }
+  return (s->C + 15ll) / 16 * param_splits(rows) * kParamThreads <= most;
 }
 
 // Workspace for the narrowest vectors (the widest partials).
@@ -828,7 +846,7 @@ semicrf_status_t run_fwd(GnArgs p, const void *x, void *y, float *stats, void *w
                                                          stats, (T *)y);
     return launch_status();
   }
-  p.lanes = team((int64_t)p.slabs * (ONE ? p.cv : p.C) / p.G);
+  p.lanes = team((int64_t)p.slabs * (ONE ? p.cv : p.C) / p.G, (int64_t)p.B * p.G);
   k_gn_stats<T><<<team_grid(p), kThreads, 0, st>>>(p, ONE ? p.cv : p.C, (const T *)x,
                                                          (const double2 *)ws, stats);
   k_gn_apply<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, stats, (T *)y);
@@ -856,7 +874,7 @@ semicrf_status_t run_bwd(GnArgs p, const void *x, const void *dy, const float *s
   float2 *coef = (float2 *)(w + sums_bytes);
   k_gn_bwd_sums<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats,
                                                            part);
-  p.lanes = team((int64_t)p.slabs * p.Cg);
+  p.lanes = team((int64_t)p.slabs * p.Cg, (int64_t)p.B * p.G);
   k_gn_bwd_group<<<team_grid(p), kThreads, 0, st>>>(p, part, coef);
   k_gn_bwd_apply<T, V, ACT, ONE><<<grid, kThreads, 0, st>>>(p, (const T *)x, (const T *)dy, stats,
                                                             coef, (T *)dx);
@@ -948,6 +966,7 @@ semicrf_status_t semicrf_groupnorm_workspace_size(const semicrf_groupnorm_shape_
   if (!bytes) return SEMICRF_ERR_NULL;
   const semicrf_status_t e = check(s);
   if (e != SEMICRF_OK) return e;
+  if (!fits(s, vector_width(s, nullptr, 0))) return SEMICRF_ERR_SHAPE;
   *bytes = need(s, backward);
   return SEMICRF_OK;
 }
@@ -965,6 +984,7 @@ semicrf_status_t semicrf_groupnorm_fwd(const semicrf_groupnorm_shape_t *s, const
   const void *ptrs[] = {x, y};
   const bool small = small_path(s);
   const int V = small ? small_width(s, ptrs, 2) : vector_width(s, ptrs, 2);
+  if (!fits(s, V)) return SEMICRF_ERR_SHAPE;
   Fwd f = {args(s, small ? 1 : V), {}, x, y, stats, workspace, (hipStream_t)stream};
   if (small) f.small = small_args(s);
   f.p.lengths = f.small.g.lengths = lengths;
@@ -988,6 +1008,7 @@ semicrf_status_t semicrf_groupnorm_bwd(const semicrf_groupnorm_shape_t *s, const
   const void *ptrs[] = {x, grad_y, grad_x};
   const bool small = small_path(s);
   const int V = small ? small_width(s, ptrs, 3) : vector_width(s, ptrs, 3);
+  if (!fits(s, V)) return SEMICRF_ERR_SHAPE;
   Bwd f = {args(s, small ? 1 : V), {}, 0, x, grad_y, stats, grad_x, grad_weight, grad_bias, workspace,
            (hipStream_t)stream};
   if (small) f.small = small_args(s);

@@ -185,3 +185,19 @@ def test_python_refuses_sizes_past_the_library_s():
     with pytest.raises(ValueError, match="sizes"):
         encoder._workspace_bytes("semicrf_groupnorm_workspace_size", encoder._GroupnormShape,
                                  (2 ** 32 + 1, 1, 8, 2, 0, 0, 1e-5), 0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    # a norm of each position by itself, for the longest sequences and for many
+    (dict(B=1 << 20, T=1, C=64, G=4), 0), (dict(B=1 << 20, T=1, C=256, G=32), 0),
+    (dict(B=908793, T=1, C=32, G=4, dtype=1), 0), (dict(B=1 << 28, T=1, C=16, G=2), 0),
+    (dict(B=1 << 20, T=1, C=8192, G=16, dtype=1), 0), (dict(B=1 << 20, T=64, C=128, G=8), 0),
+    # 2^32 threads and more
+    (dict(B=1 << 26, T=1, C=8192, G=1), 2), (dict(B=1 << 24, T=1, C=8192, G=4096), 2),
+    (dict(B=(1 << 30) + 1, T=1, C=1, G=1), 2), (dict(B=1, C=1 << 30, G=1, T=1), 2),
+])
+@pytest.mark.parametrize("backward", [0, 1])
+def test_groupnorm_sizes(lib, kw, code, backward):
+    n = ctypes.c_size_t(0)
+    assert lib.semicrf_groupnorm_workspace_size(ctypes.byref(gn(**kw)), backward,
+                                                ctypes.byref(n)) == code

@@ -305,3 +305,42 @@ def test_a_first_element_far_from_the_others(B, T, C, G):
 @pytest.mark.parametrize("spread", [1e25, 1e-25])
 def test_variances_past_float32(T, C, G, spread):
     compare(2, T, C, G, "f32", name="none", spread=spread, eps=0.0, seed=14)
+
+
+@pytest.mark.parametrize("B,C,G,dtype,act", [(1 << 20, 64, 4, "f32", "none"),
+                                             ((1 << 20) + 3, 32, 4, "bf16", "silu"),
+                                             (270001, 4096, 8, "bf16", "none")])
+def test_positions_of_the_longest_sequences(B, C, G, dtype, act):
+    """A norm of each position by itself for as many positions as the head
+    takes, and of wide ones (a workgroup each).  Rows at both ends against
+    float64, with the bars of `reference`; the parameters' gradients against
+    float64 sums over all of them: 80 e of the magnitudes, and what the parts
+    themselves are off by (16 e of each: |h| and |dy| are within about 6)."""
+    gen = torch.Generator(device=DEV).manual_seed(C)
+    x = torch.randn((B, 1, C), device=DEV, generator=gen, dtype=TYPES[dtype])
+    dy = torch.randn((B, 1, C), device=DEV, generator=gen, dtype=TYPES[dtype])
+    w, b = 1 + 0.3 * torch.randn((2, C), device=DEV, generator=gen)
+    x.requires_grad_(True), w.requires_grad_(True), b.requires_grad_(True)
+    y = encoder.group_norm(x, G, w, b, activation=act)
+    dx, dw, db = torch.autograd.grad(y, (x, w, b), dy)
+    wn, bn = (t.detach().cpu().double().numpy() for t in (w, b))
+    for rows in (slice(0, 300), slice(B - 300, B)):
+        xr, dyr = (t.detach()[rows].cpu().double().numpy() for t in (x, dy))
+        want, tol = reference(xr, wn, bn, [1] * 300, G, 1e-5, act, dyr)
+        for n, got in (("y", y), ("dx", dx)):
+            got = got.detach()[rows].cpu().double().numpy()
+            assert np.all(np.abs(got - want[n]) <= tol[n] + ULP[dtype] * np.abs(want[n])
+                          + 2.0 ** -25), n
+    sums = torch.zeros((4, C), dtype=torch.float64, device=DEV)
+    for xr, dyr in zip(x.detach().split(1 << 15), dy.split(1 << 15)):
+        u = xr.double().view(-1, G, C // G)
+        h = ((u - u.mean(2, keepdim=True)) / torch.sqrt(
+            u.var(2, unbiased=False, keepdim=True) + 1e-5)).view(-1, C)
+        z = h * w.detach().double() + b.detach().double()
+        s = torch.sigmoid(z)
+        dz = dyr.double().view(-1, C) * (s * (1 + z * (1 - s)) if act == "silu" else 1.0)
+        for i, t in enumerate((dz * h, dz)):
+            sums[i] += t.sum(0)
+            sums[2 + i] += t.abs().sum(0)
+    for got, want, size in ((dw, sums[0], sums[2]), (db, sums[1], sums[3])):
+        assert ((got.double() - want).abs() <= (80 + 16 * 6) * E * size).all()
