@@ -301,6 +301,8 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply_sums(GnArgs p, const T *x
                               y + base);
 }
 
+constexpr int kRun = 64;  // positions that are summed in float32
+
 // Partial sums of dz and dz h per channel: part[b][slab][C].
 template <typename T, int V, int ACT, bool ONE>
 __global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, const T *dy,
@@ -311,41 +313,47 @@ __global__ __launch_bounds__(kThreads) void k_gn_bwd_sums(GnArgs p, const T *x, 
   const int v = blockIdx.x % p.tiles * p.cvt + c;
   const int len = max(valid_length(p.lengths, b, p.T), 0);
   const int t1 = min(len, (s + 1) * p.slab);
-  float s1[V], s2[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) s1[i] = s2[i] = 0.f;
+  double s1[V] = {}, s2[V] = {};
   if (r < p.rows && v < p.cv) {
     const Channels<V, ONE> u(p, stats, b, v * V);
     const int64_t base = (int64_t)b * p.T * p.C + (int64_t)v * V;
+    // in float32 over kRun positions, in float64 over those
+    float f1[V], f2[V];
     auto one = [&](const Pack<T, V> &d, const Pack<T, V> &e) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float h = u.h((float)d.v[i], i);
         const float dz = (float)e.v[i] * act_slope<ACT>(h * u.w[i] + u.b[i]);
-        s1[i] += dz;
-        s2[i] += dz * h;
+        f1[i] += dz;
+        f2[i] += dz * h;
       }
     };
-    int t = s * p.slab + r;
-    for (; t + p.rows < t1; t += 2 * p.rows) {
-      Pack<T, V> d[2], e[2];
+    for (int t = s * p.slab + r; t < t1;) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int64_t at = base + (int64_t)(t + k * p.rows) * p.C;
-        d[k] = *reinterpret_cast<const Pack<T, V> *>(x + at);
-        e[k] = *reinterpret_cast<const Pack<T, V> *>(dy + at);
+      for (int i = 0; i < V; ++i) f1[i] = f2[i] = 0.f;
+      const int stop = min(t1, t + kRun * p.rows);
+      for (; t + p.rows < stop; t += 2 * p.rows) {
+        Pack<T, V> d[2], e[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int64_t at = base + (int64_t)(t + k * p.rows) * p.C;
+          d[k] = *reinterpret_cast<const Pack<T, V> *>(x + at);
+          e[k] = *reinterpret_cast<const Pack<T, V> *>(dy + at);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) one(d[k], e[k]);
+      }
+      for (; t < stop; t += p.rows) {
+        const int64_t at = base + (int64_t)t * p.C;
+        one(*reinterpret_cast<const Pack<T, V> *>(x + at),
+            *reinterpret_cast<const Pack<T, V> *>(dy + at));
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) one(d[k], e[k]);
-    }
-    for (; t < t1; t += p.rows) {
-      const int64_t at = base + (int64_t)t * p.C;
-      one(*reinterpret_cast<const Pack<T, V> *>(x + at),
-          *reinterpret_cast<const Pack<T, V> *>(dy + at));
+      for (int i = 0; i < V; ++i) s1[i] += f1[i], s2[i] += f2[i];
     }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) red[threadIdx.x * V + i] = make_float2(s1[i], s2[i]);
+  for (int i = 0; i < V; ++i) red[threadIdx.x * V + i] = make_float2((float)s1[i], (float)s2[i]);
   __syncthreads();
   if (r == 0 && v < p.cv) {
 #pragma unroll

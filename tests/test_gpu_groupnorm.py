@@ -344,3 +344,18 @@ def test_positions_of_the_longest_sequences(B, C, G, dtype, act):
             sums[2 + i] += t.abs().sum(0)
     for got, want, size in ((dw, sums[0], sums[2]), (db, sums[1], sums[3])):
         assert ((got.double() - want).abs() <= (80 + 16 * 6) * E * size).all()
+
+
+def test_sums_over_many_positions():
+    """A thread sums 512 positions of dz here.  dy = 1 + 2^-16 - 2^-23: from
+    256 on a float32 sum drops 2^-16 of it at every position, 128 e in the end.
+    db and mean(d) are within 80 e, and dx = rstd (d - mean(d) - h mean(d h))
+    within 96 e rstd of its exact 0 (the sum of h is 0)."""
+    T, C, c = 1 << 24, 64, 1 + 2.0 ** -16 - 2.0 ** -23
+    x = torch.randn((1, T, C), device=DEV, requires_grad=True)
+    b = torch.zeros(C, device=DEV, requires_grad=True)
+    dy = torch.full((1, T, C), c, device=DEV)
+    dx, db = torch.autograd.grad(encoder.group_norm(x, 8, None, b), (x, b), dy)
+    assert ((db.double() / (T * c) - 1).abs() <= 80 * E).all(), db
+    # rstd is 1 to 1e-3: 2^24 * 8 values of a variance of 1
+    assert float(dx.abs().max()) <= 97 * E
