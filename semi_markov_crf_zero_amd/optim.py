@@ -34,6 +34,11 @@ _numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
 _get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
 
+# an optimizer's state tensors by their bits
+_HELD = {32: operator.itemgetter("exp_avg", "exp_avg_sq"),
+         8: operator.itemgetter("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")}
+
+
 class _Tensor(ctypes.Structure):
     _fields_ = ([(n, ctypes.c_void_p) for n in ("p", "master", "m", "v", "m_scale", "v_scale")]
                 + [("n", ctypes.c_int64), ("first", ctypes.c_int64), ("dtype", ctypes.c_int32),
@@ -231,13 +236,16 @@ class AdamW(torch.optim.Optimizer):
         self._plans = {}
 
     def _plan(self, i, group):
-        """The group's plan, made anew when a storage in it has changed."""
-        ps = group["params"]
+        """The group's plan, made anew when a tensor in it has changed its
+        storage, size, type or layout."""
+        ps, bits = group["params"], group["bits"]
+        held = _HELD[bits]
+        tensors = []
         for p in ps:
             s = self.state[p]
             if "step" not in s:
                 s["step"] = 0
-                if group["bits"] == 8:
+                if bits == 8:
                     s["exp_avg"], s["exp_avg_scale"] = _zeros8(p, torch.float8_e4m3fn)
                     s["exp_avg_sq"], s["exp_avg_sq_scale"] = _zeros8(p, torch.uint8)
                 else:
@@ -245,19 +253,23 @@ class AdamW(torch.optim.Optimizer):
                     s["exp_avg_sq"] = torch.zeros(p.shape, dtype=torch.float32, device=p.device)
                 if group["masters"] and p.dtype != torch.float32:
                     s["master"] = p.detach().float().contiguous()
-        names = ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master")
-        key = [(p.data_ptr(), *(self.state[p][n].data_ptr() if n in self.state[p] else 0 for n in names))
-               for p in ps]
+            tensors.append(p)
+            tensors.extend(held(s))
+            if "master" in s:
+                tensors.append(s["master"])
+        key = (bits, list(map(_data_ptr, tensors)), list(map(_numel, tensors)),
+               list(map(_dtype, tensors)))
         old = self._plans.get(i)
-        if old is not None and old[0] == key:
+        # a plan takes what is contiguous only: making one refuses the rest
+        if old is not None and old[0] == key and all(map(_is_contiguous, tensors)):
             return old[1]
 
         def states(name):
-            if group["bits"] == 8:
+            if bits == 8:
                 return [(self.state[p][name], self.state[p][name + "_scale"]) for p in ps]
             return [self.state[p][name] for p in ps]
 
-        plan = AdamWPlan([p.detach() for p in ps], group["bits"], states("exp_avg"),
+        plan = AdamWPlan([p.detach() for p in ps], bits, states("exp_avg"),
                          states("exp_avg_sq"), [self.state[p].get("master") for p in ps])
         self._plans[i] = (key, plan)
         return plan

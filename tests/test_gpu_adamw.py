@@ -327,3 +327,40 @@ def test_a_copied_optimizer_steps(bits):
     after = p.detach().clone()
     other.step()
     assert torch.equal(twin, after) and torch.equal(p, after)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_parameter_that_changes_its_layout(bits):
+    """The same storage in another order, type or size is another parameter."""
+    hy = dict(lr=1e-2, weight_decay=0.0, bits=bits)
+    p = torch.nn.Parameter(torch.linspace(-1, 1, 300, device=DEV).view(15, 20))
+    opt = optim.AdamW([p], **hy)
+    p.grad = torch.linspace(-2, 1, 300, device=DEV).view(15, 20)
+    opt.step()
+    before = p.detach().clone()
+    p.data = p.data.t()
+    p.grad = torch.ones_like(p)
+    with pytest.raises(ValueError, match="contiguous"):
+        opt.step()
+    assert torch.equal(p.detach().t(), before)
+    # contiguous again: goes on, from the states of its elements in their order
+    p.data = p.data.t()
+    p.grad = torch.ones_like(p)
+    opt.step()
+    assert not torch.equal(p, before) and p.isfinite().all()
+    # another shape of the same elements is the same parameter
+    p.data = p.data.view(10, 30)
+    p.grad = torch.ones_like(p)
+    opt.step()
+
+    q = torch.nn.Parameter(torch.ones(256, device=DEV, dtype=torch.bfloat16))
+    opt = optim.AdamW([q], **hy)
+    q.grad = torch.ones_like(q)
+    opt.step()
+    q.data = q.data.view(torch.float16)  # the bits of 1 - 0.01 in bfloat16
+    start = q.detach().clone()
+    q.grad = torch.ones_like(q)
+    opt.step()
+    # a step with one sign moves a float16 by its learning rate, 1e-2, up to
+    # the roundings of float16 near 2 and of the 8-bit states (2^-4)
+    assert ((start - q).float() - 1e-2).abs().max() <= 2.0 ** -10 + 1e-2 * 2.0 ** -3
