@@ -288,8 +288,7 @@ class AdamW(torch.optim.Optimizer):
             by_step = {}
             for j, p in enumerate(group["params"]):
                 if p.grad is not None:
-                    self.state[p]["step"] += 1
-                    by_step.setdefault(int(self.state[p]["step"]), []).append(j)
+                    by_step.setdefault(int(self.state[p]["step"]) + 1, []).append(j)
             for count, who in by_step.items():
                 grads = [None] * len(group["params"])
                 for j in who:
@@ -297,6 +296,8 @@ class AdamW(torch.optim.Optimizer):
                 b1, b2 = group["betas"]
                 plan.run(grads, count, group["lr"], b1, b2, group["eps"], group["weight_decay"],
                          grad_scale)
+                for j in who:  # after the run: one that is refused does not count
+                    self.state[group["params"][j]]["step"] += 1
         return loss
 
     def load_state_dict(self, state_dict):

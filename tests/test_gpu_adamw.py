@@ -364,3 +364,20 @@ def test_a_parameter_that_changes_its_layout(bits):
     # a step with one sign moves a float16 by its learning rate, 1e-2, up to
     # the roundings of float16 near 2 and of the 8-bit states (2^-4)
     assert ((start - q).float() - 1e-2).abs().max() <= 2.0 ** -10 + 1e-2 * 2.0 ** -3
+
+
+def test_a_refused_step_does_not_count():
+    """What goes on after a refusal goes on as if it had not been tried."""
+    def make():
+        p = torch.nn.Parameter(torch.linspace(-1, 1, 300, device=DEV))
+        p.grad = torch.linspace(2, -1, 300, device=DEV)
+        return p, optim.AdamW([p], lr=1e-2)
+    (p, opt), (q, other) = make(), make()
+    opt.step()
+    other.step()
+    with pytest.raises(ValueError, match="grad_scale"):
+        opt.step(grad_scale=torch.ones(2, device=DEV))
+    assert opt.state[p]["step"] == 1
+    opt.step()
+    other.step()
+    assert opt.state[p]["step"] == 2 and torch.equal(p, q)
