@@ -86,6 +86,12 @@ def _zeros8(p, dtype):
             torch.zeros(-(-p.numel() // BLOCK), dtype=torch.float32, device=p.device))
 
 
+def _overlap(tensors):
+    """Whether two of these contiguous tensors share memory."""
+    at = sorted((t.data_ptr(), t.numel() * t.element_size()) for t in tensors if t.numel())
+    return any(start + size > after for (start, size), (after, _) in zip(at, at[1:]))
+
+
 class AdamWPlan:
     """The step for one list of parameters (one device, contiguous, stepped
     in place).  exp_avg and exp_avg_sq are lists of float32 tensors or, for
@@ -112,9 +118,9 @@ class AdamWPlan:
                     or not p.is_contiguous()):
                 raise ValueError("parameters must be contiguous float32, bfloat16 or float16 "
                                  "tensors on one GPU")
-        at = [p.data_ptr() for p in self.params if p.numel()]
-        if len(set(at)) != len(at):
-            raise ValueError("a parameter is there twice: two steps would race for it")
+        if _overlap(self.params):
+            raise ValueError("a parameter is there twice, whole or in part: two steps would race "
+                             "for it")
         self.masters = list(masters) if masters is not None else [None] * n
         for p, t in zip(self.params, self.masters):
             if t is not None:
@@ -140,6 +146,14 @@ class AdamWPlan:
             for states in (self.exp_avg, self.exp_avg_sq):
                 for p, t in zip(self.params, states):
                     self._check("a state", t, p, torch.float32)
+        held = [t for s in (self.exp_avg, self.exp_avg_sq) for t in s]
+        if bits == 8:
+            held = [t for pair in held for t in pair]
+        # a float32 parameter may be its own master copy
+        held += [t for p, t in zip(self.params, self.masters)
+                 if t is not None and t.data_ptr() != p.data_ptr()]
+        if _overlap(self.params + held):
+            raise ValueError("a state or a master copy is there twice, or is part of another")
         self.numels = [p.numel() for p in self.params]
         self._table()
 

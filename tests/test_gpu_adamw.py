@@ -381,3 +381,20 @@ def test_a_refused_step_does_not_count():
     opt.step()
     other.step()
     assert opt.state[p]["step"] == 2 and torch.equal(p, q)
+
+
+def test_parameters_that_overlap():
+    """A part of a parameter beside it; neighbours in one buffer are two."""
+    flat = torch.ones(512, device=DEV)
+    for params in ([flat, flat[256:]], [flat[100:], flat[:101]], [flat, flat[3:4]],
+                   [flat.view(torch.bfloat16)[:600], flat[299:]]):
+        with pytest.raises(ValueError, match="twice"):
+            optim.AdamWPlan(params)
+    a, b, m = torch.zeros((3, 64), device=DEV)
+    for kw in (dict(exp_avg=[m, m]), dict(exp_avg=[m, a], exp_avg_sq=[torch.zeros_like(m), m])):
+        with pytest.raises(ValueError, match="state"):
+            optim.AdamWPlan([a, b], **kw)
+    optim.AdamWPlan([a, b], masters=[a, None])  # float32: its own master copy
+    plan = optim.AdamWPlan([flat[256:], flat[:256], flat[256:256]])
+    plan.run([torch.ones(256, device=DEV), None, None], 1, lr=1e-2)
+    assert (flat[256:] < 1).all() and (flat[:256] == 1).all()
