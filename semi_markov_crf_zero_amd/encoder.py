@@ -146,6 +146,8 @@ def _linattn_check(q, k, v, log_decay, step):
     if not (1 <= Dk <= MAX_HEAD and 1 <= Dv <= MAX_HEAD):
         raise ValueError("heads are 1 to %d wide" % MAX_HEAD)
     H = max(Hq, Hk, Hv)
+    if max(B, T, H) > MAX_SIZE:
+        raise ValueError("sizes are at most %d" % MAX_SIZE)
     if min(Hq, Hk, Hv) < 1 or H % Hq or H % Hk or H % Hv:
         raise ValueError("the larger number of heads must be a multiple of the others: %s"
                          % [Hq, Hk, Hv])

@@ -567,3 +567,13 @@ def test_what_is_left_where_terms_cancel(dtype):
     (_, _, v), (o, _) = call(rows(3, t1=far, t2=near_), rows(3, t0=ones), rows(3), None)
     dv, = torch.autograd.grad(o, v, rows(3, t1=ones, t2=minus).to(o.dtype))
     near(dv[0, 0, 0, 0], left)
+
+
+def test_sizes_past_31_bits_are_refused():
+    """The library's sizes are ints: 2^32 + 1 streams would be one there."""
+    x = torch.zeros((1, 1, 1), device=DEV).expand((1 << 32) + 1, 1, 1)
+    g = torch.zeros(1, device=DEV)
+    with pytest.raises(ValueError, match="sizes"):
+        encoder.linear_attention_step(x, x, x, g, torch.zeros((1, 1, 1, 1), device=DEV))
+    with pytest.raises(ValueError, match="sizes"):
+        encoder.linear_attention(x[:, None], x[:, None], x[:, None], g)
