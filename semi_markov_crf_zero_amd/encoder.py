@@ -21,7 +21,6 @@ import ctypes
 import functools
 
 import torch
-from torch.autograd.function import once_differentiable
 from torch.autograd.graph import increment_version
 
 from . import binding as bd
@@ -162,14 +161,36 @@ def _strides(t):
     return (s[0], s[1] if len(s) == 4 else 0, s[-2])
 
 
-def _once(backward):
-    """once_differentiable, which turns gradients off around each call, only
-    where they are on (create_graph)."""
-    refusing = once_differentiable(backward)
+class _Refused(torch.autograd.Function):
+    """The first n tensors as they are, depending on the others in a way that
+    is not known: a backward pass through them fails."""
 
+    @staticmethod
+    def forward(ctx, message, n, *tensors):
+        ctx.message = message
+        return tensors[:n]
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(ctx.message)
+
+
+def _once(backward):
+    """A backward pass whose results carry no gradients: where they would be
+    recorded (create_graph), a backward pass through them fails, whether the
+    gradients it came from carry any or not."""
     @functools.wraps(backward)
     def call(ctx, *grads):
-        return (refusing if torch.is_grad_enabled() else backward)(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return backward(ctx, *grads)
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        there = [t for t in out if t is not None]
+        on = [t for t in (*ctx.saved_tensors, *grads) if t is not None and t.requires_grad]
+        there = iter(_Refused.apply("the gradients of the encoder's operators are "
+                                    "once_differentiable: they have no gradients of their own",
+                                    len(there), *there, *on))
+        return tuple(None if t is None else next(there) for t in out)
     return call
 
 

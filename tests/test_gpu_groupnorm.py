@@ -359,3 +359,18 @@ def test_sums_over_many_positions():
     assert ((db.double() / (T * c) - 1).abs() <= 80 * E).all(), db
     # rstd is 1 to 1e-3: 2^24 * 8 values of a variance of 1
     assert float(dx.abs().max()) <= 97 * E
+
+
+@pytest.mark.parametrize("way", ["backward", "grad"])
+def test_second_derivatives_are_refused_beside_others(way):
+    """The gradient of a plain sum: what comes in asks for no gradient, and
+    the penalty also depends on w by a way that is known."""
+    w = torch.full((2, 5, 8), 2.0, device=DEV, requires_grad=True)
+    a = torch.randn((2, 5, 8), device=DEV, requires_grad=True)
+    y = encoder.group_norm(w * a, 2, activation="silu")
+    g, = torch.autograd.grad(y.sum(), a, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        if way == "grad":
+            torch.autograd.grad(g.square().sum(), w)
+        else:
+            g.square().sum().backward()

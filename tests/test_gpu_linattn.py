@@ -577,3 +577,19 @@ def test_sizes_past_31_bits_are_refused():
         encoder.linear_attention_step(x, x, x, g, torch.zeros((1, 1, 1, 1), device=DEV))
     with pytest.raises(ValueError, match="sizes"):
         encoder.linear_attention(x[:, None], x[:, None], x[:, None], g)
+
+
+@pytest.mark.parametrize("way", ["backward", "grad"])
+def test_second_derivatives_are_refused_beside_others(way):
+    """The gradient of a plain sum: what comes in asks for no gradient, and
+    the penalty also depends on w by a way that is known."""
+    w = torch.full((1, 5, 2, 4), 2.0, device=DEV, requires_grad=True)
+    a = torch.randn((1, 5, 2, 4), device=DEV, requires_grad=True)
+    q = w * a
+    o = encoder.linear_attention(q, q, q, torch.full((2,), -0.1, device=DEV))
+    g, = torch.autograd.grad(o.sum(), a, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        if way == "grad":
+            torch.autograd.grad(g.square().sum(), w)
+        else:
+            g.square().sum().backward()
