@@ -145,7 +145,7 @@ def _linattn_check(q, k, v, log_decay, step):
     if not (1 <= Dk <= MAX_HEAD and 1 <= Dv <= MAX_HEAD):
         raise ValueError("heads are 1 to %d wide" % MAX_HEAD)
     H = max(Hq, Hk, Hv)
-    if max(B, T, H) > MAX_SIZE:
+    if B > MAX_SIZE or T > MAX_SIZE or H > MAX_SIZE:
         raise ValueError("sizes are at most %d" % MAX_SIZE)
     if min(Hq, Hk, Hv) < 1 or H % Hq or H % Hk or H % Hv:
         raise ValueError("the larger number of heads must be a multiple of the others: %s"
@@ -274,7 +274,9 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     state [slots, H, Dk, Dv] float32 is a pool; stream b's is state[slots[b]]
     (slots [B] int32, distinct; stream b's own row b by default) and is moved
     in place.  A stream whose slot is outside the pool is idle: its row of
-    the result [B, H, Dv] is 0.  No gradients."""
+    the result [B, H, Dv] is 0.  No gradients: a backward pass through the
+    result fails, and a state that requires a gradient is moved under
+    torch.no_grad() only."""
     dims = _linattn_check(q, k, v, log_decay, True)
     B, _, H, _, _, _, Dk, Dv, _ = dims
     dev = q.device
@@ -284,6 +286,12 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     _check("state", state, dev, torch.float32, (N, H, Dk, Dv))
     if slots is not None:
         _check("slots", slots, dev, torch.int32, (B,))
+    recorded = ()
+    if torch.is_grad_enabled():
+        if state.requires_grad:
+            raise ValueError("a state that requires a gradient cannot be moved in place")
+        if q.requires_grad or k.requires_grad or v.requires_grad:
+            recorded = [t for t in (q, k, v) if t.requires_grad]
     o = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
     if B:
         q, k, v = _rows(q), _rows(k), _rows(v)
@@ -292,6 +300,8 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
         launch(load().semicrf_linattn_step, dev, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
                _ptr(log_decay), _ptr(slots), N, _ptr(state), _ptr(o))
         increment_version(state)  # a backward pass that saved the old states must fail
+    if recorded:
+        return _Refused.apply("linear_attention_step has no gradients", 1, o, *recorded)[0]
     return o
 
 

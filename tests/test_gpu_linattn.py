@@ -593,3 +593,30 @@ def test_second_derivatives_are_refused_beside_others(way):
             torch.autograd.grad(g.square().sum(), w)
         else:
             g.square().sum().backward()
+
+
+def test_a_step_s_missing_gradients_are_noticed():
+    """The result of a step has none: a backward pass through it fails and does
+    not leave q, k and v out; a state that wants one is not moved."""
+    g = torch.full((2,), -0.1, device=DEV)
+    for i in range(3):
+        x = [torch.randn((3, 2, 4), device=DEV) for _ in range(3)]
+        pool = torch.zeros((3, 2, 4, 4), device=DEV)
+        want = encoder.linear_attention_step(*x, g, pool.clone())
+        assert not want.requires_grad
+        x[i].requires_grad_(True)
+        o = encoder.linear_attention_step(*x, g, pool)
+        assert torch.equal(o, want)
+        with pytest.raises(RuntimeError, match="no gradients"):
+            (o.sum() + x[i].sum()).backward()
+        with pytest.raises(RuntimeError, match="no gradients"):
+            torch.autograd.grad(o.sum() + x[i].sum(), x[i])
+        with torch.no_grad():
+            assert not encoder.linear_attention_step(*x, g, pool).requires_grad
+    pool = torch.zeros((3, 2, 4, 4), device=DEV, requires_grad=True)
+    with pytest.raises(ValueError, match="in place"):
+        encoder.linear_attention_step(*x, g, pool)
+    assert not pool.detach().any()
+    with torch.no_grad():
+        encoder.linear_attention_step(*x, g, pool)
+    assert pool.detach().any()
