@@ -55,9 +55,9 @@ __host__ __device__ constexpr int linattn_parts(int dtype) {
 __host__ __device__ constexpr int linattn_chunk(int parts) { return parts > 1 ? 32 : 64; }
 
 // Waves of a workgroup: one for 16 columns of the output.
-inline int linattn_waves(int Dc, bool vec) {
+inline int linattn_waves(int Dc) {
   const int w = (Dc + 15) / 16;
-  return !vec ? 4 : w <= 2 ? 2 : w <= 6 ? w : 8;
+  return w <= 2 ? 2 : w <= 6 ? w : 8;
 }
 // Waves a SIMD is to hold (what the registers are rationed to).  The waves of
 // a workgroup are dealt to the four SIMDs from the first one on, so one of
@@ -629,7 +629,7 @@ semicrf_status_t launch_one(LaArgs p, bool states, hipStream_t st) {
 
 template <typename T, int NP, typename OT, int DA>
 semicrf_status_t launch_nw(const LaArgs &p, bool states, hipStream_t st) {
-  switch (linattn_waves(p.Dc, true)) {
+  switch (linattn_waves(p.Dc)) {
     case 2: return launch_one<T, NP, OT, DA, 2, true>(p, states, st);
     case 3: return launch_one<T, NP, OT, DA, 3, true>(p, states, st);
     case 4: return launch_one<T, NP, OT, DA, 4, true>(p, states, st);
