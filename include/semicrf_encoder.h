@@ -54,7 +54,10 @@ enum { SEMICRF_ACT_NONE = 0, SEMICRF_ACT_SILU = 1, SEMICRF_ACT_GELU = 2, SEMICRF
  * gradient of a shared head is the sum over the heads that read it.  States
  * [B][H][Dk][Dv] float32 contiguous.
  *
- * 1 <= Dk, Dv <= 256; B*H*T < 2^40 elements a tensor in 64-bit offsets.
+ * 1 <= Dk, Dv <= 256 (SEMICRF_ERR_UNSUPPORTED past that); T <= 2^30; B*H <
+ * 2^24 where Dk and Dv are at most 64, 2^23 at most 128, 2^22 above
+ * (SEMICRF_ERR_SHAPE: a launch has at most 2^32 - 1 threads).  Offsets of
+ * elements are 64 bits.
  */
 typedef struct {
     int B, T, H;

@@ -43,6 +43,7 @@ namespace semicrf {
 
 namespace {
 constexpr int kThreads = 256;
+constexpr int64_t kMaxThreads = 0xffffffff;  // of a grid
 }
 
 // xs[s] from the part of segment s to X before segment s + 1, one element of
@@ -277,16 +278,34 @@ semicrf_status_t launch_step(const semicrf_linattn_shape_t &s, const void *q, co
   return launch_status();
 }
 
+// Threads for the Dc columns of a head: tiles of 16 a wave, as launch_nw has
+// them or by fours.
+int column_threads(int Dc) {
+  int most = 0;
+  for (int NW : {linattn_waves(Dc), 4}) {
+    const int n = (Dc + 16 * NW - 1) / (16 * NW) * 64 * NW;
+    if (n > most) most = n;
+  }
+  return most;
+}
+
 semicrf_status_t check(const semicrf_linattn_shape_t *s) {
   if (!s) return SEMICRF_ERR_NULL;
   if (s->B < 1 || s->T < 1 || s->H < 1 || s->Hq < 1 || s->Hk < 1 || s->Hv < 1 || s->Dk < 1 ||
       s->Dv < 1 || s->H % s->Hq || s->H % s->Hk || s->H % s->Hv)
     return SEMICRF_ERR_SHAPE;
-  // a grid counts sequences, heads, four column tiles and the segments, which
-  // are few where those are many; a state's elements over 256 threads
-  if (s->T > 1 << 30 || (int64_t)s->B * s->H * 1024 > 0x7fffffff) return SEMICRF_ERR_SHAPE;
+  if (s->T > 1 << 30) return SEMICRF_ERR_SHAPE;
+  const int64_t heads = (int64_t)s->B * s->H;
+  if (heads * 256 > kMaxThreads) return SEMICRF_ERR_SHAPE;  // the least a head takes
   if (s->Dk > 256 || s->Dv > 256) return SEMICRF_ERR_UNSUPPORTED;
   if (!dtype_ok(s->dtype)) return SEMICRF_ERR_ARG;
+  // segments are few where heads are many, so this counts the chunk kernel's
+  // threads; the scan has one for each element of a state
+  int nseg, seg;
+  segments(s, &nseg, &seg);
+  if (heads * nseg * column_threads(s->Dk > s->Dv ? s->Dk : s->Dv) > kMaxThreads ||
+      (nseg > 1 && heads * s->Dk * s->Dv + kThreads > kMaxThreads))
+    return SEMICRF_ERR_SHAPE;
   return SEMICRF_OK;
 }
 

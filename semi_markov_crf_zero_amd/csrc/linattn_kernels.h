@@ -619,7 +619,6 @@ semicrf_status_t launch_one(LaArgs p, bool states, hipStream_t st) {
   constexpr int L = linattn_chunk(NP);
   p.ctiles = (p.Dc + 16 * NW - 1) / (16 * NW);
   const int64_t grid = (int64_t)p.B * p.H * (states ? p.nseg - 1 : p.nseg) * p.ctiles;
-  if (grid > 0x7fffffff) return SEMICRF_ERR_SHAPE;
   if (states)
     k_linattn_state<T, NP, DA, NW, L, VEC><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
   else

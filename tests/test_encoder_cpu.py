@@ -201,3 +201,16 @@ def test_groupnorm_sizes(lib, kw, code, backward):
     n = ctypes.c_size_t(0)
     assert lib.semicrf_groupnorm_workspace_size(ctypes.byref(gn(**kw)), backward,
                                                 ctypes.byref(n)) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(B=(1 << 24) - 1, H=1, Dk=64, Dv=64), 0), (dict(B=1 << 24, H=1, Dk=64, Dv=64), 2),
+    (dict(B=(1 << 20) - 1, H=8, Dk=128, Dv=33), 0), (dict(B=1 << 20, H=8, Dk=33, Dv=128), 2),
+    (dict(B=(1 << 21) - 1, H=2, Dk=256, Dv=256), 0), (dict(B=1 << 21, H=2, Dk=256, Dv=8), 2),
+    (dict(B=1, T=1 << 30, H=4, Dk=256, Dv=256), 0), (dict(B=1, T=(1 << 30) + 1, H=4), 2),
+])
+@pytest.mark.parametrize("backward", [0, 1])
+def test_linattn_sizes(lib, kw, code, backward):
+    s = lin(**dict(kw, Hq=1, Hk=1, Hv=1))
+    n = ctypes.c_size_t(0)
+    assert lib.semicrf_linattn_workspace_size(ctypes.byref(s), backward, ctypes.byref(n)) == code

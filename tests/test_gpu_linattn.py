@@ -620,3 +620,30 @@ def test_a_step_s_missing_gradients_are_noticed():
     with torch.no_grad():
         encoder.linear_attention_step(*x, g, pool)
     assert pool.detach().any()
+
+
+def test_more_heads_than_two_million():
+    """2^21 + 5 sequences of two positions, written out, and as many streams.
+    `bar32`'s constants; T = 2."""
+    B, D, e = (1 << 21) + 5, 4, math.exp(-0.5)
+    g = torch.full((1,), -0.5, device=DEV)
+    q, k, v, do = (torch.randn((B, 2, 1, D), device=DEV) for _ in range(4))
+    v.requires_grad_(True)
+    o, last = encoder.linear_attention(q, k, v, g, scale=1.0, return_state=True)
+    dv, = torch.autograd.grad(o, v, do)
+    state = torch.zeros((B, 1, D, D), device=DEV)
+    v = v.detach()
+    steps = [encoder.linear_attention_step(q[:, t], k[:, t], v[:, t], g, state, scale=1.0)
+             for t in range(2)]
+    off = []
+    for f in (lambda x: x, torch.abs):
+        (q0, q1), (k0, k1), (v0, v1), (d0, d1) = (f(x.double()).unbind(1) for x in (q, k, v, do))
+        dot = lambda a, b: (a * b).sum(-1, keepdim=True)  # noqa: E731
+        off.append((torch.stack([dot(q0, k0) * v0, e * dot(q1, k0) * v0 + dot(q1, k1) * v1], 1),
+                    e * k0[..., None] * v0[..., None, :] + k1[..., None] * v1[..., None, :],
+                    torch.stack([dot(k0, q0) * d0 + e * dot(k0, q1) * d1, dot(k1, q1) * d1], 1)))
+    c = (D + 160 + 1) * 2.0 ** -24
+    for got, want, size in zip((o, last, dv), *off):
+        assert ((got.double() - want).abs() <= c * size + 1e-30).all()
+    for got, i in ((torch.stack(steps, 1), 0), (state, 1)):
+        assert ((got.double() - off[0][i]).abs() <= c * off[1][i] + 1e-30).all()
