@@ -349,9 +349,13 @@ semicrf_status_t semicrf_linattn_workspace_size(const semicrf_linattn_shape_t *s
   const semicrf_status_t e = check(s);
   if (e != SEMICRF_OK) return e;
   *bytes = state_bytes(s);
-  if (backward)
-    *bytes += share_bytes(s, s->Hq, s->Dk) + share_bytes(s, s->Hk, s->Dk) +
-             share_bytes(s, s->Hv, s->Dv);
+  if (backward) {  // one area: each gradient's parts are summed before the next one's are written
+    size_t most = 0;
+    for (const size_t n : {share_bytes(s, s->Hq, s->Dk), share_bytes(s, s->Hk, s->Dk),
+                           share_bytes(s, s->Hv, s->Dv)})
+      if (n > most) most = n;
+    *bytes += most;
+  }
   return SEMICRF_OK;
 }
 
@@ -400,14 +404,8 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
   if (need && (!workspace || workspace_bytes < need)) return SEMICRF_ERR_WORKSPACE;
   (void)hipGetLastError();
   hipStream_t st = (hipStream_t)stream;
-  char *ws = (char *)workspace;
-  float *xs = (float *)ws;
-  ws += state_bytes(s);
-  float *pq = (float *)ws;
-  ws += share_bytes(s, s->Hq, s->Dk);
-  float *pk = (float *)ws;
-  ws += share_bytes(s, s->Hk, s->Dk);
-  float *pv = (float *)ws;
+  float *const xs = (float *)workspace;
+  float *const part = (float *)((char *)workspace + state_bytes(s));
   const View vq = view(q, s->q_stride, s->H / s->Hq), vk = view(k, s->k_stride, s->H / s->Hk),
              vv = view(v, s->v_stride, s->H / s->Hv);
   const int64_t row = (int64_t)s->H * s->Dv;
@@ -422,7 +420,7 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
   auto set = [&](View a, View b, View c, int Da, int Dc) {
     p.a = a, p.b = b, p.c = c, p.Da = Da, p.Dc = Dc;
   };
-  auto run = [&](void *out, float *part, int heads) {
+  auto run = [&](void *out, int heads) {
     const bool shared = out && heads != s->H;
     p.out = shared ? part : out;
     semicrf_status_t r = launch_linattn(p, s->dtype, shared, st);
@@ -441,7 +439,7 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
     }
     p.x_tr = 1;
     set(vg, vv, vk, s->Dv, s->Dk);
-    e = run(grad_q, pq, s->Hq);
+    e = run(grad_q, s->Hq);
     if (e != SEMICRF_OK) return e;
   }
   p.xs = xs;
@@ -453,13 +451,13 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
   }
   if (grad_v || grad_state_in) {
     p.x_out = grad_state_in;
-    e = run(grad_v, pv, s->Hv);
+    e = run(grad_v, s->Hv);
     if (e != SEMICRF_OK) return e;
   }
   if (grad_k) {
     p.x_tr = 1, p.x_out = nullptr;
     set(vv, vg, vq, s->Dv, s->Dk);
-    e = run(grad_k, pk, s->Hk);
+    e = run(grad_k, s->Hk);
   }
   return e;
 }

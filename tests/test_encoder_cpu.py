@@ -214,3 +214,15 @@ def test_linattn_sizes(lib, kw, code, backward):
     s = lin(**dict(kw, Hq=1, Hk=1, Hv=1))
     n = ctypes.c_size_t(0)
     assert lib.semicrf_linattn_workspace_size(ctypes.byref(s), backward, ctypes.byref(n)) == code
+
+
+def test_linattn_workspace_of_shared_heads(lib):
+    """Parts of one gradient at a time: one float32 row a head, of the widest."""
+    def size(backward, **kw):
+        s, n = lin(B=1, T=1 << 20, H=16, Dk=64, Dv=64, **kw), ctypes.c_size_t(0)
+        assert lib.semicrf_linattn_workspace_size(ctypes.byref(s), backward, ctypes.byref(n)) == 0
+        return n.value
+    part = (1 << 20) * 16 * 64 * 4
+    for kw in (dict(Hq=1, Hk=1, Hv=1), dict(Hq=16, Hk=2, Hv=2), dict(Hq=16, Hk=16, Hv=4)):
+        assert size(1, **kw) - size(0, **kw) == part
+    assert size(1, Hq=16, Hk=16, Hv=16) == size(0, Hq=16, Hk=16, Hv=16)
