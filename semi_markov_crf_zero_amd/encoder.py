@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 
 import torch
 from torch.autograd.graph import increment_version
@@ -263,6 +264,9 @@ def linear_attention(q, k, v, log_decay, lengths=None, state=None, scale=None,
         none = q.sum() + k.sum() + v.sum()  # 0, and part of the graph
         o = none.expand(B, T, H, Dv).clone()
         last = none.float().expand(B, H, Dk, Dv).clone() if state is None else state.clone()
+        if lengths is not None:  # NaN where they are none, as with positions
+            bad = ((lengths < 0) | (lengths > T))[:, None, None, None]
+            last = torch.where(bad, math.nan, last)
     else:
         o, last = LinearAttention.apply(q, k, v, state, log_decay, lengths, dims,
                                         Dk ** -0.5 if scale is None else float(scale))

@@ -647,3 +647,14 @@ def test_more_heads_than_two_million():
         assert ((got.double() - want).abs() <= c * size + 1e-30).all()
     for got, i in ((torch.stack(steps, 1), 0), (state, 1)):
         assert ((got.double() - off[0][i]).abs() <= c * off[1][i] + 1e-30).all()
+
+
+def test_invalid_lengths_of_empty_calls():
+    q = torch.zeros((3, 0, 2, 8), device=DEV)
+    state = torch.ones((3, 2, 8, 8), device=DEV, requires_grad=True)
+    lengths = torch.tensor([0, 1, -1], dtype=torch.int32, device=DEV)
+    _, last = encoder.linear_attention(q, q, q, torch.zeros(2, device=DEV), lengths=lengths,
+                                       state=state, return_state=True)
+    assert torch.equal(last[0], state[0]) and last[1:].isnan().all()
+    g, = torch.autograd.grad(last, state, torch.ones_like(last))
+    assert (g[0] == 1).all() and (g[1:] == 0).all()
