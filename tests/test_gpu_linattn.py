@@ -658,3 +658,53 @@ def test_invalid_lengths_of_empty_calls():
     assert torch.equal(last[0], state[0]) and last[1:].isnan().all()
     g, = torch.autograd.grad(last, state, torch.ones_like(last))
     assert (g[0] == 1).all() and (g[1:] == 0).all()
+
+
+def segments_of(t):
+    """How many segments the sequences are cut into, by the states kept."""
+    B, T, Hq, Dk = t["q"].shape
+    Hk, Hv, Dv = t["k"].shape[2], *t["v"].shape[2:]
+    H = max(Hq, Hk, Hv)
+    n = encoder._workspace_bytes("semicrf_linattn_workspace_size", encoder._LinattnShape,
+                                 (B, T, H, Hq, Hk, Hv, Dk, Dv, encoder.DTYPES[t["q"].dtype], 1.0,
+                                  (0, 0, 0), (0, 0, 0), (0, 0, 0)), 0)
+    return 1 + n // (4 * B * H * Dk * Dv)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("Dk,Dv", [(40, 72), (33, 65), (96, 128), (128, 24), (130, 200), (256, 256),
+                                   (8, 96)])
+def test_widths_over_segments(Dk, Dv, dtype):
+    """Both passes over segments whose states are not square, and whose ends
+    the lengths part."""
+    t = draw(Dk + Dv, 2, 1500, (1, 1, 1), Dk, Dv, dtype, True, decay=[-1.0 / 512])
+    assert segments_of(t) > 1
+    compare(t, dtype, lengths=[1500, 777])
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 2), (1, 3, 3), (2, 2, 1)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_shared_heads_over_segments(heads, dtype):
+    t = draw(31, 2, 1400, heads, 24, 40, dtype, True)
+    assert segments_of(t) > 1
+    compare(t, dtype, lengths=[1400, 513])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("Dk,Dv", [(40, 72), (136, 48)])
+def test_rows_read_by_element_over_segments(Dk, Dv, dtype):
+    """One element past an aligned address, odd strides; NaN past the lengths."""
+    t = draw(32, 2, 1300, (1, 1, 1), Dk, Dv, dtype, True, decay=[-1.0 / 300])
+    assert segments_of(t) > 1
+    lengths = [1300, 640]
+
+    def odd_start(d):
+        out = {}
+        for n in "qkv":
+            x = torch.zeros((2, 1300, 1, d[n].shape[3] + 3), dtype=d[n].dtype, device=DEV)
+            x[..., 1:-2] = d[n]
+            for b, L in enumerate(lengths):
+                x[b, L:] = float("nan")
+            out[n] = x[..., 1:-2]
+        return out
+    compare(t, dtype, lengths=lengths, views=odd_start)
