@@ -398,3 +398,32 @@ def test_parameters_that_overlap():
     plan = optim.AdamWPlan([flat[256:], flat[:256], flat[256:256]])
     plan.run([torch.ones(256, device=DEV), None, None], 1, lr=1e-2)
     assert (flat[256:] < 1).all() and (flat[:256] == 1).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_on_another_stream_and_in_a_graph(bits):
+    """Replays of a captured run step the parameters on, as the same calls do
+    (the step's number is the captured one)."""
+    def make():
+        p, g = tensors(8, [300, 4097, 64], "f32", "f32")
+        return p, g, optim.AdamWPlan(p, bits=bits)
+    (p, g, plan), (q, h, other), (r, k, graphed) = make(), make(), make()
+    plan.run(g, 5, **HYPER)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        other.run(h, 5, **HYPER)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(p, q))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        graphed.run(k, 5, **HYPER)
+    for i in range(4):
+        if i:
+            for a, b in zip(g, k):
+                a.copy_(torch.randn_like(a))
+                b.copy_(a)
+            plan.run(g, 5, **HYPER)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(p, r)), i

@@ -374,3 +374,32 @@ def test_second_derivatives_are_refused_beside_others(way):
             torch.autograd.grad(g.square().sum(), w)
         else:
             g.square().sum().backward()
+
+
+@pytest.mark.parametrize("shape,dtype", [((2, 3000, 64), "bf16"), ((300, 1, 40), "f32")])
+def test_gradients_on_another_stream_and_in_a_graph(shape, dtype):
+    x, dy = torch.randn((2, *shape), device=DEV).to(TYPES[dtype]).unbind(0)
+    x, dy = x.clone().requires_grad_(True), dy.clone()
+    w, b = (torch.randn(shape[2], device=DEV, requires_grad=True) for _ in range(2))
+
+    def call():
+        y = encoder.group_norm(x, 8, w, b, activation="silu")
+        return (y.detach(), *torch.autograd.grad(y, (x, w, b), dy))
+    want = call()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = call()
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(a, e) for a, e in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for i in range(4):
+        with torch.no_grad():
+            x.copy_(torch.randn_like(x))
+            dy.copy_(torch.randn_like(dy))
+        want = call()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, e) for a, e in zip(got, want)), i

@@ -708,3 +708,32 @@ def test_rows_read_by_element_over_segments(Dk, Dv, dtype):
             out[n] = x[..., 1:-2]
         return out
     compare(t, dtype, lengths=lengths, views=odd_start)
+
+
+def test_steps_on_another_stream_and_in_a_graph():
+    """Replays move the pool on, as the same calls do."""
+    gen = torch.Generator(device=DEV).manual_seed(33)
+    q, k, v = (torch.randn((5, 2, 40), device=DEV, generator=gen, dtype=torch.bfloat16)
+               for _ in range(3))
+    g = torch.tensor([-0.1, -0.01], device=DEV)
+    slots = torch.tensor([7, 3, -1, 0, 5], dtype=torch.int32, device=DEV)
+    pool = torch.randn((8, 2, 40, 40), device=DEV, generator=gen)
+    other, graphed = pool.clone(), pool.clone()
+    want = encoder.linear_attention_step(q, k, v, g, pool, slots=slots)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = encoder.linear_attention_step(q, k, v, g, other, slots=slots)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got, want) and torch.equal(other, pool)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = encoder.linear_attention_step(q, k, v, g, graphed, slots=slots)
+    for i in range(4):
+        if i:
+            q.copy_(torch.randn_like(q))
+            slots.copy_(slots.roll(1))
+            want = encoder.linear_attention_step(q, k, v, g, pool, slots=slots)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want) and torch.equal(graphed, pool), i
