@@ -219,12 +219,9 @@ semicrf_status_t launch_states(const LaArgs &p, int dtype, hipStream_t st) {
 
 // Workgroups of the chunk kernel a compute unit holds.
 int resident(int Da, int Dc, int dtype) {
-  const int NP = linattn_parts(dtype), NR = 3, L = linattn_chunk(NP);
-  const int DA = Da <= 128 ? (Da + 31) / 32 * 32 : 256;
+  const int NP = linattn_parts(dtype), DA = Da <= 128 ? (Da + 31) / 32 * 32 : 256;
   const int NW = DA > 128 ? 4 : linattn_waves(Dc);
-  const int P = NP == 1 ? L : L + 4;  // a row of a part of P
-  const int lds = 2 * L * (NP * (2 * DA + 4 + 16 * NW + 16) + NR * P) + 4 * (7 * L + 3);
-  const int by_lds = (int)(163840 / lds), occ = linattn_occupancy(DA, NW);
+  const int by_lds = linattn_by_lds(NP, DA, NW), occ = linattn_occupancy(NP, DA, NW);
   const int by_waves = NW < 4 ? 4 * occ / NW : occ / ((NW + 3) / 4);
   const int n = by_lds < by_waves ? by_lds : by_waves;
   return n < 1 ? 1 : n;

@@ -59,11 +59,30 @@ inline int linattn_waves(int Dc) {
   const int w = (Dc + 15) / 16;
   return w <= 2 ? 2 : w <= 6 ? w : 8;
 }
-// Waves a SIMD is to hold (what the registers are rationed to).  The waves of
-// a workgroup are dealt to the four SIMDs from the first one on, so one of
-// five to eight waves needs two places there: four places hold two of them.
-__host__ __device__ constexpr int linattn_occupancy(int DA, int NW) {
-  return DA <= 64 ? (NW <= 4 ? 3 : 4) : DA <= 128 ? 2 : 1;
+// Elements of bfloat16 in LDS for the tiles of a chunk: A, B, C and P.
+__host__ __device__ constexpr int linattn_tiles(int NP, int DA, int NW) {
+  const int L = linattn_chunk(NP), W = 16 * NW;
+  return L * (NP * (DA + 4 + DA + (W % 32 == 16 ? W : W + 16)) + 3 * (NP == 1 ? L : L + 4));
+}
+// Workgroups a compute unit's LDS holds (the decays beside the tiles).
+__host__ __device__ constexpr int linattn_by_lds(int NP, int DA, int NW) {
+  return 163840 / (2 * linattn_tiles(NP, DA, NW) + 4 * (7 * linattn_chunk(NP) + 3));
+}
+// Waves a SIMD is to hold (what the registers are rationed to), where LDS lets
+// it.  The waves of a workgroup are dealt to the four SIMDs from the first one
+// on, so one of five to eight waves needs two places there: four places hold
+// two of them.
+__host__ __device__ constexpr int linattn_occupancy(int NP, int DA, int NW) {
+  const int waves = (linattn_by_lds(NP, DA, NW) * NW + 3) / 4;
+  const int most = DA <= 64 ? (NW <= 4 ? 3 : 4) : DA <= 128 ? 2 : 1;
+  return NW == 6 || most < waves ? most : waves;
+}
+// Twelve waves of two workgroups of six fill three places a SIMD, and the
+// compiler, which counts them so, would not ration registers to four where it
+// knows their LDS: it is told at the launch.  64 x 96 in bfloat16, 8 sequences
+// of 4096 positions of 4 heads: 49 us in the place of 57.
+__host__ __device__ constexpr bool linattn_lds_at_launch(int DA, int NW) {
+  return NW == 6 && DA <= 64;
 }
 
 // Widths of a launch: Da up to DA (a multiple of 32), NW waves for 16 NW
@@ -416,7 +435,7 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
 // units busy 60 %, the splitting into parts and the longer sums of them.
 template <typename T, int NP, typename OT, int DA, int NW, int L, bool VEC>
 __global__ __launch_bounds__(64 * NW)
-    __attribute__((amdgpu_waves_per_eu(linattn_occupancy(DA, NW)))) void k_linattn(LaArgs p) {
+    __attribute__((amdgpu_waves_per_eu(linattn_occupancy(NP, DA, NW)))) void k_linattn(LaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
   constexpr int KB = DA / 32;
   constexpr int NR = 3;  // parts of P and X
@@ -426,7 +445,12 @@ __global__ __launch_bounds__(64 * NW)
   // without padding where that lets a compute unit hold a workgroup more; with
   // it where the addresses of the other would take registers that are short
   typedef std::conditional_t<NP == 1, ByBoth<L>, ByRow<L>> LP;
-  __shared__ alignas(16) bf16 A[L * (NP * (LA::row + DA + LC::row) + NR * LP::row)];
+  constexpr int kTiles = linattn_tiles(NP, DA, NW);
+  static_assert(kTiles == L * (NP * (LA::row + LB::row + LC::row) + NR * LP::row), "");
+  constexpr bool kAtLaunch = linattn_lds_at_launch(DA, NW);
+  __shared__ alignas(16) bf16 tiles[kAtLaunch ? 1 : kTiles];
+  extern __shared__ __align__(16) unsigned char at_launch[];
+  bf16 *const A = kAtLaunch ? (bf16 *)at_launch : tiles;
   bf16 *const Bm = A + NP * L * LA::row;
   bf16 *const C = Bm + NP * L * DA;
   bf16 *const P = C + NP * L * LC::row;
@@ -622,7 +646,9 @@ semicrf_status_t launch_one(LaArgs p, bool states, hipStream_t st) {
   if (states)
     k_linattn_state<T, NP, DA, NW, L, VEC><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
   else
-    k_linattn<T, NP, OT, DA, NW, L, VEC><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
+    k_linattn<T, NP, OT, DA, NW, L, VEC>
+        <<<(unsigned)grid, 64 * NW, linattn_lds_at_launch(DA, NW) ? 2 * linattn_tiles(NP, DA, NW) : 0,
+           st>>>(p);
   return launch_status();
 }
 
