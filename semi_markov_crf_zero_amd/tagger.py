@@ -72,6 +72,11 @@ class SemiCRFTagger(nn.Module):
         """Emissions [B, T, labels] float32 of x [B, T, F], and the layers'
         states after each sequence.  lengths [B] int32; states, a list as
         returned, continues sequences (causal models)."""
+        if lengths is not None:
+            # the linear layers run over the padding too: what it holds (NaN as well) times
+            # a gradient of 0 must be 0
+            past = torch.arange(x.shape[1], device=x.device) >= lengths[:, None]
+            x = x.masked_fill(past[..., None], 0.0)
         h = self._norm(self.front(x.to(self.dtype)), self.groups, self.weight, self.bias, "silu",
                        lengths, self.causal)
         after = []

@@ -85,3 +85,28 @@ def test_optimizer_follows_a_schedule():
     before = [p.clone() for p in model.parameters()]
     opt.step()
     assert all(torch.equal(a, b) for a, b in zip(before, model.parameters()))
+
+
+@pytest.mark.parametrize("fill", [float("nan"), float("inf"), 1e30])
+@pytest.mark.parametrize("causal,dtype", [(False, torch.float32), (True, torch.float32),
+                                          (True, torch.float16)])
+def test_what_is_past_the_lengths_is_not_used(causal, dtype, fill):
+    """The same loss, gradients and segments whatever it holds."""
+    torch.manual_seed(0)
+    model = tagger.SemiCRFTagger(24, 64, 8, 16, causal=causal, dtype=dtype).to(DEV)
+    x, lengths, gold = tagger.synthetic(5, 80, 24, 8, 16, seed=3)
+    y = x.clone()
+    for b, n in enumerate(lengths.tolist()):
+        y[b, n:] = fill
+    (a, want), (b, got) = (
+        (loss, torch.autograd.grad(loss, list(model.parameters())))
+        for loss in (model.loss(t, lengths, gold).sum() for t in (x, y)))
+    assert torch.isfinite(a) and torch.allclose(a, b, rtol=1e-6, atol=0)
+    for (n, _), g, w in zip(model.named_parameters(), got, want):
+        # 8 roundings of the linear layers' type in a sum of another order
+        unit = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -20
+        assert w.isfinite().all() and g.isfinite().all(), n
+        assert float((g - w).abs().max()) <= 8 * unit * float(w.abs().max()), n
+    s, t = model.decode(x, lengths), model.decode(y, lengths)
+    for k in s:
+        assert torch.equal(s[k], t[k]), k
