@@ -233,7 +233,9 @@ class AdamWPlan:
 class AdamW(torch.optim.Optimizer):
     """torch optimizer over AdamWPlan, one plan a parameter group.  bits: 32
     or 8, how the states are held; masters: keep float32 copies of 16-bit
-    parameters.  Parameters without a gradient are left as they are."""
+    parameters, which follow a parameter that is changed from outside between
+    steps (loaded, clamped; not through .data, which leaves no trace).
+    Parameters without a gradient are left as they are."""
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 1e-2, bits: int = 32, masters: bool = False):
@@ -243,11 +245,11 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError("states are held in 32 bits or in 8")
         super().__init__(params, dict(lr=lr, betas=tuple(betas), eps=eps,
                                       weight_decay=weight_decay, bits=bits, masters=masters))
-        self._plans = {}
+        self._plans, self._versions = {}, {}
 
     def __setstate__(self, state):  # a copy, or from a file: plans are made anew
         super().__setstate__(state)
-        self._plans = {}
+        self._plans, self._versions = {}, {}
 
     def _plan(self, i, group):
         """The group's plan, made anew when a tensor in it has changed its
@@ -286,7 +288,19 @@ class AdamW(torch.optim.Optimizer):
         plan = AdamWPlan([p.detach() for p in ps], bits, states("exp_avg"),
                          states("exp_avg_sq"), [self.state[p].get("master") for p in ps])
         self._plans[i] = (key, plan)
+        self._versions.pop(i, None)
         return plan
+
+    def _follow(self, i, group):
+        """Where a parameter is no longer its master's rounding, it was changed
+        from outside since the last step: the master takes its value."""
+        kept = [p for p in group["params"] if "master" in self.state[p]]
+        now = [p._version for p in kept]
+        for p, version, last in zip(kept, now, self._versions.get(i) or [None] * len(kept)):
+            if version != last:
+                m = self.state[p]["master"]
+                torch.where(m.to(p.dtype) == p, m, p.float(), out=m)
+        return kept
 
     @torch.no_grad()
     def step(self, closure=None, grad_scale=None):
@@ -298,6 +312,7 @@ class AdamW(torch.optim.Optimizer):
             if not group["params"]:
                 continue
             plan = self._plan(i, group)
+            kept = self._follow(i, group) if group["masters"] else ()
             # parameters may have taken different numbers of steps: one run a count
             by_step = {}
             for j, p in enumerate(group["params"]):
@@ -312,6 +327,8 @@ class AdamW(torch.optim.Optimizer):
                          grad_scale)
                 for j in who:  # after the run: one that is refused does not count
                     self.state[group["params"][j]]["step"] += 1
+            if kept:
+                self._versions[i] = [p._version for p in kept]
         return loss
 
     def load_state_dict(self, state_dict):

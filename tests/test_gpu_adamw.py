@@ -427,3 +427,42 @@ def test_on_another_stream_and_in_a_graph(bits):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(p, r)), i
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_masters_follow_parameters_that_are_loaded(dtype):
+    """Weights that are put back between steps are stepped from there; those
+    that were not touched keep their masters' last bits."""
+    hy = dict(lr=1e-3, weight_decay=0.0, masters=True)
+    p, q = (torch.nn.Parameter(torch.linspace(-1, 1, 300, device=DEV).to(dtype)) for _ in range(2))
+    opt = optim.AdamW([p, q], **hy)
+    best = p.detach().clone()
+    for _ in range(3):
+        p.grad, q.grad = torch.ones_like(p), torch.ones_like(q)
+        opt.step()
+    kept = opt.state[q]["master"].clone()
+    with torch.no_grad():
+        p.copy_(best)
+        p[100:200] = q[100:200]  # these are their masters' roundings as before
+        q.copy_(q.clone())       # a new version, the same values
+    old = opt.state[p]["master"].clone()
+    same = old.to(dtype) == best  # moved by less than the type shows: still its rounding
+    assert not same.all()
+    start = torch.where(same, old, best.float())
+    start[100:200] = old[100:200]
+    opt.step()
+    # steps of one sign move by the learning rate, to 2^-20 of 1
+    assert float((opt.state[p]["master"] - (start - 1e-3)).abs().max()) <= 2.0 ** -20
+    assert float((opt.state[q]["master"] - (kept - 1e-3)).abs().max()) <= 2.0 ** -20
+    assert torch.equal(p, opt.state[p]["master"].to(dtype))
+    # a state that is loaded goes with the weights it was saved with, in either order
+    saved, weights = copy.deepcopy(opt.state_dict()), [t.detach().clone() for t in (p, q)]
+    opt.step()
+    after = [t.detach().clone() for t in (p, q)]
+    opt.step()
+    opt.load_state_dict(saved)
+    with torch.no_grad():
+        for t, w in zip((p, q), weights):
+            t.copy_(w)
+    opt.step()
+    assert torch.equal(p, after[0]) and torch.equal(q, after[1])
