@@ -184,8 +184,20 @@ class AdamWPlan:
         if rc:
             raise bd.SemiCRFError(rc, "semicrf_adamw_table")
         self.table = self.host.to(self.dev)
+        self._streams = {torch.cuda.current_stream(self.dev).cuda_stream}
         self._host, self._device = self.host.data_ptr(), self.table.data_ptr()
         self._dtypes = [], b""
+
+    def _use(self, stream):
+        """Another stream reads the table and moves the states: should the plan
+        go, their memory waits for it."""
+        current = torch.cuda.current_stream(self.dev)
+        held = [t for s in (self.exp_avg, self.exp_avg_sq) for t in s]
+        if self.bits == 8:
+            held = [t for pair in held for t in pair]
+        for t in (self.table, *held, *(t for t in self.masters if t is not None)):
+            t.record_stream(current)
+        self._streams.add(stream)
 
     def run(self, grads, step: int, lr: float = 1e-3, beta1: float = 0.9, beta2: float = 0.999,
             eps: float = 1e-8, weight_decay: float = 1e-2, grad_scale=None):
@@ -224,6 +236,9 @@ class AdamWPlan:
         if grad_scale is not None and (grad_scale.device != self.dev or grad_scale.numel() != 1
                                        or grad_scale.dtype != torch.float32):
             raise ValueError("grad_scale must be one float32 on %s" % self.dev)
+        stream = torch._C._cuda_getCurrentRawStream(self.dev.index)
+        if stream not in self._streams:
+            self._use(stream)
         launch(load().semicrf_adamw_step, self.dev, self._host, self._device, at.buffer_info()[0],
                types, len(grads), self.bits, int(step), lr, beta1, beta2, eps, weight_decay,
                None if grad_scale is None else grad_scale.data_ptr())

@@ -466,3 +466,25 @@ def test_masters_follow_parameters_that_are_loaded(dtype):
             t.copy_(w)
     opt.step()
     assert torch.equal(p, after[0]) and torch.equal(q, after[1])
+
+
+def test_a_plan_that_goes_while_another_stream_uses_it():
+    """Its table and states are not handed out again before that stream has
+    passed the step."""
+    p, g = tensors(9, [5000, 300], "f32", "f32")
+    plan = optim.AdamWPlan(p)
+    sizes = [plan.table.numel(), 4 * 5000, 4 * 300]
+    held = {t.data_ptr() for t in (plan.table, *plan.exp_avg, *plan.exp_avg_sq)}
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+        plan.run(g, 1, **HYPER)
+    del plan
+    new = [torch.full((n,), 255, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(3)]
+    assert not s.query()  # else the check below says nothing
+    assert not held & {t.data_ptr() for t in new}
+    s.synchronize()
+    want, other = tensors(9, [5000, 300], "f32", "f32")
+    optim.AdamWPlan(want).run(other, 1, **HYPER)
+    assert all(torch.equal(a, b) for a, b in zip(p, want))
