@@ -151,7 +151,7 @@ def _linattn_check(q, k, v, log_decay, step):
     if min(Hq, Hk, Hv) < 1 or H % Hq or H % Hk or H % Hv:
         raise ValueError("the larger number of heads must be a multiple of the others: %s"
                          % [Hq, Hk, Hv])
-    if log_decay.requires_grad:
+    if log_decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("log_decay is a constant of the model: it gets no gradient")
     _check("log_decay", log_decay, dev, torch.float32, (H,))
     return B, T, H, Hq, Hk, Hv, Dk, Dv, DTYPES[dtype]

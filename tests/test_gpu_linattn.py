@@ -737,3 +737,18 @@ def test_steps_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(graphed, pool), i
+
+
+def test_decays_that_ask_for_gradients_nobody_records():
+    """Refused while gradients are recorded (there is none to give), taken
+    where they are not."""
+    g = torch.full((2,), -0.1, device=DEV, requires_grad=True)
+    q = torch.randn((1, 5, 2, 4), device=DEV)
+    with torch.no_grad():
+        o = encoder.linear_attention(q, q, q, g)
+        s = encoder.linear_attention_step(q[:, 0], q[:, 0], q[:, 0], g,
+                                          torch.zeros((1, 2, 4, 4), device=DEV))
+    assert torch.equal(o, encoder.linear_attention(q, q, q, g.detach()))
+    assert s.shape == (1, 2, 4)
+    with pytest.raises(ValueError, match="log_decay"):
+        encoder.linear_attention(q, q, q, g)
