@@ -110,3 +110,26 @@ def test_what_is_past_the_lengths_is_not_used(causal, dtype, fill):
     s, t = model.decode(x, lengths), model.decode(y, lengths)
     for k in s:
         assert torch.equal(s[k], t[k]), k
+
+
+def test_the_longest_sequence():
+    """2^20 positions in one call and in three that continue each other: the
+    same sums in another order, 1e-4 of the emissions' scale, and a loss over
+    all of them with finite gradients."""
+    torch.manual_seed(0)
+    model = tagger.SemiCRFTagger(8, 32, 4, 8, heads=2, groups=4, causal=True).to(DEV)
+    T = 1 << 20
+    x = torch.randn((1, T, 8), device=DEV)
+    with torch.no_grad():
+        whole, end = model.emissions(x)
+        parts, states = [], None
+        for a, b in ((0, 300001), (300001, 999999), (999999, T)):
+            o, states = model.emissions(x[:, a:b], states=states)
+            parts.append(o)
+    scale = float(whole.abs().max())
+    assert float((torch.cat(parts, 1) - whole).abs().max()) <= 1e-4 * scale
+    for s, e in zip(states, end):
+        assert float((s - e).abs().max()) <= 1e-4 * float(e.abs().max())
+    o, _ = model.emissions(x, torch.tensor([T - 5], dtype=torch.int32, device=DEV))
+    o.square().mean().backward()
+    assert all(p.grad is None or p.grad.isfinite().all() for p in model.parameters())
