@@ -29,7 +29,7 @@ BLOCK = 256  # elements that share one scale of an 8-bit state
 MOMENT_TYPES = {torch.float8_e4m3fn: 0, torch.uint8: 1}  # codes of m; of the root of v
 
 
-_dtype = operator.attrgetter("dtype")
+_dtype, _nbytes = operator.attrgetter("dtype"), operator.attrgetter("nbytes")
 _numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
 _get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
@@ -88,8 +88,9 @@ def _zeros8(p, dtype):
 
 def _overlap(tensors):
     """Whether two of these contiguous tensors share memory."""
-    at = sorted((t.data_ptr(), t.numel() * t.element_size()) for t in tensors if t.numel())
-    return any(start + size > after for (start, size), (after, _) in zip(at, at[1:]))
+    at = sorted((start, start + size) for start, size in
+                zip(map(_data_ptr, tensors), map(_nbytes, tensors)) if size)
+    return any(end > start for (_, end), (start, _) in zip(at, at[1:]))
 
 
 class AdamWPlan:
@@ -118,9 +119,6 @@ class AdamWPlan:
                     or not p.is_contiguous()):
                 raise ValueError("parameters must be contiguous float32, bfloat16 or float16 "
                                  "tensors on one GPU")
-        if _overlap(self.params):
-            raise ValueError("a parameter is there twice, whole or in part: two steps would race "
-                             "for it")
         self.masters = list(masters) if masters is not None else [None] * n
         for p, t in zip(self.params, self.masters):
             if t is not None:
@@ -153,7 +151,9 @@ class AdamWPlan:
         held += [t for p, t in zip(self.params, self.masters)
                  if t is not None and t.data_ptr() != p.data_ptr()]
         if _overlap(self.params + held):
-            raise ValueError("a state or a master copy is there twice, or is part of another")
+            raise ValueError("a parameter is there twice, whole or in part: two steps would race "
+                             "for it" if _overlap(self.params) else
+                             "a state or a master copy is there twice, or is part of another")
         self.numels = [p.numel() for p in self.params]
         self._table()
 
