@@ -15,15 +15,17 @@
 // Bound by HBM: a forward pass reads x twice and writes y, a backward pass
 // reads x and dy twice and writes dx; what the first pass left in the caches
 // serves the second in part.  Measured: 2^20 positions of 64 channels in
-// float32, sums 62 us (4.3 TB/s), result 87 us (6.2 TB/s of reads and writes);
-// 16 sequences of 4096 positions (three quarters of them valid) of 256
-// channels in bfloat16 with SiLU, forward 8 + 4 + 15 us, backward 20 + 4 + 22 +
-// 4 us.  Fewer than eight positions a thread cost more in their channels'
+// float32, sums 60 to 78 us (4.5 to 3.5 TB/s), result 88 us (6.1 TB/s of reads
+// and writes); 16 sequences of 4096 positions (three quarters of them valid) of
+// 256 channels in bfloat16 with SiLU, forward 9 + 4 + 15 us, backward 22 + 5 +
+// 21 + 4 us.  Fewer than eight positions a thread cost more in their channels'
 // parameters than they give (result 21 us at four, 15 at eight, 14.5 at 16).
 //
 // Short sequences (a norm of each position by itself above all) take another
 // way: a workgroup holds NS whole sequences, a stretch of memory without
-// gaps, in LDS, so x is read once, whatever C and the groups are.
+// gaps, in LDS, so x is read once, whatever C and the groups are.  Positions
+// past a length lie in the stretch: they are loaded and then left out by a
+// select.
 //
 // Sums.  mean and var come from sums of (x - pivot) and its square in
 // float64, the pivot the group's first element: the subtraction takes the
@@ -301,7 +303,10 @@ __global__ __launch_bounds__(kThreads) void k_gn_apply_sums(GnArgs p, const T *x
                               y + base);
 }
 
-constexpr int kRun = 64;  // positions that are summed in float32
+// Positions a thread sums in float32 before it goes on in float64; without an
+// end their rounding grows with the sequence.  16 x 4096 x 256 in bfloat16: 21.5
+// us, 20.5 without the second level.
+constexpr int kRun = 64;
 
 // Partial sums of dz and dz h per channel: part[b][slab][C].
 template <typename T, int V, int ACT, bool ONE>

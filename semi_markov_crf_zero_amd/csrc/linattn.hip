@@ -35,8 +35,8 @@
 // 2^20 positions of 4 heads.  Without it a head would be one workgroup: 4 of
 // 256 compute units, 389 ms in the place of 0.73.
 //
-// Positions past the length are loaded as zeros (a select, so NaN there
-// stays out) and their rows of the output are written as 0.
+// Positions past the length are not loaded (zeros stand in their place, so
+// NaN there stays out) and their rows of the output are written as 0.
 #include "linattn_kernels.h"
 
 namespace semicrf {

@@ -357,7 +357,7 @@ __device__ __forceinline__ void add_chunk(f4 *X, const bf16 *Bm, const Frag<NP> 
 // Parts of X: one workgroup of NW waves per segment but the last, 16 NW
 // columns.  Writes xs[segment]; a segment past the length leaves zeros.  Bound
 // by HBM: 1.07 GB of keys and values (2^20 positions, 4 heads of 64 + 64,
-// bfloat16) in 205 to 220 us, 5 TB/s.
+// bfloat16) in 211 to 225 us, 5 TB/s.
 template <typename T, int NP, int DA, int NW, int L, bool VEC>
 __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
@@ -426,12 +426,13 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
 // A wave keeps its 16 columns of X in accumulators from chunk to chunk and
 // reads them as operands in place; P goes through LDS, as every wave needs all
 // of it.  At 64 x 64 in bfloat16 a chunk of 64 positions is 24 KB read and 8
-// written against about 1000 matrix cycles, 1600 LDS cycles and 500 vector
+// written against about 1250 matrix cycles, 1900 LDS cycles and 690 vector
 // instructions a wave: three workgroups a compute unit (54 KB of LDS, 161
-// registers) leave HBM as the bound.  Measured, 2^20 positions of 4 heads:
-// 471 us at best, 4.6 TB/s of 2.15 GB read and written (a large copy: 5.1);
-// matrix cores busy 27 %, vector units 48 %, LDS 52 % (10 % conflicts).  In
-// float32 (40 x 72 wide) 132 us for 330 MB: two workgroups of five waves, vector
+// registers), bound by HBM and nearly by the vector units.  Measured, 2^20
+// positions of 4 heads: 500 us beside the states' 225 in calls one after
+// another, 4.3 TB/s of 2.15 GB read and written (a large copy: 5.1); matrix
+// cores busy 31 %, vector units 60 %, LDS 56 % (10 % conflicts).  In float32
+// (40 x 72 wide) 126 to 133 us for 330 MB: two workgroups of five waves, vector
 // units busy 60 %, the splitting into parts and the longer sums of them.
 template <typename T, int NP, typename OT, int DA, int NW, int L, bool VEC>
 __global__ __launch_bounds__(64 * NW)

@@ -7,13 +7,13 @@ single-token form, and group norm with an activation, channels last.
     o = linear_attention_step(q, k, v, log_decay, state, slots=slots)
 
 The first two carry gradients (torch.autograd.Function over the library's
-backward entry points; a gradient of a gradient is refused); the step moves a pool of states in place.  Tensors
-are CUDA (HIP) tensors, float32, bfloat16 or float16; states, norms' weights
+backward entry points; a gradient of a gradient is refused); the step moves a
+pool of states in place and carries none.  Tensors are CUDA (HIP) tensors, float32, bfloat16 or float16; states, norms' weights
 and decays are float32, lengths and slots int32.  Outputs and workspaces are
 allocated with torch on the input's device and the work is enqueued on
 torch's current stream.  Positions at or past a sequence's length are never
-read and their rows of every output and gradient are 0; a length outside
-[0, T] gives NaN outputs and zero gradients.  There is no CPU fallback.
+read into any result (they may hold NaN) and their rows of every output and
+gradient are 0; a length outside [0, T] gives NaN outputs and zero gradients.  There is no CPU fallback.
 """
 from __future__ import annotations
 
