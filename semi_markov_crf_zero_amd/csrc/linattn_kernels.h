@@ -429,11 +429,11 @@ __global__ __launch_bounds__(64 * NW) void k_linattn_state(LaArgs p) {
 // written against about 1250 matrix cycles, 1900 LDS cycles and 690 vector
 // instructions a wave: three workgroups a compute unit (54 KB of LDS, 161
 // registers), bound by HBM and nearly by the vector units.  Measured, 2^20
-// positions of 4 heads: 500 us beside the states' 225 in calls one after
-// another, 4.3 TB/s of 2.15 GB read and written (a large copy: 5.1); matrix
-// cores busy 31 %, vector units 60 %, LDS 56 % (10 % conflicts).  In float32
-// (40 x 72 wide) 126 to 133 us for 330 MB: two workgroups of five waves, vector
-// units busy 60 %, the splitting into parts and the longer sums of them.
+// positions of 4 heads: 529 us at best, 4.1 TB/s of 2.15 GB read and written (a
+// large copy: 5.1); matrix cores busy 31 %, vector units 60 %, LDS 56 % (10 %
+// conflicts).  In float32 (40 x 72 wide) 126 to 133 us for 330 MB: two
+// workgroups of five waves, vector units busy 60 %, the splitting into parts
+// and the longer sums of them.
 template <typename T, int NP, typename OT, int DA, int NW, int L, bool VEC>
 __global__ __launch_bounds__(64 * NW)
     __attribute__((amdgpu_waves_per_eu(linattn_occupancy(NP, DA, NW)))) void k_linattn(LaArgs p) {
