@@ -1,11 +1,12 @@
 // encoder.h -- element types and small helpers shared by the encoder's and
-// the optimiser's kernels (linattn.hip, groupnorm.hip, adamw.hip).
+// the optimiser's kernels (linattn.hip, groupnorm.hip, adamw.hip, delta.hip,
+// rotary.hip, gradnorm.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "semicrf_encoder.h"
+#include "semicrf_layer.h"
 
 namespace semicrf {
 
@@ -20,6 +21,19 @@ __host__ inline bool dtype_ok(int dtype) { return dtype >= SEMICRF_F32 && dtype 
 inline semicrf_status_t launch_status() {
   return hipGetLastError() == hipSuccess ? SEMICRF_OK : SEMICRF_ERR_HIP;
 }
+
+// One tensor as the kernels read it: element strides of batch, position and
+// head, and how many heads of the call share one of its heads.
+struct View {
+  const void *p;
+  int64_t sb, st, sh;
+  int share;
+};
+
+// Sums over the heads that share one: part [rows][H][D] float32 to out
+// [rows][heads][D] of type dtype (linattn.hip).
+semicrf_status_t share_sum(int dtype, int64_t rows, int H, int heads, int D, const float *part,
+                           void *out, hipStream_t st);
 
 // Valid positions of sequence b: its length, or -1 for one outside [0, T].
 __device__ __forceinline__ int valid_length(const int32_t *lengths, int b, int T) {

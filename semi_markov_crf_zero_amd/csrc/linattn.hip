@@ -99,6 +99,19 @@ __global__ __launch_bounds__(256) void k_share_sum(const float *part, T *out, in
   }
 }
 
+semicrf_status_t share_sum(int dtype, int64_t rows, int H, int heads, int D, const float *part,
+                           void *out, hipStream_t st) {
+  const int64_t n = rows * heads * D;
+  const unsigned grid = (unsigned)(n < 256 * 8192 ? (n + 255) / 256 : 8192);
+  const int share = H / heads;
+  switch (dtype) {
+    case SEMICRF_F32: k_share_sum<<<grid, 256, 0, st>>>(part, (float *)out, rows, H, share, D); break;
+    case SEMICRF_BF16: k_share_sum<<<grid, 256, 0, st>>>(part, (bf16 *)out, rows, H, share, D); break;
+    default: k_share_sum<<<grid, 256, 0, st>>>(part, (f16 *)out, rows, H, share, D);
+  }
+  return launch_status();
+}
+
 // One position: a workgroup per stream and head.  Bound by the state's bytes:
 // 256 streams of 16 heads of 128 x 128, 537 MB, 114 us, 4.8 TB/s; 4 streams of
 // 4 heads of 64 x 64 5.1 us, a launch.  The state is read and written once, V
@@ -315,23 +328,6 @@ size_t share_bytes(const semicrf_linattn_shape_t *s, int heads, int D) {
 
 View view(const void *p, const int64_t *st, int share) { return {p, st[0], st[1], st[2], share}; }
 
-semicrf_status_t share_sum(const semicrf_linattn_shape_t *s, const float *part, void *out,
-                           int heads, int D, hipStream_t st) {
-  const int64_t rows = (int64_t)s->B * s->T, n = rows * heads * D;
-  const unsigned grid = (unsigned)(n < 256 * 8192 ? (n + 255) / 256 : 8192);
-  const int share = s->H / heads;
-  switch (s->dtype) {
-    case SEMICRF_F32:
-      k_share_sum<<<grid, 256, 0, st>>>(part, (float *)out, rows, s->H, share, D);
-      break;
-    case SEMICRF_BF16:
-      k_share_sum<<<grid, 256, 0, st>>>(part, (bf16 *)out, rows, s->H, share, D);
-      break;
-    default: k_share_sum<<<grid, 256, 0, st>>>(part, (f16 *)out, rows, s->H, share, D);
-  }
-  return launch_status();
-}
-
 }  // namespace
 
 }  // namespace semicrf
@@ -421,7 +417,8 @@ semicrf_status_t semicrf_linattn_bwd(const semicrf_linattn_shape_t *s, const voi
     const bool shared = out && heads != s->H;
     p.out = shared ? part : out;
     semicrf_status_t r = launch_linattn(p, s->dtype, shared, st);
-    if (r == SEMICRF_OK && shared) r = share_sum(s, part, out, heads, p.Dc, st);
+    if (r == SEMICRF_OK && shared)
+      r = share_sum(s->dtype, (int64_t)s->B * s->T, s->H, heads, p.Dc, part, out, st);
     return r;
   };
   if (grad_q) {

@@ -9,14 +9,6 @@
 
 namespace semicrf {
 
-// One tensor as the kernels read it: element strides of batch, position and
-// head, and how many heads of the call share one of its heads.
-struct View {
-  const void *p;
-  int64_t sb, st, sh;
-  int share;
-};
-
 struct LaArgs {
   View a, b, c;
   const float *log_decay;

@@ -1,14 +1,19 @@
 """The encoder's operators over libsemicrf.so (the C ABI in
-include/semicrf_encoder.h): linear attention with a decay for each head, its
-single-token form, and group norm with an activation, channels last.
+include/semicrf_encoder.h and semicrf_layer.h): linear attention with a decay
+for each head, the gated delta rule (a decay for each position, writes that
+take out what was there), their single-token forms, rotary positions, and
+group norm with an activation, channels last.
 
     o = linear_attention(q, k, v, log_decay, lengths=lengths)
-    y = group_norm(x, groups, weight, bias, lengths=lengths, activation="silu")
     o = linear_attention_step(q, k, v, log_decay, state, slots=slots)
+    o = gated_delta(q, k, v, log_decay, beta, lengths=lengths)
+    o = gated_delta_step(q, k, v, log_decay, beta, state, slots=slots)
+    q, k = rotary(q, k, rotary_frequencies(64, device=q.device))
+    y = group_norm(x, groups, weight, bias, lengths=lengths, activation="silu")
 
-The first two carry gradients (torch.autograd.Function over the library's
-backward entry points; a gradient of a gradient is refused); the step moves a
-pool of states in place and carries none.  Tensors are CUDA (HIP) tensors, float32, bfloat16 or float16; states, norms' weights
+The operators over sequences carry gradients (torch.autograd.Function over the
+library's backward entry points; a gradient of a gradient is refused); a step
+moves a pool of states in place and carries none.  Tensors are CUDA (HIP) tensors, float32, bfloat16 or float16; states, norms' weights
 and decays are float32, lengths and slots int32.  Outputs and workspaces are
 allocated with torch on the input's device and the work is enqueued on
 torch's current stream.  Positions at or past a sequence's length are never
@@ -31,9 +36,17 @@ EXPORTS = (
     "semicrf_linattn_step", "semicrf_groupnorm_workspace_size", "semicrf_groupnorm_fwd",
     "semicrf_groupnorm_bwd",
 )
+# declared in semicrf_layer.h
+LAYER_EXPORTS = (
+    "semicrf_delta_workspace_size", "semicrf_delta_fwd", "semicrf_delta_bwd",
+    "semicrf_delta_step", "semicrf_rotary",
+)
 DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 ACTIVATIONS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3}
-MAX_HEAD = 256  # the widest Dk and Dv
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+MAX_HEAD = 256  # the widest Dk and Dv of linear attention
+MAX_DELTA_HEAD = 128  # of the gated delta rule
+MAX_TURNED = 8192  # the widest row rotary positions turn
 MAX_SIZE = 2 ** 31 - 1  # of a dimension: the library's int
 
 
@@ -48,6 +61,13 @@ class _GroupnormShape(ctypes.Structure):
                 + [("eps", ctypes.c_float)])
 
 
+class _RotaryShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "T", "heads", "heads2", "D", "turn", "dtype",
+                                             "layout", "positions", "inverse")]
+                + [("scale", ctypes.c_float)]
+                + [(n, ctypes.c_int64 * 3) for n in ("stride", "stride2")])
+
+
 _lib = None
 
 
@@ -57,7 +77,7 @@ def load():
     if _lib is None:
         lib = bd.load()
         P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-        for name in ("linattn", "groupnorm"):
+        for name in ("linattn", "groupnorm", "delta"):
             f = getattr(lib, "semicrf_%s_workspace_size" % name)
             f.argtypes, f.restype = [P, I, ctypes.POINTER(Z)], I
         lib.semicrf_linattn_fwd.argtypes = [P] * 9 + [P, Z, P]
@@ -65,7 +85,11 @@ def load():
         lib.semicrf_linattn_step.argtypes = [P] * 6 + [I, P, P, P]
         lib.semicrf_groupnorm_fwd.argtypes = [P] * 7 + [P, Z, P]
         lib.semicrf_groupnorm_bwd.argtypes = [P] * 10 + [P, Z, P]
-        for name in EXPORTS:
+        lib.semicrf_delta_fwd.argtypes = [P] * 10 + [P, Z, P]
+        lib.semicrf_delta_bwd.argtypes = [P] * 16 + [P, Z, P]
+        lib.semicrf_delta_step.argtypes = [P] * 7 + [I, P, P, P]
+        lib.semicrf_rotary.argtypes = [P] * 8
+        for name in EXPORTS + LAYER_EXPORTS:
             getattr(lib, name).restype = I
         _lib = lib
     return _lib
@@ -123,9 +147,9 @@ def _rows(t):
     return t if t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
 
 
-def _linattn_check(q, k, v, log_decay, step):
-    """Checks q, k, v ([B, T, heads, D], or [B, heads, D] for a step) and
-    log_decay; B, T, H, Hq, Hk, Hv, Dk, Dv, dtype."""
+def _heads_check(q, k, v, step, most):
+    """Checks q, k, v ([B, T, heads, D], or [B, heads, D] for a step), heads
+    up to `most` wide; B, T, H, Hq, Hk, Hv, Dk, Dv, dtype."""
     _check_device(q)
     dev, dtype = q.device, q.dtype
     dims = 3 if step else 4
@@ -143,18 +167,50 @@ def _linattn_check(q, k, v, log_decay, step):
         raise ValueError("q, k and v must have the same B")
     if Dk2 != Dk:
         raise ValueError("q and k must have the same width")
-    if not (1 <= Dk <= MAX_HEAD and 1 <= Dv <= MAX_HEAD):
-        raise ValueError("heads are 1 to %d wide" % MAX_HEAD)
+    if not (1 <= Dk <= most and 1 <= Dv <= most):
+        raise ValueError("heads are 1 to %d wide" % most)
     H = max(Hq, Hk, Hv)
     if B > MAX_SIZE or T > MAX_SIZE or H > MAX_SIZE:
         raise ValueError("sizes are at most %d" % MAX_SIZE)
     if min(Hq, Hk, Hv) < 1 or H % Hq or H % Hk or H % Hv:
         raise ValueError("the larger number of heads must be a multiple of the others: %s"
                          % [Hq, Hk, Hv])
+    return B, T, H, Hq, Hk, Hv, Dk, Dv, DTYPES[dtype]
+
+
+def _linattn_check(q, k, v, log_decay, step):
+    dims = _heads_check(q, k, v, step, MAX_HEAD)
     if log_decay.requires_grad and torch.is_grad_enabled():
         raise ValueError("log_decay is a constant of the model: it gets no gradient")
-    _check("log_decay", log_decay, dev, torch.float32, (H,))
-    return B, T, H, Hq, Hk, Hv, Dk, Dv, DTYPES[dtype]
+    _check("log_decay", log_decay, q.device, torch.float32, (dims[2],))
+    return dims
+
+
+def _delta_check(q, k, v, log_decay, beta, step):
+    """As _linattn_check, with the gates [B, T, H] (or [B, H]); the gates
+    contiguous."""
+    dims = _heads_check(q, k, v, step, MAX_DELTA_HEAD)
+    B, T, H = dims[:3]
+    gates = []
+    for name, t in (("log_decay", log_decay), ("beta", beta)):
+        t = t.contiguous()
+        _check(name, t, q.device, torch.float32, (B, H) if step else (B, T, H))
+        gates.append(t)
+    return dims, *gates
+
+
+def _pool_check(state, slots, dims, dev):
+    """Checks a pool of states and the streams' rows; the number of rows."""
+    B, _, H, _, _, _, Dk, Dv, _ = dims
+    if state.dim() != 4 or not 1 <= state.shape[0] <= MAX_SIZE:
+        raise ValueError("state must be [slots, H, Dk, Dv] with 1 to %d slots" % MAX_SIZE)
+    N = state.shape[0]
+    _check("state", state, dev, torch.float32, (N, H, Dk, Dv))
+    if slots is not None:
+        _check("slots", slots, dev, torch.int32, (B,))
+    if state.requires_grad and torch.is_grad_enabled():
+        raise ValueError("a state that requires a gradient cannot be moved in place")
+    return N
 
 
 def _strides(t):
@@ -284,16 +340,9 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     dims = _linattn_check(q, k, v, log_decay, True)
     B, _, H, _, _, _, Dk, Dv, _ = dims
     dev = q.device
-    if state.dim() != 4 or not 1 <= state.shape[0] <= MAX_SIZE:
-        raise ValueError("state must be [slots, H, Dk, Dv] with 1 to %d slots" % MAX_SIZE)
-    N = state.shape[0]
-    _check("state", state, dev, torch.float32, (N, H, Dk, Dv))
-    if slots is not None:
-        _check("slots", slots, dev, torch.int32, (B,))
+    N = _pool_check(state, slots, dims, dev)
     recorded = ()
     if torch.is_grad_enabled():
-        if state.requires_grad:
-            raise ValueError("a state that requires a gradient cannot be moved in place")
         if q.requires_grad or k.requires_grad or v.requires_grad:
             recorded = [t for t in (q, k, v) if t.requires_grad]
     o = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
@@ -307,6 +356,222 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     if recorded:
         return _Refused.apply("linear_attention_step has no gradients", 1, o, *recorded)[0]
     return o
+
+
+class GatedDelta(torch.autograd.Function):
+    """o [B, T, H, Dv] and the state after each sequence [B, H, Dk, Dv]; dims
+    is what _delta_check gives."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, beta, state, lengths, dims, scale):
+        ctx.set_materialize_grads(False)
+        ctx.dims, ctx.scale = dims, scale
+        saved = q, k, v, log_decay, beta, lengths
+        B, T, H, _, _, _, Dk, Dv, _ = dims
+        q, k, v = _rows(q), _rows(k), _rows(v)
+        dev = q.device
+        fields = (*dims, scale, _strides(q), _strides(k), _strides(v))
+        o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
+        last = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+        ws, n = _workspace("semicrf_delta_workspace_size", _LinattnShape, fields, 0, dev)
+        launch(load().semicrf_delta_fwd, dev, ctypes.byref(_LinattnShape(*fields)), _ptr(q),
+               _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(lengths), _ptr(state), _ptr(o),
+               _ptr(last), _ptr(ws), n)
+        ctx.save_for_backward(*saved, ws)
+        return o, last
+
+    @staticmethod
+    @_once
+    def backward(ctx, do, dlast):
+        q, k, v, log_decay, beta, lengths, work = ctx.saved_tensors
+        B, T, H, _, _, _, Dk, Dv, _ = ctx.dims
+        need, dev = ctx.needs_input_grad, q.device
+        dq, dk, dv, dg, db = (torch.empty(t.shape, dtype=t.dtype, device=dev) if n else None
+                              for t, n in zip((q, k, v, log_decay, beta), need))
+        dstate = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev) if need[5] else None
+        q, k, v = _rows(q), _rows(k), _rows(v)
+        fields = (*ctx.dims, ctx.scale, _strides(q), _strides(k), _strides(v))
+        if do is None:
+            do = torch.zeros((B, T, H, Dv), dtype=q.dtype, device=dev)
+        do = do.contiguous()
+        dlast = None if dlast is None else dlast.contiguous()
+        ws, n = _workspace("semicrf_delta_workspace_size", _LinattnShape, fields, 1, dev)
+        launch(load().semicrf_delta_bwd, dev, ctypes.byref(_LinattnShape(*fields)), _ptr(q),
+               _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(lengths), _ptr(work), _ptr(do),
+               _ptr(dlast), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(db), _ptr(dstate),
+               _ptr(ws), n)
+        return dq, dk, dv, dg, db, dstate, None, None, None
+
+
+def gated_delta(q, k, v, log_decay, beta, lengths=None, state=None, scale=None,
+                return_state: bool = False):
+    """The gated delta rule, over whole sequences:
+
+        S_t = exp(log_decay_t) (I - beta_t k_t k_t^T) S_{t-1} + beta_t k_t v_t^T
+        o_t = scale S_t^T q_t
+
+    q, k, v, shared heads, lengths, state and what is returned are those of
+    linear_attention, with heads up to 128 wide.  log_decay and beta
+    [B, T, H] float32: the decays of each position and head (at most 0 in use;
+    -inf forgets) and how much of a write is taken, 0 to 1 (up to 2) for keys of
+    length 1.  Gradients flow to q, k, v, log_decay, beta and state."""
+    dims, log_decay, beta = _delta_check(q, k, v, log_decay, beta, False)
+    B, T, H, _, _, _, Dk, Dv, _ = dims
+    if lengths is not None:
+        _check("lengths", lengths, q.device, torch.int32, (B,))
+    if state is not None:
+        _check("state", state, q.device, torch.float32, (B, H, Dk, Dv))
+    if B == 0 or T == 0:
+        # 0, and part of the graph
+        none = q.sum() + k.sum() + v.sum() + (log_decay.sum() + beta.sum()).to(q.dtype)
+        o = none.expand(B, T, H, Dv).clone()
+        last = none.float().expand(B, H, Dk, Dv).clone() if state is None else state.clone()
+        if lengths is not None:  # NaN where they are none, as with positions
+            bad = ((lengths < 0) | (lengths > T))[:, None, None, None]
+            last = torch.where(bad, math.nan, last)
+    else:
+        o, last = GatedDelta.apply(q, k, v, log_decay, beta, state, lengths, dims,
+                                   Dk ** -0.5 if scale is None else float(scale))
+    return (o, last) if return_state else o
+
+
+def gated_delta_step(q, k, v, log_decay, beta, state, slots=None, scale=None):
+    """One position of B streams by the gated delta rule: q, k [B, heads, Dk],
+    v [B, heads, Dv], log_decay, beta [B, H].  The pool of states [slots, H,
+    Dk, Dv], slots, idle streams and gradients (none) are those of
+    linear_attention_step."""
+    dims, log_decay, beta = _delta_check(q, k, v, log_decay, beta, True)
+    B, _, H, _, _, _, Dk, Dv, _ = dims
+    dev = q.device
+    N = _pool_check(state, slots, dims, dev)
+    recorded = ()
+    if torch.is_grad_enabled():
+        recorded = [t for t in (q, k, v, log_decay, beta) if t.requires_grad]
+    o = torch.empty((B, H, Dv), dtype=q.dtype, device=dev)
+    if B:
+        q, k, v = _rows(q), _rows(k), _rows(v)
+        shape = _LinattnShape(*dims, Dk ** -0.5 if scale is None else scale, _strides(q),
+                              _strides(k), _strides(v))
+        launch(load().semicrf_delta_step, dev, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
+               _ptr(log_decay), _ptr(beta), _ptr(slots), N, _ptr(state), _ptr(o))
+        increment_version(state)  # a backward pass that saved the old states must fail
+    if recorded:
+        return _Refused.apply("gated_delta_step has no gradients", 1, o, *recorded)[0]
+    return o
+
+
+def rotary_frequencies(turn: int, base: float = 10000.0, stretch: float = 1.0,
+                       scaling: str = "bands", context: int = 4096, fast: float = 32.0,
+                       slow: float = 1.0, device=None):
+    """Frequencies [turn / 2] float64 for rotary: base ** (-2 i / turn) radians a
+    position, stretched for contexts `stretch` times as long as the trained
+    one by
+
+        "linear"  dividing all of them by stretch;
+        "base"    raising the base so that the slowest is divided by stretch;
+        "bands"   dividing those that turn fewer than `slow` times in `context`
+                  positions, leaving those that turn more than `fast` times, and
+                  in between a mean of both, linear in the number of turns."""
+    if turn < 2 or turn % 2:
+        raise ValueError("an even number of elements is turned")
+    if scaling not in ("linear", "base", "bands"):
+        raise ValueError('scaling must be "linear", "base" or "bands"')
+    if not (base > 0 and stretch > 0 and context > 0 and fast > slow):
+        raise ValueError("base, stretch and context must be positive, fast above slow")
+    i = torch.arange(turn // 2, dtype=torch.float64)
+    if scaling == "base" and turn > 2:
+        base = base * stretch ** (turn / (turn - 2))
+    f = base ** (-2.0 * i / turn)
+    if scaling == "linear":
+        f = f / stretch
+    elif scaling == "bands":
+        share = ((context * f / (2 * math.pi)).clamp(slow, fast) - slow) / (fast - slow)
+        f = f * share + f / stretch * (1 - share)
+    return f.to(device)
+
+
+class Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, frequencies, positions, layout, scale, inverse):
+        ctx.save_for_backward(frequencies, positions)
+        ctx.args = layout, scale, inverse
+        return _turn(q, k, frequencies, positions, layout, scale, inverse)
+
+    @staticmethod
+    @_once
+    def backward(ctx, dq, dk=None):
+        layout, scale, inverse = ctx.args
+        return *_turn(dq, dk, *ctx.saved_tensors, layout, scale, not inverse), *[None] * 5
+
+
+def _turn(q, k, frequencies, positions, layout, scale, inverse):
+    B, T, heads, D = q.shape
+    q, dev = _rows(q), q.device
+    y = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    heads2, y2, strides2 = 0, None, (0, 0, 0)
+    if k is not None:
+        k = _rows(k)
+        heads2, y2, strides2 = k.shape[2], torch.empty(k.shape, dtype=k.dtype, device=dev), _strides(k)
+    shape = _RotaryShape(B, T, heads, heads2, D, 2 * frequencies.numel(), DTYPES[q.dtype], layout,
+                         0 if positions is None else positions.dim(), inverse, scale, _strides(q),
+                         strides2)
+    launch(load().semicrf_rotary, dev, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(frequencies),
+           _ptr(positions), _ptr(y), _ptr(y2))
+    return y, y2
+
+
+def rotary(q, k, frequencies, positions=None, layout: str = "half", scale: float = 1.0):
+    """Rotary positions: each row of q [B, T, heads, D] and k [B, T, heads, D]
+    (or None) at position p is turned in its planes i by the angle
+    p frequencies[i] and multiplied by scale there; the planes are elements
+    (i, i + n) of a row ("half") or (2 i, 2 i + 1) ("interleaved") for n
+    frequencies [n] float64 (rotary_frequencies); elements from 2 n on are
+    copied.  positions: row t is at t (None), at positions[b] + t ([B] int32),
+    or at positions[b, t] ([B, T] int32).  Rows [B, heads, D] of single
+    positions are taken with positions [B].  Rows past a sequence's length
+    are turned like the others.  Returns (q', k'), or q' where k is None.
+    Gradients flow to q and k."""
+    _check_device(q)
+    dev, single = q.device, q.dim() == 3
+    for name, t in (("q", q), ("k", k)):
+        if t is not None and (t.dim() != q.dim() or q.dim() not in (3, 4) or t.dtype != q.dtype
+                              or t.device != dev or t.shape[-1] != q.shape[-1]
+                              or t.shape[:-2] != q.shape[:-2]):
+            raise ValueError("%s must be a [B, T, heads, D] or [B, heads, D] %s tensor on %s, as "
+                             "the other" % (name, q.dtype, dev))
+    D, n = q.shape[-1], frequencies.numel()
+    _check("frequencies", frequencies, dev, torch.float64, (n,))
+    if not 1 <= 2 * n <= D <= MAX_TURNED:
+        raise ValueError("between 1 frequency and one for every two elements of a row, rows of up "
+                         "to %d elements" % MAX_TURNED)
+    if layout not in ROTARY_LAYOUTS:
+        raise ValueError('layout must be "half" or "interleaved"')
+    if single:
+        if positions is None:
+            raise ValueError("single positions need positions [B]")
+        q, k = q[:, None], None if k is None else k[:, None]
+    B, T = q.shape[:2]
+    if max(B, T, q.shape[2], 0 if k is None else k.shape[2]) > MAX_SIZE:
+        raise ValueError("sizes are at most %d" % MAX_SIZE)
+    if positions is not None:
+        _check("positions", positions, dev, torch.int32,
+               (B,) if single or positions.dim() == 1 else (B, T))
+    if q.numel() == 0:  # no rows, or no heads of q: nothing or only k is turned
+        y = q.clone()
+        if k is None or k.numel() == 0:
+            y2 = None if k is None else k.clone()
+        else:
+            y2 = Rotary.apply(k, None, frequencies, positions, ROTARY_LAYOUTS[layout],
+                              float(scale), False)[0]
+    else:
+        there = k is not None and k.numel() > 0
+        y, y2 = Rotary.apply(q, k if there else None, frequencies, positions,
+                             ROTARY_LAYOUTS[layout], float(scale), False)
+        if k is not None and not there:
+            y2 = k.clone()
+    if single:
+        y, y2 = y[:, 0], None if y2 is None else y2[:, 0]
+    return y if k is None else (y, y2)
 
 
 class GroupNorm(torch.autograd.Function):

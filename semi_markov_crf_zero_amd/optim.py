@@ -4,6 +4,12 @@ include/semicrf_encoder.h, which gives the formula and the 8-bit forms).
     opt = AdamW(model.parameters(), lr=3e-4, bits=8)      # a torch optimizer
     loss.backward(); opt.step()
 
+Clipping by the global norm of the gradients, in place before the step, or with
+the coefficient alone, which the step applies as it reads them:
+
+    clip_grad_norm_(model.parameters(), 1.0); opt.step()
+    norm, c = grad_norm(model.parameters(), max_norm=1.0); opt.step(grad_scale=c)
+
 AdamWPlan is the step itself for one list of tensors: a table of their
 addresses on the device, made once, and `run(grads, step, ...)`.  One launch
 covers 416 tensors; the gradients' addresses, new in every step, go with the
@@ -14,6 +20,7 @@ optional.
 from __future__ import annotations
 
 import ctypes
+import math
 import operator
 from array import array
 
@@ -25,6 +32,9 @@ from .encoder import DTYPES, launch
 
 EXPORTS = ("semicrf_adamw_table_size", "semicrf_adamw_table", "semicrf_adamw_step",
            "semicrf_adamw_values")
+# declared in semicrf_layer.h
+LAYER_EXPORTS = ("semicrf_grad_norm_workspace_size", "semicrf_grad_norm")
+NORMS = {float("inf"): 0, 1.0: 1, 2.0: 2}
 BLOCK = 256  # elements that share one scale of an 8-bit state
 MOMENT_TYPES = {torch.float8_e4m3fn: 0, torch.uint8: 1}  # codes of m; of the root of v
 
@@ -59,7 +69,9 @@ def load():
         lib.semicrf_adamw_table.argtypes = [P, I, I, P, Z]
         lib.semicrf_adamw_step.argtypes = [P, P, P, ctypes.c_char_p, I, I, L, D, D, D, D, D, P, P]
         lib.semicrf_adamw_values.argtypes = [P, P, L, I, P, P]
-        for name in EXPORTS:
+        lib.semicrf_grad_norm_workspace_size.argtypes = [P, I, ctypes.POINTER(Z)]
+        lib.semicrf_grad_norm.argtypes = [P, P, ctypes.c_char_p, I, I, D, I, P, P, P, Z, P]
+        for name in EXPORTS + LAYER_EXPORTS:
             getattr(lib, name).restype = I
         _lib = lib
     return _lib
@@ -357,3 +369,68 @@ class AdamW(torch.optim.Optimizer):
                 if isinstance(t, torch.Tensor):
                     self.state[p][name] = t.detach().clone().to(p.device)
         self._plans = {}
+
+
+def _grad_norm(parameters, max_norm, norm_type, clip):
+    """(norm, coefficient) of the parameters' gradients, scaled if clip."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [g for g in [p.grad for p in parameters] if g is not None]
+    order = NORMS.get(float(norm_type))
+    if order is None:
+        raise ValueError("the norm is 1, 2 or inf")
+    max_norm = float(max_norm)
+    if not max_norm >= 0:
+        raise ValueError("max_norm must not be negative")
+    if not grads:
+        return torch.zeros(()), torch.ones(())
+    dev = grads[0].device
+    if dev.type != "cuda":
+        raise ValueError("gradients are normed on the GPU only; got a %s tensor" % dev.type)
+    dtypes = list(map(_dtype, grads))
+    if (not set(dtypes) <= DTYPES.keys() or set(map(_get_device, grads)) != {dev.index}
+            or any(g.layout != torch.strided for g in grads)):
+        raise ValueError("gradients must be dense float32, bfloat16 or float16 tensors on one GPU")
+    # a copy of what is not contiguous is scaled in its place and copied back
+    flat = grads if all(map(_is_contiguous, grads)) else [g.contiguous() for g in grads]
+    n = len(flat)
+    at, sizes = array("Q", map(_data_ptr, flat)), array("q", map(_numel, flat))
+    lib, size = load(), ctypes.c_size_t(0)
+    rc = lib.semicrf_grad_norm_workspace_size(sizes.buffer_info()[0], n, ctypes.byref(size))
+    if rc:
+        raise bd.SemiCRFError(rc, "semicrf_grad_norm_workspace_size")
+    # the partials, then the norm and the coefficient
+    work = torch.empty(size.value // 4 + 2, dtype=torch.float32, device=dev)
+    out = work.data_ptr() + size.value
+    if clip and _overlap(flat):
+        raise ValueError("a gradient is there twice, whole or in part: it would be scaled twice")
+    launch(lib.semicrf_grad_norm, dev, at.buffer_info()[0], sizes.buffer_info()[0],
+           bytes(map(DTYPES.get, dtypes)), n, order, max_norm, clip, out, out + 4, work.data_ptr(),
+           size.value)
+    if clip:
+        if flat is not grads:
+            for g, f in zip(grads, flat):
+                if g is not f:
+                    g.copy_(f)
+        increment_version(grads)  # a backward pass that saved the old values must fail
+    return work[-2], work[-1]
+
+
+@torch.no_grad()
+def grad_norm(parameters, max_norm=None, norm_type: float = 2.0):
+    """The norm (1, 2 or inf) of all gradients of `parameters` together, a
+    float32 tensor of no dimensions on their device; summed in float64.  With
+    max_norm, (norm, coefficient), the coefficient min(1, max_norm / (norm +
+    1e-6)) that clipping multiplies by: AdamW.step(grad_scale=coefficient)
+    applies it without another pass over the gradients."""
+    norm, coefficient = _grad_norm(parameters, math.inf if max_norm is None else max_norm,
+                                   norm_type, False)
+    return norm if max_norm is None else (norm, coefficient)
+
+
+@torch.no_grad()
+def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0):
+    """Multiplies all gradients of `parameters` by min(1, max_norm / (norm +
+    1e-6)), in place; the norm before, as grad_norm gives it.  Gradients that
+    share memory are refused."""
+    return _grad_norm(parameters, max_norm, norm_type, True)[0]
