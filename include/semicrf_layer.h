@@ -36,21 +36,23 @@ extern "C" {
  * row of its sequence and head.
  */
 
-/* Bytes of workspace of semicrf_delta_fwd (backward = 0) or _bwd (1).  The
- * forward call leaves what the backward pass reads again there. */
-semicrf_status_t semicrf_delta_workspace_size(const semicrf_linattn_shape_t *shape, int backward,
+/* Bytes of workspace of semicrf_delta_fwd (FORWARD; KEEP with its keep), or of
+ * semicrf_delta_bwd (BACKWARD). */
+enum { SEMICRF_DELTA_FORWARD = 0, SEMICRF_DELTA_KEEP = 1, SEMICRF_DELTA_BACKWARD = 2 };
+semicrf_status_t semicrf_delta_workspace_size(const semicrf_linattn_shape_t *shape, int pass,
                                               size_t *bytes);
 
-/* lengths, state_in and state_out may be NULL. */
-semicrf_status_t semicrf_delta_fwd(const semicrf_linattn_shape_t *shape, const void *q,
+/* keep != 0: what the backward pass reads again is left in the workspace.
+ * lengths, state_in and state_out may be NULL. */
+semicrf_status_t semicrf_delta_fwd(const semicrf_linattn_shape_t *shape, int keep, const void *q,
                                    const void *k, const void *v, const float *log_decay,
                                    const float *beta, const int32_t *lengths,
                                    const float *state_in, void *o, float *state_out,
                                    void *workspace, size_t workspace_bytes, void *stream);
 
 /* Gradients given grad_o and grad_state = dL/dstate_out (or NULL: 0).
- * `saved` is the forward call's workspace as that call left it (same shape, k,
- * v, log_decay, beta, lengths and state_in).  grad_log_decay and grad_beta
+ * `saved` is the workspace of a forward call with keep as that call left it
+ * (same shape, k, v, log_decay, beta, lengths and state_in).  grad_log_decay and grad_beta
  * [B][T][H] float32; the gradient of a log_decay below -104 (e^g is 0 in
  * float32) is 0.  lengths, grad_state and each output may be NULL (skipped). */
 semicrf_status_t semicrf_delta_bwd(const semicrf_linattn_shape_t *shape, const void *q,

@@ -38,7 +38,8 @@ COMMON = [
 # without this a tenth of its loop copies them from and to the accumulation
 # registers.
 EXTRA = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-         for f in ("linattn_f32.hip", "linattn_bf16.hip", "linattn_f16.hip")}
+         for f in ("linattn_f32.hip", "linattn_bf16.hip", "linattn_f16.hip",
+                   "delta_f32.hip", "delta_bf16.hip", "delta_f16.hip")}
 
 
 def _compile(src: str, asm: bool) -> str:

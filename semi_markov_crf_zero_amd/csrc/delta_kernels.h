@@ -1,0 +1,1060 @@
+// delta_kernels.h -- the chunked kernels of the gated delta rule, instantiated
+// by delta_f32.hip, delta_bf16.hip and delta_f16.hip (delta.hip says what they
+// compute).
+#pragma once
+
+#include "parts.h"
+
+namespace semicrf {
+
+// What is left of a chunk's gates: of each position the sum G of its log decays
+// from the chunk's start in two floats, e^G, e^{G_L - G}; then e^{G_L} in two.
+__host__ __device__ constexpr int delta_gates(int L) { return 4 * L + 4; }
+
+struct DeltaArgs {
+  View q, k, v;
+  const void *go;  // gradient of o [B][T][H][Dv]
+  const float *log_decay, *beta;
+  const int32_t *lengths;
+  const float *state_in;
+  float *X, *gates;  // of each chunk: [ld][ld], delta_gates
+  float *phi, *xs;   // of each segment: [Dk][Dk], [Dk][Dv]
+  float *S, *U;      // of each chunk, for the backward pass: [Dk][Dv], [L][Dv]; or NULL
+  float *D, *R;      // and its own: the gradients of the state after it and of R
+  void *o, *dq, *dk, *dv;
+  float *state_out, *dg, *db;
+  int part_q, part_k, part_v;  // gradients go to float32 [B][T][H][D]: of shared heads
+  int vec, vec_out;            // rows are read 16 bytes at a time; dq and dk written by fours
+  int nseg, seg;               // segments, chunks of one
+  int first, count;            // segments of a launch
+  int ld;                      // of X: L, or less where a sequence is one short chunk
+  float bad, scale;
+  int B, T, H, Dk, Dv, N;  // N chunks
+  int ctiles, ktiles;      // column groups of a launch; those of them that are phi's
+};
+
+// Operands are held in parts as linear attention's are; chunks are 64 positions
+// for bfloat16, 32 where inputs have more parts than one.
+__host__ __device__ constexpr int delta_parts(int dtype) {
+  return dtype == SEMICRF_F32 ? 3 : dtype == SEMICRF_F16 ? 2 : 1;
+}
+__host__ __device__ constexpr int delta_chunk(int parts) { return parts > 1 ? 32 : 64; }
+// Waves of a workgroup that walks along a sequence: one for 16 columns.
+inline int delta_waves(int Dv) { return Dv <= 32 ? 2 : Dv <= 64 ? 4 : 8; }
+
+enum DeltaPass { DELTA_INVERSE, DELTA_COMPOSE, DELTA_FORWARD, DELTA_COMPOSE_BACK, DELTA_BACK, DELTA_GRADS };
+semicrf_status_t delta_f32(const DeltaArgs &p, DeltaPass pass, hipStream_t st);
+semicrf_status_t delta_bf16(const DeltaArgs &p, DeltaPass pass, hipStream_t st);
+semicrf_status_t delta_f16(const DeltaArgs &p, DeltaPass pass, hipStream_t st);
+
+namespace {
+
+template <int L>
+struct Gates {
+  float hi[L], lo[L], from[L], to[L], all, low, none[2];
+  // e^{G_i - G_j}
+  __device__ __forceinline__ float decay(int i, int j) const {
+    return __expf((hi[i] - hi[j]) + (lo[i] - lo[j]));
+  }
+};
+template <int L, int NT>
+struct GatesTile {
+  static constexpr int all = delta_gates(L), N = (all + NT - 1) / NT;
+  float r[N];
+  __device__ __forceinline__ void fetch(int tid, const float *src) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (tid + k * NT < all) r[k] = src[tid + k * NT];
+  }
+  __device__ __forceinline__ void put(int tid, Gates<L> &g) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (tid + k * NT < all) (&g.hi[0])[tid + k * NT] = r[k];
+  }
+};
+
+// A float32 matrix of `rows` rows (ld apart) and W columns, in three parts in
+// LDS, zeros past n rows and D columns; LOWER: blocks of 32 above the diagonal are
+// not read (nor written).
+template <typename Lay, int W, int ROWS, int NT, bool LOWER>
+struct Tile32 {
+  static constexpr int per = W / 4, all = ROWS * per, N = (all + NT - 1) / NT;
+  static constexpr int plane = ROWS * Lay::row;
+  f4 r[N];
+  // vec: every row's start is on 16 bytes and D a multiple of 4
+  __device__ __forceinline__ void fetch(int tid, const float *src, int64_t ld, int n, int D,
+                                        bool vec) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int e = tid + k * NT, i = e / per, c = e % per * 4;
+      r[k] = f4{0.f, 0.f, 0.f, 0.f};
+      if ((all % NT && e >= all) || (LOWER && c / 32 > i / 32) || i >= n) continue;
+      if (vec) {
+        if (c < D) r[k] = *reinterpret_cast<const f4 *>(src + i * ld + c);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (c + q < D) r[k][q] = src[i * ld + c + q];
+      }
+    }
+  }
+  __device__ __forceinline__ void put(int tid, bf16 *lds) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int e = tid + k * NT, i = e / per, c = e % per * 4;
+      if ((all % NT && e >= all) || (LOWER && c / 32 > i / 32)) continue;
+      f2 lo = {r[k][0], r[k][1]}, hi = {r[k][2], r[k][3]};
+#pragma unroll
+      for (int m = 0; m < 3; ++m) {
+        const b2 a = part2(lo), b = part2(hi);
+        *reinterpret_cast<Pack<bf16, 4> *>(lds + m * plane + Lay::at(i, c / 4)) =
+            Pack<bf16, 4>{{a[0], a[1], b[0], b[1]}};
+      }
+    }
+  }
+};
+
+// The tiles of 16 rows 2 b and 2 b + 1 of an accumulated matrix as an operand whose
+// contraction runs over them.
+__device__ __forceinline__ Frag<3> frag_of(const f4 &a, const f4 &b) {
+  float x[8];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) x[r] = a[r], x[4 + r] = b[r];
+  return split<3>(x);
+}
+
+template <typename T>
+__device__ __forceinline__ const T *view_rows(const View &v, int b, int h) {
+  return (const T *)v.p + (int64_t)b * v.sb + (int64_t)(h / v.share) * v.sh;
+}
+
+__device__ __forceinline__ f4 mfma32(float a, float b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
+}  // namespace
+
+// X = (I + diag(b) m)^-1 diag(b) and the gates of a chunk, a workgroup of four
+// waves each.  M = diag(b) m on the matrix cores; its 16 x 16 blocks on the diagonal
+// are inverted by substitution, a column a lane, and put together by
+//   (I + M)^-1 = [T1, 0; -T2 M21 T1, T2]
+// to 32 and 64 with float32 matrix instructions: what substitution gives, whatever
+// the keys' lengths.
+template <typename T, int NP, int DK, int L>
+__global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs p) {
+  constexpr int KB = DK / 32, NT = L / 16, LD = L + 4;
+  typedef ByRow<DK> LK;
+  __shared__ alignas(16) bf16 K[NP * L * LK::row];
+  __shared__ alignas(16) float M[L * LD], X[L * LD], Xt[L * LD];  // Xt: by columns
+  __shared__ Gates<L> s;
+  __shared__ float beta[L];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  const int h = blockIdx.x % p.H, n = blockIdx.x / p.H % p.N, b = blockIdx.x / p.H / p.N;
+  const int t0 = n * L, count = min(L, max(valid_length(p.lengths, b, p.T), 0) - t0);
+  if (count <= 0) return;
+  const int64_t at = ((int64_t)b * p.H + h) * p.N + n;
+  const T *k = view_rows<T>(p.k, b, h) + t0 * p.k.st;
+  Tile<T, NP, LK, DK, L, 256> tk;
+  if (p.vec) tk.fetch(threadIdx.x, k, (int)p.k.st, p.Dk, count, 0, 1, 0);
+  if (w == 0) {
+    float gi = 0.f, bt = 0.f;
+    if (lane < count) {
+      const int64_t e = ((int64_t)b * p.T + t0 + lane) * p.H + h;
+      gi = p.log_decay[e], bt = p.beta[e];
+      if (gi < -200.f) gi = -200.f;
+      if (fabsf(bt) < 0x1p-96f) bt = copysignf(0x1p-96f, bt);
+    }
+    double G = gi;
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+      const double y = __shfl_up(G, o);
+      if (lane >= o) G += y;
+    }
+    const double last = __shfl(G, L - 1);
+    if (lane < L) {
+      const float hi = (float)G;
+      s.hi[lane] = hi, s.lo[lane] = (float)(G - hi);
+      s.from[lane] = (float)exp(G), s.to[lane] = (float)exp(last - G);
+      beta[lane] = bt;
+    }
+    if (lane == 0) {
+      const double all = exp(last);
+      s.all = (float)all, s.low = (float)(all - s.all), s.none[0] = s.none[1] = 0.f;
+    }
+  }
+  if (p.vec)
+    tk.put(threadIdx.x, K);
+  else
+    stage<T, NP, LK, DK, L, 256>(K, k, p.k.st, p.Dk, count, 0);
+  __syncthreads();
+  // M by rows: a tile is computed transposed, so that a lane holds four neighbours
+  for (int t = w; t < NT * (NT + 1) / 2; t += 4) {
+    int it = 0, jt = t;
+    while (jt > it) jt -= ++it;
+    f4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb)
+      acc = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * jt, kb, lane),
+                   frag_row<NP, LK>(K, L * LK::row, 16 * it, kb, lane), acc);
+    const int i = 16 * it + l16, j = 16 * jt + 4 * g;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) acc[r] = j + r < i ? beta[i] * s.decay(i, j + r) * acc[r] : 0.f;
+    *reinterpret_cast<f4 *>(M + i * LD + j) = acc;
+  }
+  for (int e = threadIdx.x; e < L * L / 4; e += 256) {
+    const int i = e / (L / 4), j = e % (L / 4) * 4;
+    if (j / 16 > i / 16) *reinterpret_cast<f4 *>(X + i * LD + j) = f4{0.f, 0.f, 0.f, 0.f};
+  }
+  for (int e = threadIdx.x; e < delta_gates(L); e += 256)
+    p.gates[at * delta_gates(L) + e] = (&s.hi[0])[e];
+  __syncthreads();
+  if (w < NT) {
+    float x[16];
+    const float *m = M + 16 * w * LD + 16 * w;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float y = i == l16 ? 1.f : 0.f;
+#pragma unroll
+      for (int l = 0; l < i; ++l) y = fmaf(-m[i * LD + l], x[l], y);
+      x[i] = y;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i / 4 == g) {
+        X[(16 * w + i) * LD + 16 * w + l16] = x[i];
+        Xt[(16 * w + l16) * LD + 16 * w + i] = x[i];
+      }
+  }
+  __syncthreads();
+  // blocks of n16 tiles beside each other: rows it, columns ct of the lower left
+  // one of a pair, T2 and T1 in X and Xt
+#pragma unroll
+  for (int n16 = 1; n16 < NT; n16 *= 2) {
+    const int pairs = NT / (2 * n16), jobs = pairs * n16 * n16;
+    f4 out = {0.f, 0.f, 0.f, 0.f};
+    int it = 0, ct = 0;
+    if (w < jobs) {
+      const int base = w / (n16 * n16) * 2 * n16;
+      it = base + n16 + w / n16 % n16, ct = base + w % n16;
+      for (int mt = base + n16; mt <= it; ++mt) {
+        f4 y = {0.f, 0.f, 0.f, 0.f};  // rows of tile mt of M21 T1
+        for (int jt = ct; jt < base + n16; ++jt) {
+          const f4 a = *reinterpret_cast<const f4 *>(M + (16 * mt + l16) * LD + 16 * jt + 4 * g);
+          const f4 c = *reinterpret_cast<const f4 *>(Xt + (16 * ct + l16) * LD + 16 * jt + 4 * g);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y = mfma32(a[r], c[r], y);
+        }
+        const f4 a = *reinterpret_cast<const f4 *>(X + (16 * it + l16) * LD + 16 * mt + 4 * g);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) out = mfma32(a[r], -y[r], out);
+      }
+    }
+    __syncthreads();
+    if (w < jobs) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) X[(16 * it + 4 * g + r) * LD + 16 * ct + l16] = out[r];
+      *reinterpret_cast<f4 *>(Xt + (16 * ct + l16) * LD + 16 * it + 4 * g) = out;
+    }
+    __syncthreads();
+  }
+  const int ld = p.ld;
+  for (int e = threadIdx.x; e < ld * ld / 4; e += 256) {
+    const int i = e / (ld / 4), j = e % (ld / 4) * 4;
+    f4 x = *reinterpret_cast<const f4 *>(X + i * LD + j);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] *= beta[j + r];
+    *reinterpret_cast<f4 *>(p.X + at * ld * ld + i * ld + j) = x;
+  }
+}
+
+// The chunks of a segment one after another, 16 columns of the state a wave, in
+// accumulators from the first chunk to the last.  COMPOSE: the columns of the
+// segment's transition [phi | sum], from [I | 0], with values of 0 for the first; else
+// the outputs (and what the backward pass reads again) from the state before it.
+template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
+__global__ __launch_bounds__(64 * NW) void k_delta_chunks(DeltaArgs p) {
+  constexpr int kCols = 16 * NW, kThreads = 64 * NW;
+  constexpr int KB = DK / 32, NT = L / 16, JB = L / 32;
+  typedef ByBoth<DK> LK;
+  typedef ByRow<DK> LQ;
+  typedef ByColumn<kCols> LV;
+  typedef ByRow<L> LX;
+  __shared__ alignas(16) bf16 K[NP * L * LK::row];
+  __shared__ alignas(16) bf16 V[NP * L * LV::row];
+  __shared__ alignas(16) bf16 X[3 * L * LX::row];
+  __shared__ alignas(16) bf16 Q[COMPOSE ? 8 : NP * L * LQ::row];
+  __shared__ alignas(16) bf16 P[COMPOSE ? 8 : 3 * L * LX::row];
+  __shared__ Gates<L> gs;
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  int ct = blockIdx.x % p.ctiles;
+  const int seg = p.first + blockIdx.x / p.ctiles % p.count;
+  const int64_t bh = blockIdx.x / p.ctiles / p.count;
+  const int h = (int)(bh % p.H), b = (int)(bh / p.H);
+  const bool phi = COMPOSE && ct < p.ktiles;
+  if (COMPOSE && !phi) ct -= p.ktiles;
+  const int c0 = ct * kCols, xc = c0 + 16 * w + l16, width = phi ? p.Dk : p.Dv;
+  const int valid = valid_length(p.lengths, b, p.T), len = max(valid, 0);
+  const int chunks = (len + L - 1) / L;
+  const int lo = seg * p.seg, hi = min(chunks, lo + p.seg);
+
+  const T *q = view_rows<T>(p.q, b, h), *k = view_rows<T>(p.k, b, h), *v = view_rows<T>(p.v, b, h);
+  Tile<T, NP, LK, DK, L, kThreads> tk;
+  Tile<T, NP, LQ, DK, L, kThreads> tq;
+  Tile<T, NP, LV, kCols, L, kThreads> tv;
+  Tile32<LX, L, L, kThreads, true> tx;
+  GatesTile<L, kThreads> tg;
+  auto fetch = [&](int n) {
+    const int64_t t0 = (int64_t)n * L;
+    const int m = (int)min((int64_t)L, len - t0);
+    const int64_t at = bh * p.N + n;
+    tg.fetch(threadIdx.x, p.gates + at * delta_gates(L));
+    tx.fetch(threadIdx.x, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld, true);
+    if (!p.vec) return;
+    tk.fetch(threadIdx.x, k + t0 * p.k.st, (int)p.k.st, p.Dk, m, 0, 1, 0);
+    if (!COMPOSE) tq.fetch(threadIdx.x, q + t0 * p.q.st, (int)p.q.st, p.Dk, m, 0, 1, 0);
+    tv.fetch(threadIdx.x, v + t0 * p.v.st, (int)p.v.st, p.Dv, phi ? 0 : m, 0, 1, c0);
+  };
+  auto put = [&](int n) {
+    tg.put(threadIdx.x, gs);
+    tx.put(threadIdx.x, X);
+    if (p.vec) {
+      tk.put(threadIdx.x, K);
+      if (!COMPOSE) tq.put(threadIdx.x, Q);
+      tv.put(threadIdx.x, V);
+    } else {
+      const int64_t t0 = (int64_t)n * L;
+      const int m = (int)min((int64_t)L, len - t0);
+      stage<T, NP, LK, DK, L, kThreads>(K, k + t0 * p.k.st, p.k.st, p.Dk, m, 0);
+      if (!COMPOSE) stage<T, NP, LQ, DK, L, kThreads>(Q, q + t0 * p.q.st, p.q.st, p.Dk, m, 0);
+      stage<T, NP, LV, kCols, L, kThreads>(V, v + t0 * p.v.st, p.v.st, p.Dv, phi ? 0 : m, c0);
+    }
+  };
+  if (lo < hi) fetch(lo);
+
+  // state tile i: rows 16 i + 4 g + r of column xc
+  f4 S[2 * KB];
+  const int64_t size = (int64_t)p.Dk * p.Dv;
+  const float *s0 = COMPOSE ? nullptr
+                    : seg   ? p.xs + (bh * p.nseg + seg - 1) * size
+                            : p.state_in ? p.state_in + bh * size : nullptr;
+#pragma unroll
+  for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * g + r;
+      S[i][r] = phi ? (row == xc ? 1.f : 0.f)
+                    : s0 && row < p.Dk && xc < p.Dv ? s0[row * p.Dv + xc] : 0.f;
+    }
+  if (lo < hi) put(lo);
+
+  T *out = (T *)p.o + ((int64_t)b * p.T * p.H + h) * p.Dv;
+  const int64_t so = (int64_t)p.H * p.Dv;
+  for (int n = lo; n < hi; ++n) {
+    const int m = min(L, len - n * L);
+    __syncthreads();
+    if (n + 1 < hi) fetch(n + 1);
+    if (!COMPOSE && p.S && xc < p.Dv) {
+      float *to = p.S + (bh * p.N + n) * size + xc;
+#pragma unroll
+      for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * i + 4 * g + r < p.Dk) to[(16 * i + 4 * g + r) * p.Dv] = S[i][r];
+    }
+    if (!COMPOSE) {
+      // P: wave w its rows of 16, up to the diagonal and the tile beside it
+      for (int it = w; it < NT; it += NW) {
+        Frag<NP> qf[KB];
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+          qf[kb] = frag_row<NP, LQ>(Q, L * LQ::row, 16 * it, kb, lane);
+        const int i = 16 * it + l16;
+#pragma unroll
+        for (int jt = 0; jt < NT; ++jt) {
+          if (jt > (it | 1)) continue;
+          f4 acc = {0.f, 0.f, 0.f, 0.f};
+          if (jt <= it) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+              acc = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * jt, kb, lane), qf[kb], acc);
+            const int j = 16 * jt + 4 * g;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[r] = j + r <= i ? p.scale * gs.decay(i, j + r) * acc[r] : 0.f;
+          }
+          f2 x = {acc[0], acc[1]}, y = {acc[2], acc[3]};
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const b2 a = part2(x), d = part2(y);
+            *reinterpret_cast<Pack<bf16, 4> *>(P + c * L * LX::row + LX::at(i, 4 * jt + g)) =
+                Pack<bf16, 4>{{a[0], a[1], d[0], d[1]}};
+          }
+        }
+      }
+    }
+    Frag<3> sf[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) sf[kb] = frag_of(S[2 * kb], S[2 * kb + 1]);
+    // R = V - E K S
+    f4 U[NT];
+#pragma unroll
+    for (int it = 0; it < NT; ++it) U[it] = f4{0.f, 0.f, 0.f, 0.f};
+    Frag<3> rf[JB];
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb) {
+      f4 ks[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        ks[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+          ks[t] = mma<3>(frag_row<NP, LK>(K, L * LK::row, 32 * jb + 16 * t, kb, lane), sf[kb], ks[t]);
+      }
+      float x[8];
+      values(frag_col<NP, LV>(V, L * LV::row, 32 * jb, w, lane), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] -= gs.from[32 * jb + 16 * (e >> 2) + 4 * g + (e & 3)] * ks[e >> 2][e & 3];
+      rf[jb] = split<3>(x);
+    }
+    // U = X R
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb)
+#pragma unroll
+      for (int it = 2 * jb; it < NT; ++it)
+        U[it] = mma<3>(frag_row<3, LX>(X, L * LX::row, 16 * it, jb, lane), rf[jb], U[it]);
+    if (!COMPOSE && p.U && xc < p.Dv) {
+      float *to = p.U + (bh * p.N + n) * L * p.Dv + xc;
+#pragma unroll
+      for (int it = 0; it < NT; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[(int64_t)(16 * it + 4 * g + r) * p.Dv] = U[it][r];
+    }
+    // what the state gives, transposed: a lane holds four neighbours of a row of O
+    f4 O[NT];
+    if (!COMPOSE) {
+#pragma unroll
+      for (int it = 0; it < NT; ++it) {
+        O[it] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+          O[it] = mma<3>(sf[kb], frag_row<NP, LQ>(Q, L * LQ::row, 16 * it, kb, lane), O[it]);
+        const float d = p.scale * gs.from[16 * it + l16];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[it][r] *= d;
+      }
+    }
+    // S <- e^{G_L} S + K^T (e^{G_L - G} U)
+    Frag<3> uf[JB];
+    const float all = gs.all, low = gs.low;
+#pragma unroll
+    for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S[i][r] = fmaf(S[i][r], low, S[i][r] * all);
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb) {
+      if (!COMPOSE) uf[jb] = frag_of(U[2 * jb], U[2 * jb + 1]);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = U[2 * jb + (e >> 2)][e & 3] * gs.to[32 * jb + 16 * (e >> 2) + 4 * g + (e & 3)];
+      const Frag<3> tf = split<3>(x);
+#pragma unroll
+      for (int i = 0; i < 2 * KB; ++i)
+        S[i] = mma<3>(frag_col<NP, LK>(K, L * LK::row, 32 * jb, i, lane), tf, S[i]);
+    }
+    __syncthreads();
+    if (!COMPOSE) {
+      const int col = c0 + 16 * w + 4 * g;
+#pragma unroll
+      for (int it = 0; it < NT; ++it) {
+        const int i = 16 * it + l16;
+#pragma unroll
+        for (int jb = 0; jb <= it / 2; ++jb)
+          O[it] = mma<3>(uf[jb], frag_row<3, LX>(P, L * LX::row, 16 * it, jb, lane), O[it]);
+        if (i < m && col < p.Dv) {
+          T *to = out + ((int64_t)n * L + i) * so + col;
+          if (p.vec) {
+            Pack<T, 4> x;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x.v[r] = (T)O[it][r];
+            *reinterpret_cast<Pack<T, 4> *>(to) = x;
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (col + r < p.Dv) to[r] = (T)O[it][r];
+          }
+        }
+      }
+    }
+    if (n + 1 < hi) put(n + 1);
+  }
+
+  if (COMPOSE) {
+    float *to = phi ? p.phi + (bh * p.nseg + seg) * p.Dk * p.Dk : p.xs + (bh * p.nseg + seg) * size;
+#pragma unroll
+    for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + 4 * g + r;
+        if (row < p.Dk && xc < width) to[row * width + xc] = S[i][r];
+      }
+    return;
+  }
+  const T fill = (T)(valid < 0 ? p.bad : 0.f);
+  const int64_t f0 = max((int64_t)len, (int64_t)lo * L),
+                f1 = min((int64_t)p.T, ((int64_t)lo + p.seg) * L);
+  for (int64_t e = threadIdx.x; e < (f1 - f0) * kCols; e += kThreads) {
+    const int col = c0 + (int)(e % kCols);
+    if (col < p.Dv) out[(f0 + e / kCols) * so + col] = fill;
+  }
+  // the segment that holds the last valid position (the first, if none)
+  if (p.state_out && hi == chunks && (lo < chunks || seg == 0)) {
+#pragma unroll
+    for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + 4 * g + r;
+        if (row < p.Dk && xc < p.Dv)
+          p.state_out[bh * size + row * p.Dv + xc] = valid < 0 ? p.bad : S[i][r];
+      }
+  }
+}
+
+// The chunks of a segment from the last to the first, 16 columns of the gradient
+// of the state a wave.  COMPOSE: from 0 to what the segment adds; else from the
+// gradient after the segment, leaving that after each chunk in D, the gradients of
+// R in R and of the values in dv.
+template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
+__global__ __launch_bounds__(64 * NW) void k_delta_back(DeltaArgs p) {
+  constexpr int kCols = 16 * NW, kThreads = 64 * NW;
+  constexpr int KB = DK / 32, NT = L / 16, JB = L / 32;
+  typedef ByBoth<DK> LK;
+  typedef ByColumn<kCols> LV;
+  typedef ByColumn<L> LX;
+  __shared__ alignas(16) bf16 K[NP * L * LK::row];
+  __shared__ alignas(16) bf16 Q[NP * L * LK::row];
+  __shared__ alignas(16) bf16 G[NP * L * LV::row];
+  __shared__ alignas(16) bf16 X[3 * L * LX::row];
+  __shared__ alignas(16) bf16 P[3 * L * LX::row];
+  __shared__ Gates<L> gs;
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  const int ct = blockIdx.x % p.ctiles, seg = p.first + blockIdx.x / p.ctiles % p.count;
+  const int64_t bh = blockIdx.x / p.ctiles / p.count;
+  const int h = (int)(bh % p.H), b = (int)(bh / p.H);
+  const int c0 = ct * kCols, xc = c0 + 16 * w + l16;
+  const int valid = valid_length(p.lengths, b, p.T), len = max(valid, 0);
+  const int chunks = (len + L - 1) / L;
+  const int lo = seg * p.seg, hi = min(chunks, lo + p.seg);
+
+  const T *q = view_rows<T>(p.q, b, h), *k = view_rows<T>(p.k, b, h);
+  const int64_t so = (int64_t)p.H * p.Dv;
+  const T *go = (const T *)p.go + ((int64_t)b * p.T * p.H + h) * p.Dv;
+  Tile<T, NP, LK, DK, L, kThreads> tk, tq;
+  Tile<T, NP, LV, kCols, L, kThreads> to;
+  Tile32<LX, L, L, kThreads, true> tx;
+  GatesTile<L, kThreads> tg;
+  auto fetch = [&](int n) {
+    const int64_t t0 = (int64_t)n * L;
+    const int m = (int)min((int64_t)L, len - t0);
+    const int64_t at = bh * p.N + n;
+    tg.fetch(threadIdx.x, p.gates + at * delta_gates(L));
+    tx.fetch(threadIdx.x, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld, true);
+    if (!p.vec) return;
+    tk.fetch(threadIdx.x, k + t0 * p.k.st, (int)p.k.st, p.Dk, m, 0, 1, 0);
+    tq.fetch(threadIdx.x, q + t0 * p.q.st, (int)p.q.st, p.Dk, m, 0, 1, 0);
+    to.fetch(threadIdx.x, go + t0 * so, (int)so, p.Dv, m, 0, 1, c0);
+  };
+  auto put = [&](int n) {
+    tg.put(threadIdx.x, gs);
+    tx.put(threadIdx.x, X);
+    if (p.vec) {
+      tk.put(threadIdx.x, K);
+      tq.put(threadIdx.x, Q);
+      to.put(threadIdx.x, G);
+    } else {
+      const int64_t t0 = (int64_t)n * L;
+      const int m = (int)min((int64_t)L, len - t0);
+      stage<T, NP, LK, DK, L, kThreads>(K, k + t0 * p.k.st, p.k.st, p.Dk, m, 0);
+      stage<T, NP, LK, DK, L, kThreads>(Q, q + t0 * p.q.st, p.q.st, p.Dk, m, 0);
+      stage<T, NP, LV, kCols, L, kThreads>(G, go + t0 * so, so, p.Dv, m, c0);
+    }
+  };
+  if (lo < hi) fetch(hi - 1);
+  f4 D[2 * KB];
+  const int64_t size = (int64_t)p.Dk * p.Dv;
+  const float *d0 = COMPOSE              ? nullptr
+                    : seg + 1 < p.nseg   ? p.xs + (bh * p.nseg + seg + 1) * size
+                            : p.state_in ? p.state_in + bh * size : nullptr;
+#pragma unroll
+  for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = 16 * i + 4 * g + r;
+      D[i][r] = d0 && row < p.Dk && xc < p.Dv ? d0[row * p.Dv + xc] : 0.f;
+    }
+  if (lo < hi) put(hi - 1);
+
+  for (int n = hi - 1; n >= lo; --n) {
+    const int m = min(L, len - n * L);
+    __syncthreads();
+    if (n > lo) fetch(n - 1);
+    if (!COMPOSE && xc < p.Dv) {
+      float *at = p.D + (bh * p.N + n) * size + xc;
+#pragma unroll
+      for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (16 * i + 4 * g + r < p.Dk) at[(16 * i + 4 * g + r) * p.Dv] = D[i][r];
+    }
+    for (int it = w; it < NT; it += NW) {
+      Frag<NP> qf[KB];
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        qf[kb] = frag_row<NP, LK>(Q, L * LK::row, 16 * it, kb, lane);
+      const int i = 16 * it + l16;
+#pragma unroll
+      for (int jt = 0; jt < NT; ++jt) {
+        if (jt > (it | 1)) continue;
+        f4 acc = {0.f, 0.f, 0.f, 0.f};
+        if (jt <= it) {
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+            acc = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * jt, kb, lane), qf[kb], acc);
+          const int j = 16 * jt + 4 * g;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[r] = j + r <= i ? p.scale * gs.decay(i, j + r) * acc[r] : 0.f;
+        }
+        f2 x = {acc[0], acc[1]}, y = {acc[2], acc[3]};
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          const b2 a = part2(x), d = part2(y);
+          *reinterpret_cast<Pack<bf16, 4> *>(P + c * L * LX::row + LX::at(i, 4 * jt + g)) =
+              Pack<bf16, 4>{{a[0], a[1], d[0], d[1]}};
+        }
+      }
+    }
+    // dU = P^T dO + e^{G_L - G} K dS
+    f4 dU[NT];
+#pragma unroll
+    for (int jt = 0; jt < NT; ++jt) dU[jt] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      const Frag<3> df = frag_of(D[2 * kb], D[2 * kb + 1]);
+#pragma unroll
+      for (int jt = 0; jt < NT; ++jt)
+        dU[jt] = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * jt, kb, lane), df, dU[jt]);
+    }
+#pragma unroll
+    for (int jt = 0; jt < NT; ++jt)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dU[jt][r] *= gs.to[16 * jt + 4 * g + r];
+    // dS <- e^{G_L} dS + scale (E Q)^T dO - (E K)^T dR
+    const float all = gs.all, low = gs.low;
+#pragma unroll
+    for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) D[i][r] = fmaf(D[i][r], low, D[i][r] * all);
+    Frag<NP> gf[JB];
+#pragma unroll
+    for (int ib = 0; ib < JB; ++ib) {
+      gf[ib] = frag_col<NP, LV>(G, L * LV::row, 32 * ib, w, lane);
+      float x[8];
+      values(gf[ib], x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] *= p.scale * gs.from[32 * ib + 16 * (e >> 2) + 4 * g + (e & 3)];
+      const Frag<3> ef = split<3>(x);
+#pragma unroll
+      for (int i = 0; i < 2 * KB; ++i)
+        D[i] = mma<3>(frag_col<NP, LK>(Q, L * LK::row, 32 * ib, i, lane), ef, D[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int ib = 0; ib < JB; ++ib)
+#pragma unroll
+      for (int jt = 0; jt <= 2 * ib + 1; ++jt)
+        dU[jt] = mma<3>(frag_col<3, LX>(P, L * LX::row, 32 * ib, jt, lane), gf[ib], dU[jt]);
+    f4 dR[NT];
+#pragma unroll
+    for (int jt = 0; jt < NT; ++jt) dR[jt] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ib = 0; ib < JB; ++ib) {
+      const Frag<3> df = frag_of(dU[2 * ib], dU[2 * ib + 1]);
+#pragma unroll
+      for (int jt = 0; jt <= 2 * ib + 1; ++jt)
+        dR[jt] = mma<3>(frag_col<3, LX>(X, L * LX::row, 32 * ib, jt, lane), df, dR[jt]);
+    }
+    if (!COMPOSE && xc < p.Dv) {
+      float *at = p.R + (bh * p.N + n) * L * p.Dv + xc;
+#pragma unroll
+      for (int jt = 0; jt < NT; ++jt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int j = 16 * jt + 4 * g + r;
+          at[(int64_t)j * p.Dv] = dR[jt][r];
+          if (p.dv && j < m) {
+            const int64_t e = (((int64_t)b * p.T + n * (int64_t)L + j) * p.H + h) * p.Dv + xc;
+            if (p.part_v)
+              ((float *)p.dv)[e] = dR[jt][r];
+            else
+              ((T *)p.dv)[e] = (T)dR[jt][r];
+          }
+        }
+    }
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        x[e] = dR[2 * jb + (e >> 2)][e & 3] * -gs.from[32 * jb + 16 * (e >> 2) + 4 * g + (e & 3)];
+      const Frag<3> rf = split<3>(x);
+#pragma unroll
+      for (int i = 0; i < 2 * KB; ++i)
+        D[i] = mma<3>(frag_col<NP, LK>(K, L * LK::row, 32 * jb, i, lane), rf, D[i]);
+    }
+    __syncthreads();
+    if (n > lo) put(n - 1);
+  }
+
+  float *to_d = COMPOSE ? p.xs + (bh * p.nseg + seg) * size
+                : p.state_out && seg == 0 ? p.state_out + bh * size : nullptr;
+  if (to_d) {
+#pragma unroll
+    for (int i = 0; i < 2 * KB; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * i + 4 * g + r;
+        if (row < p.Dk && xc < p.Dv)
+          to_d[row * p.Dv + xc] = !COMPOSE && valid < 0 ? p.bad : D[i][r];
+      }
+  }
+  if (!COMPOSE && p.dv) {
+    const int64_t f0 = max((int64_t)len, (int64_t)lo * L),
+                  f1 = min((int64_t)p.T, ((int64_t)lo + p.seg) * L);
+    for (int64_t e = threadIdx.x; e < (f1 - f0) * kCols; e += kThreads) {
+      const int col = c0 + (int)(e % kCols);
+      if (col >= p.Dv) continue;
+      const int64_t to = (((int64_t)b * p.T + f0 + e / kCols) * p.H + h) * p.Dv + col;
+      if (p.part_v)
+        ((float *)p.dv)[to] = 0.f;
+      else
+        ((T *)p.dv)[to] = (T)0.f;
+    }
+  }
+}
+
+// The gradients of q, k, the log decays and betas of a chunk, four waves each: a
+// wave has 16 positions (of L = 32, 16 positions and half of the keys' columns).
+// Contractions over the values' columns go in slices of 32; dP and dM are computed
+// twice, once as operands for the sums over what was written before a position
+// (by rows), once for those over what reads it (by columns): each time the layout
+// of the accumulators is that of the operand.
+template <typename T, int NP, int DK, int L>
+__global__ __launch_bounds__(256) void k_delta_grads(DeltaArgs p) {
+  constexpr int NT = L / 16, JB = L / 32, DS = 4 / NT, DT = DK / 16 / DS;
+  typedef ByRow<32> LS;
+  typedef ByColumn<DK> LK;
+  constexpr int kSlice = (6 * L + NP * L + 6 * DK) * LS::row, kKeys = 2 * NP * L * LK::row;
+  __shared__ alignas(16) bf16 tiles[kSlice > kKeys ? kSlice : kKeys];
+  bf16 *const U = tiles, *const R = U + 3 * L * LS::row, *const G = R + 3 * L * LS::row,
+             *const S = G + NP * L * LS::row, *const D = S + 3 * DK * LS::row;
+  bf16 *const K = tiles, *const Q = K + NP * L * LK::row;
+  __shared__ Gates<L> gs;
+  __shared__ float inv[L];
+  __shared__ double red[4], cs[DS][L], es[DS][L];
+
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  const int h = blockIdx.x % p.H, n = blockIdx.x / p.H % p.N, b = blockIdx.x / p.H / p.N;
+  const int t0 = n * L, count = min(L, max(valid_length(p.lengths, b, p.T), 0) - t0);
+  const int rest = min(L, p.T - t0);
+  const int64_t row0 = ((int64_t)b * p.T + t0) * p.H + h;
+  for (int e = threadIdx.x; e < rest * p.Dk; e += 256) {
+    const int i = e / p.Dk, d = e % p.Dk;
+    if (i < count) continue;
+    const int64_t row = row0 + (int64_t)i * p.H, to = row * p.Dk + d;
+    if (p.dq) { if (p.part_q) ((float *)p.dq)[to] = 0.f; else ((T *)p.dq)[to] = (T)0.f; }
+    if (p.dk) { if (p.part_k) ((float *)p.dk)[to] = 0.f; else ((T *)p.dk)[to] = (T)0.f; }
+    if (d == 0 && p.dg) p.dg[row] = 0.f;
+    if (d == 0 && p.db) p.db[row] = 0.f;
+  }
+  if (count <= 0) return;
+  const int64_t at = ((int64_t)b * p.H + h) * p.N + n, size = (int64_t)p.Dk * p.Dv;
+  const T *q = view_rows<T>(p.q, b, h) + t0 * p.q.st, *k = view_rows<T>(p.k, b, h) + t0 * p.k.st;
+  const int64_t so = (int64_t)p.H * p.Dv;
+  const T *go = (const T *)p.go + row0 * p.Dv;
+  const float *u = p.U + at * L * p.Dv, *dr = p.R + at * L * p.Dv, *s = p.S + at * size,
+              *ds = p.D + at * size;
+  const bool even = p.Dv % 4 == 0;
+  Tile32<LS, 32, L, 256, false> tu, tr;
+  Tile32<LS, 32, DK, 256, false> ts, td;
+  Tile<T, NP, LS, 32, L, 256> tg;
+  auto fetch = [&](int c0) {
+    tu.fetch(threadIdx.x, u + c0, p.Dv, L, p.Dv - c0, even);
+    tr.fetch(threadIdx.x, dr + c0, p.Dv, L, p.Dv - c0, even);
+    ts.fetch(threadIdx.x, s + c0, p.Dv, p.Dk, p.Dv - c0, even);
+    td.fetch(threadIdx.x, ds + c0, p.Dv, p.Dk, p.Dv - c0, even);
+    if (p.vec) tg.fetch(threadIdx.x, go, (int)so, p.Dv, count, 0, 1, c0);
+  };
+  fetch(0);
+  if (threadIdx.x < L) {
+    float bt = 1.f;
+    if (threadIdx.x < count) bt = p.beta[row0 + (int64_t)threadIdx.x * p.H];
+    if (fabsf(bt) < 0x1p-96f) bt = copysignf(0x1p-96f, bt);
+    inv[threadIdx.x] = 1.f / bt;
+  }
+  for (int e = threadIdx.x; e < delta_gates(L); e += 256)
+    (&gs.hi[0])[e] = p.gates[at * delta_gates(L) + e];
+  const int pt = w % NT, d0 = w / NT * DT;
+  f4 dq[DT], df[DT], dw[DT], pr[NT], pc[NT], mr[NT], mc[NT];
+  const f4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < DT; ++i) dq[i] = df[i] = dw[i] = zero;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) pr[i] = pc[i] = mr[i] = mc[i] = zero;
+  double dot = 0;               // S . dS', this thread's share
+  float dbs[decltype(tu)::N];   // (dR / b) . (U / b) of the rows it reads
+#pragma unroll
+  for (int i = 0; i < decltype(tu)::N; ++i) dbs[i] = 0.f;
+  for (int c0 = 0; c0 < p.Dv; c0 += 32) {
+    __syncthreads();
+    tu.put(threadIdx.x, U);
+    tr.put(threadIdx.x, R);
+    ts.put(threadIdx.x, S);
+    td.put(threadIdx.x, D);
+    if (p.vec)
+      tg.put(threadIdx.x, G);
+    else
+      stage<T, NP, LS, 32, L, 256>(G, go, so, p.Dv, count, c0);
+#pragma unroll
+    for (int i = 0; i < decltype(tu)::N; ++i) {
+      const float iv = inv[(threadIdx.x + i * 256) / 8 % L];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dbs[i] = fmaf(tr.r[i][r] * iv, tu.r[i][r] * iv, dbs[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < decltype(ts)::N; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) dot += (double)ts.r[i][r] * td.r[i][r];
+    __syncthreads();
+    if (c0 + 32 < p.Dv) fetch(c0 + 32);
+    const Frag<NP> gf = frag_row<NP, LS>(G, L * LS::row, 16 * pt, 0, lane);
+    const Frag<3> uf = frag_row<3, LS>(U, L * LS::row, 16 * pt, 0, lane);
+    const Frag<3> rf = frag_row<3, LS>(R, L * LS::row, 16 * pt, 0, lane);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t <= pt) {
+        const Frag<3> x = frag_row<3, LS>(U, L * LS::row, 16 * t, 0, lane);
+        pr[t] = mma<3>(x, gf, pr[t]);
+        mr[t] = mma<3>(x, rf, mr[t]);
+      }
+      if (t >= pt) {
+        pc[t] = mma<3>(frag_row<NP, LS>(G, L * LS::row, 16 * t, 0, lane), uf, pc[t]);
+        mc[t] = mma<3>(frag_row<3, LS>(R, L * LS::row, 16 * t, 0, lane), uf, mc[t]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      const Frag<3> x = frag_row<3, LS>(S, DK * LS::row, 16 * (d0 + i), 0, lane);
+      dq[i] = mma<3>(x, gf, dq[i]);
+      df[i] = mma<3>(x, rf, df[i]);
+      dw[i] = mma<3>(frag_row<3, LS>(D, DK * LS::row, 16 * (d0 + i), 0, lane), uf, dw[i]);
+    }
+  }
+  Tile<T, NP, LK, DK, L, 256> tk, tq;
+  if (p.vec) {
+    tk.fetch(threadIdx.x, k, (int)p.k.st, p.Dk, count, 0, 1, 0);
+    tq.fetch(threadIdx.x, q, (int)p.q.st, p.Dk, count, 0, 1, 0);
+  }
+  __syncthreads();
+  if (p.vec) {
+    tk.put(threadIdx.x, K);
+    tq.put(threadIdx.x, Q);
+  } else {
+    stage<T, NP, LK, DK, L, 256>(K, k, p.k.st, p.Dk, count, 0);
+    stage<T, NP, LK, DK, L, 256>(Q, q, p.q.st, p.Dk, count, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < decltype(tu)::N; ++i) {
+    float x = dbs[i];
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) x += __shfl_xor(x, o);
+    const int e = threadIdx.x + i * 256, row = e / 8;
+    if (p.db && e < decltype(tu)::all && e % 8 == 0 && row < count)
+      p.db[row0 + (int64_t)row * p.H] = x;
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) dot += __shfl_xor(dot, o);
+  if (lane == 0) red[w] = dot;
+  __syncthreads();
+  const int mine = 16 * pt + l16;
+  const float from = gs.from[mine], to = gs.to[mine];
+  // four neighbours of this position's row of K or Q
+  auto four = [&](const bf16 *t, int i) {
+    f4 x = zero;
+#pragma unroll
+    for (int m = 0; m < NP; ++m) {
+      const Pack<bf16, 4> y = *reinterpret_cast<const Pack<bf16, 4> *>(
+          t + m * L * LK::row + LK::at(mine, 4 * (d0 + i) + g));
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] += (float)y.v[r];
+    }
+    return x;
+  };
+  float c = 0.f, e = 0.f;
+#pragma unroll
+  for (int i = 0; i < DT; ++i) {
+    const f4 kv = four(K, i);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      dq[i][r] *= p.scale * from;
+      df[i][r] *= -from;
+      dw[i][r] *= to;
+      e += kv[r] * dw[i][r];
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int o = 16 * t + 4 * g + r;
+      const float before = t <= pt && o <= mine ? gs.decay(mine, o) : 0.f;
+      const float later = t >= pt && o >= mine ? gs.decay(o, mine) : 0.f;
+      pr[t][r] *= p.scale * before;
+      pc[t][r] *= p.scale * later;
+      mr[t][r] *= o < mine ? -before : 0.f;
+      mc[t][r] *= o > mine ? -later : 0.f;
+    }
+#pragma unroll
+  for (int jb = 0; jb < JB; ++jb) {
+    if (2 * jb <= pt) {
+      const Frag<3> a = frag_of(pr[2 * jb], pr[2 * jb + 1]), m = frag_of(mr[2 * jb], mr[2 * jb + 1]);
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        const Frag<NP> x = frag_col<NP, LK>(K, L * LK::row, 32 * jb, d0 + i, lane);
+        dq[i] = mma<3>(x, a, dq[i]);
+        df[i] = mma<3>(x, m, df[i]);
+      }
+    }
+    if (2 * jb + 1 >= pt) {
+      const Frag<3> a = frag_of(pc[2 * jb], pc[2 * jb + 1]), m = frag_of(mc[2 * jb], mc[2 * jb + 1]);
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        dw[i] = mma<3>(frag_col<NP, LK>(Q, L * LK::row, 32 * jb, d0 + i, lane), a, dw[i]);
+        dw[i] = mma<3>(frag_col<NP, LK>(K, L * LK::row, 32 * jb, d0 + i, lane), m, dw[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < DT; ++i) {
+    const f4 kv = four(K, i), qv = four(Q, i);
+    const int d = 16 * (d0 + i) + 4 * g;
+    f4 sum;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      c += qv[r] * dq[i][r] + kv[r] * (df[i][r] - dw[i][r]);
+      sum[r] = df[i][r] + dw[i][r];
+    }
+    if (mine >= count || d >= p.Dk) continue;
+    const int64_t to = (row0 + (int64_t)mine * p.H) * p.Dk + d;
+    auto give = [&](void *out, int part, const f4 &x) {
+      if (p.vec_out) {
+        if (part) {
+          *reinterpret_cast<f4 *>((float *)out + to) = x;
+        } else {
+          Pack<T, 4> y;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y.v[r] = (T)x[r];
+          *reinterpret_cast<Pack<T, 4> *>((T *)out + to) = y;
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (d + r < p.Dk) {
+            if (part)
+              ((float *)out)[to + r] = x[r];
+            else
+              ((T *)out)[to + r] = (T)x[r];
+          }
+      }
+    };
+    if (p.dq) give(p.dq, p.part_q, dq[i]);
+    if (p.dk) give(p.dk, p.part_k, sum);
+  }
+#pragma unroll
+  for (int o = 16; o < 64; o <<= 1) c += __shfl_xor(c, o), e += __shfl_xor(e, o);
+  if (g == 0) cs[w / NT][mine] = c, es[w / NT][mine] = e;
+  __syncthreads();
+  if (w == 0 && p.dg) {
+    double x = 0, y = 0;
+    if (lane < L)
+#pragma unroll
+      for (int i = 0; i < DS; ++i) x += cs[i][lane], y += es[i][lane];
+#pragma unroll
+    for (int o = 32; o; o >>= 1) y += __shfl_xor(y, o);
+    y += ((double)gs.all + gs.low) * (red[0] + red[1] + red[2] + red[3]);
+    // sums from a position to the chunk's end
+#pragma unroll
+    for (int o = 1; o < L; o <<= 1) {
+      const double z = __shfl_down(x, o);
+      if (lane + o < L) x += z;
+    }
+    if (lane < count) {
+      const int64_t row = row0 + (int64_t)lane * p.H;
+      p.dg[row] = p.log_decay[row] < -104.f ? 0.f : (float)(x + y);
+    }
+  }
+}
+
+namespace {
+
+template <typename T, int NP, int DK, int NW>
+semicrf_status_t delta_walk(DeltaArgs p, DeltaPass pass, hipStream_t st) {
+  constexpr int L = delta_chunk(NP);
+  const int vt = (p.Dv + 16 * NW - 1) / (16 * NW);
+  p.ktiles = pass == DELTA_COMPOSE ? (p.Dk + 16 * NW - 1) / (16 * NW) : 0;
+  p.ctiles = vt + p.ktiles;
+  const int64_t grid = (int64_t)p.B * p.H * p.count * p.ctiles;
+  if (pass == DELTA_COMPOSE)
+    k_delta_chunks<T, NP, DK, NW, L, true><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
+  else if (pass == DELTA_FORWARD)
+    k_delta_chunks<T, NP, DK, NW, L, false><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
+  else if (pass == DELTA_COMPOSE_BACK)
+    k_delta_back<T, NP, DK, NW, L, true><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
+  else
+    k_delta_back<T, NP, DK, NW, L, false><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
+  return launch_status();
+}
+
+template <typename T, int NP, int DK>
+semicrf_status_t delta_width(const DeltaArgs &p, DeltaPass pass, hipStream_t st) {
+  constexpr int L = delta_chunk(NP);
+  const unsigned grid = (unsigned)((int64_t)p.B * p.H * p.N);
+  if (pass == DELTA_INVERSE) {
+    k_delta_inverse<T, NP, DK, L><<<grid, 256, 0, st>>>(p);
+    return launch_status();
+  }
+  if (pass == DELTA_GRADS) {
+    k_delta_grads<T, NP, DK, L><<<grid, 256, 0, st>>>(p);
+    return launch_status();
+  }
+  switch (delta_waves(p.Dv)) {
+    case 2: return delta_walk<T, NP, DK, 2>(p, pass, st);
+    case 4: return delta_walk<T, NP, DK, 4>(p, pass, st);
+    default: return delta_walk<T, NP, DK, 8>(p, pass, st);
+  }
+}
+
+template <typename T, int NP>
+semicrf_status_t delta_type(const DeltaArgs &p, DeltaPass pass, hipStream_t st) {
+  if (p.Dk <= 32) return delta_width<T, NP, 32>(p, pass, st);
+  if (p.Dk <= 64) return delta_width<T, NP, 64>(p, pass, st);
+  return delta_width<T, NP, 128>(p, pass, st);
+}
+
+}  // namespace
+
+}  // namespace semicrf

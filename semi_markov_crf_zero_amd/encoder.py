@@ -85,7 +85,7 @@ def load():
         lib.semicrf_linattn_step.argtypes = [P] * 6 + [I, P, P, P]
         lib.semicrf_groupnorm_fwd.argtypes = [P] * 7 + [P, Z, P]
         lib.semicrf_groupnorm_bwd.argtypes = [P] * 10 + [P, Z, P]
-        lib.semicrf_delta_fwd.argtypes = [P] * 10 + [P, Z, P]
+        lib.semicrf_delta_fwd.argtypes = [P, I] + [P] * 9 + [P, Z, P]
         lib.semicrf_delta_bwd.argtypes = [P] * 16 + [P, Z, P]
         lib.semicrf_delta_step.argtypes = [P] * 7 + [I, P, P, P]
         lib.semicrf_rotary.argtypes = [P] * 8
@@ -363,7 +363,7 @@ class GatedDelta(torch.autograd.Function):
     is what _delta_check gives."""
 
     @staticmethod
-    def forward(ctx, q, k, v, log_decay, beta, state, lengths, dims, scale):
+    def forward(ctx, q, k, v, log_decay, beta, state, lengths, dims, scale, keep):
         ctx.set_materialize_grads(False)
         ctx.dims, ctx.scale = dims, scale
         saved = q, k, v, log_decay, beta, lengths
@@ -373,8 +373,8 @@ class GatedDelta(torch.autograd.Function):
         fields = (*dims, scale, _strides(q), _strides(k), _strides(v))
         o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
         last = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
-        ws, n = _workspace("semicrf_delta_workspace_size", _LinattnShape, fields, 0, dev)
-        launch(load().semicrf_delta_fwd, dev, ctypes.byref(_LinattnShape(*fields)), _ptr(q),
+        ws, n = _workspace("semicrf_delta_workspace_size", _LinattnShape, fields, int(keep), dev)
+        launch(load().semicrf_delta_fwd, dev, ctypes.byref(_LinattnShape(*fields)), keep, _ptr(q),
                _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(lengths), _ptr(state), _ptr(o),
                _ptr(last), _ptr(ws), n)
         ctx.save_for_backward(*saved, ws)
@@ -395,12 +395,12 @@ class GatedDelta(torch.autograd.Function):
             do = torch.zeros((B, T, H, Dv), dtype=q.dtype, device=dev)
         do = do.contiguous()
         dlast = None if dlast is None else dlast.contiguous()
-        ws, n = _workspace("semicrf_delta_workspace_size", _LinattnShape, fields, 1, dev)
+        ws, n = _workspace("semicrf_delta_workspace_size", _LinattnShape, fields, 2, dev)
         launch(load().semicrf_delta_bwd, dev, ctypes.byref(_LinattnShape(*fields)), _ptr(q),
                _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(lengths), _ptr(work), _ptr(do),
                _ptr(dlast), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(db), _ptr(dstate),
                _ptr(ws), n)
-        return dq, dk, dv, dg, db, dstate, None, None, None
+        return dq, dk, dv, dg, db, dstate, None, None, None, None
 
 
 def gated_delta(q, k, v, log_decay, beta, lengths=None, state=None, scale=None,
@@ -430,8 +430,10 @@ def gated_delta(q, k, v, log_decay, beta, lengths=None, state=None, scale=None,
             bad = ((lengths < 0) | (lengths > T))[:, None, None, None]
             last = torch.where(bad, math.nan, last)
     else:
+        keep = torch.is_grad_enabled() and any(
+            t is not None and t.requires_grad for t in (q, k, v, log_decay, beta, state))
         o, last = GatedDelta.apply(q, k, v, log_decay, beta, state, lengths, dims,
-                                   Dk ** -0.5 if scale is None else float(scale))
+                                   Dk ** -0.5 if scale is None else float(scale), keep)
     return (o, last) if return_state else o
 
 

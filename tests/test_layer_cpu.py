@@ -46,7 +46,7 @@ def test_delta_shapes_refused(lib, kw, code):
     s, n = shape(**kw), ctypes.c_size_t(0)
     r = ctypes.byref(s)
     assert lib.semicrf_delta_workspace_size(r, 0, ctypes.byref(n)) == code
-    assert lib.semicrf_delta_fwd(r, P, P, P, P, P, None, None, P, None, P, 1 << 60, None) == code
+    assert lib.semicrf_delta_fwd(r, 0, P, P, P, P, P, None, None, P, None, P, 1 << 60, None) == code
     assert lib.semicrf_delta_bwd(r, P, P, P, P, P, None, P, P, None, P, P, P, P, P, None, P, 1 << 60,
                                  None) == code
 
@@ -56,12 +56,13 @@ def test_delta_null_and_workspace(lib):
     r = ctypes.byref(s)
     assert lib.semicrf_delta_workspace_size(r, 1, None) == 1
     assert lib.semicrf_delta_workspace_size(None, 1, ctypes.byref(n)) == 1
-    for back in (0, 1):
-        assert lib.semicrf_delta_workspace_size(r, back, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.semicrf_delta_workspace_size(r, 3, ctypes.byref(n)) == 6
+    for way in (0, 1, 2):
+        assert lib.semicrf_delta_workspace_size(r, way, ctypes.byref(n)) == 0 and n.value > 0
     for i in (0, 1, 2, 3, 4, 7):
         a = [P, P, P, P, P, None, None, P, None]
         a[i] = None
-        assert lib.semicrf_delta_fwd(r, *a, P, 1 << 40, None) == 1
+        assert lib.semicrf_delta_fwd(r, 1, *a, P, 1 << 40, None) == 1
     for i in (0, 1, 2, 3, 4, 6, 7):
         b = [P, P, P, P, P, None, P, P, None, P, P, P, P, P, P]
         b[i] = None
@@ -69,8 +70,9 @@ def test_delta_null_and_workspace(lib):
     b = [P, P, P, P, P, None, P, P, None, P, P, P, P, P, P]
     assert lib.semicrf_delta_bwd(r, *b, P, n.value - 1, None) == 4
     assert lib.semicrf_delta_bwd(r, *b, None, n.value, None) == 4
-    assert lib.semicrf_delta_workspace_size(r, 0, ctypes.byref(n)) == 0
-    assert lib.semicrf_delta_fwd(r, P, P, P, P, P, None, None, P, None, P, n.value - 1, None) == 4
+    for keep in (0, 1):
+        assert lib.semicrf_delta_workspace_size(r, keep, ctypes.byref(n)) == 0
+        assert lib.semicrf_delta_fwd(r, keep, P, P, P, P, P, None, None, P, None, P, n.value - 1, None) == 4
     step = [P, P, P, P, P, None, 4, P, P]
     assert lib.semicrf_delta_step(r, *step, None) == 2  # T is not 1
     s.T = 1
