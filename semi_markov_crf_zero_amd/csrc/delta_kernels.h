@@ -141,11 +141,16 @@ __device__ __forceinline__ f4 mfma32(float a, float b, f4 c) {
 // to 32 and 64 with float32 matrix instructions: what substitution gives, whatever
 // the keys' lengths.
 template <typename T, int NP, int DK, int L>
-__global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs p) {
-  constexpr int KB = DK / 32, NT = L / 16, LD = L + 4;
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k_delta_inverse(
+    DeltaArgs p) {
+  constexpr int KB = DK / 32, NT = L / 16, LD = L + 4, LT = L / 2 + 4;
   typedef ByRow<DK> LK;
-  __shared__ alignas(16) bf16 K[NP * L * LK::row];
-  __shared__ alignas(16) float M[L * LD], X[L * LD], Xt[L * LD];  // Xt: by columns
+  // the inverse takes M's place block by block; T1 by columns, of tiles 0, 1 (whole)
+  // and 2 (its first 16 rows); K is done with by then
+  constexpr int kKeys = NP * L * LK::row, kCols = (L == 64 ? 48 : 16) * LT;
+  __shared__ alignas(16) float M[L * LD];
+  __shared__ alignas(16) float Xt[kCols > kKeys / 2 ? kCols : kKeys / 2];
+  bf16 *const K = (bf16 *)Xt;
   __shared__ Gates<L> s;
   __shared__ float beta[L];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
@@ -201,16 +206,12 @@ __global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs p) {
     for (int r = 0; r < 4; ++r) acc[r] = j + r < i ? beta[i] * s.decay(i, j + r) * acc[r] : 0.f;
     *reinterpret_cast<f4 *>(M + i * LD + j) = acc;
   }
-  for (int e = threadIdx.x; e < L * L / 4; e += 256) {
-    const int i = e / (L / 4), j = e % (L / 4) * 4;
-    if (j / 16 > i / 16) *reinterpret_cast<f4 *>(X + i * LD + j) = f4{0.f, 0.f, 0.f, 0.f};
-  }
   for (int e = threadIdx.x; e < delta_gates(L); e += 256)
     p.gates[at * delta_gates(L) + e] = (&s.hi[0])[e];
   __syncthreads();
   if (w < NT) {
     float x[16];
-    const float *m = M + 16 * w * LD + 16 * w;
+    float *m = M + 16 * w * LD + 16 * w;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float y = i == l16 ? 1.f : 0.f;
@@ -221,13 +222,13 @@ __global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs p) {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (i / 4 == g) {
-        X[(16 * w + i) * LD + 16 * w + l16] = x[i];
-        Xt[(16 * w + l16) * LD + 16 * w + i] = x[i];
+        M[(16 * w + i) * LD + 16 * w + l16] = x[i];
+        if (w < kCols / LT / 16) Xt[(16 * w + l16) * LT + (16 * w + i) % (L / 2)] = x[i];
       }
   }
   __syncthreads();
   // blocks of n16 tiles beside each other: rows it, columns ct of the lower left
-  // one of a pair, T2 and T1 in X and Xt
+  // one of a pair
 #pragma unroll
   for (int n16 = 1; n16 < NT; n16 *= 2) {
     const int pairs = NT / (2 * n16), jobs = pairs * n16 * n16;
@@ -240,11 +241,12 @@ __global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs p) {
         f4 y = {0.f, 0.f, 0.f, 0.f};  // rows of tile mt of M21 T1
         for (int jt = ct; jt < base + n16; ++jt) {
           const f4 a = *reinterpret_cast<const f4 *>(M + (16 * mt + l16) * LD + 16 * jt + 4 * g);
-          const f4 c = *reinterpret_cast<const f4 *>(Xt + (16 * ct + l16) * LD + 16 * jt + 4 * g);
+          const f4 c = *reinterpret_cast<const f4 *>(Xt + (16 * ct + l16) * LT +
+                                                     (16 * jt + 4 * g) % (L / 2));
 #pragma unroll
           for (int r = 0; r < 4; ++r) y = mfma32(a[r], c[r], y);
         }
-        const f4 a = *reinterpret_cast<const f4 *>(X + (16 * it + l16) * LD + 16 * mt + 4 * g);
+        const f4 a = *reinterpret_cast<const f4 *>(M + (16 * it + l16) * LD + 16 * mt + 4 * g);
 #pragma unroll
         for (int r = 0; r < 4; ++r) out = mfma32(a[r], -y[r], out);
       }
@@ -252,17 +254,17 @@ __global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs p) {
     __syncthreads();
     if (w < jobs) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) X[(16 * it + 4 * g + r) * LD + 16 * ct + l16] = out[r];
-      *reinterpret_cast<f4 *>(Xt + (16 * ct + l16) * LD + 16 * it + 4 * g) = out;
+      for (int r = 0; r < 4; ++r) M[(16 * it + 4 * g + r) * LD + 16 * ct + l16] = out[r];
+      if (it < NT / 2) *reinterpret_cast<f4 *>(Xt + (16 * ct + l16) * LT + 16 * it + 4 * g) = out;
     }
     __syncthreads();
   }
   const int ld = p.ld;
   for (int e = threadIdx.x; e < ld * ld / 4; e += 256) {
     const int i = e / (ld / 4), j = e % (ld / 4) * 4;
-    f4 x = *reinterpret_cast<const f4 *>(X + i * LD + j);
+    f4 x = *reinterpret_cast<const f4 *>(M + i * LD + j);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) x[r] *= beta[j + r];
+    for (int r = 0; r < 4; ++r) x[r] = j / 16 > i / 16 ? 0.f : x[r] * beta[j + r];
     *reinterpret_cast<f4 *>(p.X + at * ld * ld + i * ld + j) = x;
   }
 }
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(256) void k_delta_inverse(DeltaArgs p) {
 // segment's transition [phi | sum], from [I | 0], with values of 0 for the first; else
 // the outputs (and what the backward pass reads again) from the state before it.
 template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
-__global__ __launch_bounds__(64 * NW) void k_delta_chunks(DeltaArgs p) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_chunks(DeltaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
   constexpr int KB = DK / 32, NT = L / 16, JB = L / 32;
   typedef ByBoth<DK> LK;
@@ -527,12 +529,12 @@ __global__ __launch_bounds__(64 * NW) void k_delta_chunks(DeltaArgs p) {
 // gradient after the segment, leaving that after each chunk in D, the gradients of
 // R in R and of the values in dv.
 template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
-__global__ __launch_bounds__(64 * NW) void k_delta_back(DeltaArgs p) {
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_back(DeltaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
   constexpr int KB = DK / 32, NT = L / 16, JB = L / 32;
   typedef ByBoth<DK> LK;
   typedef ByColumn<kCols> LV;
-  typedef ByColumn<L> LX;
+  typedef ByBoth<L> LX;
   __shared__ alignas(16) bf16 K[NP * L * LK::row];
   __shared__ alignas(16) bf16 Q[NP * L * LK::row];
   __shared__ alignas(16) bf16 G[NP * L * LV::row];
@@ -754,7 +756,7 @@ __global__ __launch_bounds__(64 * NW) void k_delta_back(DeltaArgs p) {
 // (by rows), once for those over what reads it (by columns): each time the layout
 // of the accumulators is that of the operand.
 template <typename T, int NP, int DK, int L>
-__global__ __launch_bounds__(256) void k_delta_grads(DeltaArgs p) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_grads(DeltaArgs p) {
   constexpr int NT = L / 16, JB = L / 32, DS = 4 / NT, DT = DK / 16 / DS;
   typedef ByRow<32> LS;
   typedef ByColumn<DK> LK;
