@@ -114,6 +114,14 @@ struct Tile32 {
   }
 };
 
+// A number as something new to the compiler: what follows from it (addresses in
+// LDS) is then computed again in every chunk instead of being kept in registers
+// all along.  The load of a spilled register would wait for every tile on its way.
+__device__ __forceinline__ int delta_fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // The tiles of 16 rows 2 b and 2 b + 1 of an accumulated matrix as an operand whose
 // contraction runs over them.
 __device__ __forceinline__ Frag<3> frag_of(const f4 &a, const f4 &b) {
@@ -288,14 +296,14 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   __shared__ alignas(16) bf16 P[COMPOSE ? 8 : 3 * L * LX::row];
   __shared__ Gates<L> gs;
 
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  const int tid = threadIdx.x, w = tid >> 6, g0 = (tid & 63) >> 4, l0 = tid & 15;
   int ct = blockIdx.x % p.ctiles;
   const int seg = p.first + blockIdx.x / p.ctiles % p.count;
   const int64_t bh = blockIdx.x / p.ctiles / p.count;
   const int h = (int)(bh % p.H), b = (int)(bh / p.H);
   const bool phi = COMPOSE && ct < p.ktiles;
   if (COMPOSE && !phi) ct -= p.ktiles;
-  const int c0 = ct * kCols, xc = c0 + 16 * w + l16, width = phi ? p.Dk : p.Dv;
+  const int c0 = ct * kCols, xc = c0 + 16 * w + l0, width = phi ? p.Dk : p.Dv;
   const int valid = valid_length(p.lengths, b, p.T), len = max(valid, 0);
   const int chunks = (len + L - 1) / L;
   const int lo = seg * p.seg, hi = min(chunks, lo + p.seg);
@@ -307,23 +315,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   Tile32<LX, L, L, kThreads, true> tx;
   GatesTile<L, kThreads> tg;
   auto fetch = [&](int n) {
+    const int tid = delta_fresh(threadIdx.x);
     const int64_t t0 = (int64_t)n * L;
     const int m = (int)min((int64_t)L, len - t0);
     const int64_t at = bh * p.N + n;
-    tg.fetch(threadIdx.x, p.gates + at * delta_gates(L));
-    tx.fetch(threadIdx.x, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld, true);
+    tg.fetch(tid, p.gates + at * delta_gates(L));
+    tx.fetch(tid, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld, true);
     if (!p.vec) return;
-    tk.fetch(threadIdx.x, k + t0 * p.k.st, (int)p.k.st, p.Dk, m, 0, 1, 0);
-    if (!COMPOSE) tq.fetch(threadIdx.x, q + t0 * p.q.st, (int)p.q.st, p.Dk, m, 0, 1, 0);
-    tv.fetch(threadIdx.x, v + t0 * p.v.st, (int)p.v.st, p.Dv, phi ? 0 : m, 0, 1, c0);
+    tk.fetch(tid, k + t0 * p.k.st, (int)p.k.st, p.Dk, m, 0, 1, 0);
+    if (!COMPOSE) tq.fetch(tid, q + t0 * p.q.st, (int)p.q.st, p.Dk, m, 0, 1, 0);
+    tv.fetch(tid, v + t0 * p.v.st, (int)p.v.st, p.Dv, phi ? 0 : m, 0, 1, c0);
   };
   auto put = [&](int n) {
-    tg.put(threadIdx.x, gs);
-    tx.put(threadIdx.x, X);
+    const int tid = delta_fresh(threadIdx.x);
+    tg.put(tid, gs);
+    tx.put(tid, X);
     if (p.vec) {
-      tk.put(threadIdx.x, K);
-      if (!COMPOSE) tq.put(threadIdx.x, Q);
-      tv.put(threadIdx.x, V);
+      tk.put(tid, K);
+      if (!COMPOSE) tq.put(tid, Q);
+      tv.put(tid, V);
     } else {
       const int64_t t0 = (int64_t)n * L;
       const int m = (int)min((int64_t)L, len - t0);
@@ -344,7 +354,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = 16 * i + 4 * g + r;
+      const int row = 16 * i + 4 * g0 + r;
       S[i][r] = phi ? (row == xc ? 1.f : 0.f)
                     : s0 && row < p.Dk && xc < p.Dv ? s0[row * p.Dv + xc] : 0.f;
     }
@@ -355,6 +365,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   for (int n = lo; n < hi; ++n) {
     const int m = min(L, len - n * L);
     __syncthreads();
+    const int lane = delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
     if (n + 1 < hi) fetch(n + 1);
     if (!COMPOSE && p.S && xc < p.Dv) {
       float *to = p.S + (bh * p.N + n) * size + xc;
@@ -420,19 +431,6 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         x[e] -= gs.from[32 * jb + 16 * (e >> 2) + 4 * g + (e & 3)] * ks[e >> 2][e & 3];
       rf[jb] = split<3>(x);
     }
-    // U = X R
-#pragma unroll
-    for (int jb = 0; jb < JB; ++jb)
-#pragma unroll
-      for (int it = 2 * jb; it < NT; ++it)
-        U[it] = mma<3>(frag_row<3, LX>(X, L * LX::row, 16 * it, jb, lane), rf[jb], U[it]);
-    if (!COMPOSE && p.U && xc < p.Dv) {
-      float *to = p.U + (bh * p.N + n) * L * p.Dv + xc;
-#pragma unroll
-      for (int it = 0; it < NT; ++it)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) to[(int64_t)(16 * it + 4 * g + r) * p.Dv] = U[it][r];
-    }
     // what the state gives, transposed: a lane holds four neighbours of a row of O
     f4 O[NT];
     if (!COMPOSE) {
@@ -446,6 +444,19 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
         for (int r = 0; r < 4; ++r) O[it][r] *= d;
       }
+    }
+    // U = X R
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb)
+#pragma unroll
+      for (int it = 2 * jb; it < NT; ++it)
+        U[it] = mma<3>(frag_row<3, LX>(X, L * LX::row, 16 * it, jb, lane), rf[jb], U[it]);
+    if (!COMPOSE && p.U && xc < p.Dv) {
+      float *to = p.U + (bh * p.N + n) * L * p.Dv + xc;
+#pragma unroll
+      for (int it = 0; it < NT; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) to[(int64_t)(16 * it + 4 * g + r) * p.Dv] = U[it][r];
     }
     // S <- e^{G_L} S + K^T (e^{G_L - G} U)
     Frag<3> uf[JB];
@@ -499,7 +510,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * g + r;
+        const int row = 16 * i + 4 * g0 + r;
         if (row < p.Dk && xc < width) to[row * width + xc] = S[i][r];
       }
     return;
@@ -517,7 +528,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * g + r;
+        const int row = 16 * i + 4 * g0 + r;
         if (row < p.Dk && xc < p.Dv)
           p.state_out[bh * size + row * p.Dv + xc] = valid < 0 ? p.bad : S[i][r];
       }
@@ -542,11 +553,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   __shared__ alignas(16) bf16 P[3 * L * LX::row];
   __shared__ Gates<L> gs;
 
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  const int tid = threadIdx.x, w = tid >> 6, g0 = (tid & 63) >> 4, l0 = tid & 15;
   const int ct = blockIdx.x % p.ctiles, seg = p.first + blockIdx.x / p.ctiles % p.count;
   const int64_t bh = blockIdx.x / p.ctiles / p.count;
   const int h = (int)(bh % p.H), b = (int)(bh / p.H);
-  const int c0 = ct * kCols, xc = c0 + 16 * w + l16;
+  const int c0 = ct * kCols, xc = c0 + 16 * w + l0;
   const int valid = valid_length(p.lengths, b, p.T), len = max(valid, 0);
   const int chunks = (len + L - 1) / L;
   const int lo = seg * p.seg, hi = min(chunks, lo + p.seg);
@@ -559,23 +570,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   Tile32<LX, L, L, kThreads, true> tx;
   GatesTile<L, kThreads> tg;
   auto fetch = [&](int n) {
+    const int tid = delta_fresh(threadIdx.x);
     const int64_t t0 = (int64_t)n * L;
     const int m = (int)min((int64_t)L, len - t0);
     const int64_t at = bh * p.N + n;
-    tg.fetch(threadIdx.x, p.gates + at * delta_gates(L));
-    tx.fetch(threadIdx.x, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld, true);
+    tg.fetch(tid, p.gates + at * delta_gates(L));
+    tx.fetch(tid, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld, true);
     if (!p.vec) return;
-    tk.fetch(threadIdx.x, k + t0 * p.k.st, (int)p.k.st, p.Dk, m, 0, 1, 0);
-    tq.fetch(threadIdx.x, q + t0 * p.q.st, (int)p.q.st, p.Dk, m, 0, 1, 0);
-    to.fetch(threadIdx.x, go + t0 * so, (int)so, p.Dv, m, 0, 1, c0);
+    tk.fetch(tid, k + t0 * p.k.st, (int)p.k.st, p.Dk, m, 0, 1, 0);
+    tq.fetch(tid, q + t0 * p.q.st, (int)p.q.st, p.Dk, m, 0, 1, 0);
+    to.fetch(tid, go + t0 * so, (int)so, p.Dv, m, 0, 1, c0);
   };
   auto put = [&](int n) {
-    tg.put(threadIdx.x, gs);
-    tx.put(threadIdx.x, X);
+    const int tid = delta_fresh(threadIdx.x);
+    tg.put(tid, gs);
+    tx.put(tid, X);
     if (p.vec) {
-      tk.put(threadIdx.x, K);
-      tq.put(threadIdx.x, Q);
-      to.put(threadIdx.x, G);
+      tk.put(tid, K);
+      tq.put(tid, Q);
+      to.put(tid, G);
     } else {
       const int64_t t0 = (int64_t)n * L;
       const int m = (int)min((int64_t)L, len - t0);
@@ -594,7 +607,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int row = 16 * i + 4 * g + r;
+      const int row = 16 * i + 4 * g0 + r;
       D[i][r] = d0 && row < p.Dk && xc < p.Dv ? d0[row * p.Dv + xc] : 0.f;
     }
   if (lo < hi) put(hi - 1);
@@ -602,6 +615,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   for (int n = hi - 1; n >= lo; --n) {
     const int m = min(L, len - n * L);
     __syncthreads();
+    const int lane = delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
     if (n > lo) fetch(n - 1);
     if (!COMPOSE && xc < p.Dv) {
       float *at = p.D + (bh * p.N + n) * size + xc;
@@ -729,7 +743,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int row = 16 * i + 4 * g + r;
+        const int row = 16 * i + 4 * g0 + r;
         if (row < p.Dk && xc < p.Dv)
           to_d[row * p.Dv + xc] = !COMPOSE && valid < 0 ? p.bad : D[i][r];
       }
