@@ -29,7 +29,7 @@ extern "C" {
  *
  * The shape, the layout of q, k, v, o and their gradients, shared heads and
  * states are linear attention's.  1 <= Dk, Dv <= 128 (SEMICRF_ERR_UNSUPPORTED
- * past that); T <= 2^30; B * H * ceil(T / 32) < 2^24 (SEMICRF_ERR_SHAPE: a
+ * past that); T <= 2^30; B * H * ceil(T / 32) < 2^23 (SEMICRF_ERR_SHAPE: a
  * launch has at most 2^32 - 1 threads).
  *
  * Non-finite inputs are not checked: one at a valid position may reach any

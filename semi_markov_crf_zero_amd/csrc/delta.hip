@@ -44,77 +44,82 @@ constexpr int kScanThreads = 256;
 
 // X <- phi X + sum over the segments, 16 columns a workgroup of four waves; X after
 // segment s takes the place of its sum.  REV: from the last segment on, with phi^T.  A
-// wave has DK / 64 tiles of rows; X is read by all from LDS, by columns.
+// wave has DK / 64 tiles of rows; X is read by all from LDS, by columns.  A step is
+// 500 cycles of one matrix product after the other (DK = 64) and loads take 2000:
+// they are AHEAD steps ahead.
 template <int DK, bool REV>
 __global__ __launch_bounds__(kScanThreads) void k_delta_scan(DeltaArgs p) {
-  constexpr int MT = DK / 16, MW = (MT + 3) / 4, LD = DK + 4;
+  constexpr int MT = DK / 16, MW = (MT + 3) / 4, LD = DK + 4, AHEAD = DK <= 64 ? 4 : 2;
   __shared__ alignas(16) float xs[2][16 * LD];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int ct = (p.Dv + 15) / 16, c = blockIdx.x % ct * 16 + l16;
-  const int64_t bh = blockIdx.x / ct, size = (int64_t)p.Dk * p.Dv;
-  f4 A[MW][MT], sum[MW];
-  auto fetch = [&](int i) {
+  const int64_t bh = blockIdx.x / ct, size = (int64_t)p.Dk * p.lv;
+  const int steps = p.nseg - 1;
+  f4 ahead[AHEAD][MW][MT], sums[AHEAD][MW];
+  auto fetch = [&](int i, f4(&A)[MW][MT], f4(&sum)[MW]) {
     const int s = REV ? p.nseg - 1 - i : i;
-    const float *phi = p.phi + (bh * p.nseg + s) * p.Dk * p.Dk;
-    const float *add = p.xs + (bh * p.nseg + s) * size;
+    const auto phi = whole_range((REV ? p.phit : p.phi) + (bh * p.nseg + s) * p.Dk * p.lk);
+    const auto add = whole_range(p.xs + (bh * p.nseg + s) * size);
 #pragma unroll
     for (int a = 0; a < MW; ++a) {
       const int mt = w + 4 * a, row = 16 * mt + l16;
 #pragma unroll
       for (int kt = 0; kt < MT; ++kt) {
         const int k = 16 * kt + 4 * g;
-        A[a][kt] = f4{0.f, 0.f, 0.f, 0.f};
-        if (mt >= MT || row >= p.Dk) continue;
-        if (!REV && p.Dk % 4 == 0) {
-          if (k < p.Dk) A[a][kt] = *reinterpret_cast<const f4 *>(phi + row * p.Dk + k);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (k + r < p.Dk) A[a][kt][r] = phi[REV ? (k + r) * p.Dk + row : row * p.Dk + k + r];
-        }
+        const bool on = row < p.Dk && k < p.lk;
+        A[a][kt] = __builtin_bit_cast(
+            f4, __builtin_amdgcn_raw_buffer_load_b128(phi, on ? 4 * (row * p.lk + k) : -1, 0, 0));
       }
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int d = 16 * mt + 4 * g + r;
-        sum[a][r] = mt < MT && d < p.Dk && c < p.Dv ? add[d * p.Dv + c] : 0.f;
+        const bool on = d < p.Dk && c < p.lv;
+        sum[a][r] = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(add, on ? 4 * (d * p.lv + c) : -1, 0, 0));
       }
     }
   };
-  fetch(0);
+#pragma unroll
+  for (int n = 0; n < AHEAD; ++n)
+    if (n < steps) fetch(n, ahead[n], sums[n]);
   for (int e = threadIdx.x; e < DK * 16; e += kScanThreads) {
     const int d = e / 16, col = blockIdx.x % ct * 16 + e % 16;
     xs[0][e % 16 * LD + d] =
-        p.state_in && d < p.Dk && col < p.Dv ? p.state_in[bh * size + d * p.Dv + col] : 0.f;
+        p.state_in && d < p.Dk && col < p.Dv ? p.state_in[(bh * p.Dk + d) * p.Dv + col] : 0.f;
   }
   __syncthreads();
-  for (int i = 0; i < p.nseg - 1; ++i) {
-    const float *x = xs[i & 1];
-    float *to = xs[i & 1 ^ 1], *out = p.xs + (bh * p.nseg + (REV ? p.nseg - 1 - i : i)) * size;
-    f4 y[MW];
+  for (int i0 = 0; i0 < steps; i0 += AHEAD)
 #pragma unroll
-    for (int a = 0; a < MW; ++a) y[a] = sum[a];
+    for (int n = 0; n < AHEAD; ++n) {
+      const int i = i0 + n;
+      if (i >= steps) break;
+      const float *x = xs[i & 1];
+      float *to = xs[(i & 1) ^ 1], *out = p.xs + (bh * p.nseg + (REV ? p.nseg - 1 - i : i)) * size;
+      f4 y[MW];
 #pragma unroll
-    for (int kt = 0; kt < MT; ++kt) {
-      const f4 b = *reinterpret_cast<const f4 *>(x + l16 * LD + 16 * kt + 4 * g);
+      for (int a = 0; a < MW; ++a) y[a] = sums[n][a];
 #pragma unroll
-      for (int a = 0; a < MW; ++a)
+      for (int kt = 0; kt < MT; ++kt) {
+        const f4 b = *reinterpret_cast<const f4 *>(x + l16 * LD + 16 * kt + 4 * g);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) y[a] = mfma32(A[a][kt][r], b[r], y[a]);
-    }
-    if (i + 2 < p.nseg) fetch(i + 1);
+        for (int a = 0; a < MW; ++a)
 #pragma unroll
-    for (int a = 0; a < MW; ++a) {
-      const int mt = w + 4 * a;
-      if (mt >= MT) continue;
-      *reinterpret_cast<f4 *>(to + l16 * LD + 16 * mt + 4 * g) = y[a];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int d = 16 * mt + 4 * g + r;
-        if (d < p.Dk && c < p.Dv) out[d * p.Dv + c] = y[a][r];
+          for (int r = 0; r < 4; ++r) y[a] = mfma32(ahead[n][a][kt][r], b[r], y[a]);
       }
+      if (i + AHEAD < steps) fetch(i + AHEAD, ahead[n], sums[n]);
+#pragma unroll
+      for (int a = 0; a < MW; ++a) {
+        const int mt = w + 4 * a;
+        if (mt >= MT) continue;
+        *reinterpret_cast<f4 *>(to + l16 * LD + 16 * mt + 4 * g) = y[a];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int d = 16 * mt + 4 * g + r;
+          if (d < p.Dk && c < p.lv) out[d * p.lv + c] = y[a][r];
+        }
+      }
+      __syncthreads();
     }
-    __syncthreads();
-  }
 }
 
 // One position: a workgroup per stream and head, a thread V neighbouring
@@ -255,13 +260,15 @@ semicrf_status_t check(const semicrf_linattn_shape_t *s) {
       s->Dv < 1 || s->H % s->Hq || s->H % s->Hk || s->H % s->Hv)
     return SEMICRF_ERR_SHAPE;
   if (s->T > 1 << 30) return SEMICRF_ERR_SHAPE;
-  // segments are few where heads are many: the chunks' workgroups of 256 threads are
-  // the most, or one walk a head of up to 512
+  // the chunks' workgroups of 512 threads are the most: segments are few where heads
+  // are many
   const int64_t heads = (int64_t)s->B * s->H, chunks = (s->T + 31) / 32;
-  if (heads * 512 > kMaxThreads || heads * chunks * 256 > kMaxThreads) return SEMICRF_ERR_SHAPE;
+  if (heads * chunks * 512 > kMaxThreads) return SEMICRF_ERR_SHAPE;
   if (s->Dk > kMaxHead || s->Dv > kMaxHead) return SEMICRF_ERR_UNSUPPORTED;
   return dtype_ok(s->dtype) ? SEMICRF_OK : SEMICRF_ERR_ARG;
 }
+
+int up4(int n) { return (n + 3) / 4 * 4; }
 
 // The workspaces' areas, each on 256 bytes.
 struct Areas {
@@ -282,11 +289,15 @@ size_t forward_areas(const semicrf_linattn_shape_t *s, void *ws, bool keep, Delt
   p->ld = N > 1 || s->T > L - 16 ? L : (s->T + 15) / 16 * 16;
   p->X = a.take(heads * N * p->ld * p->ld);
   p->gates = a.take(heads * N * delta_gates(L));
-  p->phi = a.take(p->nseg > 1 ? heads * p->nseg * s->Dk * s->Dk : 0);
-  p->xs = a.take(p->nseg > 1 ? heads * p->nseg * s->Dk * s->Dv : 0);
+  const int lk = up4(s->Dk), lv = up4(s->Dv);
+  const int64_t parts = p->nseg > 1 ? heads * p->nseg * s->Dk : 0;
+  p->phi = a.take(parts * lk);
+  p->xs = a.take(parts * lv);
+  p->phit = p->S = p->U = nullptr;
   if (keep) {
-    p->S = a.take(heads * N * s->Dk * s->Dv);
-    p->U = a.take(heads * N * L * s->Dv);
+    p->phit = a.take(parts * lk);
+    p->S = a.take(heads * N * s->Dk * lv);
+    p->U = a.take(heads * N * L * lv);
   }
   return a.at - (char *)ws;
 }
@@ -295,9 +306,10 @@ size_t backward_areas(const semicrf_linattn_shape_t *s, void *ws, DeltaArgs *p, 
   const int L = delta_chunk(delta_parts(s->dtype));
   const int64_t heads = (int64_t)s->B * s->H, N = chunks_of(s), rows = heads * s->T;
   segments(s, &p->nseg, &p->seg);
-  p->D = a.take(heads * N * s->Dk * s->Dv);
-  p->R = a.take(heads * N * L * s->Dv);
-  p->xs = a.take(p->nseg > 1 ? heads * p->nseg * s->Dk * s->Dv : 0);
+  const int lv = up4(s->Dv);
+  p->D = a.take(heads * N * s->Dk * lv);
+  p->R = a.take(heads * N * L * lv);
+  p->xs = a.take(p->nseg > 1 ? heads * p->nseg * s->Dk * lv : 0);
   part[0] = a.take(s->Hq == s->H ? 0 : rows * s->Dk);
   part[1] = a.take(s->Hk == s->H ? 0 : rows * s->Dk);
   part[2] = a.take(s->Hv == s->H ? 0 : rows * s->Dv);
@@ -320,7 +332,7 @@ void fill(DeltaArgs *p, const semicrf_linattn_shape_t *s, const void *q, const v
   p->log_decay = log_decay, p->beta = beta, p->lengths = lengths;
   p->scale = s->scale;
   p->B = s->B, p->T = s->T, p->H = s->H, p->Dk = s->Dk, p->Dv = s->Dv;
-  p->N = (int)chunks_of(s);
+  p->N = (int)chunks_of(s), p->lk = up4(s->Dk), p->lv = up4(s->Dv);
 }
 
 semicrf_status_t run(const DeltaArgs &p, int dtype, DeltaPass pass, hipStream_t st) {
@@ -337,6 +349,8 @@ semicrf_status_t scan(const DeltaArgs &p, hipStream_t st) {
     k_delta_scan<32, REV><<<grid, kScanThreads, 0, st>>>(p);
   else if (p.Dk <= 64)
     k_delta_scan<64, REV><<<grid, kScanThreads, 0, st>>>(p);
+  else if (p.Dk <= 96)
+    k_delta_scan<96, REV><<<grid, kScanThreads, 0, st>>>(p);
   else
     k_delta_scan<128, REV><<<grid, kScanThreads, 0, st>>>(p);
   return launch_status();

@@ -18,9 +18,10 @@ struct DeltaArgs {
   const int32_t *lengths;
   const float *state_in;
   float *X, *gates;  // of each chunk: [ld][ld], delta_gates
-  float *phi, *xs;   // of each segment: [Dk][Dk], [Dk][Dv]
-  float *S, *U;      // of each chunk, for the backward pass: [Dk][Dv], [L][Dv]; or NULL
-  float *D, *R;      // and its own: the gradients of the state after it and of R
+  // Rows of the following are lk or lv apart, Dk or Dv rounded up to fours (zeros there).
+  float *phi, *phit, *xs;  // of each segment: [Dk][Dk], its transpose (or NULL), [Dk][Dv]
+  float *S, *U;            // of each chunk, for the backward pass: [Dk][Dv], [L][Dv]; or NULL
+  float *D, *R;            // and its own: the gradients of the state after it and of R
   void *o, *dq, *dk, *dv;
   float *state_out, *dg, *db;
   int part_q, part_k, part_v;  // gradients go to float32 [B][T][H][D]: of shared heads
@@ -30,7 +31,8 @@ struct DeltaArgs {
   int ld;                      // of X: L, or less where a sequence is one short chunk
   float bad, scale;
   int B, T, H, Dk, Dv, N;  // N chunks
-  int ctiles, ktiles;      // column groups of a launch; those of them that are phi's
+  int lk, lv;
+  int ctiles;              // column groups of a launch
 };
 
 // Operands are held in parts as linear attention's are; chunks are 64 positions
@@ -40,7 +42,9 @@ __host__ __device__ constexpr int delta_parts(int dtype) {
 }
 __host__ __device__ constexpr int delta_chunk(int parts) { return parts > 1 ? 32 : 64; }
 // Waves of a workgroup that walks along a sequence: one for 16 columns.
-inline int delta_waves(int Dv) { return Dv <= 32 ? 2 : Dv <= 64 ? 4 : 8; }
+inline int delta_waves(int Dv) {
+  return Dv <= 32 ? 2 : Dv <= 64 ? 4 : Dv <= 80 ? 5 : Dv <= 96 ? 6 : 8;
+}
 
 enum DeltaPass { DELTA_INVERSE, DELTA_COMPOSE, DELTA_FORWARD, DELTA_COMPOSE_BACK, DELTA_BACK, DELTA_GRADS };
 semicrf_status_t delta_f32(const DeltaArgs &p, DeltaPass pass, hipStream_t st);
@@ -57,14 +61,23 @@ struct Gates {
     return __expf((hi[i] - hi[j]) + (lo[i] - lo[j]));
   }
 };
+// Loads go through buffer descriptors, like Tile's: what is not wanted lies past the
+// range and reads 0 without a branch.
+__device__ __forceinline__ auto whole_range(const void *p) {
+  return __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, kRange, kRawBuffer);
+}
 template <int L, int NT>
 struct GatesTile {
   static constexpr int all = delta_gates(L), N = (all + NT - 1) / NT;
   float r[N];
   __device__ __forceinline__ void fetch(int tid, const float *src) {
+    const auto rsrc = whole_range(src);
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (tid + k * NT < all) r[k] = src[tid + k * NT];
+    for (int k = 0; k < N; ++k) {
+      const int e = tid + k * NT;
+      r[k] = __builtin_bit_cast(
+          float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, e < all ? 4 * e : -1, 0, 0));
+    }
   }
   __device__ __forceinline__ void put(int tid, Gates<L> &g) const {
 #pragma unroll
@@ -73,29 +86,22 @@ struct GatesTile {
   }
 };
 
-// A float32 matrix of `rows` rows (ld apart) and W columns, in three parts in
-// LDS, zeros past n rows and D columns; LOWER: blocks of 32 above the diagonal are
-// not read (nor written).
+// A float32 matrix of `ROWS` rows (ld apart, 16 bytes aligned) and W columns, in three
+// parts in LDS, zeros past n rows and D columns (a multiple of 4); LOWER: blocks of
+// 32 above the diagonal are not read (nor written).
 template <typename Lay, int W, int ROWS, int NT, bool LOWER>
 struct Tile32 {
   static constexpr int per = W / 4, all = ROWS * per, N = (all + NT - 1) / NT;
   static constexpr int plane = ROWS * Lay::row;
   f4 r[N];
-  // vec: every row's start is on 16 bytes and D a multiple of 4
-  __device__ __forceinline__ void fetch(int tid, const float *src, int64_t ld, int n, int D,
-                                        bool vec) {
+  __device__ __forceinline__ void fetch(int tid, const float *src, int ld, int n, int D) {
+    const auto rsrc = whole_range(src);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int e = tid + k * NT, i = e / per, c = e % per * 4;
-      r[k] = f4{0.f, 0.f, 0.f, 0.f};
-      if ((all % NT && e >= all) || (LOWER && c / 32 > i / 32) || i >= n) continue;
-      if (vec) {
-        if (c < D) r[k] = *reinterpret_cast<const f4 *>(src + i * ld + c);
-      } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (c + q < D) r[k][q] = src[i * ld + c + q];
-      }
+      const bool on = i < n && c < D && !(LOWER && c / 32 > i / 32);
+      r[k] = __builtin_bit_cast(
+          f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, on ? 4 * (i * ld + c) : -1, 0, 0));
     }
   }
   __device__ __forceinline__ void put(int tid, bf16 *lds) const {
@@ -183,16 +189,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
       const double y = __shfl_up(G, o);
       if (lane >= o) G += y;
     }
-    const double last = __shfl(G, L - 1);
     if (lane < L) {
       const float hi = (float)G;
       s.hi[lane] = hi, s.lo[lane] = (float)(G - hi);
-      s.from[lane] = (float)exp(G), s.to[lane] = (float)exp(last - G);
       beta[lane] = bt;
-    }
-    if (lane == 0) {
-      const double all = exp(last);
-      s.all = (float)all, s.low = (float)(all - s.all), s.none[0] = s.none[1] = 0.f;
     }
   }
   if (p.vec)
@@ -214,8 +214,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
     for (int r = 0; r < 4; ++r) acc[r] = j + r < i ? beta[i] * s.decay(i, j + r) * acc[r] : 0.f;
     *reinterpret_cast<f4 *>(M + i * LD + j) = acc;
   }
-  for (int e = threadIdx.x; e < delta_gates(L); e += 256)
-    p.gates[at * delta_gates(L) + e] = (&s.hi[0])[e];
   __syncthreads();
   if (w < NT) {
     float x[16];
@@ -267,6 +265,23 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
     }
     __syncthreads();
   }
+  // the other gates, for the walks: e^{hi + lo} = e^hi (1 + lo)
+  float *out = p.gates + at * delta_gates(L);
+  if (lane < L) {
+    const float hi = s.hi[lane], lo = s.lo[lane];
+    if (w == 0) out[lane] = hi, out[L + lane] = lo;
+    if (w == 1) out[2 * L + lane] = fmaf(expf(hi), lo, expf(hi));
+    if (w == 2) {
+      const double d = ((double)s.hi[L - 1] - hi) + ((double)s.lo[L - 1] - lo);
+      const float x = (float)d, y = expf(x);
+      out[3 * L + lane] = fmaf(y, (float)(d - x), y);
+    }
+    if (w == 3 && lane < 4) {
+      const double all = exp((double)s.hi[L - 1] + s.lo[L - 1]);
+      const float x = (float)all;
+      out[4 * L + lane] = lane == 0 ? x : lane == 1 ? (float)(all - x) : 0.f;
+    }
+  }
   const int ld = p.ld;
   for (int e = threadIdx.x; e < ld * ld / 4; e += 256) {
     const int i = e / (ld / 4), j = e % (ld / 4) * 4;
@@ -278,13 +293,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
 }
 
 // The chunks of a segment one after another, 16 columns of the state a wave, in
-// accumulators from the first chunk to the last.  COMPOSE: the columns of the
-// segment's transition [phi | sum], from [I | 0], with values of 0 for the first; else
-// the outputs (and what the backward pass reads again) from the state before it.
+// accumulators from the first chunk to the last.  COMPOSE: 16 columns of the
+// segment's transition phi, from I with values of 0, and of its sum, from 0: two
+// independent chains that read the same operands; else the outputs (and what the
+// backward pass reads again) from the state before it.
 template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_chunks(DeltaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
-  constexpr int KB = DK / 32, NT = L / 16, JB = L / 32;
+  constexpr int KB = DK / 32, NT = L / 16, JB = L / 32, NC = COMPOSE ? 2 : 1;
   typedef ByBoth<DK> LK;
   typedef ByRow<DK> LQ;
   typedef ByColumn<kCols> LV;
@@ -297,13 +313,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   __shared__ Gates<L> gs;
 
   const int tid = threadIdx.x, w = tid >> 6, g0 = (tid & 63) >> 4, l0 = tid & 15;
-  int ct = blockIdx.x % p.ctiles;
+  const int ct = blockIdx.x % p.ctiles;
   const int seg = p.first + blockIdx.x / p.ctiles % p.count;
   const int64_t bh = blockIdx.x / p.ctiles / p.count;
   const int h = (int)(bh % p.H), b = (int)(bh / p.H);
-  const bool phi = COMPOSE && ct < p.ktiles;
-  if (COMPOSE && !phi) ct -= p.ktiles;
-  const int c0 = ct * kCols, xc = c0 + 16 * w + l0, width = phi ? p.Dk : p.Dv;
+  const int c0 = ct * kCols, xc = c0 + 16 * w + l0;
   const int valid = valid_length(p.lengths, b, p.T), len = max(valid, 0);
   const int chunks = (len + L - 1) / L;
   const int lo = seg * p.seg, hi = min(chunks, lo + p.seg);
@@ -320,11 +334,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     const int m = (int)min((int64_t)L, len - t0);
     const int64_t at = bh * p.N + n;
     tg.fetch(tid, p.gates + at * delta_gates(L));
-    tx.fetch(tid, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld, true);
+    tx.fetch(tid, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld);
     if (!p.vec) return;
     tk.fetch(tid, k + t0 * p.k.st, (int)p.k.st, p.Dk, m, 0, 1, 0);
     if (!COMPOSE) tq.fetch(tid, q + t0 * p.q.st, (int)p.q.st, p.Dk, m, 0, 1, 0);
-    tv.fetch(tid, v + t0 * p.v.st, (int)p.v.st, p.Dv, phi ? 0 : m, 0, 1, c0);
+    tv.fetch(tid, v + t0 * p.v.st, (int)p.v.st, p.Dv, m, 0, 1, c0);
   };
   auto put = [&](int n) {
     const int tid = delta_fresh(threadIdx.x);
@@ -339,24 +353,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       const int m = (int)min((int64_t)L, len - t0);
       stage<T, NP, LK, DK, L, kThreads>(K, k + t0 * p.k.st, p.k.st, p.Dk, m, 0);
       if (!COMPOSE) stage<T, NP, LQ, DK, L, kThreads>(Q, q + t0 * p.q.st, p.q.st, p.Dk, m, 0);
-      stage<T, NP, LV, kCols, L, kThreads>(V, v + t0 * p.v.st, p.v.st, p.Dv, phi ? 0 : m, c0);
+      stage<T, NP, LV, kCols, L, kThreads>(V, v + t0 * p.v.st, p.v.st, p.Dv, m, c0);
     }
   };
   if (lo < hi) fetch(lo);
 
   // state tile i: rows 16 i + 4 g + r of column xc
-  f4 S[2 * KB];
-  const int64_t size = (int64_t)p.Dk * p.Dv;
+  f4 S[NC][2 * KB];
+  const int64_t size = (int64_t)p.Dk * p.lv;
   const float *s0 = COMPOSE ? nullptr
                     : seg   ? p.xs + (bh * p.nseg + seg - 1) * size
-                            : p.state_in ? p.state_in + bh * size : nullptr;
+                            : p.state_in ? p.state_in + bh * p.Dk * p.Dv : nullptr;
+  const int l0v = seg ? p.lv : p.Dv;
 #pragma unroll
   for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * i + 4 * g0 + r;
-      S[i][r] = phi ? (row == xc ? 1.f : 0.f)
-                    : s0 && row < p.Dk && xc < p.Dv ? s0[row * p.Dv + xc] : 0.f;
+      S[0][i][r] = s0 && row < p.Dk && xc < p.Dv ? s0[row * l0v + xc] : 0.f;
+      if (NC > 1) S[NC - 1][i][r] = row == xc ? 1.f : 0.f;  // phi
     }
   if (lo < hi) put(lo);
 
@@ -367,13 +382,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     __syncthreads();
     const int lane = delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
     if (n + 1 < hi) fetch(n + 1);
-    if (!COMPOSE && p.S && xc < p.Dv) {
+    if (!COMPOSE && p.S && xc < p.lv) {
       float *to = p.S + (bh * p.N + n) * size + xc;
 #pragma unroll
       for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (16 * i + 4 * g + r < p.Dk) to[(16 * i + 4 * g + r) * p.Dv] = S[i][r];
+          if (16 * i + 4 * g + r < p.Dk) to[(16 * i + 4 * g + r) * p.lv] = S[0][i][r];
     }
     if (!COMPOSE) {
       // P: wave w its rows of 16, up to the diagonal and the tile beside it
@@ -406,30 +421,38 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         }
       }
     }
-    Frag<3> sf[KB];
+    Frag<3> sf[NC][KB];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) sf[kb] = frag_of(S[2 * kb], S[2 * kb + 1]);
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) sf[c][kb] = frag_of(S[c][2 * kb], S[c][2 * kb + 1]);
     // R = V - E K S
-    f4 U[NT];
-#pragma unroll
-    for (int it = 0; it < NT; ++it) U[it] = f4{0.f, 0.f, 0.f, 0.f};
-    Frag<3> rf[JB];
+    Frag<3> rf[NC][JB];
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb) {
-      f4 ks[2];
+      f4 ks[NC][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        ks[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          ks[t] = mma<3>(frag_row<NP, LK>(K, L * LK::row, 32 * jb + 16 * t, kb, lane), sf[kb], ks[t]);
+        for (int c = 0; c < NC; ++c) ks[c][t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+          const Frag<NP> kf = frag_row<NP, LK>(K, L * LK::row, 32 * jb + 16 * t, kb, lane);
+#pragma unroll
+          for (int c = 0; c < NC; ++c) ks[c][t] = mma<3>(kf, sf[c][kb], ks[c][t]);
+        }
       }
-      float x[8];
-      values(frag_col<NP, LV>(V, L * LV::row, 32 * jb, w, lane), x);
+      float v8[8];
+      values(frag_col<NP, LV>(V, L * LV::row, 32 * jb, w, lane), v8);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] -= gs.from[32 * jb + 16 * (e >> 2) + 4 * g + (e & 3)] * ks[e >> 2][e & 3];
-      rf[jb] = split<3>(x);
+      for (int c = 0; c < NC; ++c) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[e] = (c ? 0.f : v8[e]) -
+                 gs.from[32 * jb + 16 * (e >> 2) + 4 * g + (e & 3)] * ks[c][e >> 2][e & 3];
+        rf[c][jb] = split<3>(x);
+      }
     }
     // what the state gives, transposed: a lane holds four neighbours of a row of O
     f4 O[NT];
@@ -439,43 +462,60 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         O[it] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
-          O[it] = mma<3>(sf[kb], frag_row<NP, LQ>(Q, L * LQ::row, 16 * it, kb, lane), O[it]);
+          O[it] = mma<3>(sf[0][kb], frag_row<NP, LQ>(Q, L * LQ::row, 16 * it, kb, lane), O[it]);
         const float d = p.scale * gs.from[16 * it + l16];
 #pragma unroll
         for (int r = 0; r < 4; ++r) O[it][r] *= d;
       }
     }
     // U = X R
+    f4 U[NC][NT];
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int it = 0; it < NT; ++it) U[c][it] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
-      for (int it = 2 * jb; it < NT; ++it)
-        U[it] = mma<3>(frag_row<3, LX>(X, L * LX::row, 16 * it, jb, lane), rf[jb], U[it]);
-    if (!COMPOSE && p.U && xc < p.Dv) {
-      float *to = p.U + (bh * p.N + n) * L * p.Dv + xc;
+      for (int it = 2 * jb; it < NT; ++it) {
+        const Frag<3> xf = frag_row<3, LX>(X, L * LX::row, 16 * it, jb, lane);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) U[c][it] = mma<3>(xf, rf[c][jb], U[c][it]);
+      }
+    if (!COMPOSE && p.U && xc < p.lv) {
+      float *to = p.U + (bh * p.N + n) * L * p.lv + xc;
 #pragma unroll
       for (int it = 0; it < NT; ++it)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) to[(int64_t)(16 * it + 4 * g + r) * p.Dv] = U[it][r];
+        for (int r = 0; r < 4; ++r) to[(16 * it + 4 * g + r) * p.lv] = U[0][it][r];
     }
     // S <- e^{G_L} S + K^T (e^{G_L - G} U)
     Frag<3> uf[JB];
     const float all = gs.all, low = gs.low;
 #pragma unroll
-    for (int i = 0; i < 2 * KB; ++i)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[i][r] = fmaf(S[i][r], low, S[i][r] * all);
-#pragma unroll
-    for (int jb = 0; jb < JB; ++jb) {
-      if (!COMPOSE) uf[jb] = frag_of(U[2 * jb], U[2 * jb + 1]);
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = U[2 * jb + (e >> 2)][e & 3] * gs.to[32 * jb + 16 * (e >> 2) + 4 * g + (e & 3)];
-      const Frag<3> tf = split<3>(x);
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int i = 0; i < 2 * KB; ++i)
-        S[i] = mma<3>(frag_col<NP, LK>(K, L * LK::row, 32 * jb, i, lane), tf, S[i]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) S[c][i][r] = fmaf(S[c][i][r], low, S[c][i][r] * all);
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb) {
+      if (!COMPOSE) uf[jb] = frag_of(U[0][2 * jb], U[0][2 * jb + 1]);
+      Frag<3> tf[NC];
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          x[e] = U[c][2 * jb + (e >> 2)][e & 3] * gs.to[32 * jb + 16 * (e >> 2) + 4 * g + (e & 3)];
+        tf[c] = split<3>(x);
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * KB; ++i) {
+        const Frag<NP> kf = frag_col<NP, LK>(K, L * LK::row, 32 * jb, i, lane);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) S[c][i] = mma<3>(kf, tf[c], S[c][i]);
+      }
     }
     __syncthreads();
     if (!COMPOSE) {
@@ -505,14 +545,19 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   }
 
   if (COMPOSE) {
-    float *to = phi ? p.phi + (bh * p.nseg + seg) * p.Dk * p.Dk : p.xs + (bh * p.nseg + seg) * size;
+    float *sum = p.xs + (bh * p.nseg + seg) * size;
+    const int64_t at = (bh * p.nseg + seg) * p.Dk * p.lk;
 #pragma unroll
-    for (int i = 0; i < 2 * KB; ++i)
+    for (int i = 0; i < 2 * KB; ++i) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * i + 4 * g0 + r;
-        if (row < p.Dk && xc < width) to[row * width + xc] = S[i][r];
+        if (row < p.Dk && xc < p.lv) sum[row * p.lv + xc] = S[0][i][r];
+        if (row < p.Dk && xc < p.lk) p.phi[at + row * p.lk + xc] = S[NC - 1][i][r];
       }
+      if (p.phit && 16 * i + 4 * g0 < p.lk && xc < p.Dk)
+        *reinterpret_cast<f4 *>(p.phit + at + xc * p.lk + 16 * i + 4 * g0) = S[NC - 1][i];
+    }
     return;
   }
   const T fill = (T)(valid < 0 ? p.bad : 0.f);
@@ -530,7 +575,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * i + 4 * g0 + r;
         if (row < p.Dk && xc < p.Dv)
-          p.state_out[bh * size + row * p.Dv + xc] = valid < 0 ? p.bad : S[i][r];
+          p.state_out[(bh * p.Dk + row) * p.Dv + xc] = valid < 0 ? p.bad : S[0][i][r];
       }
   }
 }
@@ -575,7 +620,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     const int m = (int)min((int64_t)L, len - t0);
     const int64_t at = bh * p.N + n;
     tg.fetch(tid, p.gates + at * delta_gates(L));
-    tx.fetch(tid, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld, true);
+    tx.fetch(tid, p.X + at * p.ld * p.ld, p.ld, p.ld, p.ld);
     if (!p.vec) return;
     tk.fetch(tid, k + t0 * p.k.st, (int)p.k.st, p.Dk, m, 0, 1, 0);
     tq.fetch(tid, q + t0 * p.q.st, (int)p.q.st, p.Dk, m, 0, 1, 0);
@@ -599,16 +644,17 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   };
   if (lo < hi) fetch(hi - 1);
   f4 D[2 * KB];
-  const int64_t size = (int64_t)p.Dk * p.Dv;
+  const int64_t size = (int64_t)p.Dk * p.lv;
   const float *d0 = COMPOSE              ? nullptr
                     : seg + 1 < p.nseg   ? p.xs + (bh * p.nseg + seg + 1) * size
-                            : p.state_in ? p.state_in + bh * size : nullptr;
+                            : p.state_in ? p.state_in + bh * p.Dk * p.Dv : nullptr;
+  const int l0v = seg + 1 < p.nseg ? p.lv : p.Dv;
 #pragma unroll
   for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int row = 16 * i + 4 * g0 + r;
-      D[i][r] = d0 && row < p.Dk && xc < p.Dv ? d0[row * p.Dv + xc] : 0.f;
+      D[i][r] = d0 && row < p.Dk && xc < p.Dv ? d0[row * l0v + xc] : 0.f;
     }
   if (lo < hi) put(hi - 1);
 
@@ -617,13 +663,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     __syncthreads();
     const int lane = delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
     if (n > lo) fetch(n - 1);
-    if (!COMPOSE && xc < p.Dv) {
+    if (!COMPOSE && xc < p.lv) {
       float *at = p.D + (bh * p.N + n) * size + xc;
 #pragma unroll
       for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          if (16 * i + 4 * g + r < p.Dk) at[(16 * i + 4 * g + r) * p.Dv] = D[i][r];
+          if (16 * i + 4 * g + r < p.Dk) at[(16 * i + 4 * g + r) * p.lv] = D[i][r];
     }
     for (int it = w; it < NT; it += NW) {
       Frag<NP> qf[KB];
@@ -704,15 +750,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       for (int jt = 0; jt <= 2 * ib + 1; ++jt)
         dR[jt] = mma<3>(frag_col<3, LX>(X, L * LX::row, 32 * ib, jt, lane), df, dR[jt]);
     }
-    if (!COMPOSE && xc < p.Dv) {
-      float *at = p.R + (bh * p.N + n) * L * p.Dv + xc;
+    if (!COMPOSE && xc < p.lv) {
+      float *at = p.R + (bh * p.N + n) * L * p.lv + xc;
 #pragma unroll
       for (int jt = 0; jt < NT; ++jt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int j = 16 * jt + 4 * g + r;
-          at[(int64_t)j * p.Dv] = dR[jt][r];
-          if (p.dv && j < m) {
+          at[j * p.lv] = dR[jt][r];
+          if (p.dv && j < m && xc < p.Dv) {
             const int64_t e = (((int64_t)b * p.T + n * (int64_t)L + j) * p.H + h) * p.Dv + xc;
             if (p.part_v)
               ((float *)p.dv)[e] = dR[jt][r];
@@ -737,15 +783,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   }
 
   float *to_d = COMPOSE ? p.xs + (bh * p.nseg + seg) * size
-                : p.state_out && seg == 0 ? p.state_out + bh * size : nullptr;
-  if (to_d) {
+                : p.state_out && seg == 0 ? p.state_out + bh * p.Dk * p.Dv : nullptr;
+  const int ld = COMPOSE ? p.lv : p.Dv;
+  if (to_d && xc < ld) {
 #pragma unroll
     for (int i = 0; i < 2 * KB; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = 16 * i + 4 * g0 + r;
-        if (row < p.Dk && xc < p.Dv)
-          to_d[row * p.Dv + xc] = !COMPOSE && valid < 0 ? p.bad : D[i][r];
+        if (row < p.Dk) to_d[row * ld + xc] = !COMPOSE && valid < 0 ? p.bad : D[i][r];
       }
   }
   if (!COMPOSE && p.dv) {
@@ -763,151 +809,171 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   }
 }
 
-// The gradients of q, k, the log decays and betas of a chunk, four waves each: a
-// wave has 16 positions (of L = 32, 16 positions and half of the keys' columns).
-// Contractions over the values' columns go in slices of 32; dP and dM are computed
-// twice, once as operands for the sums over what was written before a position
-// (by rows), once for those over what reads it (by columns): each time the layout
-// of the accumulators is that of the operand.
+// The gradients of q, k, the log decays and betas of a chunk, eight waves each.  Half
+// of the waves have rows of 16 positions that ask (dq, and what dM and the state
+// give to dk), half have rows that are asked (the rest of dk); for L = 32 two
+// waves share the keys' columns of a row.  Contractions over the values' columns
+// go in slices of 32.  dP and dM are computed by rows by the first and by columns
+// by the others: the accumulators' layout is then that of the operand they become,
+// and the triangles' rows and columns on a SIMD add up to the same.
 template <typename T, int NP, int DK, int L>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_grads(DeltaArgs p) {
-  constexpr int NT = L / 16, JB = L / 32, DS = 4 / NT, DT = DK / 16 / DS;
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void k_delta_grads(
+    DeltaArgs p) {
+  constexpr int NT = L / 16, JB = L / 32, DS = 4 / NT, DT = DK / 16 / DS, kThreads = 512;
   typedef ByRow<32> LS;
   typedef ByColumn<DK> LK;
-  constexpr int kSlice = (6 * L + NP * L + 6 * DK) * LS::row, kKeys = 2 * NP * L * LK::row;
-  __shared__ alignas(16) bf16 tiles[kSlice > kKeys ? kSlice : kKeys];
+  constexpr int kSlice = (6 * L + NP * L + 6 * DK) * LS::row;
+  constexpr int kKeys = 2 * NP * L * LK::row, LW = DK + 4;
+  static_assert(kKeys + 2 * L * LW <= kSlice, "");
+  __shared__ alignas(16) bf16 tiles[kSlice];
   bf16 *const U = tiles, *const R = U + 3 * L * LS::row, *const G = R + 3 * L * LS::row,
              *const S = G + NP * L * LS::row, *const D = S + 3 * DK * LS::row;
+  // after the slices: the keys, the queries and the others' share of dk
   bf16 *const K = tiles, *const Q = K + NP * L * LK::row;
+  float *const dks = (float *)(tiles + kKeys);
   __shared__ Gates<L> gs;
   __shared__ float inv[L];
-  __shared__ double red[4], cs[DS][L], es[DS][L];
+  __shared__ double red[8];
+  __shared__ float cs[2 * DS][L], es[DS][L];
 
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
+  const int tid = threadIdx.x, w = tid >> 6;
   const int h = blockIdx.x % p.H, n = blockIdx.x / p.H % p.N, b = blockIdx.x / p.H / p.N;
   const int t0 = n * L, count = min(L, max(valid_length(p.lengths, b, p.T), 0) - t0);
   const int rest = min(L, p.T - t0);
   const int64_t row0 = ((int64_t)b * p.T + t0) * p.H + h;
-  for (int e = threadIdx.x; e < rest * p.Dk; e += 256) {
-    const int i = e / p.Dk, d = e % p.Dk;
-    if (i < count) continue;
-    const int64_t row = row0 + (int64_t)i * p.H, to = row * p.Dk + d;
+  for (int e = max(count, 0) * p.Dk + tid; e < rest * p.Dk; e += kThreads) {
+    const int64_t row = row0 + (int64_t)(e / p.Dk) * p.H, to = row * p.Dk + e % p.Dk;
     if (p.dq) { if (p.part_q) ((float *)p.dq)[to] = 0.f; else ((T *)p.dq)[to] = (T)0.f; }
     if (p.dk) { if (p.part_k) ((float *)p.dk)[to] = 0.f; else ((T *)p.dk)[to] = (T)0.f; }
-    if (d == 0 && p.dg) p.dg[row] = 0.f;
-    if (d == 0 && p.db) p.db[row] = 0.f;
+    if (e % p.Dk == 0 && p.dg) p.dg[row] = 0.f;
+    if (e % p.Dk == 0 && p.db) p.db[row] = 0.f;
   }
   if (count <= 0) return;
-  const int64_t at = ((int64_t)b * p.H + h) * p.N + n, size = (int64_t)p.Dk * p.Dv;
+  const int64_t at = ((int64_t)b * p.H + h) * p.N + n, size = (int64_t)p.Dk * p.lv;
   const T *q = view_rows<T>(p.q, b, h) + t0 * p.q.st, *k = view_rows<T>(p.k, b, h) + t0 * p.k.st;
   const int64_t so = (int64_t)p.H * p.Dv;
   const T *go = (const T *)p.go + row0 * p.Dv;
-  const float *u = p.U + at * L * p.Dv, *dr = p.R + at * L * p.Dv, *s = p.S + at * size,
+  const float *u = p.U + at * L * p.lv, *dr = p.R + at * L * p.lv, *s = p.S + at * size,
               *ds = p.D + at * size;
-  const bool even = p.Dv % 4 == 0;
-  Tile32<LS, 32, L, 256, false> tu, tr;
-  Tile32<LS, 32, DK, 256, false> ts, td;
-  Tile<T, NP, LS, 32, L, 256> tg;
+  Tile32<LS, 32, L, kThreads, false> tu, tr;
+  Tile32<LS, 32, DK, kThreads, false> ts, td;
+  Tile<T, NP, LS, 32, L, kThreads> tg;
+  Tile<T, NP, LK, DK, L, kThreads> tk, tq;
   auto fetch = [&](int c0) {
-    tu.fetch(threadIdx.x, u + c0, p.Dv, L, p.Dv - c0, even);
-    tr.fetch(threadIdx.x, dr + c0, p.Dv, L, p.Dv - c0, even);
-    ts.fetch(threadIdx.x, s + c0, p.Dv, p.Dk, p.Dv - c0, even);
-    td.fetch(threadIdx.x, ds + c0, p.Dv, p.Dk, p.Dv - c0, even);
-    if (p.vec) tg.fetch(threadIdx.x, go, (int)so, p.Dv, count, 0, 1, c0);
+    const int tid = delta_fresh(threadIdx.x);
+    tu.fetch(tid, u + c0, p.lv, L, p.lv - c0);
+    tr.fetch(tid, dr + c0, p.lv, L, p.lv - c0);
+    ts.fetch(tid, s + c0, p.lv, p.Dk, p.lv - c0);
+    td.fetch(tid, ds + c0, p.lv, p.Dk, p.lv - c0);
+    if (p.vec) tg.fetch(tid, go, (int)so, p.Dv, count, 0, 1, c0);
   };
   fetch(0);
-  if (threadIdx.x < L) {
+  if (tid < L) {
     float bt = 1.f;
-    if (threadIdx.x < count) bt = p.beta[row0 + (int64_t)threadIdx.x * p.H];
+    if (tid < count) bt = p.beta[row0 + (int64_t)tid * p.H];
     if (fabsf(bt) < 0x1p-96f) bt = copysignf(0x1p-96f, bt);
-    inv[threadIdx.x] = 1.f / bt;
+    inv[tid] = 1.f / bt;
   }
-  for (int e = threadIdx.x; e < delta_gates(L); e += 256)
-    (&gs.hi[0])[e] = p.gates[at * delta_gates(L) + e];
-  const int pt = w % NT, d0 = w / NT * DT;
-  f4 dq[DT], df[DT], dw[DT], pr[NT], pc[NT], mr[NT], mc[NT];
+  if (tid < delta_gates(L)) (&gs.hi[0])[tid] = p.gates[at * delta_gates(L) + tid];
+  const int pt = w % NT, part = w / NT / 2, d0 = part * DT;
+  const bool asks = w / NT % 2 == 0;
+  // of rows that ask: dq and its like from dR; of the others: what is written
+  f4 a0[DT], a1[DT], p0[NT], p1[NT];
   const f4 zero = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < DT; ++i) dq[i] = df[i] = dw[i] = zero;
+  for (int i = 0; i < DT; ++i) a0[i] = a1[i] = zero;
 #pragma unroll
-  for (int i = 0; i < NT; ++i) pr[i] = pc[i] = mr[i] = mc[i] = zero;
-  double dot = 0;               // S . dS', this thread's share
-  float dbs[decltype(tu)::N];   // (dR / b) . (U / b) of the rows it reads
+  for (int i = 0; i < NT; ++i) p0[i] = p1[i] = zero;
+  constexpr int UN = decltype(tu)::N;
+  double dot = 0;  // S . dS', this thread's share
+  float dbs[UN];   // (dR / b) . (U / b) of the rows it reads
 #pragma unroll
-  for (int i = 0; i < decltype(tu)::N; ++i) dbs[i] = 0.f;
+  for (int i = 0; i < UN; ++i) dbs[i] = 0.f;
   for (int c0 = 0; c0 < p.Dv; c0 += 32) {
     __syncthreads();
-    tu.put(threadIdx.x, U);
-    tr.put(threadIdx.x, R);
-    ts.put(threadIdx.x, S);
-    td.put(threadIdx.x, D);
-    if (p.vec)
-      tg.put(threadIdx.x, G);
-    else
-      stage<T, NP, LS, 32, L, 256>(G, go, so, p.Dv, count, c0);
+    {
+      const int tid = delta_fresh(threadIdx.x);
+      tu.put(tid, U);
+      tr.put(tid, R);
+      ts.put(tid, S);
+      td.put(tid, D);
+      if (p.vec)
+        tg.put(tid, G);
+      else
+        stage<T, NP, LS, 32, L, kThreads>(G, go, so, p.Dv, count, c0);
 #pragma unroll
-    for (int i = 0; i < decltype(tu)::N; ++i) {
-      const float iv = inv[(threadIdx.x + i * 256) / 8 % L];
+      for (int i = 0; i < UN; ++i) {
+        const float iv = inv[(tid + i * kThreads) / 8 % L];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dbs[i] = fmaf(tr.r[i][r] * iv, tu.r[i][r] * iv, dbs[i]);
+        for (int r = 0; r < 4; ++r) dbs[i] = fmaf(tr.r[i][r] * iv, tu.r[i][r] * iv, dbs[i]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < decltype(ts)::N; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dot += (double)ts.r[i][r] * td.r[i][r];
     __syncthreads();
-    if (c0 + 32 < p.Dv) fetch(c0 + 32);
-    const Frag<NP> gf = frag_row<NP, LS>(G, L * LS::row, 16 * pt, 0, lane);
-    const Frag<3> uf = frag_row<3, LS>(U, L * LS::row, 16 * pt, 0, lane);
-    const Frag<3> rf = frag_row<3, LS>(R, L * LS::row, 16 * pt, 0, lane);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (t <= pt) {
-        const Frag<3> x = frag_row<3, LS>(U, L * LS::row, 16 * t, 0, lane);
-        pr[t] = mma<3>(x, gf, pr[t]);
-        mr[t] = mma<3>(x, rf, mr[t]);
-      }
-      if (t >= pt) {
-        pc[t] = mma<3>(frag_row<NP, LS>(G, L * LS::row, 16 * t, 0, lane), uf, pc[t]);
-        mc[t] = mma<3>(frag_row<3, LS>(R, L * LS::row, 16 * t, 0, lane), uf, mc[t]);
-      }
+    if (c0 + 32 < p.Dv) {
+      fetch(c0 + 32);
+    } else if (p.vec) {
+      const int tid = delta_fresh(threadIdx.x);
+      tk.fetch(tid, k, (int)p.k.st, p.Dk, count, 0, 1, 0);
+      tq.fetch(tid, q, (int)p.q.st, p.Dk, count, 0, 1, 0);
     }
+    const int lane = delta_fresh(tid & 63);
+    if (asks) {
+      const Frag<NP> gf = frag_row<NP, LS>(G, L * LS::row, 16 * pt, 0, lane);
+      const Frag<3> rf = frag_row<3, LS>(R, L * LS::row, 16 * pt, 0, lane);
 #pragma unroll
-    for (int i = 0; i < DT; ++i) {
-      const Frag<3> x = frag_row<3, LS>(S, DK * LS::row, 16 * (d0 + i), 0, lane);
-      dq[i] = mma<3>(x, gf, dq[i]);
-      df[i] = mma<3>(x, rf, df[i]);
-      dw[i] = mma<3>(frag_row<3, LS>(D, DK * LS::row, 16 * (d0 + i), 0, lane), uf, dw[i]);
+      for (int t = 0; t < NT; ++t)
+        if (t <= pt) {
+          const Frag<3> x = frag_row<3, LS>(U, L * LS::row, 16 * t, 0, lane);
+          p0[t] = mma<3>(x, gf, p0[t]);
+          p1[t] = mma<3>(x, rf, p1[t]);
+        }
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        const Frag<3> x = frag_row<3, LS>(S, DK * LS::row, 16 * (d0 + i), 0, lane);
+        a0[i] = mma<3>(x, gf, a0[i]);
+        a1[i] = mma<3>(x, rf, a1[i]);
+      }
+    } else {
+      const Frag<3> uf = frag_row<3, LS>(U, L * LS::row, 16 * pt, 0, lane);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        if (t >= pt) {
+          p0[t] = mma<3>(frag_row<NP, LS>(G, L * LS::row, 16 * t, 0, lane), uf, p0[t]);
+          p1[t] = mma<3>(frag_row<3, LS>(R, L * LS::row, 16 * t, 0, lane), uf, p1[t]);
+        }
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+        a0[i] = mma<3>(frag_row<3, LS>(D, DK * LS::row, 16 * (d0 + i), 0, lane), uf, a0[i]);
     }
-  }
-  Tile<T, NP, LK, DK, L, 256> tk, tq;
-  if (p.vec) {
-    tk.fetch(threadIdx.x, k, (int)p.k.st, p.Dk, count, 0, 1, 0);
-    tq.fetch(threadIdx.x, q, (int)p.q.st, p.Dk, count, 0, 1, 0);
   }
   __syncthreads();
   if (p.vec) {
-    tk.put(threadIdx.x, K);
-    tq.put(threadIdx.x, Q);
+    const int tid = delta_fresh(threadIdx.x);
+    tk.put(tid, K);
+    tq.put(tid, Q);
   } else {
-    stage<T, NP, LK, DK, L, 256>(K, k, p.k.st, p.Dk, count, 0);
-    stage<T, NP, LK, DK, L, 256>(Q, q, p.q.st, p.Dk, count, 0);
+    stage<T, NP, LK, DK, L, kThreads>(K, k, p.k.st, p.Dk, count, 0);
+    stage<T, NP, LK, DK, L, kThreads>(Q, q, p.q.st, p.Dk, count, 0);
   }
 #pragma unroll
-  for (int i = 0; i < decltype(tu)::N; ++i) {
+  for (int i = 0; i < UN; ++i) {
     float x = dbs[i];
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) x += __shfl_xor(x, o);
-    const int e = threadIdx.x + i * 256, row = e / 8;
+    const int e = tid + i * kThreads, row = e / 8;
     if (p.db && e < decltype(tu)::all && e % 8 == 0 && row < count)
       p.db[row0 + (int64_t)row * p.H] = x;
   }
+  const int lane = delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
 #pragma unroll
   for (int o = 32; o; o >>= 1) dot += __shfl_xor(dot, o);
   if (lane == 0) red[w] = dot;
   __syncthreads();
   const int mine = 16 * pt + l16;
-  const float from = gs.from[mine], to = gs.to[mine];
   // four neighbours of this position's row of K or Q
   auto four = [&](const bf16 *t, int i) {
     f4 x = zero;
@@ -920,98 +986,134 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
     }
     return x;
   };
-  float c = 0.f, e = 0.f;
-#pragma unroll
-  for (int i = 0; i < DT; ++i) {
-    const f4 kv = four(K, i);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      dq[i][r] *= p.scale * from;
-      df[i][r] *= -from;
-      dw[i][r] *= to;
-      e += kv[r] * dw[i][r];
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int o = 16 * t + 4 * g + r;
-      const float before = t <= pt && o <= mine ? gs.decay(mine, o) : 0.f;
-      const float later = t >= pt && o >= mine ? gs.decay(o, mine) : 0.f;
-      pr[t][r] *= p.scale * before;
-      pc[t][r] *= p.scale * later;
-      mr[t][r] *= o < mine ? -before : 0.f;
-      mc[t][r] *= o > mine ? -later : 0.f;
-    }
-#pragma unroll
-  for (int jb = 0; jb < JB; ++jb) {
-    if (2 * jb <= pt) {
-      const Frag<3> a = frag_of(pr[2 * jb], pr[2 * jb + 1]), m = frag_of(mr[2 * jb], mr[2 * jb + 1]);
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        const Frag<NP> x = frag_col<NP, LK>(K, L * LK::row, 32 * jb, d0 + i, lane);
-        dq[i] = mma<3>(x, a, dq[i]);
-        df[i] = mma<3>(x, m, df[i]);
-      }
-    }
-    if (2 * jb + 1 >= pt) {
-      const Frag<3> a = frag_of(pc[2 * jb], pc[2 * jb + 1]), m = frag_of(mc[2 * jb], mc[2 * jb + 1]);
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-        dw[i] = mma<3>(frag_col<NP, LK>(Q, L * LK::row, 32 * jb, d0 + i, lane), a, dw[i]);
-        dw[i] = mma<3>(frag_col<NP, LK>(K, L * LK::row, 32 * jb, d0 + i, lane), m, dw[i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < DT; ++i) {
-    const f4 kv = four(K, i), qv = four(Q, i);
+  auto give = [&](void *out, int whole, int i, const f4 &x) {
     const int d = 16 * (d0 + i) + 4 * g;
-    f4 sum;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      c += qv[r] * dq[i][r] + kv[r] * (df[i][r] - dw[i][r]);
-      sum[r] = df[i][r] + dw[i][r];
-    }
-    if (mine >= count || d >= p.Dk) continue;
+    if (mine >= count || d >= p.Dk) return;
     const int64_t to = (row0 + (int64_t)mine * p.H) * p.Dk + d;
-    auto give = [&](void *out, int part, const f4 &x) {
-      if (p.vec_out) {
-        if (part) {
-          *reinterpret_cast<f4 *>((float *)out + to) = x;
-        } else {
-          Pack<T, 4> y;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) y.v[r] = (T)x[r];
-          *reinterpret_cast<Pack<T, 4> *>((T *)out + to) = y;
-        }
+    if (p.vec_out) {
+      if (whole) {
+        *reinterpret_cast<f4 *>((float *)out + to) = x;
       } else {
+        Pack<T, 4> y;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (d + r < p.Dk) {
-            if (part)
-              ((float *)out)[to + r] = x[r];
-            else
-              ((T *)out)[to + r] = (T)x[r];
-          }
+        for (int r = 0; r < 4; ++r) y.v[r] = (T)x[r];
+        *reinterpret_cast<Pack<T, 4> *>((T *)out + to) = y;
       }
-    };
-    if (p.dq) give(p.dq, p.part_q, dq[i]);
-    if (p.dk) give(p.dk, p.part_k, sum);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (d + r < p.Dk) {
+          if (whole)
+            ((float *)out)[to + r] = x[r];
+          else
+            ((T *)out)[to + r] = (T)x[r];
+        }
+    }
+  };
+  float c = 0.f;
+  if (asks) {
+    const float from = gs.from[mine];
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) a0[i][r] *= p.scale * from, a1[i][r] *= -from;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int o = 16 * t + 4 * g + r;
+        const float d = t <= pt && o <= mine ? gs.decay(mine, o) : 0.f;
+        p0[t][r] *= p.scale * d;
+        p1[t][r] *= o < mine ? -d : 0.f;
+      }
+#pragma unroll
+    for (int jb = 0; jb < JB; ++jb)
+      if (2 * jb <= pt) {
+        const Frag<3> f0 = frag_of(p0[2 * jb], p0[2 * jb + 1]), f1 = frag_of(p1[2 * jb], p1[2 * jb + 1]);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          const Frag<NP> x = frag_col<NP, LK>(K, L * LK::row, 32 * jb, d0 + i, lane);
+          a0[i] = mma<3>(x, f0, a0[i]);
+          a1[i] = mma<3>(x, f1, a1[i]);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      const f4 kv = four(K, i), qv = four(Q, i);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) c += qv[r] * a0[i][r] + kv[r] * a1[i][r];
+      if (p.dq) give(p.dq, p.part_q, i, a0[i]);
+    }
+  } else {
+    const float to = gs.to[mine];
+    float e = 0.f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      const f4 kv = four(K, i);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        a0[i][r] *= to;
+        e += kv[r] * a0[i][r];
+      }
+    }
+#pragma unroll
+    for (int o = 16; o < 64; o <<= 1) e += __shfl_xor(e, o);
+    if (g == 0) es[part][mine] = e;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int o = 16 * t + 4 * g + r;
+        const float d = t >= pt && o >= mine ? gs.decay(o, mine) : 0.f;
+        p0[t][r] *= p.scale * d;
+        p1[t][r] *= o > mine ? -d : 0.f;
+      }
+#pragma unroll
+    for (int ib = 0; ib < JB; ++ib)
+      if (2 * ib + 1 >= pt) {
+        const Frag<3> f0 = frag_of(p0[2 * ib], p0[2 * ib + 1]), f1 = frag_of(p1[2 * ib], p1[2 * ib + 1]);
+#pragma unroll
+        for (int i = 0; i < DT; ++i) {
+          a0[i] = mma<3>(frag_col<NP, LK>(Q, L * LK::row, 32 * ib, d0 + i, lane), f0, a0[i]);
+          a0[i] = mma<3>(frag_col<NP, LK>(K, L * LK::row, 32 * ib, d0 + i, lane), f1, a0[i]);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      const f4 kv = four(K, i);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) c -= kv[r] * a0[i][r];
+      *reinterpret_cast<f4 *>(dks + mine * LW + 16 * (d0 + i) + 4 * g) = a0[i];
+    }
   }
 #pragma unroll
-  for (int o = 16; o < 64; o <<= 1) c += __shfl_xor(c, o), e += __shfl_xor(e, o);
-  if (g == 0) cs[w / NT][mine] = c, es[w / NT][mine] = e;
+  for (int o = 16; o < 64; o <<= 1) c += __shfl_xor(c, o);
+  if (g == 0) cs[w / NT][mine] = c;
   __syncthreads();
-  if (w == 0 && p.dg) {
-    double x = 0, y = 0;
-    if (lane < L)
+  if (asks && p.dk) {
 #pragma unroll
-      for (int i = 0; i < DS; ++i) x += cs[i][lane], y += es[i][lane];
+    for (int i = 0; i < DT; ++i) {
+      const f4 x = *reinterpret_cast<const f4 *>(dks + mine * LW + 16 * (d0 + i) + 4 * g);
+      f4 y;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] = a1[i][r] + x[r];
+      give(p.dk, p.part_k, i, y);
+    }
+  }
+  if (w == 7 && p.dg) {
+    double x = 0, y = 0;
+    if (lane < L) {
+#pragma unroll
+      for (int i = 0; i < 2 * DS; ++i) x += cs[i][lane];
+#pragma unroll
+      for (int i = 0; i < DS; ++i) y += es[i][lane];
+    }
 #pragma unroll
     for (int o = 32; o; o >>= 1) y += __shfl_xor(y, o);
-    y += ((double)gs.all + gs.low) * (red[0] + red[1] + red[2] + red[3]);
+    double all = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all += red[i];
+    y += ((double)gs.all + gs.low) * all;
     // sums from a position to the chunk's end
 #pragma unroll
     for (int o = 1; o < L; o <<= 1) {
@@ -1031,8 +1133,9 @@ template <typename T, int NP, int DK, int NW>
 semicrf_status_t delta_walk(DeltaArgs p, DeltaPass pass, hipStream_t st) {
   constexpr int L = delta_chunk(NP);
   const int vt = (p.Dv + 16 * NW - 1) / (16 * NW);
-  p.ktiles = pass == DELTA_COMPOSE ? (p.Dk + 16 * NW - 1) / (16 * NW) : 0;
-  p.ctiles = vt + p.ktiles;
+  // composing, the columns of phi go beside those of the sum
+  const int kt = pass == DELTA_COMPOSE ? (p.Dk + 16 * NW - 1) / (16 * NW) : 0;
+  p.ctiles = kt > vt ? kt : vt;
   const int64_t grid = (int64_t)p.B * p.H * p.count * p.ctiles;
   if (pass == DELTA_COMPOSE)
     k_delta_chunks<T, NP, DK, NW, L, true><<<(unsigned)grid, 64 * NW, 0, st>>>(p);
@@ -1054,12 +1157,14 @@ semicrf_status_t delta_width(const DeltaArgs &p, DeltaPass pass, hipStream_t st)
     return launch_status();
   }
   if (pass == DELTA_GRADS) {
-    k_delta_grads<T, NP, DK, L><<<grid, 256, 0, st>>>(p);
+    k_delta_grads<T, NP, DK, L><<<grid, 512, 0, st>>>(p);
     return launch_status();
   }
   switch (delta_waves(p.Dv)) {
     case 2: return delta_walk<T, NP, DK, 2>(p, pass, st);
     case 4: return delta_walk<T, NP, DK, 4>(p, pass, st);
+    case 5: return delta_walk<T, NP, DK, 5>(p, pass, st);
+    case 6: return delta_walk<T, NP, DK, 6>(p, pass, st);
     default: return delta_walk<T, NP, DK, 8>(p, pass, st);
   }
 }
@@ -1068,6 +1173,7 @@ template <typename T, int NP>
 semicrf_status_t delta_type(const DeltaArgs &p, DeltaPass pass, hipStream_t st) {
   if (p.Dk <= 32) return delta_width<T, NP, 32>(p, pass, st);
   if (p.Dk <= 64) return delta_width<T, NP, 64>(p, pass, st);
+  if (p.Dk <= 96) return delta_width<T, NP, 96>(p, pass, st);
   return delta_width<T, NP, 128>(p, pass, st);
 }
 
