@@ -817,8 +817,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 // by the others: the accumulators' layout is then that of the operand they become,
 // and the triangles' rows and columns on a SIMD add up to the same.
 template <typename T, int NP, int DK, int L>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void k_delta_grads(
-    DeltaArgs p) {
+__global__ __launch_bounds__(512)
+    __attribute__((amdgpu_waves_per_eu(NP == 1 && DK > 64 ? 2 : 4))) void k_delta_grads(DeltaArgs p) {
   constexpr int NT = L / 16, JB = L / 32, DS = 4 / NT, DT = DK / 16 / DS, kThreads = 512;
   typedef ByRow<32> LS;
   typedef ByColumn<DK> LK;
@@ -867,7 +867,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void k
     td.fetch(tid, ds + c0, p.lv, p.Dk, p.lv - c0);
     if (p.vec) tg.fetch(tid, go, (int)so, p.Dv, count, 0, 1, c0);
   };
-  fetch(0);
   if (tid < L) {
     float bt = 1.f;
     if (tid < count) bt = p.beta[row0 + (int64_t)tid * p.H];
@@ -889,7 +888,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void k
   float dbs[UN];   // (dR / b) . (U / b) of the rows it reads
 #pragma unroll
   for (int i = 0; i < UN; ++i) dbs[i] = 0.f;
+  // no slice ahead: the registers it would take are worth more as the second
+  // workgroup's on the compute unit
   for (int c0 = 0; c0 < p.Dv; c0 += 32) {
+    fetch(c0);
     __syncthreads();
     {
       const int tid = delta_fresh(threadIdx.x);
@@ -913,13 +915,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void k
 #pragma unroll
       for (int r = 0; r < 4; ++r) dot += (double)ts.r[i][r] * td.r[i][r];
     __syncthreads();
-    if (c0 + 32 < p.Dv) {
-      fetch(c0 + 32);
-    } else if (p.vec) {
-      const int tid = delta_fresh(threadIdx.x);
-      tk.fetch(tid, k, (int)p.k.st, p.Dk, count, 0, 1, 0);
-      tq.fetch(tid, q, (int)p.q.st, p.Dk, count, 0, 1, 0);
-    }
     const int lane = delta_fresh(tid & 63);
     if (asks) {
       const Frag<NP> gf = frag_row<NP, LS>(G, L * LS::row, 16 * pt, 0, lane);
@@ -949,6 +944,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(4))) void k
       for (int i = 0; i < DT; ++i)
         a0[i] = mma<3>(frag_row<3, LS>(D, DK * LS::row, 16 * (d0 + i), 0, lane), uf, a0[i]);
     }
+  }
+  if (p.vec) {
+    const int tid = delta_fresh(threadIdx.x);
+    tk.fetch(tid, k, (int)p.k.st, p.Dk, count, 0, 1, 0);
+    tq.fetch(tid, q, (int)p.q.st, p.Dk, count, 0, 1, 0);
   }
   __syncthreads();
   if (p.vec) {
