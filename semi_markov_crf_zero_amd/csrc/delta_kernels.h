@@ -215,9 +215,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
     *reinterpret_cast<f4 *>(M + i * LD + j) = acc;
   }
   __syncthreads();
-  if (w < NT) {
+  if (w == 0 && g < NT) {
     float x[16];
-    float *m = M + 16 * w * LD + 16 * w;
+    float *m = M + 16 * g * LD + 16 * g;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float y = i == l16 ? 1.f : 0.f;
@@ -226,11 +226,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
       x[i] = y;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i / 4 == g) {
-        M[(16 * w + i) * LD + 16 * w + l16] = x[i];
-        if (w < kCols / LT / 16) Xt[(16 * w + l16) * LT + (16 * w + i) % (L / 2)] = x[i];
-      }
+    for (int i = 0; i < 16; ++i) m[i * LD + l16] = x[i];
+    if (g < kCols / LT / 16) {
+      float *t = Xt + (16 * g + l16) * LT + 16 * g % (L / 2);
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) *reinterpret_cast<f4 *>(t + i) = f4{x[i], x[i + 1], x[i + 2], x[i + 3]};
+    }
   }
   __syncthreads();
   // blocks of n16 tiles beside each other: rows it, columns ct of the lower left
@@ -380,7 +381,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   for (int n = lo; n < hi; ++n) {
     const int m = min(L, len - n * L);
     __syncthreads();
-    const int lane = delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
+    const int lane = DK <= 64 ? tid & 63 : delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
     if (n + 1 < hi) fetch(n + 1);
     if (!COMPOSE && p.S && xc < p.lv) {
       float *to = p.S + (bh * p.N + n) * size + xc;
@@ -661,7 +662,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   for (int n = hi - 1; n >= lo; --n) {
     const int m = min(L, len - n * L);
     __syncthreads();
-    const int lane = delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
+    const int lane = DK <= 64 ? tid & 63 : delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
     if (n > lo) fetch(n - 1);
     if (!COMPOSE && xc < p.lv) {
       float *at = p.D + (bh * p.N + n) * size + xc;
