@@ -296,8 +296,8 @@ size_t forward_areas(const semicrf_linattn_shape_t *s, void *ws, bool keep, Delt
   p->phit = p->S = p->U = nullptr;
   if (keep) {
     p->phit = a.take(parts * lk);
-    p->S = a.take(heads * N * s->Dk * lv);
-    p->U = a.take(heads * N * L * lv);
+    p->S = a.take(heads * N * s->Dv * lk);
+    p->U = a.take(heads * N * s->Dv * L);
   }
   return a.at - (char *)ws;
 }
@@ -306,9 +306,9 @@ size_t backward_areas(const semicrf_linattn_shape_t *s, void *ws, DeltaArgs *p, 
   const int L = delta_chunk(delta_parts(s->dtype));
   const int64_t heads = (int64_t)s->B * s->H, N = chunks_of(s), rows = heads * s->T;
   segments(s, &p->nseg, &p->seg);
-  const int lv = up4(s->Dv);
-  p->D = a.take(heads * N * s->Dk * lv);
-  p->R = a.take(heads * N * L * lv);
+  const int lk = up4(s->Dk), lv = up4(s->Dv);
+  p->D = a.take(heads * N * s->Dv * lk);
+  p->R = a.take(heads * N * s->Dv * L);
   p->xs = a.take(p->nseg > 1 ? heads * p->nseg * s->Dk * lv : 0);
   part[0] = a.take(s->Hq == s->H ? 0 : rows * s->Dk);
   part[1] = a.take(s->Hk == s->H ? 0 : rows * s->Dk);

@@ -3,6 +3,8 @@
 // compute).
 #pragma once
 
+#include <type_traits>
+
 #include "parts.h"
 
 namespace semicrf {
@@ -18,10 +20,11 @@ struct DeltaArgs {
   const int32_t *lengths;
   const float *state_in;
   float *X, *gates;  // of each chunk: [ld][ld], delta_gates
-  // Rows of the following are lk or lv apart, Dk or Dv rounded up to fours (zeros there).
+  // Rows of Dk or Dv of the following are lk or lv apart, rounded up to fours (zeros there).
   float *phi, *phit, *xs;  // of each segment: [Dk][Dk], its transpose (or NULL), [Dk][Dv]
-  float *S, *U;            // of each chunk, for the backward pass: [Dk][Dv], [L][Dv]; or NULL
-  float *D, *R;            // and its own: the gradients of the state after it and of R
+  // of each chunk, by columns, which lanes hold four neighbours of:
+  float *S, *U;  // for the backward pass: [Dv][Dk], [Dv][L]; or NULL
+  float *D, *R;  // and its own: the gradients of the state after it and of R
   void *o, *dq, *dk, *dv;
   float *state_out, *dg, *db;
   int part_q, part_k, part_v;  // gradients go to float32 [B][T][H][D]: of shared heads
@@ -52,6 +55,26 @@ semicrf_status_t delta_bf16(const DeltaArgs &p, DeltaPass pass, hipStream_t st);
 semicrf_status_t delta_f16(const DeltaArgs &p, DeltaPass pass, hipStream_t st);
 
 namespace {
+
+// part2 with one instruction for what an element's rounding leaves: the dot product
+// with (-1, 0) or (0, -1), which is exact (the same bits for 2^22 values of all
+// exponents).  Seven instructions in the place of eleven for a pair's three parts take
+// a little longer, but fewer registers: for the kernel that is short of them.  The
+// constants are kept from being folded into the instruction, whose literals are not
+// halves.
+__device__ __forceinline__ b2 part2_dot(f2 &x) {
+  unsigned first, second;
+  asm("" : "=s"(first) : "0"(0x0000bf80u));
+  asm("" : "=s"(second) : "0"(0xbf800000u));
+  const b2 y = __builtin_convertvector(x, b2);
+  x[0] = __builtin_amdgcn_fdot2_f32_bf16(y, __builtin_bit_cast(b2, first), x[0], false);
+  x[1] = __builtin_amdgcn_fdot2_f32_bf16(y, __builtin_bit_cast(b2, second), x[1], false);
+  return y;
+}
+template <bool DOT>
+__device__ __forceinline__ b2 part2_of(f2 &x) {
+  return DOT ? part2_dot(x) : part2(x);
+}
 
 template <int L>
 struct Gates {
@@ -89,7 +112,7 @@ struct GatesTile {
 // A float32 matrix of `ROWS` rows (ld apart, 16 bytes aligned) and W columns, in three
 // parts in LDS, zeros past n rows and D columns (a multiple of 4); LOWER: blocks of
 // 32 above the diagonal are not read (nor written).
-template <typename Lay, int W, int ROWS, int NT, bool LOWER>
+template <typename Lay, int W, int ROWS, int NT, bool LOWER, bool DOT = false>
 struct Tile32 {
   static constexpr int per = W / 4, all = ROWS * per, N = (all + NT - 1) / NT;
   static constexpr int plane = ROWS * Lay::row;
@@ -99,7 +122,7 @@ struct Tile32 {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const int e = tid + k * NT, i = e / per, c = e % per * 4;
-      const bool on = i < n && c < D && !(LOWER && c / 32 > i / 32);
+      const bool on = e < all && i < n && c < D && !(LOWER && c / 32 > i / 32);
       r[k] = __builtin_bit_cast(
           f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, on ? 4 * (i * ld + c) : -1, 0, 0));
     }
@@ -130,11 +153,30 @@ __device__ __forceinline__ int delta_fresh(int x) {
 
 // The tiles of 16 rows 2 b and 2 b + 1 of an accumulated matrix as an operand whose
 // contraction runs over them.
+template <bool DOT = false>
 __device__ __forceinline__ Frag<3> frag_of(const f4 &a, const f4 &b) {
-  float x[8];
+  Frag<3> f;
 #pragma unroll
-  for (int r = 0; r < 4; ++r) x[r] = a[r], x[4 + r] = b[r];
-  return split<3>(x);
+  for (int e = 0; e < 8; e += 2) {
+    f2 r = e < 4 ? f2{a[e], a[e + 1]} : f2{b[e - 4], b[e - 3]};
+#pragma unroll
+    for (int n = 0; n < 3; ++n) {
+      const b2 y = part2_of<DOT>(r);
+      f.v[n][e] = y[0];
+      f.v[n][e + 1] = y[1];
+    }
+  }
+  return f;
+}
+
+// Zeros in the tiles (2 b, 2 b + 1) of three parts of an L x L matrix in LDS.
+template <typename Lay, int L, int NT>
+__device__ __forceinline__ void beside_diagonal(bf16 *P) {
+  for (int e = threadIdx.x; e < 3 * L / 2 * 4; e += NT) {
+    const int part = e / (2 * L), row = e / 4 % (L / 2), i = row / 16 * 32 + row % 16;
+    *reinterpret_cast<Pack<bf16, 4> *>(P + part * L * Lay::row +
+                                       Lay::at(i, row / 16 * 8 + 4 + e % 4)) = Pack<bf16, 4>{};
+  }
 }
 
 template <typename T>
@@ -375,6 +417,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       if (NC > 1) S[NC - 1][i][r] = row == xc ? 1.f : 0.f;  // phi
     }
   if (lo < hi) put(lo);
+  // the tiles of P beside the diagonal that products of 32 columns read
+  if (!COMPOSE) beside_diagonal<LX, L, kThreads>(P);
 
   T *out = (T *)p.o + ((int64_t)b * p.T * p.H + h) * p.Dv;
   const int64_t so = (int64_t)p.H * p.Dv;
@@ -383,42 +427,32 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
     __syncthreads();
     const int lane = DK <= 64 ? tid & 63 : delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
     if (n + 1 < hi) fetch(n + 1);
-    if (!COMPOSE && p.S && xc < p.lv) {
-      float *to = p.S + (bh * p.N + n) * size + xc;
+    if (!COMPOSE && p.S && xc < p.Dv) {
+      float *to = p.S + ((bh * p.N + n) * p.Dv + xc) * p.lk + 4 * g;
 #pragma unroll
       for (int i = 0; i < 2 * KB; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * i + 4 * g + r < p.Dk) to[(16 * i + 4 * g + r) * p.lv] = S[0][i][r];
+        if (16 * i + 4 * g < p.lk) *reinterpret_cast<f4 *>(to + 16 * i) = S[0][i];
     }
     if (!COMPOSE) {
-      // P: wave w its rows of 16, up to the diagonal and the tile beside it
-      for (int it = w; it < NT; it += NW) {
-        Frag<NP> qf[KB];
+      // P, up to the diagonal, a tile a wave at a time
+      for (int t = w; t < NT * (NT + 1) / 2; t += NW) {
+        int it = 0, jt = t;
+        while (jt > it) jt -= ++it;
+        f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
-          qf[kb] = frag_row<NP, LQ>(Q, L * LQ::row, 16 * it, kb, lane);
-        const int i = 16 * it + l16;
+          acc = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * jt, kb, lane),
+                       frag_row<NP, LQ>(Q, L * LQ::row, 16 * it, kb, lane), acc);
+        const int i = 16 * it + l16, j = 16 * jt + 4 * g;
 #pragma unroll
-        for (int jt = 0; jt < NT; ++jt) {
-          if (jt > (it | 1)) continue;
-          f4 acc = {0.f, 0.f, 0.f, 0.f};
-          if (jt <= it) {
+        for (int r = 0; r < 4; ++r)
+          acc[r] = j + r <= i ? p.scale * gs.decay(i, j + r) * acc[r] : 0.f;
+        f2 x = {acc[0], acc[1]}, y = {acc[2], acc[3]};
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-              acc = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * jt, kb, lane), qf[kb], acc);
-            const int j = 16 * jt + 4 * g;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[r] = j + r <= i ? p.scale * gs.decay(i, j + r) * acc[r] : 0.f;
-          }
-          f2 x = {acc[0], acc[1]}, y = {acc[2], acc[3]};
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const b2 a = part2(x), d = part2(y);
-            *reinterpret_cast<Pack<bf16, 4> *>(P + c * L * LX::row + LX::at(i, 4 * jt + g)) =
-                Pack<bf16, 4>{{a[0], a[1], d[0], d[1]}};
-          }
+        for (int c = 0; c < 3; ++c) {
+          const b2 a = part2(x), d = part2(y);
+          *reinterpret_cast<Pack<bf16, 4> *>(P + c * L * LX::row + LX::at(i, 4 * jt + g)) =
+              Pack<bf16, 4>{{a[0], a[1], d[0], d[1]}};
         }
       }
     }
@@ -483,12 +517,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 #pragma unroll
         for (int c = 0; c < NC; ++c) U[c][it] = mma<3>(xf, rf[c][jb], U[c][it]);
       }
-    if (!COMPOSE && p.U && xc < p.lv) {
-      float *to = p.U + (bh * p.N + n) * L * p.lv + xc;
+    if (!COMPOSE && p.U && xc < p.Dv) {
+      float *to = p.U + ((bh * p.N + n) * p.Dv + xc) * L + 4 * g;
 #pragma unroll
-      for (int it = 0; it < NT; ++it)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) to[(16 * it + 4 * g + r) * p.lv] = U[0][it][r];
+      for (int it = 0; it < NT; ++it) *reinterpret_cast<f4 *>(to + 16 * it) = U[0][it];
     }
     // S <- e^{G_L} S + K^T (e^{G_L - G} U)
     Frag<3> uf[JB];
@@ -658,46 +690,38 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       D[i][r] = d0 && row < p.Dk && xc < p.Dv ? d0[row * l0v + xc] : 0.f;
     }
   if (lo < hi) put(hi - 1);
+  beside_diagonal<LX, L, kThreads>(P);
 
   for (int n = hi - 1; n >= lo; --n) {
     const int m = min(L, len - n * L);
     __syncthreads();
     const int lane = DK <= 64 ? tid & 63 : delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
     if (n > lo) fetch(n - 1);
-    if (!COMPOSE && xc < p.lv) {
-      float *at = p.D + (bh * p.N + n) * size + xc;
+    if (!COMPOSE && xc < p.Dv) {
+      float *at = p.D + ((bh * p.N + n) * p.Dv + xc) * p.lk + 4 * g;
 #pragma unroll
       for (int i = 0; i < 2 * KB; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          if (16 * i + 4 * g + r < p.Dk) at[(16 * i + 4 * g + r) * p.lv] = D[i][r];
+        if (16 * i + 4 * g < p.lk) *reinterpret_cast<f4 *>(at + 16 * i) = D[i];
     }
-    for (int it = w; it < NT; it += NW) {
-      Frag<NP> qf[KB];
+    // P, up to the diagonal, a tile a wave at a time
+    for (int t = w; t < NT * (NT + 1) / 2; t += NW) {
+      int it = 0, jt = t;
+      while (jt > it) jt -= ++it;
+      f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
-        qf[kb] = frag_row<NP, LK>(Q, L * LK::row, 16 * it, kb, lane);
-      const int i = 16 * it + l16;
+        acc = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * jt, kb, lane),
+                     frag_row<NP, LK>(Q, L * LK::row, 16 * it, kb, lane), acc);
+      const int i = 16 * it + l16, j = 16 * jt + 4 * g;
 #pragma unroll
-      for (int jt = 0; jt < NT; ++jt) {
-        if (jt > (it | 1)) continue;
-        f4 acc = {0.f, 0.f, 0.f, 0.f};
-        if (jt <= it) {
+      for (int r = 0; r < 4; ++r)
+        acc[r] = j + r <= i ? p.scale * gs.decay(i, j + r) * acc[r] : 0.f;
+      f2 x = {acc[0], acc[1]}, y = {acc[2], acc[3]};
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-            acc = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * jt, kb, lane), qf[kb], acc);
-          const int j = 16 * jt + 4 * g;
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[r] = j + r <= i ? p.scale * gs.decay(i, j + r) * acc[r] : 0.f;
-        }
-        f2 x = {acc[0], acc[1]}, y = {acc[2], acc[3]};
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-          const b2 a = part2(x), d = part2(y);
-          *reinterpret_cast<Pack<bf16, 4> *>(P + c * L * LX::row + LX::at(i, 4 * jt + g)) =
-              Pack<bf16, 4>{{a[0], a[1], d[0], d[1]}};
-        }
+      for (int c = 0; c < 3; ++c) {
+        const b2 a = part2(x), d = part2(y);
+        *reinterpret_cast<Pack<bf16, 4> *>(P + c * L * LX::row + LX::at(i, 4 * jt + g)) =
+            Pack<bf16, 4>{{a[0], a[1], d[0], d[1]}};
       }
     }
     // dU = P^T dO + e^{G_L - G} K dS
@@ -751,22 +775,23 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       for (int jt = 0; jt <= 2 * ib + 1; ++jt)
         dR[jt] = mma<3>(frag_col<3, LX>(X, L * LX::row, 32 * ib, jt, lane), df, dR[jt]);
     }
-    if (!COMPOSE && xc < p.lv) {
-      float *at = p.R + (bh * p.N + n) * L * p.lv + xc;
+    if (!COMPOSE && xc < p.Dv) {
+      float *at = p.R + ((bh * p.N + n) * p.Dv + xc) * L + 4 * g;
 #pragma unroll
-      for (int jt = 0; jt < NT; ++jt)
+      for (int jt = 0; jt < NT; ++jt) {
+        *reinterpret_cast<f4 *>(at + 16 * jt) = dR[jt];
+        if (!p.dv) continue;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int j = 16 * jt + 4 * g + r;
-          at[j * p.lv] = dR[jt][r];
-          if (p.dv && j < m && xc < p.Dv) {
-            const int64_t e = (((int64_t)b * p.T + n * (int64_t)L + j) * p.H + h) * p.Dv + xc;
-            if (p.part_v)
-              ((float *)p.dv)[e] = dR[jt][r];
-            else
-              ((T *)p.dv)[e] = (T)dR[jt][r];
-          }
+          if (j >= m) continue;
+          const int64_t e = (((int64_t)b * p.T + n * (int64_t)L + j) * p.H + h) * p.Dv + xc;
+          if (p.part_v)
+            ((float *)p.dv)[e] = dR[jt][r];
+          else
+            ((T *)p.dv)[e] = (T)dR[jt][r];
         }
+      }
     }
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb) {
@@ -821,19 +846,23 @@ template <typename T, int NP, int DK, int L>
 __global__ __launch_bounds__(512)
     __attribute__((amdgpu_waves_per_eu(NP == 1 && DK > 64 ? 2 : 4))) void k_delta_grads(DeltaArgs p) {
   constexpr int NT = L / 16, JB = L / 32, DS = 4 / NT, DT = DK / 16 / DS, kThreads = 512;
-  typedef ByRow<32> LS;
+  typedef ByRow<32> LG;
+  // 32 columns of U and R as rows of L; of S and D of DK.  Padded, they take fewer
+  // registers for addresses; at DK = 128 a second workgroup has room without.
+  typedef std::conditional_t<(DK <= 64), ByColumn<L>, ByBoth<L>> LU;
+  typedef std::conditional_t<(DK <= 64), ByColumn<DK>, ByBoth<DK>> LS;
   typedef ByColumn<DK> LK;
-  constexpr int kSlice = (6 * L + NP * L + 6 * DK) * LS::row;
-  constexpr int kKeys = 2 * NP * L * LK::row, LW = DK + 4;
-  static_assert(kKeys + 2 * L * LW <= kSlice, "");
-  __shared__ alignas(16) bf16 tiles[kSlice];
-  bf16 *const U = tiles, *const R = U + 3 * L * LS::row, *const G = R + 3 * L * LS::row,
-             *const S = G + NP * L * LS::row, *const D = S + 3 * DK * LS::row;
+  constexpr int PU = 32 * LU::row, PS = 32 * LS::row;
+  constexpr int kSlice = 6 * PU + 6 * PS + NP * L * LG::row;
+  constexpr int kKeys = 2 * NP * L * LK::row, LW = DK + 4, kAfter = kKeys + 2 * L * LW;
+  __shared__ alignas(16) bf16 tiles[kSlice > kAfter ? kSlice : kAfter];
+  bf16 *const U = tiles, *const R = U + 3 * PU, *const S = R + 3 * PU, *const D = S + 3 * PS,
+             *const G = D + 3 * PS;
   // after the slices: the keys, the queries and the others' share of dk
   bf16 *const K = tiles, *const Q = K + NP * L * LK::row;
   float *const dks = (float *)(tiles + kKeys);
   __shared__ Gates<L> gs;
-  __shared__ float inv[L];
+  __shared__ alignas(16) float inv[L], dbs[8][L];
   __shared__ double red[8];
   __shared__ float cs[2 * DS][L], es[DS][L];
 
@@ -850,22 +879,22 @@ __global__ __launch_bounds__(512)
     if (e % p.Dk == 0 && p.db) p.db[row] = 0.f;
   }
   if (count <= 0) return;
-  const int64_t at = ((int64_t)b * p.H + h) * p.N + n, size = (int64_t)p.Dk * p.lv;
+  const int64_t at = ((int64_t)b * p.H + h) * p.N + n, size = (int64_t)p.Dv * p.lk;
   const T *q = view_rows<T>(p.q, b, h) + t0 * p.q.st, *k = view_rows<T>(p.k, b, h) + t0 * p.k.st;
   const int64_t so = (int64_t)p.H * p.Dv;
   const T *go = (const T *)p.go + row0 * p.Dv;
-  const float *u = p.U + at * L * p.lv, *dr = p.R + at * L * p.lv, *s = p.S + at * size,
+  const float *u = p.U + at * L * p.Dv, *dr = p.R + at * L * p.Dv, *s = p.S + at * size,
               *ds = p.D + at * size;
-  Tile32<LS, 32, L, kThreads, false> tu, tr;
-  Tile32<LS, 32, DK, kThreads, false> ts, td;
-  Tile<T, NP, LS, 32, L, kThreads> tg;
+  Tile32<LU, L, 32, kThreads, false, true> tu, tr;
+  Tile32<LS, DK, 32, kThreads, false, true> ts, td;
+  Tile<T, NP, LG, 32, L, kThreads> tg;
   Tile<T, NP, LK, DK, L, kThreads> tk, tq;
   auto fetch = [&](int c0) {
     const int tid = delta_fresh(threadIdx.x);
-    tu.fetch(tid, u + c0, p.lv, L, p.lv - c0);
-    tr.fetch(tid, dr + c0, p.lv, L, p.lv - c0);
-    ts.fetch(tid, s + c0, p.lv, p.Dk, p.lv - c0);
-    td.fetch(tid, ds + c0, p.lv, p.Dk, p.lv - c0);
+    tu.fetch(tid, u + c0 * L, L, p.Dv - c0, L);
+    tr.fetch(tid, dr + c0 * L, L, p.Dv - c0, L);
+    ts.fetch(tid, s + c0 * p.lk, p.lk, p.Dv - c0, p.lk);
+    td.fetch(tid, ds + c0 * p.lk, p.lk, p.Dv - c0, p.lk);
     if (p.vec) tg.fetch(tid, go, (int)so, p.Dv, count, 0, 1, c0);
   };
   if (tid < L) {
@@ -884,11 +913,9 @@ __global__ __launch_bounds__(512)
   for (int i = 0; i < DT; ++i) a0[i] = a1[i] = zero;
 #pragma unroll
   for (int i = 0; i < NT; ++i) p0[i] = p1[i] = zero;
-  constexpr int UN = decltype(tu)::N;
-  double dot = 0;  // S . dS', this thread's share
-  float dbs[UN];   // (dR / b) . (U / b) of the rows it reads
-#pragma unroll
-  for (int i = 0; i < UN; ++i) dbs[i] = 0.f;
+  static_assert(decltype(tu)::N == 1, "");
+  float dot = 0.f;  // S . dS', this thread's share: a few products a slice
+  f4 db4 = zero;   // (dR / b) . (U / b) of four positions, this thread's columns
   // no slice ahead: the registers it would take are worth more as the second
   // workgroup's on the compute unit
   for (int c0 = 0; c0 < p.Dv; c0 += 32) {
@@ -896,54 +923,57 @@ __global__ __launch_bounds__(512)
     __syncthreads();
     {
       const int tid = delta_fresh(threadIdx.x);
+      // one after another (the barriers to the scheduler): 128 registers are all there
+      // are, and a spilled accumulator costs more than the wait
       tu.put(tid, U);
+      __builtin_amdgcn_sched_barrier(0);
       tr.put(tid, R);
+      __builtin_amdgcn_sched_barrier(0);
       ts.put(tid, S);
+      __builtin_amdgcn_sched_barrier(0);
       td.put(tid, D);
+      __builtin_amdgcn_sched_barrier(0);
       if (p.vec)
         tg.put(tid, G);
       else
-        stage<T, NP, LS, 32, L, kThreads>(G, go, so, p.Dv, count, c0);
+        stage<T, NP, LG, 32, L, kThreads>(G, go, so, p.Dv, count, c0);
+      const f4 iv = *reinterpret_cast<const f4 *>(inv + tid % (L / 4) * 4);
 #pragma unroll
-      for (int i = 0; i < UN; ++i) {
-        const float iv = inv[(tid + i * kThreads) / 8 % L];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) dbs[i] = fmaf(tr.r[i][r] * iv, tu.r[i][r] * iv, dbs[i]);
-      }
+      for (int r = 0; r < 4; ++r) db4[r] = fmaf(tr.r[0][r] * iv[r], tu.r[0][r] * iv[r], db4[r]);
     }
 #pragma unroll
     for (int i = 0; i < decltype(ts)::N; ++i)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dot += (double)ts.r[i][r] * td.r[i][r];
+      for (int r = 0; r < 4; ++r) dot = fmaf(ts.r[i][r], td.r[i][r], dot);
     __syncthreads();
     const int lane = delta_fresh(tid & 63);
     if (asks) {
-      const Frag<NP> gf = frag_row<NP, LS>(G, L * LS::row, 16 * pt, 0, lane);
-      const Frag<3> rf = frag_row<3, LS>(R, L * LS::row, 16 * pt, 0, lane);
+      const Frag<NP> gf = frag_row<NP, LG>(G, L * LG::row, 16 * pt, 0, lane);
+      const Frag<3> rf = frag_col<3, LU>(R, PU, 0, pt, lane);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         if (t <= pt) {
-          const Frag<3> x = frag_row<3, LS>(U, L * LS::row, 16 * t, 0, lane);
+          const Frag<3> x = frag_col<3, LU>(U, PU, 0, t, lane);
           p0[t] = mma<3>(x, gf, p0[t]);
           p1[t] = mma<3>(x, rf, p1[t]);
         }
 #pragma unroll
       for (int i = 0; i < DT; ++i) {
-        const Frag<3> x = frag_row<3, LS>(S, DK * LS::row, 16 * (d0 + i), 0, lane);
+        const Frag<3> x = frag_col<3, LS>(S, PS, 0, d0 + i, lane);
         a0[i] = mma<3>(x, gf, a0[i]);
         a1[i] = mma<3>(x, rf, a1[i]);
       }
     } else {
-      const Frag<3> uf = frag_row<3, LS>(U, L * LS::row, 16 * pt, 0, lane);
+      const Frag<3> uf = frag_col<3, LU>(U, PU, 0, pt, lane);
 #pragma unroll
       for (int t = 0; t < NT; ++t)
         if (t >= pt) {
-          p0[t] = mma<3>(frag_row<NP, LS>(G, L * LS::row, 16 * t, 0, lane), uf, p0[t]);
-          p1[t] = mma<3>(frag_row<3, LS>(R, L * LS::row, 16 * t, 0, lane), uf, p1[t]);
+          p0[t] = mma<3>(frag_row<NP, LG>(G, L * LG::row, 16 * t, 0, lane), uf, p0[t]);
+          p1[t] = mma<3>(frag_col<3, LU>(R, PU, 0, t, lane), uf, p1[t]);
         }
 #pragma unroll
       for (int i = 0; i < DT; ++i)
-        a0[i] = mma<3>(frag_row<3, LS>(D, DK * LS::row, 16 * (d0 + i), 0, lane), uf, a0[i]);
+        a0[i] = mma<3>(frag_col<3, LS>(D, PS, 0, d0 + i, lane), uf, a0[i]);
     }
   }
   if (p.vec) {
@@ -960,19 +990,17 @@ __global__ __launch_bounds__(512)
     stage<T, NP, LK, DK, L, kThreads>(K, k, p.k.st, p.Dk, count, 0);
     stage<T, NP, LK, DK, L, kThreads>(Q, q, p.q.st, p.Dk, count, 0);
   }
+  // lanes L / 4 apart have the same positions
 #pragma unroll
-  for (int i = 0; i < UN; ++i) {
-    float x = dbs[i];
+  for (int o = L / 4; o < 64; o <<= 1)
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) x += __shfl_xor(x, o);
-    const int e = tid + i * kThreads, row = e / 8;
-    if (p.db && e < decltype(tu)::all && e % 8 == 0 && row < count)
-      p.db[row0 + (int64_t)row * p.H] = x;
-  }
+    for (int r = 0; r < 4; ++r) db4[r] += __shfl_xor(db4[r], o);
+  if ((tid & 63) < L / 4) *reinterpret_cast<f4 *>(&dbs[w][4 * (tid & 63)]) = db4;
   const int lane = delta_fresh(tid & 63), g = lane >> 4, l16 = lane & 15;
+  double all_dot = dot;
 #pragma unroll
-  for (int o = 32; o; o >>= 1) dot += __shfl_xor(dot, o);
-  if (lane == 0) red[w] = dot;
+  for (int o = 32; o; o >>= 1) all_dot += __shfl_xor(all_dot, o);
+  if (lane == 0) red[w] = all_dot;
   __syncthreads();
   const int mine = 16 * pt + l16;
   // four neighbours of this position's row of K or Q
@@ -1030,7 +1058,7 @@ __global__ __launch_bounds__(512)
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb)
       if (2 * jb <= pt) {
-        const Frag<3> f0 = frag_of(p0[2 * jb], p0[2 * jb + 1]), f1 = frag_of(p1[2 * jb], p1[2 * jb + 1]);
+        const Frag<3> f0 = frag_of<true>(p0[2 * jb], p0[2 * jb + 1]), f1 = frag_of<true>(p1[2 * jb], p1[2 * jb + 1]);
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
           const Frag<NP> x = frag_col<NP, LK>(K, L * LK::row, 32 * jb, d0 + i, lane);
@@ -1072,7 +1100,7 @@ __global__ __launch_bounds__(512)
 #pragma unroll
     for (int ib = 0; ib < JB; ++ib)
       if (2 * ib + 1 >= pt) {
-        const Frag<3> f0 = frag_of(p0[2 * ib], p0[2 * ib + 1]), f1 = frag_of(p1[2 * ib], p1[2 * ib + 1]);
+        const Frag<3> f0 = frag_of<true>(p0[2 * ib], p0[2 * ib + 1]), f1 = frag_of<true>(p1[2 * ib], p1[2 * ib + 1]);
 #pragma unroll
         for (int i = 0; i < DT; ++i) {
           a0[i] = mma<3>(frag_col<NP, LK>(Q, L * LK::row, 32 * ib, d0 + i, lane), f0, a0[i]);
@@ -1100,6 +1128,12 @@ __global__ __launch_bounds__(512)
       for (int r = 0; r < 4; ++r) y[r] = a1[i][r] + x[r];
       give(p.dk, p.part_k, i, y);
     }
+  }
+  if (w == 6 && lane < count && p.db) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x += dbs[i][lane];
+    p.db[row0 + (int64_t)lane * p.H] = x;
   }
   if (w == 7 && p.dg) {
     double x = 0, y = 0;
