@@ -240,16 +240,32 @@ int64_t chunks_of(const semicrf_linattn_shape_t *s) {
   return (s->T + (int64_t)L - 1) / L;
 }
 
-// Segments: as many as give the GPU two workgroups a compute unit, of four chunks at
-// least.
+// Segments.  A chunk takes a walk about 6 us where it has a compute unit to itself,
+// 9 where two share it (up to four waves each; more do not fit); with segments the
+// walk that composes adds three quarters, and two launches and the scan 10 us and
+// 0.4 a segment.  The number that this puts first, of those that give every compute
+// unit 1, 2, ... walks over up to two rounds.  Measured: 32 sequences of 512 positions
+// of 4 heads of 64, 73 us in one segment each, 78 in two; 1024 positions 115 us in one, 66 in four, 48 in eight;
+// 2^20 positions 100 ms in one, 5.7 ms in 32, 2.4 in 128; four sequences of 20001 positions
+// of 4 heads of 128 (one walk a compute unit) 538 us in 16, 597 in 32.
 void segments(const semicrf_linattn_shape_t *s, int *nseg, int *seg) {
-  const int NW = delta_waves(s->Dv);
-  const int64_t chunks = chunks_of(s);
+  const int NW = delta_waves(s->Dv), resident = NW <= 4 ? 2 : 1;
+  const int64_t chunks = chunks_of(s), slots = 256 * resident;
   const int64_t walks = (int64_t)s->B * s->H * ((s->Dv + 16 * NW - 1) / (16 * NW));
-  int64_t n = 512 / walks;
-  if (n > chunks / 4) n = chunks / 4;
-  if (n < 2) n = 1;
-  const int64_t per = (chunks + n - 1) / n;
+  int64_t best_n = 1;
+  double best = 0;
+  for (int k = 0; k <= 2 * resident; ++k) {
+    int64_t n = k ? 256 * k / walks : 1;
+    if (n > chunks / 2) n = chunks / 2;
+    if (n < 1) n = 1;
+    const int64_t per = (chunks + n - 1) / n;
+    n = (chunks + per - 1) / per;
+    const int64_t all = walks * n;
+    double us = (double)per * ((all + slots - 1) / slots) * (all > 256 && resident > 1 ? 9 : 6);
+    if (n > 1) us = 1.75 * us + 10 + 0.4 * n;
+    if (!k || us < best) best = us, best_n = n;
+  }
+  const int64_t per = (chunks + best_n - 1) / best_n;
   *seg = (int)per;
   *nseg = (int)((chunks + per - 1) / per);
 }
