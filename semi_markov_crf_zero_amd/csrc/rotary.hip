@@ -15,8 +15,18 @@ namespace semicrf {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPlanes = 4096;  // planes of the positions of a workgroup, in LDS
+constexpr int kPlanes = 1024;  // planes of the positions of a workgroup, in LDS
+constexpr int kMaxPlanes = 4096;  // of a position: then in more of it
+constexpr int kAhead = 4;
 constexpr int64_t kMaxGrid = 1 << 20;
+
+// n / d by a product where n d < 2^32 (m = ceil(2^32 / d)); m = 0: the quotient itself.
+struct Divisor {
+  uint32_t d, m;
+};
+__device__ __forceinline__ uint32_t quotient(uint32_t n, Divisor v) {
+  return v.m ? __umulhi(n, v.m) : n / v.d;
+}
 
 struct RotaryArgs {
   semicrf_rotary_shape_t s;
@@ -24,12 +34,17 @@ struct RotaryArgs {
   void *y[2];
   const double *frequency;
   const int32_t *position;
-  int rows;       // positions of a workgroup at a time
-  int turned, units;  // vectors of a head that are turned, and all of them
+  int rows;           // positions of a workgroup at a time
+  int turned;         // vectors of a head that are turned
+  Divisor units, per;  // vectors of a head, and of all heads of a position
 };
 
 struct Turn {
   float c, s;
+};
+// A position: its number, and where its rows lie in both tensors.
+struct Row {
+  int64_t position, x[2];
 };
 
 __device__ __forceinline__ Turn turn_of(int64_t position, double frequency, float scale,
@@ -50,76 +65,93 @@ __device__ __forceinline__ Turn turn_of(int64_t position, double frequency, floa
 
 template <typename T, int V, bool HALF>
 __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs p) {
-  __shared__ Turn turns[kPlanes];
+  extern __shared__ __align__(16) unsigned char lds[];
+  Row *const at = (Row *)lds;
+  Turn *const turns = (Turn *)(at + p.rows);
   const semicrf_rotary_shape_t &s = p.s;
-  const int half = s.turn / 2, heads = s.heads + s.heads2;
+  const int half = s.turn / 2;
   const int64_t all = (int64_t)s.B * s.T;
   for (int64_t first = (int64_t)blockIdx.x * p.rows; first < all;
        first += (int64_t)gridDim.x * p.rows) {
     const int rows = (int)min((int64_t)p.rows, all - first);
     __syncthreads();
-    for (int e = threadIdx.x; e < rows * half; e += kThreads) {
-      const int64_t row = first + e / half;
-      const int64_t b = row / s.T, t = row % s.T;
-      const int64_t at = s.positions == SEMICRF_POSITION_EACH       ? p.position[row]
-                         : s.positions == SEMICRF_POSITION_SEQUENCE ? p.position[b] + t
-                                                                    : t;
-      turns[e] = turn_of(at, p.frequency[e % half], s.scale, s.inverse);
+    for (int r = threadIdx.x; r < rows; r += kThreads) {
+      const int64_t row = first + r, b = row / s.T, t = row - b * s.T;
+      at[r].position = s.positions == SEMICRF_POSITION_EACH       ? p.position[row]
+                       : s.positions == SEMICRF_POSITION_SEQUENCE ? p.position[b] + t
+                                                                  : t;
+      at[r].x[0] = b * s.stride[0] + t * s.stride[1];
+      at[r].x[1] = b * s.stride2[0] + t * s.stride2[1];
     }
     __syncthreads();
-    const int per = heads * p.units;
-    for (int e = threadIdx.x; e < rows * per; e += kThreads) {
-      const int r = e / per, left = e % per, head = left / p.units, u = left % p.units;
-      const int64_t row = first + r, b = row / s.T, t = row % s.T;
-      const bool second = head >= s.heads;
-      const int h = second ? head - s.heads : head;
-      const int64_t *st = second ? s.stride2 : s.stride;
-      const T *x = (const T *)p.x[second] + b * st[0] + t * st[1] + h * st[2];
-      T *y = (T *)p.y[second] + (row * (second ? s.heads2 : s.heads) + h) * s.D;
-      const Turn *turn = turns + r * half;
-      if (u >= p.turned) {
-        const int d = s.turn + (u - p.turned) * V;
-        *reinterpret_cast<Pack<T, V> *>(y + d) = *reinterpret_cast<const Pack<T, V> *>(x + d);
-      } else if (HALF) {
-        const int d = u * V;
-        const Pack<T, V> lo = *reinterpret_cast<const Pack<T, V> *>(x + d);
-        const Pack<T, V> hi = *reinterpret_cast<const Pack<T, V> *>(x + d + half);
-        Pack<T, V> a, c;
+    // kAhead vectors (pairs of them) a thread on their way, the first ones while the
+    // cosines and sines are worked out
+    constexpr int W = HALF ? V : V == 1 ? 2 : V;  // elements from one turned unit to the next
+    constexpr int C = HALF || V == 1 ? 2 * V : V;  // of a copied one: two loads where turning has two
+    const int all_units = rows * (int)p.per.d;
+    Pack<T, V> lo[kAhead], hi[kAhead];
+    T *to[kAhead];
+    int unit[kAhead], row_of[kAhead];
+    auto load = [&](int e0) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const Turn z = turn[d + i];
-          const float f = (float)lo.v[i], g = (float)hi.v[i];
-          a.v[i] = (T)(f * z.c - g * z.s);
-          c.v[i] = (T)(f * z.s + g * z.c);
-        }
-        *reinterpret_cast<Pack<T, V> *>(y + d) = a;
-        *reinterpret_cast<Pack<T, V> *>(y + d + half) = c;
-      } else {
-        // V neighbours hold V / 2 planes; one by one, a unit is a plane
-        constexpr int W = V == 1 ? 2 : V;
-        const int d = u * W;
-        T in[W], out[W];
-        if (V == 1) {
-          in[0] = x[d], in[1] = x[d + 1];
-        } else {
-          const Pack<T, V> a = *reinterpret_cast<const Pack<T, V> *>(x + d);
+      for (int n = 0; n < kAhead; ++n) {
+        // loads without branches: past the end the last one again
+        const int e = min(e0 + n * kThreads, all_units - 1);
+        const int r = (int)quotient(e, p.per), left = e - r * (int)p.per.d;
+        const int head = (int)quotient(left, p.units), u = left - head * (int)p.units.d;
+        const bool second = head >= s.heads;
+        const int h = second ? head - s.heads : head;
+        const T *x = (const T *)p.x[second] + at[r].x[second] + h * (second ? s.stride2 : s.stride)[2];
+        to[n] = (T *)p.y[second] + ((first + r) * (second ? s.heads2 : s.heads) + h) * s.D;
+        unit[n] = u, row_of[n] = r;
+        const int d = u < p.turned ? u * W : s.turn + (u - p.turned) * C;
+        lo[n] = *reinterpret_cast<const Pack<T, V> *>(x + d);
+        if (HALF || V == 1)
+          hi[n] = *reinterpret_cast<const Pack<T, V> *>(
+              x + (u < p.turned ? d + (HALF ? half : 1) : min(d + V, s.D - V)));
+      }
+    };
+    load(threadIdx.x);
+    for (int e = threadIdx.x; e < rows * half; e += kThreads) {
+      const int r = e / half;
+      turns[e] = turn_of(at[r].position, p.frequency[e - r * half], s.scale, s.inverse);
+    }
+    __syncthreads();
+    for (int e0 = threadIdx.x; e0 < all_units; e0 += kAhead * kThreads) {
+      if (e0 >= kAhead * kThreads) load(e0);
 #pragma unroll
-          for (int i = 0; i < V; ++i) in[i] = a.v[i];
-        }
+      for (int n = 0; n < kAhead; ++n) {
+        if (e0 + n * kThreads >= all_units) break;
+        T *y = to[n];
+        const int u = unit[n];
+        const Turn *turn = turns + row_of[n] * half;
+        if (u >= p.turned) {
+          const int d = s.turn + (u - p.turned) * C;
+          *reinterpret_cast<Pack<T, V> *>(y + d) = lo[n];
+          if (C > V && d + V < s.D) *reinterpret_cast<Pack<T, V> *>(y + d + V) = hi[n];
+        } else if (HALF || V == 1) {
+          // vectors of first and of second elements; one by one, a plane
+          const int d = u * W;
+          Pack<T, V> a, c;
 #pragma unroll
-        for (int i = 0; i < W; i += 2) {
-          const Turn z = turn[(d + i) / 2];
-          const float f = (float)in[i], g = (float)in[i + 1];
-          out[i] = (T)(f * z.c - g * z.s);
-          out[i + 1] = (T)(f * z.s + g * z.c);
-        }
-        if (V == 1) {
-          y[d] = out[0], y[d + 1] = out[1];
+          for (int i = 0; i < V; ++i) {
+            const Turn z = turn[HALF ? d + i : u];
+            const float f = (float)lo[n].v[i], g = (float)hi[n].v[i];
+            a.v[i] = (T)(f * z.c - g * z.s);
+            c.v[i] = (T)(f * z.s + g * z.c);
+          }
+          *reinterpret_cast<Pack<T, V> *>(y + d) = a;
+          *reinterpret_cast<Pack<T, V> *>(y + d + (HALF ? half : 1)) = c;
         } else {
           Pack<T, V> a;
 #pragma unroll
-          for (int i = 0; i < V; ++i) a.v[i] = out[i];
-          *reinterpret_cast<Pack<T, V> *>(y + d) = a;
+          for (int i = 0; i + 1 < V; i += 2) {
+            const Turn z = turn[(u * V + i) / 2];
+            const float f = (float)lo[n].v[i], g = (float)lo[n].v[i + 1];
+            a.v[i] = (T)(f * z.c - g * z.s);
+            a.v[i + 1] = (T)(f * z.s + g * z.c);
+          }
+          *reinterpret_cast<Pack<T, V> *>(y + u * V) = a;
         }
       }
     }
@@ -153,19 +185,26 @@ semicrf_status_t launch(RotaryArgs p, hipStream_t st) {
   const semicrf_rotary_shape_t &s = p.s;
   const bool half = s.layout == SEMICRF_ROTARY_HALF;
   p.turned = half || V == 1 ? s.turn / 2 / (half ? V : 1) : s.turn / V;
-  p.units = p.turned + (s.D - s.turn) / V;
+  const int copied = half || V == 1 ? 2 * V : V;
+  const int units = p.turned + (s.D - s.turn + copied - 1) / copied;
   // four vectors a thread, as far as the planes fit
-  const int64_t per = (int64_t)(s.heads + s.heads2) * p.units, all = (int64_t)s.B * s.T;
-  int64_t rows = 4 * kThreads / per;
+  const int64_t per = (int64_t)(s.heads + s.heads2) * units, all = (int64_t)s.B * s.T;
+  int64_t rows = kAhead * kThreads / per;
   if (rows > kPlanes / (s.turn / 2)) rows = kPlanes / (s.turn / 2);
   if (rows < 1) rows = 1;
   p.rows = (int)rows;
+  auto divisor = [](int64_t d, int64_t most) {
+    return Divisor{(uint32_t)d, d > 1 && most * d < (int64_t)1 << 32
+                                    ? (uint32_t)((((int64_t)1 << 32) + d - 1) / d) : 0};
+  };
+  p.per = divisor(per, rows * per), p.units = divisor(units, per);
+  const size_t lds = rows * (sizeof(Row) + s.turn / 2 * sizeof(Turn));
   int64_t grid = (all + rows - 1) / rows;
   if (grid > kMaxGrid) grid = kMaxGrid;
   if (half)
-    k_rotary<T, V, true><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    k_rotary<T, V, true><<<(unsigned)grid, kThreads, lds, st>>>(p);
   else
-    k_rotary<T, V, false><<<(unsigned)grid, kThreads, 0, st>>>(p);
+    k_rotary<T, V, false><<<(unsigned)grid, kThreads, lds, st>>>(p);
   return launch_status();
 }
 template <typename T>
@@ -194,7 +233,7 @@ extern "C" semicrf_status_t semicrf_rotary(const semicrf_rotary_shape_t *s, cons
       s->T > most || s->heads > most || s->heads2 > most)
     return SEMICRF_ERR_SHAPE;
   if (s->turn < 2 || s->turn % 2 || s->turn > s->D) return SEMICRF_ERR_SHAPE;
-  if (s->D > 2 * kPlanes) return SEMICRF_ERR_UNSUPPORTED;
+  if (s->D > 2 * kMaxPlanes) return SEMICRF_ERR_UNSUPPORTED;
   const int64_t heads = (int64_t)s->heads + s->heads2;
   if (heads * s->D >= 1 << 28) return SEMICRF_ERR_SHAPE;
   if (!dtype_ok(s->dtype) || s->layout < 0 || s->layout > SEMICRF_ROTARY_INTERLEAVED ||

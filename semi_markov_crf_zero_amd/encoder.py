@@ -358,26 +358,31 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     return o
 
 
+def _delta(q, k, v, log_decay, beta, state, lengths, dims, scale, keep):
+    """o, the states after, and the workspace, which with keep holds what the
+    backward pass reads again."""
+    B, T, H, _, _, _, Dk, Dv, _ = dims
+    q, k, v, dev = _rows(q), _rows(k), _rows(v), q.device
+    fields = (*dims, scale, _strides(q), _strides(k), _strides(v))
+    o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
+    last = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
+    ws, n = _workspace("semicrf_delta_workspace_size", _LinattnShape, fields, keep, dev)
+    launch(load().semicrf_delta_fwd, dev, ctypes.byref(_LinattnShape(*fields)), keep, _ptr(q),
+           _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(lengths), _ptr(state), _ptr(o),
+           _ptr(last), _ptr(ws), n)
+    return o, last, ws
+
+
 class GatedDelta(torch.autograd.Function):
     """o [B, T, H, Dv] and the state after each sequence [B, H, Dk, Dv]; dims
     is what _delta_check gives."""
 
     @staticmethod
-    def forward(ctx, q, k, v, log_decay, beta, state, lengths, dims, scale, keep):
+    def forward(ctx, q, k, v, log_decay, beta, state, lengths, dims, scale):
         ctx.set_materialize_grads(False)
         ctx.dims, ctx.scale = dims, scale
-        saved = q, k, v, log_decay, beta, lengths
-        B, T, H, _, _, _, Dk, Dv, _ = dims
-        q, k, v = _rows(q), _rows(k), _rows(v)
-        dev = q.device
-        fields = (*dims, scale, _strides(q), _strides(k), _strides(v))
-        o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
-        last = torch.empty((B, H, Dk, Dv), dtype=torch.float32, device=dev)
-        ws, n = _workspace("semicrf_delta_workspace_size", _LinattnShape, fields, int(keep), dev)
-        launch(load().semicrf_delta_fwd, dev, ctypes.byref(_LinattnShape(*fields)), keep, _ptr(q),
-               _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(lengths), _ptr(state), _ptr(o),
-               _ptr(last), _ptr(ws), n)
-        ctx.save_for_backward(*saved, ws)
+        o, last, work = _delta(q, k, v, log_decay, beta, state, lengths, dims, scale, 1)
+        ctx.save_for_backward(q, k, v, log_decay, beta, lengths, work)
         return o, last
 
     @staticmethod
@@ -400,7 +405,7 @@ class GatedDelta(torch.autograd.Function):
                _ptr(k), _ptr(v), _ptr(log_decay), _ptr(beta), _ptr(lengths), _ptr(work), _ptr(do),
                _ptr(dlast), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(db), _ptr(dstate),
                _ptr(ws), n)
-        return dq, dk, dv, dg, db, dstate, None, None, None, None
+        return dq, dk, dv, dg, db, dstate, None, None, None
 
 
 def gated_delta(q, k, v, log_decay, beta, lengths=None, state=None, scale=None,
@@ -430,10 +435,12 @@ def gated_delta(q, k, v, log_decay, beta, lengths=None, state=None, scale=None,
             bad = ((lengths < 0) | (lengths > T))[:, None, None, None]
             last = torch.where(bad, math.nan, last)
     else:
-        keep = torch.is_grad_enabled() and any(
-            t is not None and t.requires_grad for t in (q, k, v, log_decay, beta, state))
-        o, last = GatedDelta.apply(q, k, v, log_decay, beta, state, lengths, dims,
-                                   Dk ** -0.5 if scale is None else float(scale), keep)
+        scale = Dk ** -0.5 if scale is None else float(scale)
+        args = q, k, v, log_decay, beta, state, lengths, dims, scale
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in args[:6]):
+            o, last = GatedDelta.apply(*args)
+        else:
+            o, last, _ = _delta(*args, 0)
     return (o, last) if return_state else o
 
 
@@ -541,6 +548,8 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", scale: float
                               or t.shape[:-2] != q.shape[:-2]):
             raise ValueError("%s must be a [B, T, heads, D] or [B, heads, D] %s tensor on %s, as "
                              "the other" % (name, q.dtype, dev))
+    if frequencies.requires_grad and torch.is_grad_enabled():
+        raise ValueError("frequencies are constants of the model: they get no gradient")
     D, n = q.shape[-1], frequencies.numel()
     _check("frequencies", frequencies, dev, torch.float64, (n,))
     if not 1 <= 2 * n <= D <= MAX_TURNED:
@@ -567,8 +576,10 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", scale: float
                               float(scale), False)[0]
     else:
         there = k is not None and k.numel() > 0
-        y, y2 = Rotary.apply(q, k if there else None, frequencies, positions,
-                             ROTARY_LAYOUTS[layout], float(scale), False)
+        recorded = torch.is_grad_enabled() and (q.requires_grad or there and k.requires_grad)
+        y, y2 = (Rotary.apply if recorded else _turn)(
+            q, k if there else None, frequencies, positions, ROTARY_LAYOUTS[layout], float(scale),
+            False)
         if k is not None and not there:
             y2 = k.clone()
     if single:

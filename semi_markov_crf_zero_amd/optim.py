@@ -41,6 +41,8 @@ MOMENT_TYPES = {torch.float8_e4m3fn: 0, torch.uint8: 1}  # codes of m; of the ro
 
 _dtype, _nbytes = operator.attrgetter("dtype"), operator.attrgetter("nbytes")
 _numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
+_layout = operator.attrgetter("layout")
+_TWICE = "a gradient is there twice, whole or in part: it would be scaled twice"
 _get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
 
@@ -389,7 +391,7 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
         raise ValueError("gradients are normed on the GPU only; got a %s tensor" % dev.type)
     dtypes = list(map(_dtype, grads))
     if (not set(dtypes) <= DTYPES.keys() or set(map(_get_device, grads)) != {dev.index}
-            or any(g.layout != torch.strided for g in grads)):
+            or set(map(_layout, grads)) != {torch.strided}):
         raise ValueError("gradients must be dense float32, bfloat16 or float16 tensors on one GPU")
     # a copy of what is not contiguous is scaled in its place and copied back
     flat = grads if all(map(_is_contiguous, grads)) else [g.contiguous() for g in grads]
@@ -402,11 +404,18 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
     # the partials, then the norm and the coefficient
     work = torch.empty(size.value // 4 + 2, dtype=torch.float32, device=dev)
     out = work.data_ptr() + size.value
-    if clip and _overlap(flat):
-        raise ValueError("a gradient is there twice, whole or in part: it would be scaled twice")
-    launch(lib.semicrf_grad_norm, dev, at.buffer_info()[0], sizes.buffer_info()[0],
-           bytes(map(DTYPES.get, dtypes)), n, order, max_norm, clip, out, out + 4, work.data_ptr(),
-           size.value)
+    if clip and flat is not grads and (
+            len(set(map(_data_ptr, grads))) < n
+            or any(torch._debug_has_internal_overlap(g) == 1 for g in grads)):
+        raise ValueError(_TWICE)
+    try:
+        launch(lib.semicrf_grad_norm, dev, at.buffer_info()[0], sizes.buffer_info()[0],
+               bytes(map(DTYPES.get, dtypes)), n, order, max_norm, clip, out, out + 4,
+               work.data_ptr(), size.value)
+    except bd.SemiCRFError as e:
+        if clip and e.code == 6:  # the one argument that was not looked at above
+            raise ValueError(_TWICE) from None
+        raise
     if clip:
         if flat is not grads:
             for g, f in zip(grads, flat):

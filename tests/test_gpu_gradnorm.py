@@ -149,7 +149,11 @@ def test_shared_memory_is_refused():
         optim.clip_grad_norm_([p, q], 1.0)
     with pytest.raises(ValueError, match="twice"):
         optim.clip_grad_norm_([p, p], 1.0)
-    assert (flat == 1).all()
+    w = torch.zeros((4, 4), device=DEV, requires_grad=True)
+    w.grad = torch.ones((1, 4), device=DEV).expand(4, 4)
+    with pytest.raises(ValueError, match="twice"):
+        optim.clip_grad_norm_([w], 1.0)
+    assert (flat == 1).all() and (w.grad == 1).all()
     assert float(optim.grad_norm([p, q])) == pytest.approx(math.sqrt(200))
 
 
