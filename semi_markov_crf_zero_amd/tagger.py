@@ -9,16 +9,23 @@ position.
               by itself, a group a head
     emissions linear
 
+With memory="delta" attention is the gated delta rule: keys and queries of
+length 1, decays and shares of a write from a linear layer (a memory of 8 to
+2048 positions over the heads at the start).  With rotary=True keys and queries
+are turned by their positions.
+
 The front's norm runs over a whole sequence, or, with causal=True, over each
 position by itself: then every position depends on those before it only, and
 `step` gives for a stream what `emissions` gives for the sequence.
 
     model = SemiCRFTagger(features=40, channels=128, labels=16, max_duration=32).cuda()
     opt = optim.AdamW(model.parameters(), lr=1e-3, bits=8)
-    loss = model.loss(x, lengths, gold).mean(); loss.backward(); opt.step()
+    loss = model.loss(x, lengths, gold).mean(); loss.backward()
+    norm, clip = optim.grad_norm(model.parameters(), max_norm=1.0); opt.step(grad_scale=clip)
     segments = model.decode(x, lengths)
 
     python -m semi_markov_crf_zero_amd.tagger --steps 60     # synthetic segments
+    python -m semi_markov_crf_zero_amd.tagger --memory delta --rotary --clip 1.0
 """
 from __future__ import annotations
 
@@ -26,40 +33,59 @@ import torch
 from torch import nn
 
 from . import binding as bd
-from .encoder import group_norm, linear_attention, linear_attention_step
+from .encoder import (gated_delta, gated_delta_step, group_norm, linear_attention,
+                      linear_attention_step, rotary, rotary_frequencies)
 from .training import semicrf_nll
 
 
 class _Layer(nn.Module):
-    def __init__(self, channels, dtype):
+    def __init__(self, channels, dtype, gates=None):
+        """gates: the log decays that a delta layer's heads start from."""
         super().__init__()
         self.qkv = nn.Linear(channels, 3 * channels, bias=False, dtype=dtype)
         self.weight = nn.Parameter(torch.ones(channels))
         self.bias = nn.Parameter(torch.zeros(channels))
         self.out = nn.Linear(channels, channels, dtype=dtype)
+        self.gates = None
+        if gates is not None:
+            # log decay = -softplus(first half), share of a write = sigmoid(second half)
+            self.gates = nn.Linear(channels, 2 * len(gates), dtype=dtype)
+            with torch.no_grad():
+                self.gates.weight.mul_(0.1)
+                self.gates.bias[:len(gates)] = torch.log(torch.expm1(-gates.double())).to(dtype)
+                self.gates.bias[len(gates):] = 0.0
 
 
 class SemiCRFTagger(nn.Module):
     """dtype: of the linear layers and what flows between them (float32,
     bfloat16 or float16); norms' parameters, states, emissions and the head
-    are float32."""
+    are float32.  memory: "linear" (linear attention with fixed decays) or
+    "delta" (the gated delta rule)."""
 
     def __init__(self, features: int, channels: int, labels: int, max_duration: int,
                  heads: int = 4, layers: int = 2, groups: int = 8, causal: bool = False,
-                 dtype=torch.float32):
+                 dtype=torch.float32, memory: str = "linear", rotary: bool = False):
         super().__init__()
+        if memory not in ("linear", "delta"):
+            raise ValueError('memory must be "linear" or "delta"')
         if channels % heads or channels % groups:
             raise ValueError("heads and groups must divide the channels")
         self.heads, self.groups, self.causal, self.dtype = heads, groups, causal, dtype
         self.front = nn.Linear(features, channels, dtype=dtype)
         self.weight = nn.Parameter(torch.ones(channels))
         self.bias = nn.Parameter(torch.zeros(channels))
-        self.layers = nn.ModuleList(_Layer(channels, dtype) for _ in range(layers))
+        memories = torch.logspace(3, 11, heads, base=2.0) if heads > 1 else torch.tensor([128.0])
+        decays = torch.log1p(-1.0 / memories)
+        self.layers = nn.ModuleList(_Layer(channels, dtype, decays if memory == "delta" else None)
+                                    for _ in range(layers))
         self.emit = nn.Linear(channels, labels, dtype=dtype)
         self.trans = nn.Parameter(torch.zeros(labels, labels))
         self.dur = nn.Parameter(torch.zeros(max_duration, labels))
-        memory = torch.logspace(3, 11, heads, base=2.0) if heads > 1 else torch.tensor([128.0])
-        self.register_buffer("log_decay", torch.log1p(-1.0 / memory))
+        self.register_buffer("log_decay", decays)
+        if rotary and channels // heads < 2:
+            raise ValueError("heads of one channel cannot be turned")
+        self.register_buffer("frequencies", rotary_frequencies(channels // heads // 2 * 2)
+                             if rotary else None, persistent=False)
 
     def _norm(self, x, groups, weight, bias, act, lengths=None, alone=True):
         """The norm of each position by itself, or over the sequence."""
@@ -68,10 +94,27 @@ class SemiCRFTagger(nn.Module):
         flat = x.reshape(-1, 1, x.shape[-1])
         return group_norm(flat, groups, weight, bias, activation=act).view(x.shape)
 
-    def emissions(self, x, lengths=None, states=None):
+    def _mixed(self, layer, h, positions):
+        """A layer's queries, keys and values of h [..., channels], and the
+        delta rule's log decays and betas."""
+        dim = h.dim() - 1
+        q, k, v = layer.qkv(h).unflatten(-1, (3, self.heads, -1)).unbind(dim)
+        gates = ()
+        if layer.gates is not None:
+            q, k = (nn.functional.normalize(t.float(), dim=-1).to(t.dtype) for t in (q, k))
+            a, b = layer.gates(h).float().unflatten(-1, (2, self.heads)).unbind(dim)
+            gates = -nn.functional.softplus(a), torch.sigmoid(b)
+        if self.frequencies is not None:
+            q, k = rotary(q, k, self.frequencies, positions=positions)
+        return q, k, v, gates
+
+    def emissions(self, x, lengths=None, states=None, starts=None):
         """Emissions [B, T, labels] float32 of x [B, T, F], and the layers'
         states after each sequence.  lengths [B] int32; states, a list as
-        returned, continues sequences (causal models)."""
+        returned, continues sequences (causal models), with rotary from
+        position starts [B] int32 on."""
+        if self.frequencies is not None and states is not None and starts is None:
+            raise ValueError("a rotary tagger continues sequences from given starts")
         if lengths is not None:
             # the linear layers run over the padding too: what it holds (NaN as well) times
             # a gradient of 0 must be 0
@@ -81,10 +124,10 @@ class SemiCRFTagger(nn.Module):
                        lengths, self.causal)
         after = []
         for i, layer in enumerate(self.layers):
-            q, k, v = layer.qkv(h).unflatten(-1, (3, self.heads, -1)).unbind(2)
-            o, state = linear_attention(q, k, v, self.log_decay, lengths=lengths,
-                                        state=None if states is None else states[i],
-                                        return_state=True)
+            q, k, v, gates = self._mixed(layer, h, starts)
+            attention, gates = (gated_delta, gates) if gates else (linear_attention, (self.log_decay,))
+            o, state = attention(q, k, v, *gates, lengths=lengths,
+                                 state=None if states is None else states[i], return_state=True)
             after.append(state)
             h = h + layer.out(self._norm(o.flatten(2), self.heads, layer.weight, layer.bias, "none"))
         return self.emit(h).float(), after
@@ -107,16 +150,22 @@ class SemiCRFTagger(nn.Module):
                 for _ in self.layers]
 
     @torch.no_grad()
-    def step(self, x, states, slots=None):
+    def step(self, x, states, slots=None, positions=None):
         """Emissions [B, labels] of the next position x [B, F] of B streams
         (causal models); moves the streams' rows of the pools in `states`.
-        slots [B] int32: each stream's row (its own number by default)."""
+        slots [B] int32: each stream's row (its own number by default);
+        positions [B] int32 where rotary: how many each has taken before."""
         if not self.causal:
             raise ValueError("only a causal tagger can take single positions")
+        if self.frequencies is not None and positions is None:
+            raise ValueError("a rotary tagger needs the streams' positions")
         h = self._norm(self.front(x.to(self.dtype)), self.groups, self.weight, self.bias, "silu")
         for layer, state in zip(self.layers, states):
-            q, k, v = layer.qkv(h).unflatten(-1, (3, self.heads, -1)).unbind(1)
-            o = linear_attention_step(q, k, v, self.log_decay, state, slots=slots)
+            q, k, v, gates = self._mixed(layer, h, positions)
+            if gates:
+                o = gated_delta_step(q, k, v, *gates, state, slots=slots)
+            else:
+                o = linear_attention_step(q, k, v, self.log_decay, state, slots=slots)
             h = h + layer.out(self._norm(o.flatten(1), self.heads, layer.weight, layer.bias, "none"))
         return self.emit(h).float()
 
@@ -152,11 +201,14 @@ def main(argv=None):
     p = argparse.ArgumentParser(description="Trains a small tagger on synthetic segments.")
     p.add_argument("--steps", type=int, default=60)
     p.add_argument("--bits", type=int, default=32, choices=(32, 8))
+    p.add_argument("--memory", default="linear", choices=("linear", "delta"))
+    p.add_argument("--rotary", action="store_true")
+    p.add_argument("--clip", type=float, default=None, help="largest norm of the gradients")
     p.add_argument("--dtype", default="float32", choices=("float32", "bfloat16"))
     a = p.parse_args(argv)
     torch.manual_seed(0)
     dtype = getattr(torch, a.dtype)
-    model = SemiCRFTagger(24, 64, 8, 16, dtype=dtype).cuda()
+    model = SemiCRFTagger(24, 64, 8, 16, dtype=dtype, memory=a.memory, rotary=a.rotary).cuda()
     opt = optim.AdamW(model.parameters(), lr=3e-3, bits=a.bits, masters=dtype != torch.float32)
     losses = []
     for i in range(a.steps):
@@ -164,7 +216,10 @@ def main(argv=None):
         loss = (model.loss(x, lengths, gold) / lengths).mean()
         opt.zero_grad()
         loss.backward()
-        opt.step()
+        clip = None
+        if a.clip is not None:
+            _, clip = optim.grad_norm(model.parameters(), max_norm=a.clip)
+        opt.step(grad_scale=clip)
         losses.append(float(loss.detach()))
         if i % 10 == 0 or i == a.steps - 1:
             print("step %d: %.4f nats a position" % (i, losses[-1]), flush=True)
