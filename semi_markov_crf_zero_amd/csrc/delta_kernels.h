@@ -190,8 +190,8 @@ __device__ __forceinline__ f4 mfma32(float a, float b, f4 c) {
 
 }  // namespace
 
-// X = (I + diag(b) m)^-1 diag(b) and the gates of a chunk, a workgroup of four
-// waves each.  M = diag(b) m on the matrix cores; its 16 x 16 blocks on the diagonal
+// X = (I + diag(b) m)^-1 diag(b) (blocks of 32 up to the diagonal) and the gates of a
+// chunk, a workgroup of four waves each.  M = diag(b) m on the matrix cores; its 16 x 16 blocks on the diagonal
 // are inverted by substitution, a column a lane, and put together by
 //   (I + M)^-1 = [T1, 0; -T2 M21 T1, T2]
 // to 32 and 64 with float32 matrix instructions: what substitution gives, whatever
@@ -328,6 +328,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
   const int ld = p.ld;
   for (int e = threadIdx.x; e < ld * ld / 4; e += 256) {
     const int i = e / (ld / 4), j = e % (ld / 4) * 4;
+    if (j / 32 > i / 32) continue;  // not read
     f4 x = *reinterpret_cast<const f4 *>(M + i * LD + j);
 #pragma unroll
     for (int r = 0; r < 4; ++r) x[r] = j / 16 > i / 16 ? 0.f : x[r] * beta[j + r];

@@ -385,7 +385,7 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
     if not max_norm >= 0:
         raise ValueError("max_norm must not be negative")
     if not grads:
-        return torch.zeros(()), torch.ones(())
+        return torch.zeros(()), torch.ones(())  # on the host: no gradient names a device
     dev = grads[0].device
     if dev.type != "cuda":
         raise ValueError("gradients are normed on the GPU only; got a %s tensor" % dev.type)
@@ -401,17 +401,17 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
     rc = lib.semicrf_grad_norm_workspace_size(sizes.buffer_info()[0], n, ctypes.byref(size))
     if rc:
         raise bd.SemiCRFError(rc, "semicrf_grad_norm_workspace_size")
-    # the partials, then the norm and the coefficient
-    work = torch.empty(size.value // 4 + 2, dtype=torch.float32, device=dev)
-    out = work.data_ptr() + size.value
+    work = torch.empty(size.value, dtype=torch.uint8, device=dev)
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    coefficient = None if clip else torch.empty_like(norm)
     if clip and flat is not grads and (
             len(set(map(_data_ptr, grads))) < n
             or any(torch._debug_has_internal_overlap(g) == 1 for g in grads)):
         raise ValueError(_TWICE)
     try:
         launch(lib.semicrf_grad_norm, dev, at.buffer_info()[0], sizes.buffer_info()[0],
-               bytes(map(DTYPES.get, dtypes)), n, order, max_norm, clip, out, out + 4,
-               work.data_ptr(), size.value)
+               bytes(map(DTYPES.get, dtypes)), n, order, max_norm, clip, norm.data_ptr(),
+               None if clip else coefficient.data_ptr(), work.data_ptr(), size.value)
     except bd.SemiCRFError as e:
         if clip and e.code == 6:  # the one argument that was not looked at above
             raise ValueError(_TWICE) from None
@@ -422,7 +422,7 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
                 if g is not f:
                     g.copy_(f)
         increment_version(grads)  # a backward pass that saved the old values must fail
-    return work[-2], work[-1]
+    return norm, coefficient
 
 
 @torch.no_grad()

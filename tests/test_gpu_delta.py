@@ -603,3 +603,53 @@ def test_steps_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(got, want) and torch.equal(held, pool), i
+
+
+def test_many_short_sequences():
+    """2^20 sequences and heads of one position: o = scale (q . k) b v, and a state in."""
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    B, H, D = 1 << 18, 4, 8
+    q, k, v = (torch.randn((B, 1, H, D), device=DEV, generator=gen) for _ in range(3))
+    k = k / k.norm(dim=-1, keepdim=True)
+    g, b = -torch.rand((B, 1, H), device=DEV, generator=gen), torch.rand((B, 1, H), device=DEV, generator=gen)
+    o, last = encoder.gated_delta(q, k, v, g, b, return_state=True)
+    d = [t.double() for t in (q, k, v, b)]
+    want = D ** -0.5 * (d[0] * d[1]).sum(-1, keepdim=True) * d[3][..., None] * d[2]
+    assert ((o - want).abs() <= 64 * 2.0 ** -24 * (q.norm(dim=-1, keepdim=True) * v.abs())).all()
+    want = d[3][:, 0, :, None, None] * d[1][:, 0, :, :, None] * d[2][:, 0, :, None, :]
+    assert ((last - want).abs() <= 8 * 2.0 ** -24 * want.abs() + 2.0 ** -40).all()
+
+
+def test_infinities_in_what_is_masked():
+    """Infinite values past the lengths, and keys of 0 with infinite queries there."""
+    t = draw(23, 2, 80, (2, 2, 2), 32, 32, "bf16")
+    d = {n: x.to(DEV) for n, x in t.items()}
+    lt = torch.tensor([33, 64], dtype=torch.int32, device=DEV)
+    want = call(d, lt)
+    for b, n in enumerate([33, 64]):
+        for name in ("q", "k", "v"):
+            d[name][b, n:] = math.inf
+        d["g"][b, n:], d["b"][b, n:] = math.inf, -math.inf
+    got = call(d, lt)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gradients_over_segments(dtype):
+    """One sequence of few heads, cut into segments on the way: against the same in pieces of
+    64 positions, one segment each, tied by autograd."""
+    t = draw(24, 1, 1500, (1, 1, 1), 48, 40, dtype)
+    d = {n: x.to(DEV) for n, x in t.items()}
+    for n in NAMES:
+        d[n].requires_grad_(True)
+    o, last = call(d, None)
+    got = torch.autograd.grad((o, last), [d[n] for n in NAMES], (d["do"], d["ds"]))
+    parts, s = [], d["state"]
+    for i in range(0, 1500, 64):
+        x, s = call({**{n: y if n in ("state", "ds") else y[:, i:i + 64] for n, y in d.items()}, "state": s}, None)
+        parts.append(x)
+    x = torch.cat(parts, 1)
+    want = torch.autograd.grad((x, s), [d[n] for n in NAMES], (d["do"], d["ds"]))
+    tol = 2.0 ** -18 if dtype == "f32" else 2.0 ** -18 + 2 * ULP["bf16"]
+    for n, a, b in zip(("o", "last", *NAMES), (o, last, *got), (x, s, *want)):
+        assert (a.float() - b.float()).norm() <= tol * b.float().norm(), n
