@@ -345,6 +345,7 @@ template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_chunks(DeltaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
   constexpr int KB = DK / 32, NT = L / 16, JB = L / 32, NC = COMPOSE ? 2 : 1;
+  constexpr int TILES = NT * (NT + 1) / 2;
   typedef ByBoth<DK> LK;
   typedef ByRow<DK> LQ;
   typedef ByColumn<kCols> LV;
@@ -435,10 +436,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         if (16 * i + 4 * g < p.lk) *reinterpret_cast<f4 *>(to + 16 * i) = S[0][i];
     }
     if (!COMPOSE) {
-      // P, up to the diagonal, a tile a wave at a time
-      for (int t = w; t < NT * (NT + 1) / 2; t += NW) {
-        int it = 0, jt = t;
-        while (jt > it) jt -= ++it;
+      // P, up to the diagonal, a tile a wave at a time (of bfloat16 the last one again
+      // where they do not divide: without a branch, the chain's products go in between)
+#pragma unroll
+      for (int n = 0; n < (TILES + NW - 1) / NW; ++n) {
+        if (NP > 1 && w + n * NW >= TILES) break;
+        const int t = min(w + n * NW, TILES - 1);
+        const int it = (t > 0) + (t > 2) + (t > 5), jt = t - it * (it + 1) / 2;
         f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
@@ -621,7 +625,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_back(DeltaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
-  constexpr int KB = DK / 32, NT = L / 16, JB = L / 32;
+  constexpr int KB = DK / 32, NT = L / 16, JB = L / 32, TILES = NT * (NT + 1) / 2;
   typedef ByBoth<DK> LK;
   typedef ByColumn<kCols> LV;
   typedef ByBoth<L> LX;
@@ -704,10 +708,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
       for (int i = 0; i < 2 * KB; ++i)
         if (16 * i + 4 * g < p.lk) *reinterpret_cast<f4 *>(at + 16 * i) = D[i];
     }
-    // P, up to the diagonal, a tile a wave at a time
-    for (int t = w; t < NT * (NT + 1) / 2; t += NW) {
-      int it = 0, jt = t;
-      while (jt > it) jt -= ++it;
+    // P, as k_delta_chunks has it
+#pragma unroll
+    for (int n = 0; n < (TILES + NW - 1) / NW; ++n) {
+      if (NP > 1 && w + n * NW >= TILES) break;
+      const int t = min(w + n * NW, TILES - 1);
+      const int it = (t > 0) + (t > 2) + (t > 5), jt = t - it * (it + 1) / 2;
       f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb)
