@@ -195,7 +195,11 @@ __device__ __forceinline__ f4 mfma32(float a, float b, f4 c) {
 // are inverted by substitution, a column a lane, and put together by
 //   (I + M)^-1 = [T1, 0; -T2 M21 T1, T2]
 // to 32 and 64 with float32 matrix instructions: what substitution gives, whatever
-// the keys' lengths.
+// the keys' lengths.  65536 chunks of 64 keys of 64 in bfloat16: 480 to 510 us, 1.3 GB
+// read and written (2.6 TB/s).  A chunk is a chain of seven barriers, so occupancy counts: two
+// workgroups a compute unit took 920 us; four, with the inverse in M's place, 710; the
+// rest came from one wave for the diagonal's blocks, 16 lanes each, which left a
+// lane a quarter of the registers.
 template <typename T, int NP, int DK, int L>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k_delta_inverse(
     DeltaArgs p) {
@@ -341,6 +345,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
 // segment's transition phi, from I with values of 0, and of its sum, from 0: two
 // independent chains that read the same operands; else the outputs (and what the
 // backward pass reads again) from the state before it.
+//
+// A chunk of 64 x 64 in bfloat16 is 150 matrix instructions a wave (2400 cycles) and
+// 1260 vector ones, a third of them the splitting of S, R and U into parts.  2^20
+// positions of 4 heads, two workgroups of four waves a compute unit (80 KB of LDS):
+// 1.06 to 1.17 ms, 9 us a chunk, vector units busy 66 %; composing 0.89 to 0.96 ms, 85 %.
+// Measured on the way: addresses computed again in each chunk and no spilled register
+// 1.56 -> 1.20 ms; both chains in one wave when composing 1.19 -> 0.95; part2_dot in
+// the place of part2 3 % more.
 template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_chunks(DeltaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
@@ -621,7 +633,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 // The chunks of a segment from the last to the first, 16 columns of the gradient
 // of the state a wave.  COMPOSE: from 0 to what the segment adds; else from the
 // gradient after the segment, leaving that after each chunk in D, the gradients of
-// R in R and of the values in dv.
+// R in R and of the values in dv.  Bound as k_delta_chunks is: 16 x 4096 positions of 4
+// heads of 64 in bfloat16 99 us, composing 64 (80004 positions of 4 heads of 40 x 72 in
+// float32: 250 and 180).
 template <typename T, int NP, int DK, int NW, int L, bool COMPOSE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) void k_delta_back(DeltaArgs p) {
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
@@ -849,6 +863,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 // go in slices of 32.  dP and dM are computed by rows by the first and by columns
 // by the others: the accumulators' layout is then that of the operand they become,
 // and the triangles' rows and columns on a SIMD add up to the same.
+//
+// Bound by the wait for its loads: 4096 chunks of 64 x 64 in bfloat16 are 430 MB, 84 us
+// at a copy's rate, and take 130 with two workgroups of eight waves a compute unit; 185 with
+// four waves and all triangles twice, 177 with one workgroup, 225 with the next slice's
+// loads ahead (accumulators spilled).
 template <typename T, int NP, int DK, int L>
 __global__ __launch_bounds__(512)
     __attribute__((amdgpu_waves_per_eu(NP == 1 && DK > 64 ? 2 : 4))) void k_delta_grads(DeltaArgs p) {

@@ -8,6 +8,10 @@
 // for another) and scales; without clipping k_norm_end adds them alone.
 // Squares are exact in float64, whatever the magnitudes.  The tensors' addresses,
 // new in every step of a training loop, come with the kernel's arguments.
+//
+// Bound by HBM: 80 million bfloat16 elements in 64 tensors, 27 us for the norm (5.9 TB/s)
+// and 51 for scaling (6.3: part of them are in the last cache from the first pass); 1.5
+// million in 120 tensors 5 and 5.5 us, launches.
 #include <algorithm>
 #include <new>
 #include <vector>

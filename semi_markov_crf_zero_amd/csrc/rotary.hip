@@ -8,6 +8,12 @@
 // allows.  Angles are formed and reduced to a turn in float64 (at 2^20 a float32
 // angle is off by a 16th): r = z / 2 pi less its nearest whole number, sine and
 // cosine of r's float32 part and one term for the rest of it.
+//
+// Bound by HBM: 2^20 positions of 4 + 4 heads of 64 in bfloat16, half of each turned,
+// 2.15 GB: 402 to 411 us, 5.2 TB/s, a copy's rate.  Two loads a lane also where a
+// row is copied (one of them twice: 600 us), without branches around them (695 us).
+// 80004 positions of 4 + 2 heads of 40 in float32 28 to 33 us; 256 of 16 + 16 heads of 128
+// 5.5 us, a launch.
 #include "encoder.h"
 
 namespace semicrf {
