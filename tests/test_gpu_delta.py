@@ -653,3 +653,37 @@ def test_gradients_over_segments(dtype):
     tol = 2.0 ** -18 if dtype == "f32" else 2.0 ** -18 + 2 * ULP["bf16"]
     for n, a, b in zip(("o", "last", *NAMES), (o, last, *got), (x, s, *want)):
         assert (a.float() - b.float()).norm() <= tol * b.float().norm(), n
+
+
+def test_refusals():
+    x = torch.zeros((2, 5, 2, 8), device=DEV)
+    g = torch.zeros((2, 5, 2), device=DEV)
+    wide = torch.zeros((2, 5, 2, 129), device=DEV)
+    for args, kw in (((x, x, wide, g, g), {}), ((wide, wide, x, g, g), {}), ((x, x[:, :4], x, g, g), {}),
+                     ((x, x.half(), x, g, g), {}), ((x, x, x, g[..., :1], g), {}), ((x, x, x, g, g.half()), {}),
+                     ((x, x, x, g.cpu(), g), {}), ((x.double(), x.double(), x.double(), g, g), {}),
+                     ((x, x, x[:, :, :1].expand(2, 5, 3, 8), g, g), {}),
+                     ((x, x, x, g, g), dict(state=torch.zeros((2, 2, 8, 7), device=DEV))),
+                     ((x, x, x, g, g), dict(lengths=torch.zeros(2, device=DEV)))):
+        with pytest.raises(ValueError):
+            encoder.gated_delta(*args, **kw)
+    pool = torch.zeros((3, 2, 8, 8), device=DEV)
+    one = x[:, 0], x[:, 0], x[:, 0], g[:, 0], g[:, 0]
+    for args, kw in (((*one, pool[:, :1]), {}), ((*one, pool.half()), {}), ((*one, pool.transpose(2, 3)), {}),
+                     ((*one[:4], g, pool), {}), ((*one, pool), dict(slots=torch.zeros(2, device=DEV))),
+                     ((*one, pool.clone().requires_grad_(True)), {})):
+        with pytest.raises(ValueError):
+            encoder.gated_delta_step(*args, **kw)
+    assert not pool.any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("beta", [1.0, 1.95])
+def test_the_same_key_all_along(dtype, beta):
+    """Writes that undo each other: the triangles' inverses have entries that alternate
+    with hardly a decay."""
+    t = draw(25, 1, 200, (2, 2, 2), 32, 32, dtype)
+    t["k"] = t["k"][:, :1].expand(1, 200, 2, 32).contiguous()
+    t["g"] = t["g"] * 1e-3
+    t["b"] = torch.full_like(t["b"], beta)
+    compare(t, dtype)

@@ -208,3 +208,17 @@ def test_clipping_is_seen_by_autograd():
     optim.clip_grad_norm_([p], 0.5)
     with pytest.raises(RuntimeError, match="inplace operation"):
         y.backward()
+
+
+def test_refusals():
+    p = torch.zeros(4, device=DEV, requires_grad=True, dtype=torch.float64)
+    p.grad = torch.zeros(4, device=DEV, dtype=torch.float64)
+    q = torch.zeros(4, device=DEV, requires_grad=True)
+    q.grad = torch.zeros(4, device=DEV)
+    cpu = torch.zeros(4, requires_grad=True)
+    cpu.grad = torch.zeros(4)
+    for params in ([p], [q, p], [q, cpu]):
+        with pytest.raises(ValueError):
+            optim.grad_norm(params)
+    with pytest.raises(ValueError):
+        optim.grad_norm([q], norm_type=0.5)

@@ -210,3 +210,16 @@ def test_second_derivatives_are_refused():
     g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         g.square().sum().backward()
+
+
+def test_refusals():
+    q, k = torch.zeros((2, 5, 2, 8), device=DEV), torch.zeros((2, 5, 1, 8), device=DEV)
+    f = encoder.rotary_frequencies(8, device=DEV)
+    at = torch.zeros(2, dtype=torch.int32, device=DEV)
+    for args, kw in (((q, k[:, :4], f), {}), ((q, k.half(), f), {}), ((q, k[..., :6], f), {}),
+                     ((q, k, f.float()), {}), ((q, k, f.cpu()), {}), ((q[..., :6], k[..., :6], f), {}),
+                     ((q, k, f), dict(layout="other")), ((q, k, f), dict(positions=at.long())),
+                     ((q, k, f), dict(positions=at[:1])), ((q[:, 0], k[:, 0], f), {}), ((q[0, 0], None, f), {}),
+                     ((q, k, f.clone().requires_grad_(True)), {}), ((q.double(), None, f), {})):
+        with pytest.raises(ValueError):
+            encoder.rotary(*args, **kw)
