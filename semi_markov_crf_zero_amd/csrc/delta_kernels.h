@@ -358,6 +358,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
   constexpr int kCols = 16 * NW, kThreads = 64 * NW;
   constexpr int KB = DK / 32, NT = L / 16, JB = L / 32, NC = COMPOSE ? 2 : 1;
   constexpr int TILES = NT * (NT + 1) / 2;
+  // operands of three parts are not read far ahead (the barriers to the scheduler)
+  // where 128 rows of state leave no registers for them: 250 bytes a lane were spilled
+  // (4 x 8192 positions of 4 heads of 128 x 64: 333 -> 309 us)
+  constexpr bool kTight = NP == 3 && DK > 64;
   typedef ByBoth<DK> LK;
   typedef ByRow<DK> LQ;
   typedef ByColumn<kCols> LV;
@@ -492,6 +496,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
           const Frag<NP> kf = frag_row<NP, LK>(K, L * LK::row, 32 * jb + 16 * t, kb, lane);
 #pragma unroll
           for (int c = 0; c < NC; ++c) ks[c][t] = mma<3>(kf, sf[c][kb], ks[c][t]);
+          if (kTight) __builtin_amdgcn_sched_barrier(0);
         }
       }
       float v8[8];
@@ -514,7 +519,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         O[it] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
+        {
           O[it] = mma<3>(sf[0][kb], frag_row<NP, LQ>(Q, L * LQ::row, 16 * it, kb, lane), O[it]);
+          if (kTight) __builtin_amdgcn_sched_barrier(0);
+        }
         const float d = p.scale * gs.from[16 * it + l16];
 #pragma unroll
         for (int r = 0; r < 4; ++r) O[it][r] *= d;
@@ -565,6 +573,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
         const Frag<NP> kf = frag_col<NP, LK>(K, L * LK::row, 32 * jb, i, lane);
 #pragma unroll
         for (int c = 0; c < NC; ++c) S[c][i] = mma<3>(kf, tf[c], S[c][i]);
+        if (kTight) __builtin_amdgcn_sched_barrier(0);
       }
     }
     __syncthreads();

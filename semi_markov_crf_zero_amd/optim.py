@@ -41,7 +41,6 @@ MOMENT_TYPES = {torch.float8_e4m3fn: 0, torch.uint8: 1}  # codes of m; of the ro
 
 _dtype, _nbytes = operator.attrgetter("dtype"), operator.attrgetter("nbytes")
 _numel, _data_ptr = torch.Tensor.numel, torch.Tensor.data_ptr
-_layout = operator.attrgetter("layout")
 _TWICE = "a gradient is there twice, whole or in part: it would be scaled twice"
 _get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
@@ -377,7 +376,7 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
     """(norm, coefficient) of the parameters' gradients, scaled if clip."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
-    grads = [g for g in [p.grad for p in parameters] if g is not None]
+    grads = [g for p in parameters if (g := p.grad) is not None]
     order = NORMS.get(float(norm_type))
     if order is None:
         raise ValueError("the norm is 1, 2 or inf")
@@ -390,10 +389,10 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
     if dev.type != "cuda":
         raise ValueError("gradients are normed on the GPU only; got a %s tensor" % dev.type)
     dtypes = list(map(_dtype, grads))
-    if (not set(dtypes) <= DTYPES.keys() or set(map(_get_device, grads)) != {dev.index}
-            or set(map(_layout, grads)) != {torch.strided}):
+    if not set(dtypes) <= DTYPES.keys() or set(map(_get_device, grads)) != {dev.index}:
         raise ValueError("gradients must be dense float32, bfloat16 or float16 tensors on one GPU")
-    # a copy of what is not contiguous is scaled in its place and copied back
+    # a copy of what is not contiguous is scaled in its place and copied back (torch
+    # refuses the question for sparse gradients)
     flat = grads if all(map(_is_contiguous, grads)) else [g.contiguous() for g in grads]
     n = len(flat)
     at, sizes = array("Q", map(_data_ptr, flat)), array("q", map(_numel, flat))
