@@ -52,8 +52,8 @@ semicrf_status_t semicrf_delta_fwd(const semicrf_linattn_shape_t *shape, int kee
 
 /* Gradients given grad_o and grad_state = dL/dstate_out (or NULL: 0).
  * `saved` is the workspace of a forward call with keep as that call left it
- * (same shape, k, v, log_decay, beta, lengths and state_in).  grad_log_decay and grad_beta
- * [B][T][H] float32; the gradient of a log_decay below -104 (e^g is 0 in
+ * (same shape, k, v, log_decay, beta, lengths and state_in).  grad_log_decay and
+ * grad_beta [B][T][H] float32; the gradient of a log_decay below -104 (e^g is 0 in
  * float32) is 0.  lengths, grad_state and each output may be NULL (skipped). */
 semicrf_status_t semicrf_delta_bwd(const semicrf_linattn_shape_t *shape, const void *q,
                                    const void *k, const void *v, const float *log_decay,
@@ -117,7 +117,9 @@ semicrf_status_t semicrf_rotary(const semicrf_rotary_shape_t *shape, const void 
  * elements and types.  norm, coefficient: device floats, each may be NULL.
  * clip != 0: every element is then multiplied by the coefficient in float32
  * and rounded to its type, in place (tensors are left as they are where the
- * coefficient is 1). */
+ * coefficient is 1).  Tensors that share memory are then refused
+ * (SEMICRF_ERR_ARG): their addresses are sorted in host memory allocated for the
+ * call (SEMICRF_ERR_WORKSPACE where there is none). */
 enum { SEMICRF_NORM_MAX = 0, SEMICRF_NORM_1 = 1, SEMICRF_NORM_2 = 2 };
 
 semicrf_status_t semicrf_grad_norm_workspace_size(const int64_t *sizes, int count, size_t *bytes);
