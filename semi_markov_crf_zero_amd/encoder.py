@@ -18,7 +18,8 @@ and decays are float32, lengths and slots int32.  Outputs and workspaces are
 allocated with torch on the input's device and the work is enqueued on
 torch's current stream.  Positions at or past a sequence's length are never
 read into any result (they may hold NaN) and their rows of every output and
-gradient are 0; a length outside [0, T] gives NaN outputs and zero gradients.  There is no CPU fallback.
+gradient are 0; a length outside [0, T] gives NaN outputs and zero gradients (rotary has
+no lengths: it turns every row as it is).  There is no CPU fallback.
 """
 from __future__ import annotations
 
