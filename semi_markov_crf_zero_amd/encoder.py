@@ -12,9 +12,10 @@ group norm with an activation, channels last.
     y = group_norm(x, groups, weight, bias, lengths=lengths, activation="silu")
 
 The operators over sequences carry gradients (torch.autograd.Function over the
-library's backward entry points; a gradient of a gradient is refused); a step
-moves a pool of states in place and carries none.  Tensors are CUDA (HIP) tensors, float32, bfloat16 or float16; states, norms' weights
-and decays are float32, lengths and slots int32.  Outputs and workspaces are
+library's backward entry points; a gradient of a gradient, forward-mode tangents and,
+but for group norm, tracing are refused); a step moves a pool of states in place and
+carries none.  Tensors are CUDA (HIP) tensors, float32, bfloat16 or float16; states,
+norms' weights and decays are float32, lengths and slots int32.  Outputs and workspaces are
 allocated with torch on the input's device and the work is enqueued on
 torch's current stream.  Positions at or past a sequence's length are never
 read into any result (they may hold NaN) and their rows of every output and
@@ -28,6 +29,7 @@ import functools
 import math
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.graph import increment_version
 
 from . import binding as bd
@@ -141,6 +143,21 @@ def _check_device(t):
                          % t.device.type)
     if t.dtype not in DTYPES:
         raise ValueError("unsupported type %s (float32, bfloat16 or float16)" % t.dtype)
+
+
+def _refuse_tangents(*tensors):
+    if forward_ad._current_level >= 0 and any(
+            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+        raise NotImplementedError("the library's operators have no forward-mode derivatives")
+
+
+def refuse_modes(*tensors):
+    """Refuses what would otherwise go wrong without a word: a traced call (the graph
+    would hold its empty outputs and no operator) and forward-mode tangents (the result
+    would have none)."""
+    if torch._C._get_tracing_state() is not None:
+        raise RuntimeError("the library's operators cannot be traced")
+    _refuse_tangents(*tensors)
 
 
 def _rows(t):
@@ -312,6 +329,7 @@ def linear_attention(q, k, v, log_decay, lengths=None, state=None, scale=None,
     after each sequence's last position).  Gradients flow to q, k, v and
     state."""
     dims = _linattn_check(q, k, v, log_decay, False)
+    refuse_modes(q, k, v, log_decay, state)
     B, T, H, _, _, _, Dk, Dv, _ = dims
     if lengths is not None:
         _check("lengths", lengths, q.device, torch.int32, (B,))
@@ -339,6 +357,7 @@ def linear_attention_step(q, k, v, log_decay, state, slots=None, scale=None):
     result fails, and a state that requires a gradient is moved under
     torch.no_grad() only."""
     dims = _linattn_check(q, k, v, log_decay, True)
+    refuse_modes(q, k, v, log_decay, state)
     B, _, H, _, _, _, Dk, Dv, _ = dims
     dev = q.device
     N = _pool_check(state, slots, dims, dev)
@@ -422,6 +441,7 @@ def gated_delta(q, k, v, log_decay, beta, lengths=None, state=None, scale=None,
     -inf forgets) and how much of a write is taken, 0 to 1 (up to 2) for keys of
     length 1.  Gradients flow to q, k, v, log_decay, beta and state."""
     dims, log_decay, beta = _delta_check(q, k, v, log_decay, beta, False)
+    refuse_modes(q, k, v, log_decay, beta, state)
     B, T, H, _, _, _, Dk, Dv, _ = dims
     if lengths is not None:
         _check("lengths", lengths, q.device, torch.int32, (B,))
@@ -451,6 +471,7 @@ def gated_delta_step(q, k, v, log_decay, beta, state, slots=None, scale=None):
     Dk, Dv], slots, idle streams and gradients (none) are those of
     linear_attention_step."""
     dims, log_decay, beta = _delta_check(q, k, v, log_decay, beta, True)
+    refuse_modes(q, k, v, log_decay, beta, state)
     B, _, H, _, _, _, Dk, Dv, _ = dims
     dev = q.device
     N = _pool_check(state, slots, dims, dev)
@@ -542,6 +563,7 @@ def rotary(q, k, frequencies, positions=None, layout: str = "half", scale: float
     are turned like the others.  Returns (q', k'), or q' where k is None.
     Gradients flow to q and k."""
     _check_device(q)
+    refuse_modes(q, k, frequencies)
     dev, single = q.device, q.dim() == 3
     for name, t in (("q", q), ("k", k)):
         if t is not None and (t.dim() != q.dim() or q.dim() not in (3, 4) or t.dtype != q.dtype

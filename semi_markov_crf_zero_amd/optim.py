@@ -28,7 +28,7 @@ import torch
 from torch.autograd.graph import increment_version
 
 from . import binding as bd
-from .encoder import DTYPES, launch
+from .encoder import DTYPES, launch, refuse_modes
 
 EXPORTS = ("semicrf_adamw_table_size", "semicrf_adamw_table", "semicrf_adamw_step",
            "semicrf_adamw_values")
@@ -385,6 +385,7 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
         raise ValueError("max_norm must not be negative")
     if not grads:
         return torch.zeros(()), torch.ones(())  # on the host: no gradient names a device
+    refuse_modes(*grads)
     dev = grads[0].device
     if dev.type != "cuda":
         raise ValueError("gradients are normed on the GPU only; got a %s tensor" % dev.type)

@@ -1,0 +1,68 @@
+"""Forward-mode derivatives and traces of the operators' entry points: refused, whichever way a
+call takes past autograd.  No GPU: launches are recorded and not made."""
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from semi_markov_crf_zero_amd import encoder, optim
+
+
+@pytest.fixture
+def launched(monkeypatch):
+    made = []
+    monkeypatch.setattr(encoder, "_check_device", lambda t: None)
+    monkeypatch.setattr(encoder, "launch", lambda fn, dev, *args: made.append(fn.__name__))
+    return made
+
+
+def calls():
+    gen = torch.Generator().manual_seed(0)
+    q = torch.randn((2, 5, 2, 8), generator=gen)
+    g, b = -torch.rand((2, 5, 2), generator=gen), torch.rand((2, 5, 2), generator=gen)
+    f, decay = encoder.rotary_frequencies(8), torch.tensor([-0.1, -0.2])
+    pool, state = torch.zeros((2, 2, 8, 8)), torch.ones((2, 2, 8, 8))
+    return {
+        "linear_attention": (lambda q, g, s: encoder.linear_attention(q, q, q, g, state=s), (q, decay, state)),
+        "linear_attention_step": (lambda q, g, s: encoder.linear_attention_step(q, q, q, g, s),
+                                  (q[:, 0], decay, pool)),
+        "gated_delta": (lambda q, g, b, s: encoder.gated_delta(q, q, q, g, b, state=s), (q, g, b, state)),
+        "gated_delta_step": (lambda q, g, b, s: encoder.gated_delta_step(q, q, q, g, b, s),
+                             (q[:, 0], g[:, 0], b[:, 0], pool)),
+        "rotary": (lambda q, f: encoder.rotary(q, None, f), (q, f)),
+        "rotary of both": (lambda q, k: torch.cat(encoder.rotary(q, k, f)), (q, q + 1)),
+    }
+
+
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("name", list(calls()))
+def test_tangents_are_refused(name, grad, launched):
+    fn, args = calls()[name]
+    with torch.set_grad_enabled(grad):
+        for i in range(len(args)):
+            with forward_ad.dual_level():
+                x = list(args)
+                x[i] = forward_ad.make_dual(x[i], torch.ones_like(x[i]))
+                with pytest.raises(NotImplementedError):
+                    fn(*x)
+    assert not launched
+    with forward_ad.dual_level():  # a level without a tangent among the arguments
+        fn(*args)
+    assert len(launched) == 1
+
+
+@pytest.mark.parametrize("grad", [True, False])
+@pytest.mark.parametrize("name", list(calls()))
+def test_traces_are_refused(name, grad, launched):
+    fn, args = calls()[name]
+    with torch.set_grad_enabled(grad), pytest.raises(RuntimeError, match="cannot be traced"):
+        torch.jit.trace(fn, args, check_trace=False)
+    assert not launched
+
+
+def test_gradients_with_tangents_are_not_clipped():
+    p = torch.zeros(3, requires_grad=True)
+    with forward_ad.dual_level():
+        p.grad = forward_ad.make_dual(torch.ones(3), torch.ones(3))
+        for fn in (optim.clip_grad_norm_, optim.grad_norm):
+            with pytest.raises(NotImplementedError):
+                fn([p], 1.0)
