@@ -256,6 +256,7 @@ def _once(backward):
     gradients it came from carry any or not."""
     @functools.wraps(backward)
     def call(ctx, *grads):
+        _refuse_tangents(*grads)
         if not torch.is_grad_enabled():
             return backward(ctx, *grads)
         with torch.no_grad():

@@ -66,3 +66,20 @@ def test_gradients_with_tangents_are_not_clipped():
         for fn in (optim.clip_grad_norm_, optim.grad_norm):
             with pytest.raises(NotImplementedError):
                 fn([p], 1.0)
+
+
+@pytest.mark.parametrize("name", ["linear_attention", "gated_delta", "rotary", "group_norm"])
+def test_incoming_gradients_with_tangents_are_refused(name, launched):
+    """A tangent that comes in behind the operator would be lost on its way back."""
+    q = calls()["rotary"][1][0].requires_grad_(True)
+    if name == "group_norm":
+        y = encoder.group_norm(q.flatten(2), 4)
+    else:
+        fn, args = calls()[name]
+        y = fn(q, *args[1:])
+    forwards = len(launched)
+    with forward_ad.dual_level():
+        w = forward_ad.make_dual(torch.ones_like(y), torch.ones_like(y))
+        with pytest.raises(NotImplementedError):
+            torch.autograd.grad((y * w).sum(), q)
+    assert len(launched) == forwards == 1
