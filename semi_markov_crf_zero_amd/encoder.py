@@ -72,6 +72,7 @@ class _RotaryShape(ctypes.Structure):
 
 
 _lib = None
+_dispatch_mode, _PROXY = torch._C._get_dispatch_mode, torch._C._TorchDispatchModeKey.PROXY
 
 
 def load():
@@ -103,7 +104,10 @@ def _ptr(t):
 
 
 def launch(fn, dev, *args):
-    """fn(*args, stream) on `dev`'s current stream, with `dev` current."""
+    """fn(*args, stream) on `dev`'s current stream, with `dev` current.  Refused while a
+    graph of torch's operators is recorded from real tensors: the call would not be in it."""
+    if _dispatch_mode(_PROXY) is not None:
+        raise RuntimeError("the library's operators cannot be traced")
     was = torch._C._cuda_getDevice()
     if was == dev.index:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(was))

@@ -3,6 +3,7 @@ call takes past autograd.  No GPU: launches are recorded and not made."""
 import pytest
 import torch
 from torch.autograd import forward_ad
+from torch.fx.experimental.proxy_tensor import make_fx
 
 from semi_markov_crf_zero_amd import encoder, optim
 
@@ -83,3 +84,13 @@ def test_incoming_gradients_with_tangents_are_refused(name, launched):
         with pytest.raises(NotImplementedError):
             torch.autograd.grad((y * w).sum(), q)
     assert len(launched) == forwards == 1
+
+
+@pytest.mark.parametrize("mode", ["real", "fake"])
+@pytest.mark.parametrize("name", [*calls(), "group_norm"])
+def test_recorded_graphs_are_refused(name, mode, monkeypatch):
+    """Graphs of torch's operators, from real tensors too: the launch itself says no."""
+    monkeypatch.setattr(encoder, "_check_device", lambda t: None)
+    fn, args = calls().get(name, (lambda x: encoder.group_norm(x, 4), (torch.randn(2, 5, 8),)))
+    with pytest.raises(RuntimeError, match="cannot be traced" if mode == "real" else "data pointer"):
+        make_fx(fn, tracing_mode=mode)(*args)
