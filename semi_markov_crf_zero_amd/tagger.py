@@ -87,6 +87,15 @@ class SemiCRFTagger(nn.Module):
         self.register_buffer("frequencies", rotary_frequencies(channels // heads // 2 * 2)
                              if rotary else None, persistent=False)
 
+    def _apply(self, fn, recurse=True):
+        """Frequencies follow the device and keep their type, which rotary asks for: angles
+        of float32 ones are off by 2^-4 at position 2^20."""
+        held = self.frequencies
+        super()._apply(fn, recurse)
+        if held is not None and self.frequencies.dtype != held.dtype:
+            self.frequencies = held.to(self.frequencies.device)
+        return self
+
     def _norm(self, x, groups, weight, bias, act, lengths=None, alone=True):
         """The norm of each position by itself, or over the sequence."""
         if not alone:
