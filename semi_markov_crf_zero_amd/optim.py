@@ -404,8 +404,9 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
     work = torch.empty(size.value, dtype=torch.uint8, device=dev)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     coefficient = None if clip else torch.empty_like(norm)
+    there = [g for g in grads if g.numel()]  # empty ones are all at address 0
     if clip and flat is not grads and (
-            len(set(map(_data_ptr, grads))) < n
+            len(set(map(_data_ptr, there))) < len(there)
             or any(torch._debug_has_internal_overlap(g) == 1 for g in grads)):
         raise ValueError(_TWICE)
     try:
