@@ -24,6 +24,7 @@ import math
 import operator
 from array import array
 
+import numpy as np
 import torch
 from torch.autograd.graph import increment_version
 
@@ -372,6 +373,62 @@ class AdamW(torch.optim.Optimizer):
         self._plans = {}
 
 
+class _Layout:
+    """The memory of a tensor as numpy is told of it, which asks about addresses and reads
+    nothing."""
+
+    def __init__(self, t):
+        size = t.element_size()
+        self.__array_interface__ = {
+            "version": 3, "data": (t.data_ptr(), True), "typestr": "<u%d" % size,
+            "shape": tuple(t.shape), "strides": tuple(size * n for n in t.stride())}
+
+
+def _folded(t):
+    """Whether two elements of a tensor are one in memory."""
+    dims = sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1)
+    reach = 1
+    for s, n in dims:
+        if s < reach:  # dimensions that interlock: by counting
+            at = torch.zeros(1, dtype=torch.int64)
+            for s, n in dims:
+                at = (at[:, None] + s * torch.arange(n)).flatten()
+            return at.unique().numel() < t.numel()
+        reach += s * (n - 1)
+    return False
+
+
+def _shared(grads):
+    """Whether some memory is twice in these gradients where one of them is not contiguous (the
+    library looks at the others)."""
+    spans = []
+    for g in grads:
+        if not g.numel():  # empty ones are all at address 0
+            continue
+        start, size = g.data_ptr(), g.nbytes
+        inside = torch._debug_has_internal_overlap(g)  # 0: no, and no gaps; 1: yes
+        if inside:
+            last = sum((n - 1) * s for n, s in zip(g.shape, g.stride()))
+            if inside == 1 or last < g.numel() - 1 or _folded(g):
+                return True
+            size = g.element_size() * (last + 1)
+        spans.append((start, start + size, g, g.is_contiguous()))
+    spans.sort(key=operator.itemgetter(0))
+    before = []  # those that reach past the next one's start
+    for start, end, g, whole in spans:
+        before = [x for x in before if x[0] > start]
+        for _, h, w in before:
+            if w and whole:
+                continue
+            try:
+                if np.shares_memory(*(np.asarray(_Layout(t)) for t in (g, h)), max_work=1 << 20):
+                    return True
+            except np.exceptions.TooHardError:
+                return True
+        before.append((end, g, whole))
+    return False
+
+
 def _grad_norm(parameters, max_norm, norm_type, clip):
     """(norm, coefficient) of the parameters' gradients, scaled if clip."""
     if isinstance(parameters, torch.Tensor):
@@ -404,10 +461,7 @@ def _grad_norm(parameters, max_norm, norm_type, clip):
     work = torch.empty(size.value, dtype=torch.uint8, device=dev)
     norm = torch.empty((), dtype=torch.float32, device=dev)
     coefficient = None if clip else torch.empty_like(norm)
-    there = [g for g in grads if g.numel()]  # empty ones are all at address 0
-    if clip and flat is not grads and (
-            len(set(map(_data_ptr, there))) < len(there)
-            or any(torch._debug_has_internal_overlap(g) == 1 for g in grads)):
+    if clip and flat is not grads and _shared(grads):
         raise ValueError(_TWICE)
     try:
         launch(lib.semicrf_grad_norm, dev, at.buffer_info()[0], sizes.buffer_info()[0],
