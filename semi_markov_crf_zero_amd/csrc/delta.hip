@@ -282,7 +282,7 @@ semicrf_status_t check(const semicrf_linattn_shape_t *s) {
   // the chunks' workgroups of 512 threads are the most: segments are few where heads
   // are many
   const int64_t heads = (int64_t)s->B * s->H, chunks = (s->T + 31) / 32;
-  if (heads * chunks * 512 > kMaxThreads) return SEMICRF_ERR_SHAPE;
+  if (heads > kMaxThreads / (chunks * 512)) return SEMICRF_ERR_SHAPE;
   if (s->Dk > kMaxHead || s->Dv > kMaxHead) return SEMICRF_ERR_UNSUPPORTED;
   return dtype_ok(s->dtype) ? SEMICRF_OK : SEMICRF_ERR_ARG;
 }

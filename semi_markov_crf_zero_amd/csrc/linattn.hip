@@ -306,7 +306,7 @@ semicrf_status_t check(const semicrf_linattn_shape_t *s) {
     return SEMICRF_ERR_SHAPE;
   if (s->T > 1 << 30) return SEMICRF_ERR_SHAPE;
   const int64_t heads = (int64_t)s->B * s->H;
-  if (heads * 256 > kMaxThreads) return SEMICRF_ERR_SHAPE;  // the least a head takes
+  if (heads > kMaxThreads / 256) return SEMICRF_ERR_SHAPE;  // the least a head takes
   if (s->Dk > 256 || s->Dv > 256) return SEMICRF_ERR_UNSUPPORTED;
   if (!dtype_ok(s->dtype)) return SEMICRF_ERR_ARG;
   // segments are few where heads are many, so this counts the chunk kernel's
