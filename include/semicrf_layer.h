@@ -25,7 +25,7 @@ extern "C" {
  * at most 0 in use (-inf forgets everything before the position; larger
  * values grow as the formula says), b in [0, 1], up to 2, for keys of length
  * at most 1: the rule is then a contraction.  Longer keys with b |k|^2 > 2
- * make S grow as the formula says.  |b| below 2^-96 counts as 2^-96.
+ * make S grow as the formula says.  |b| below 2^-64 counts as 2^-64.
  *
  * The shape, the layout of q, k, v, o and their gradients, shared heads and
  * states are linear attention's.  1 <= Dk, Dv <= 128 (SEMICRF_ERR_UNSUPPORTED

@@ -29,7 +29,7 @@
 // segments, and each is walked from its own state.  The backward pass has its own
 // sums and phi^T.
 //
-// b = 0 would make the quotient in db 0 / 0: it counts as 2^-96, whose writes
+// b = 0 would make the quotient in db 0 / 0: it counts as 2^-64, whose writes
 // are below any rounding.  e^g below float32's range counts as e^-200.
 // G is summed in float64 and kept in two floats: no quotient of decays is formed.
 #include "delta_kernels.h"

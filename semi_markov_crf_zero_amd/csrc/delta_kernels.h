@@ -151,6 +151,12 @@ __device__ __forceinline__ int delta_fresh(int x) {
   return x;
 }
 
+// What a beta of 0 counts as.  The write and its gradient are this times the value's and the
+// incoming gradient's size and lose digits below 2^-126: those of up to 2^-62 keep theirs.
+__device__ __forceinline__ float least_beta(float b) {
+  return fabsf(b) < 0x1p-64f ? copysignf(0x1p-64f, b) : b;
+}
+
 // The tiles of 16 rows 2 b and 2 b + 1 of an accumulated matrix as an operand whose
 // contraction runs over them.
 template <bool DOT = false>
@@ -227,7 +233,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void k
       const int64_t e = ((int64_t)b * p.T + t0 + lane) * p.H + h;
       gi = p.log_decay[e], bt = p.beta[e];
       if (gi < -200.f) gi = -200.f;
-      if (fabsf(bt) < 0x1p-96f) bt = copysignf(0x1p-96f, bt);
+      bt = least_beta(bt);
     }
     double G = gi;
 #pragma unroll
@@ -935,7 +941,7 @@ __global__ __launch_bounds__(512)
   if (tid < L) {
     float bt = 1.f;
     if (tid < count) bt = p.beta[row0 + (int64_t)tid * p.H];
-    if (fabsf(bt) < 0x1p-96f) bt = copysignf(0x1p-96f, bt);
+    bt = least_beta(bt);
     inv[tid] = 1.f / bt;
   }
   if (tid < delta_gates(L)) (&gs.hi[0])[tid] = p.gates[at * delta_gates(L) + tid];
