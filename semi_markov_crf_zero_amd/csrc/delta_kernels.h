@@ -59,9 +59,9 @@ namespace {
 // part2 with one instruction for what an element's rounding leaves: the dot product
 // with (-1, 0) or (0, -1), which is exact (the same bits for 2^22 values of all
 // exponents).  Seven instructions in the place of eleven for a pair's three parts take
-// a little longer, but fewer registers: for the kernel that is short of them.  The
-// constants are kept from being folded into the instruction, whose literals are not
-// halves.
+// a little longer, but fewer registers: for the operands that k_delta_grads makes of its
+// accumulators, where it is short of them.  The constants are kept from being folded
+// into the instruction, whose literals are not halves.
 __device__ __forceinline__ b2 part2_dot(f2 &x) {
   unsigned first, second;
   asm("" : "=s"(first) : "0"(0x0000bf80u));
@@ -112,7 +112,7 @@ struct GatesTile {
 // A float32 matrix of `ROWS` rows (ld apart, 16 bytes aligned) and W columns, in three
 // parts in LDS, zeros past n rows and D columns (a multiple of 4); LOWER: blocks of
 // 32 above the diagonal are not read (nor written).
-template <typename Lay, int W, int ROWS, int NT, bool LOWER, bool DOT = false>
+template <typename Lay, int W, int ROWS, int NT, bool LOWER>
 struct Tile32 {
   static constexpr int per = W / 4, all = ROWS * per, N = (all + NT - 1) / NT;
   static constexpr int plane = ROWS * Lay::row;
@@ -926,8 +926,8 @@ __global__ __launch_bounds__(512)
   const T *go = (const T *)p.go + row0 * p.Dv;
   const float *u = p.U + at * L * p.Dv, *dr = p.R + at * L * p.Dv, *s = p.S + at * size,
               *ds = p.D + at * size;
-  Tile32<LU, L, 32, kThreads, false, true> tu, tr;
-  Tile32<LS, DK, 32, kThreads, false, true> ts, td;
+  Tile32<LU, L, 32, kThreads, false> tu, tr;
+  Tile32<LS, DK, 32, kThreads, false> ts, td;
   Tile<T, NP, LG, 32, L, kThreads> tg;
   Tile<T, NP, LK, DK, L, kThreads> tk, tq;
   auto fetch = [&](int c0) {
