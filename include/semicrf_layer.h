@@ -53,8 +53,9 @@ semicrf_status_t semicrf_delta_fwd(const semicrf_linattn_shape_t *shape, int kee
 /* Gradients given grad_o and grad_state = dL/dstate_out (or NULL: 0).
  * `saved` is the workspace of a forward call with keep as that call left it
  * (same shape, k, v, log_decay, beta, lengths and state_in).  grad_log_decay and
- * grad_beta [B][T][H] float32; the gradient of a log_decay below -104 (e^g is 0 in
- * float32) is 0.  lengths, grad_state and each output may be NULL (skipped). */
+ * grad_beta [B][T][H] float32; a log_decay's gradient is as small as e^g and keeps its
+ * digits down to float32's range, below -104 (e^g is 0 in float32) it is 0.  lengths,
+ * grad_state and each output may be NULL (skipped). */
 semicrf_status_t semicrf_delta_bwd(const semicrf_linattn_shape_t *shape, const void *q,
                                    const void *k, const void *v, const float *log_decay,
                                    const float *beta, const int32_t *lengths, const void *saved,

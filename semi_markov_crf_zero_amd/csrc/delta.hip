@@ -17,9 +17,13 @@
 //   dQ = scale E dO S^T + dP K
 //   dK = (dM K - E dR S^T) + (dP^T Q + dM^T K + diag(e^{G_L - G}) U dS'^T)
 //   db_i = (dR_i / b_i) . (U_i / b_i)
-// The first bracket of dK comes from k as what asks (its position decays from the
-// state: +G), the second from k as what is written (-G), so with c_i = q_i . dq_i +
-// k_i . (first - second), dg_i = sum_{j >= i} c_j + S' . dS' over the chunk.
+// and the gradient of a decay from what crosses its position,
+//   a_i = q_i . (scale E dO S^T)_i - k_i . (E dR S^T)_i    what i asks of the state,
+//   e_j = k_j . (diag(e^{G_L - G}) U dS'^T)_j              what j gives to the state after,
+//   W_ij = dP_ij q_i . k_j + dM_ij k_i . k_j               what j gives to i,
+//   dg_t = sum_{i >= t} a_i + sum_{j < t} e_j + sum_{i >= t > j} W_ij + e^{G_L} S . dS',
+// all of which has the factor e^{g_t}: a strong decay's gradient, as small as that, keeps its
+// digits (as sums of q . dq and k . dk, in which terms on one side of t cancel, it had none).
 //   k_delta_back      dS', dR and dV, the chunks one after another from the last;
 //   k_delta_grads     the rest, chunks side by side.
 //

@@ -194,6 +194,25 @@ __device__ __forceinline__ f4 mfma32(float a, float b, f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
 }
 
+// x of another lane, 0 where there is none.
+template <int CTRL, int ROWS = 15>
+__device__ __forceinline__ float lanes(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, ROWS, 15, false));
+}
+// Sums up to a lane, of its 16 or of all 64; of those before it.
+__device__ __forceinline__ float sum_row(float x) {
+  x += lanes<0x111>(x);  // 1, 2, 4, 8 lanes before
+  x += lanes<0x112>(x);
+  x += lanes<0x114>(x);
+  return x + lanes<0x118>(x);
+}
+__device__ __forceinline__ float sum_up(float x) {
+  x = sum_row(x);
+  x += lanes<0x142, 10>(x);  // the last of the row before, for the second and the fourth
+  return x + lanes<0x143, 12>(x);  // the 32nd, for the upper half
+}
+__device__ __forceinline__ float exclusive(float x) { return lanes<0x138>(x); }  // one before
+
 }  // namespace
 
 // X = (I + diag(b) m)^-1 diag(b) (blocks of 32 up to the diagonal) and the gates of a
@@ -879,10 +898,16 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 // by the others: the accumulators' layout is then that of the operand they become,
 // and the triangles' rows and columns on a SIMD add up to the same.
 //
+// The decays' gradients are sums over rectangles of a triangle (i >= t > j).  With rows and columns
+// in tiles of 16 they are what a row has from the tiles before its own, what a column has from
+// the tiles of rows below, a whole tile, and in the diagonal tile the product with a triangle of
+// ones on the matrix cores, then sums over 16 lanes: no scan along a row.
+//
 // Bound by the wait for its loads: 4096 chunks of 64 x 64 in bfloat16 are 430 MB, 84 us
-// at a copy's rate, and take 130 with two workgroups of eight waves a compute unit; 185 with
-// four waves and all triangles twice, 177 with one workgroup, 225 with the next slice's
-// loads ahead (accumulators spilled).
+// at a copy's rate, and take 136 with two workgroups of eight waves a compute unit (6 of them
+// for the decays' rectangles; 18 with scans by shuffles, 13 with 8-byte reads of the rows, which
+// conflict).  Before the rectangles: 130; 185 with four waves and all triangles twice, 177 with one
+// workgroup, 225 with the next slice's loads ahead (accumulators spilled).
 template <typename T, int NP, int DK, int L>
 __global__ __launch_bounds__(512)
     __attribute__((amdgpu_waves_per_eu(NP == 1 && DK > 64 ? 2 : 4))) void k_delta_grads(DeltaArgs p) {
@@ -892,7 +917,10 @@ __global__ __launch_bounds__(512)
   // registers for addresses; at DK = 128 a second workgroup has room without.
   typedef std::conditional_t<(DK <= 64), ByColumn<L>, ByBoth<L>> LU;
   typedef std::conditional_t<(DK <= 64), ByColumn<DK>, ByBoth<DK>> LS;
-  typedef ByColumn<DK> LK;
+  // keys and queries are read by rows and by columns: rows of one part 16 bytes at a time, which
+  // the padding serves, of more parts 8, for which padded rows would have four lanes on a bank
+  // (80004 positions of 4 heads of 40 x 72 in float32: 338 -> 325 us)
+  typedef std::conditional_t<(NP == 1), ByColumn<DK>, ByBoth<DK>> LK;
   constexpr int PU = 32 * LU::row, PS = 32 * LS::row;
   constexpr int kSlice = 6 * PU + 6 * PS + NP * L * LG::row;
   constexpr int kKeys = 2 * NP * L * LK::row, LW = DK + 4, kAfter = kKeys + 2 * L * LW;
@@ -904,8 +932,12 @@ __global__ __launch_bounds__(512)
   float *const dks = (float *)(tiles + kKeys);
   __shared__ Gates<L> gs;
   __shared__ alignas(16) float inv[L], dbs[8][L];
+  __shared__ float decays[L];
   __shared__ double red[8];
-  __shared__ float cs[2 * DS][L], es[DS][L];
+  // d g_t by its terms: what positions from t on ask of the state, what those before t
+  // give to the state after, and what those before t give to those from t on (by tiles
+  // of rows; a row's before its own tile)
+  __shared__ float as[DS][L], es[DS][L], rs[DS][NT][L], ps[DS][L];
 
   const int tid = threadIdx.x, w = tid >> 6;
   const int h = blockIdx.x % p.H, n = blockIdx.x / p.H % p.N, b = blockIdx.x / p.H / p.N;
@@ -939,10 +971,13 @@ __global__ __launch_bounds__(512)
     if (p.vec) tg.fetch(tid, go, (int)so, p.Dv, count, 0, 1, c0);
   };
   if (tid < L) {
-    float bt = 1.f;
-    if (tid < count) bt = p.beta[row0 + (int64_t)tid * p.H];
-    bt = least_beta(bt);
-    inv[tid] = 1.f / bt;
+    float bt = 1.f, gi = 0.f;
+    if (tid < count) {
+      const int64_t row = row0 + (int64_t)tid * p.H;
+      bt = p.beta[row], gi = p.log_decay[row];
+    }
+    inv[tid] = 1.f / least_beta(bt);
+    decays[tid] = gi;
   }
   if (tid < delta_gates(L)) (&gs.hi[0])[tid] = p.gates[at * delta_gates(L) + tid];
   const int pt = w % NT, part = w / NT / 2, d0 = part * DT;
@@ -1056,6 +1091,37 @@ __global__ __launch_bounds__(512)
     }
     return x;
   };
+  // products of this wave's rows of `rows` with the keys of tile t, times y; rows 16 bytes at a
+  // time where they are padded (any order of the contraction will do)
+  auto scores = [&](const bf16 *rows, int t, const f4 &y) {
+    f4 x = zero;
+#pragma unroll
+    for (int kb = 0; kb < DK / 32; ++kb) {
+      if constexpr (NP == 1) {
+        const int at = l16 * LK::row + 32 * kb + 8 * g;
+        x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            *reinterpret_cast<const bf8 *>(K + 16 * t * LK::row + at),
+            *reinterpret_cast<const bf8 *>(rows + 16 * pt * LK::row + at), x, 0, 0, 0);
+      } else {
+        x = mma<3>(frag_row<NP, LK>(K, L * LK::row, 16 * t, kb, lane),
+                   frag_row<NP, LK>(rows, L * LK::row, 16 * pt, kb, lane), x);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] *= y[r];
+    return x;
+  };
+  // sums of x over the 16 lanes that have the same four rows of tile t
+  auto columns = [&](float *out, int t, const f4 &x) {
+    const bool odd = l16 & 1, high = l16 & 2;
+    float a = odd ? x[2] : x[0], c = odd ? x[3] : x[1];
+    a += lanes<0xb1>(odd ? x[0] : x[2]), c += lanes<0xb1>(odd ? x[1] : x[3]);  // of lane ^ 1
+    float y = high ? c : a;
+    y += lanes<0x4e>(high ? a : c);  // ^ 2
+    y += lanes<0x124>(y);            // 4 and 8 further
+    y += lanes<0x128>(y);
+    if (l16 < 4) out[16 * t + 4 * g + 2 * odd + high] = y;
+  };
   auto give = [&](void *out, int whole, int i, const f4 &x) {
     const int d = 16 * (d0 + i) + 4 * g;
     if (mine >= count || d >= p.Dk) return;
@@ -1080,13 +1146,22 @@ __global__ __launch_bounds__(512)
         }
     }
   };
-  float c = 0.f;
   if (asks) {
     const float from = gs.from[mine];
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
       for (int r = 0; r < 4; ++r) a0[i][r] *= p.scale * from, a1[i][r] *= -from;
+    float c = 0.f;
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      const f4 kv = four(K, i), qv = four(Q, i);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) c += qv[r] * a0[i][r] + kv[r] * a1[i][r];
+    }
+#pragma unroll
+    for (int o = 16; o < 64; o <<= 1) c += __shfl_xor(c, o);
+    if (g == 0) as[part][mine] = c;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -1096,6 +1171,29 @@ __global__ __launch_bounds__(512)
         p0[t][r] *= p.scale * d;
         p1[t][r] *= o < mine ? -d : 0.f;
       }
+    // W_ij, what j gives to i: sums over the columns before each of the rows from it on in
+    // the diagonal tile, over rows and over columns in the others
+    float row = 0.f;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (t <= pt) {
+        f4 x = zero;
+        if (part == 0) x = scores(Q, t, p0[t]);
+        if (part == DS - 1) x += scores(K, t, p1[t]);
+        if (t == pt) {
+          f4 y = zero;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) y = mfma32(4 * g + r < l16 ? 1.f : 0.f, x[r], y);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) x[r] = 4 * g + r <= l16 ? y[r] : 0.f;
+        } else {
+          row += (x[0] + x[1]) + (x[2] + x[3]);
+        }
+        columns(rs[part][pt], t, x);
+      }
+#pragma unroll
+    for (int o = 16; o < 64; o <<= 1) row += __shfl_xor(row, o);
+    if (g == 0) ps[part][mine] = row;
 #pragma unroll
     for (int jb = 0; jb < JB; ++jb)
       if (2 * jb <= pt) {
@@ -1108,12 +1206,8 @@ __global__ __launch_bounds__(512)
         }
       }
 #pragma unroll
-    for (int i = 0; i < DT; ++i) {
-      const f4 kv = four(K, i), qv = four(Q, i);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) c += qv[r] * a0[i][r] + kv[r] * a1[i][r];
+    for (int i = 0; i < DT; ++i)
       if (p.dq) give(p.dq, p.part_q, i, a0[i]);
-    }
   } else {
     const float to = gs.to[mine];
     float e = 0.f;
@@ -1149,16 +1243,9 @@ __global__ __launch_bounds__(512)
         }
       }
 #pragma unroll
-    for (int i = 0; i < DT; ++i) {
-      const f4 kv = four(K, i);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) c -= kv[r] * a0[i][r];
+    for (int i = 0; i < DT; ++i)
       *reinterpret_cast<f4 *>(dks + mine * LW + 16 * (d0 + i) + 4 * g) = a0[i];
-    }
   }
-#pragma unroll
-  for (int o = 16; o < 64; o <<= 1) c += __shfl_xor(c, o);
-  if (g == 0) cs[w / NT][mine] = c;
   __syncthreads();
   if (asks && p.dk) {
 #pragma unroll
@@ -1177,29 +1264,32 @@ __global__ __launch_bounds__(512)
     p.db[row0 + (int64_t)lane * p.H] = x;
   }
   if (w == 7 && p.dg) {
-    double x = 0, y = 0;
+    const int tile = lane / 16;
+    float x = 0.f, y = 0.f, z = 0.f, own = 0.f, h[NT] = {};
     if (lane < L) {
 #pragma unroll
-      for (int i = 0; i < 2 * DS; ++i) x += cs[i][lane];
+      for (int i = 0; i < DS; ++i) {
+        x += as[i][L - 1 - lane], z += ps[i][L - 1 - lane], y += es[i][lane];
+        own += rs[i][tile][lane];
 #pragma unroll
-      for (int i = 0; i < DS; ++i) y += es[i][lane];
+        for (int t = 1; t < NT; ++t) h[t] += tile < t ? rs[i][t][lane] : 0.f;
+      }
     }
+    // sums from a position on, to the chunk's end and to its tile's; and up to it
+    x = sum_up(x) + sum_row(z);
+    double sum = own + exclusive(sum_up(y));
 #pragma unroll
-    for (int o = 32; o; o >>= 1) y += __shfl_xor(y, o);
+    for (int t = 1; t < NT; ++t) {
+      const float u = exclusive(sum_up(h[t]));
+      if (tile < t) sum += u;
+    }
+    sum += __shfl(x, (L - 1 - lane) & 63);
     double all = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) all += red[i];
-    y += ((double)gs.all + gs.low) * all;
-    // sums from a position to the chunk's end
-#pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-      const double z = __shfl_down(x, o);
-      if (lane + o < L) x += z;
-    }
-    if (lane < count) {
-      const int64_t row = row0 + (int64_t)lane * p.H;
-      p.dg[row] = p.log_decay[row] < -104.f ? 0.f : (float)(x + y);
-    }
+    sum += ((double)gs.all + gs.low) * all;
+    if (lane < count)
+      p.dg[row0 + (int64_t)lane * p.H] = decays[lane] < -104.f ? 0.f : (float)sum;
   }
 }
 
