@@ -73,6 +73,7 @@ class _RotaryShape(ctypes.Structure):
 
 _lib = None
 _dispatch_mode, _PROXY = torch._C._get_dispatch_mode, torch._C._TorchDispatchModeKey.PROXY
+_is_tracing = torch._C._is_tracing
 
 
 def load():
@@ -159,7 +160,7 @@ def refuse_modes(*tensors):
     """Refuses what would otherwise go wrong without a word: a traced call (the graph
     would hold its empty outputs and no operator) and forward-mode tangents (the result
     would have none)."""
-    if torch._C._get_tracing_state() is not None:
+    if _is_tracing():
         raise RuntimeError("the library's operators cannot be traced")
     _refuse_tangents(*tensors)
 
@@ -504,7 +505,8 @@ def rotary_frequencies(turn: int, base: float = 10000.0, stretch: float = 1.0,
     one by
 
         "linear"  dividing all of them by stretch;
-        "base"    raising the base so that the slowest is divided by stretch;
+        "base"    raising the base so that the slowest is divided by stretch (a single
+                  frequency, 1, stays);
         "bands"   dividing those that turn fewer than `slow` times in `context`
                   positions, leaving those that turn more than `fast` times, and
                   in between a mean of both, linear in the number of turns."""
