@@ -89,11 +89,16 @@ class SemiCRFTagger(nn.Module):
 
     def _apply(self, fn, recurse=True):
         """Frequencies follow the device and keep their type, which rotary asks for: angles
-        of float32 ones are off by 2^-4 at position 2^20."""
+        of float32 ones are off by 2^-4 at position 2^20.  A model made without memory
+        (on "meta") gets them with it: no state dict holds them."""
         held = self.frequencies
         super()._apply(fn, recurse)
-        if held is not None and self.frequencies.dtype != held.dtype:
-            self.frequencies = held.to(self.frequencies.device)
+        if held is not None:
+            dev = self.frequencies.device
+            if held.is_meta and dev.type != "meta":
+                self.frequencies = rotary_frequencies(2 * held.numel(), device=dev)
+            elif self.frequencies.dtype != held.dtype:
+                self.frequencies = held.to(dev)
         return self
 
     def _norm(self, x, groups, weight, bias, act, lengths=None, alone=True):

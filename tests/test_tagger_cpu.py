@@ -30,3 +30,12 @@ def test_other_devices_are_followed():
     model = make().to("meta", torch.float32)
     assert model.frequencies.device.type == "meta" and model.frequencies.dtype == torch.float64
     assert tagger.SemiCRFTagger(24, 64, 8, 16).float().frequencies is None
+
+
+def test_a_model_without_memory_gets_its_frequencies():
+    with torch.device("meta"):
+        model = make()
+    assert model.frequencies.is_meta
+    model = model.to_empty(device="cpu")
+    assert torch.equal(model.frequencies, encoder.rotary_frequencies(16))
+    assert torch.equal(model.to("cpu").frequencies, encoder.rotary_frequencies(16))
