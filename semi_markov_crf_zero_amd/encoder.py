@@ -151,8 +151,7 @@ def _check_device(t):
 
 
 def _refuse_tangents(*tensors):
-    if forward_ad._current_level >= 0 and any(
-            t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
+    if any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors):
         raise NotImplementedError("the library's operators have no forward-mode derivatives")
 
 
@@ -162,7 +161,8 @@ def refuse_modes(*tensors):
     would have none)."""
     if _is_tracing():
         raise RuntimeError("the library's operators cannot be traced")
-    _refuse_tangents(*tensors)
+    if forward_ad._current_level >= 0:
+        _refuse_tangents(*tensors)
 
 
 def _rows(t):
@@ -261,7 +261,8 @@ def _once(backward):
     gradients it came from carry any or not."""
     @functools.wraps(backward)
     def call(ctx, *grads):
-        _refuse_tangents(*grads)
+        if forward_ad._current_level >= 0:
+            _refuse_tangents(*grads)
         if not torch.is_grad_enabled():
             return backward(ctx, *grads)
         with torch.no_grad():
