@@ -904,7 +904,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2))) vo
 // ones on the matrix cores, then sums over 16 lanes: no scan along a row.
 //
 // Bound by the wait for its loads: 4096 chunks of 64 x 64 in bfloat16 are 430 MB, 84 us
-// at a copy's rate, and take 136 with two workgroups of eight waves a compute unit (6 of them
+// at a copy's rate, and take 136 to 139 with two workgroups of eight waves a compute unit (6 of them
 // for the decays' rectangles; 18 with scans by shuffles, 13 with 8-byte reads of the rows, which
 // conflict).  Before the rectangles: 130; 185 with four waves and all triangles twice, 177 with one
 // workgroup, 225 with the next slice's loads ahead (accumulators spilled).
@@ -914,7 +914,7 @@ __global__ __launch_bounds__(512)
   constexpr int NT = L / 16, JB = L / 32, DS = 4 / NT, DT = DK / 16 / DS, kThreads = 512;
   typedef ByRow<32> LG;
   // 32 columns of U and R as rows of L; of S and D of DK.  Padded, they take fewer
-  // registers for addresses; at DK = 128 a second workgroup has room without.
+  // registers for addresses; at DK = 128 a second workgroup has room without (but for one part).
   typedef std::conditional_t<(DK <= 64), ByColumn<L>, ByBoth<L>> LU;
   typedef std::conditional_t<(DK <= 64), ByColumn<DK>, ByBoth<DK>> LS;
   // keys and queries are read by rows and by columns: rows of one part 16 bytes at a time, which
